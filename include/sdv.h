@@ -198,6 +198,40 @@ int sdv_accept_greedy(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_ro
                       int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
                       int32_t *d_new_len, void *stream);
 
+/* Sampled acceptance: drafts verified against the target's probabilities, for
+ * drafters that draw from a distribution of their own. The pages accept by
+ * matching tokens (sdv_accept_greedy); this is the rejection rule of
+ * speculative sampling, whose committed tokens are distributed as the target's
+ * own samples whatever the drafter's distribution is.
+ * Row r of sequence b (temperature T_b) has p_r = softmax(logits_r / T_b), or
+ * for T_b <= 0 all on the lowest index of the maximum. The draft d in row r + 1
+ * was drawn from q_r = d_draft_probs[r]; NULL means each draft was certain
+ * (n-gram lookup, a table): q_r all on d. d is accepted iff
+ * uniform[r] * q_r(d) < p_r(d). m_b = the drafts accepted before the first
+ * refusal; the token committed after them is drawn at row m_b from
+ * max(p - q, 0) after a refusal (from p if nothing is left), from p at the
+ * span's last row: argmax_v w_v / noise[b][v], lowest index on a tie, a draw in
+ * proportion to w for exponential noise. Outputs, empty spans and loop state as
+ * sdv_accept_greedy, with the accepted drafts and then the drawn token as the
+ * committed ones; elements of d_committed past them keep what they held.
+ *   d_logits      [R] rows of fp32, logits_stride floats apart (>= vocab), as
+ *                 sdv_spec_forward writes them. -inf masks a token; NaN counts
+ *                 as -inf.
+ *   d_uniform     [R] fp32 in [0, 1), one for each row.
+ *   d_noise       [B] rows of fp32 > 0, noise_stride floats apart: draws of the
+ *                 exponential distribution, fresh for every call.
+ *   d_draft_probs [R] rows of fp32, probs_stride floats apart, or NULL (the
+ *                 stride is then ignored). The last row of a span is not read.
+ *   max_commit    row stride of d_committed; a span longer than it is refused.
+ * Device errors: a refused span (SDV_ERR_ARG; outputs as for an empty one); a
+ * draft outside [0, vocab) counts as refused and a row without a logit above
+ * -inf commits token 0 (SDV_ERR_DEVICE). Workspace: the context's. */
+int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_row_off, const float *d_logits,
+                       int64_t logits_stride, const float *d_temperature, const float *d_uniform,
+                       const float *d_noise, int64_t noise_stride, const float *d_draft_probs, int64_t probs_stride,
+                       int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
+                       int32_t *d_new_len, void *stream);
+
 /* [TS] SpecRewindCache; [PI] LIFO drop; [CA] rollback == do not advance.
  * Set each length to d_length[b] (< 0: leave b alone), which must not pass
  * the written length (else SDV_ERR_ARG in the device status, nothing
@@ -355,6 +389,87 @@ int sdv_paged_attention_noalloc(const void *d_q, const void *d_kv_layer, const i
  * sdv_paged_attention_noalloc call on it to *h_status (SDV_OK if none ran) and
  * clear it. Allocates nothing. The pages have no counterpart of this call. */
 int sdv_noalloc_status(int32_t *h_status);
+
+/* ---- 8-bit KV cache. The pages keep K and V in 16 bits; these calls hold them
+ * in e4m3 with a scale for each block of tokens and head, at half the bytes a
+ * token. A cache has its own pool, addressed through page tables that the
+ * caller keeps; those of sdv_page_table with the same page size, pool size and
+ * context limit serve both pools.
+ *   codes  [layer][page][K = 0, V = 1][kv_head][slot (page_size)][head_dim] e4m3
+ *   scales [layer][page][K, V][kv_head][page_size / scale_block] fp32
+ * Position p of sequence b lives in page table[b][p / page_size], slot
+ * p % page_size; its value is code * scale of the slot's block. Scales that the
+ * library writes are powers of two (2^-126 or more); attention and read take
+ * any positive finite scale. Codes must not be NaN (0x7f, 0xff): a NaN in a
+ * masked position would reach the rows that do not see it. sdv_qcache_write
+ * stores none.
+ * Spans are packed as everywhere: row row_off[b] + i is position base[b] + i of
+ * sequence b. A span longer than max_span or outside [0, max_rows) sets
+ * SDV_ERR_ARG, one past max_context SDV_ERR_CAPACITY: its rows are not written
+ * or read, and come back from attention as NaN. A page id outside
+ * [0, n_pages) sets SDV_ERR_CAPACITY and is not accessed; it reads as zeros. */
+#define SDV_BF16 0
+#define SDV_FP16 1
+#define SDV_FP32 2
+
+typedef struct sdv_qcache sdv_qcache; /* opaque; owns only host-side state */
+typedef struct {
+    int n_layers, n_q_heads, n_kv_heads, head_dim; /* head_dim 64 or 128; n_kv_heads divides n_q_heads */
+    int page_size, n_pages;                        /* tokens a page (any), pages in the pool */
+    int scale_block;                               /* tokens a scale; divides page_size */
+    int max_batch;                                 /* sequences a call, <= 256 */
+    int max_rows, max_span, max_context; /* rows of a call, rows of a sequence in it, positions of a sequence */
+} sdv_qcache_cfg;
+
+/* Bytes of the caller-owned buffers: codes and scales (16-byte aligned) and
+ * workspace (256-byte aligned; the status word and attention's partial
+ * results). Ask on the device that the cache will use. */
+int sdv_qcache_bytes(const sdv_qcache_cfg *cfg, size_t *codes, size_t *scales, size_t *workspace);
+
+/* Create a cache on the current device; clears codes and scales on `stream`.
+ * Later calls must be made with that device current (else SDV_ERR_ARG). Calls
+ * on one cache share its workspace: order them on one stream or by events,
+ * replays of captured graphs included. */
+int sdv_qcache_create(const sdv_qcache_cfg *cfg, void *d_codes, void *d_scales, void *d_workspace, void *stream,
+                      sdv_qcache **out);
+int sdv_qcache_destroy(sdv_qcache *cache);
+
+/* Quantise the rows of each span into their pages. d_k and d_v hold rows of
+ * [n_kv_heads][head_dim] of `dtype` (SDV_BF16, SDV_FP16, SDV_FP32), k_stride
+ * and v_stride elements apart. d_page_table is [B][ceil(max_context /
+ * page_size)]. Each block takes the smallest power of two with
+ * amax <= 448 * scale over the rows that this call writes to it; a block that
+ * the span starts inside of keeps its scale if that is larger, and where its
+ * scale grows the rows below the span are rounded again to the new one.
+ * Positions at or past the span's end (rejected drafts of an earlier write) do
+ * not count and are left as they are. With scale_block 1 a row's codes depend
+ * on the row alone, so rejected drafts leave no trace. An infinity is stored as
+ * +-448 scale and a NaN as zero, neither counts for the scale, and either sets
+ * SDV_ERR_DEVICE. Spans of one call must not share pages that they write. */
+int sdv_qcache_write(sdv_qcache *cache, int layer, const void *d_k, int64_t k_stride, const void *d_v, int64_t v_stride,
+                     int dtype, const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
+                     int max_span, void *stream);
+
+/* Read the rows of each span back: d_k, d_v as in sdv_qcache_write, as outputs.
+ * code * scale in fp32, rounded once to `dtype`. Rows of no span keep what they
+ * held. */
+int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, const int32_t *d_row_off,
+                    const int32_t *d_base, int B, int max_span, void *d_k, int64_t k_stride, void *d_v,
+                    int64_t v_stride, int dtype, void *stream);
+
+/* Paged attention over the codes, as sdv_op_attention over 16 bits: the row at
+ * position p attends positions 0..p, or max(0, p - window + 1)..p for
+ * window > 0; the span's own rows must have been written. d_q and d_out hold
+ * rows of [n_q_heads][head_dim] of `dtype` (SDV_BF16, SDV_FP16), q_stride and
+ * out_stride elements apart; q after RoPE; scores are q.k / sqrt(head_dim).
+ * A row's result depends on its own sequence, B, max_span and window only, not
+ * on the other sequences. */
+int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t q_stride, int dtype,
+                         const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
+                         int max_span, int window, void *d_out, int64_t out_stride, void *stream);
+
+/* As sdv_get_status, for the cache's own status word. */
+int sdv_qcache_get_status(sdv_qcache *cache, int32_t *h_status);
 
 /* Speculation cost governor ([TS] SpeculationCostGovernor and the paragraphs on
  * the shared governor): a host-side policy, one per (model, drafter, device),

@@ -32,9 +32,11 @@ from .pages import PagePool, CapacityError
 from .spec import accept_greedy, ngram_propose, adapt_k, ngram_propose_multi, required_order, NgramIndex
 from .loop import generate, StepRecord
 from .sampling import draw_rows, perturbed, gumbel, uniforms
+from .quant import QuantPool, accept_sampled, code_values, e4m3, needed_scale
 
 __all__ = [
     "DenseDecoder", "SeqCache", "round_bf16", "rmsnorm", "silu", "rope_neox", "attention_rows", "argmax_lowest",
     "PagePool", "CapacityError", "accept_greedy", "ngram_propose", "adapt_k", "generate", "StepRecord",
     "draw_rows", "perturbed", "gumbel", "uniforms", "ngram_propose_multi", "required_order", "NgramIndex",
+    "QuantPool", "accept_sampled", "code_values", "e4m3", "needed_scale",
 ]

@@ -33,6 +33,8 @@ EXPORTS = (
     "sdv_op_attention", "sdv_profile_enable", "sdv_profile_read", "sdv_paged_attention_noalloc",
     "sdv_fwd_trace", "sdv_noalloc_status", "sdv_ngram_params", "sdv_governor_create", "sdv_governor_destroy",
     "sdv_governor_decide", "sdv_governor_record", "sdv_governor_new_request", "sdv_governor_stats",
+    "sdv_accept_sampled", "sdv_qcache_bytes", "sdv_qcache_create", "sdv_qcache_destroy", "sdv_qcache_write",
+    "sdv_qcache_read", "sdv_qcache_attention", "sdv_qcache_get_status",
 )
 PHASES = ("prepare", "qkv_gemm", "attention", "o_gemm", "gateup_gemm", "down_gemm", "lmhead_gemm")
 # sdv_fwd_trace: stamps per CTA, CTAs per region (one region per launch of a forward)
@@ -56,6 +58,11 @@ class CacheCfg(ctypes.Structure):
     _fields_ = [("page_size", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_batch", ctypes.c_int),
                 ("max_rows", ctypes.c_int), ("max_span", ctypes.c_int), ("max_context", ctypes.c_int),
                 ("ngram_capacity", ctypes.c_int), ("ngram_max_order", ctypes.c_int)]
+
+
+class QCacheCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_layers", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                                            "scale_block", "max_batch", "max_rows", "max_span", "max_context")]
 
 
 class GovernorCfg(ctypes.Structure):
@@ -102,6 +109,15 @@ def lib():
     L.sdv_spec_forward.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp]
     L.sdv_spec_forward_sampled.argtypes = [vp, vp, vp, i32, i32, i32, vp, ctypes.c_uint64, vp, vp, vp]
     L.sdv_accept_greedy.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]
+    i64 = ctypes.c_int64
+    L.sdv_accept_sampled.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp]
+    L.sdv_qcache_bytes.argtypes = [P(QCacheCfg), P(sz), P(sz), P(sz)]
+    L.sdv_qcache_create.argtypes = [P(QCacheCfg), vp, vp, vp, vp, P(vp)]
+    L.sdv_qcache_destroy.argtypes = [vp]
+    L.sdv_qcache_write.argtypes = [vp, i32, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, vp]
+    L.sdv_qcache_read.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp]
+    L.sdv_qcache_attention.argtypes = [vp, i32, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp]
+    L.sdv_qcache_get_status.argtypes = [vp, P(ctypes.c_int32)]
     L.sdv_rewind_cache.argtypes = [vp, vp, i32, vp]
     L.sdv_cache_seq_len.argtypes = [vp, vp, vp]
     L.sdv_page_table.argtypes = [vp, vp, vp, vp, vp]
@@ -167,6 +183,30 @@ def _stream(stream) -> int:
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
+
+
+# Argument checks of the calls that take strides and types from their tensors. Plain comparisons of
+# attributes: they cost about as much as the ctypes call itself.
+def _expect(t, name, rows):
+    if t.shape[0] < rows:
+        raise ValueError(f"{name}: {t.shape[0]} rows, {rows} are needed")
+
+
+def _vector(t, n, name, dtype):
+    """A contiguous device tensor of at least n elements."""
+    import torch
+    if t.dtype is not getattr(torch, dtype) or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: a contiguous {dtype} device tensor of at least {n} elements is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _f32_rows(t, cols, name):
+    """Row stride of a device matrix of float32 rows of at least `cols` elements."""
+    import torch
+    if t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[1] < cols or t.stride(1) != 1:
+        raise ValueError(f"{name}: a float32 device matrix of rows of {cols} is needed, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
 
 
 def paged_attention_noalloc(q, kv_layer, page_table, pages_per_seq, page_size, n_pages, row_off, base, B,
@@ -297,6 +337,28 @@ class Verifier:
                                        _ptr(n_accept), _ptr(committed), _ptr(n_commit), _ptr(new_len),
                                        _stream(stream)), "accept_greedy")
 
+    def accept_sampled(self, tokens, row_off, logits, temperature, uniforms, noise, B, max_commit, n_accept, committed,
+                       n_commit, new_len, draft_probs=None, stream=None):
+        """Drafts verified against the target's probabilities (logits [R, vocab], temperature [B])
+        with the given random numbers: uniforms [R] in [0, 1) and exponential noise [B, vocab].
+        draft_probs [R, vocab]: the distribution each draft was drawn from, row r for the draft in
+        row r + 1; None: every draft was certain. All float32; the outputs as accept_greedy."""
+        V = self.mcfg.vocab
+        rows = _f32_rows(logits, V, "logits"), _f32_rows(noise, V, "noise")
+        q_stride = 0 if draft_probs is None else _f32_rows(draft_probs, V, "draft_probs")
+        _expect(noise, "noise", B)
+        if draft_probs is not None:
+            _expect(draft_probs, "draft_probs", min(logits.shape[0], self.ccfg.max_rows))
+        _vector(temperature, B, "temperature", "float32")
+        _vector(uniforms, min(logits.shape[0], self.ccfg.max_rows), "uniforms", "float32")
+        for t, n, name in ((row_off, B + 1, "row_off"), (n_accept, B, "n_accept"), (n_commit, B, "n_commit"),
+                           (new_len, B, "new_len"), (committed, B * max_commit, "committed"), (tokens, 1, "tokens")):
+            _vector(t, n, name, "int32")
+        _check(lib().sdv_accept_sampled(self.ctx, _ptr(tokens), _ptr(row_off), _ptr(logits), rows[0],
+                                        _ptr(temperature), _ptr(uniforms), _ptr(noise), rows[1], _ptr(draft_probs),
+                                        q_stride, B, max_commit, _ptr(n_accept), _ptr(committed), _ptr(n_commit),
+                                        _ptr(new_len), _stream(stream)), "accept_sampled")
+
     def rewind_cache(self, length, B, stream=None):
         _check(lib().sdv_rewind_cache(self.ctx, _ptr(length), B, _stream(stream)), "rewind_cache")
 
@@ -349,3 +411,97 @@ class Verifier:
     def op_attention(self, layer, q, row_off, base, B, max_span, out, stream=None):
         _check(lib().sdv_op_attention(self.ctx, layer, _ptr(q), _ptr(row_off), _ptr(base), B, max_span, _ptr(out),
                                       _stream(stream)), "op_attention")
+
+
+class QuantCache:
+    """A paged KV cache in e4m3 with a power-of-two scale for each block of `scale_block` tokens and
+    head: quantising writes, reads and attention over the codes. `codes` is the uint8 pool
+    [layer, page, K|V, kv head, slot, dim], `scales` float32 [layer, page, K|V, kv head, block]; page
+    tables are the caller's (int32 [B, pages_per_seq]). Calls on one cache share its workspace: order
+    them on one stream."""
+
+    def __init__(self, n_layers, n_q_heads, n_kv_heads, head_dim, page_size=16, n_pages=1024, max_batch=1, max_rows=32,
+                 max_span=17, max_context=4096, scale_block=16, stream=None):
+        import torch
+        self.cache = None
+        self.cfg = QCacheCfg(n_layers, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, scale_block, max_batch,
+                             max_rows, max_span, max_context)
+        sizes = [ctypes.c_size_t() for _ in range(3)]
+        _check(lib().sdv_qcache_bytes(ctypes.byref(self.cfg), *(ctypes.byref(n) for n in sizes)), "qcache_bytes")
+        self.codes = torch.empty(n_layers, n_pages, 2, n_kv_heads, page_size, head_dim, dtype=torch.uint8, device="cuda")
+        self.scales = torch.empty(n_layers, n_pages, 2, n_kv_heads, page_size // scale_block, dtype=torch.float32,
+                                  device="cuda")
+        self.workspace = torch.empty(sizes[2].value + 256, dtype=torch.uint8, device="cuda")
+        c = ctypes.c_void_p()
+        _check(lib().sdv_qcache_create(ctypes.byref(self.cfg), _ptr(self.codes), _ptr(self.scales),
+                                       (_ptr(self.workspace) + 255) // 256 * 256, _stream(stream), ctypes.byref(c)),
+               "qcache_create")
+        self.cache = c
+        self.pages_per_seq = -(-max_context // page_size)
+        self._dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        self._kv, self._q = (n_kv_heads, head_dim), (n_q_heads, head_dim)
+
+    def close(self):
+        if self.cache:
+            lib().sdv_qcache_destroy(self.cache)
+            self.cache = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _rows(self, t, heads, name, floats=3):
+        """(row stride, type) of a device tensor [R, heads, dim] with dense rows."""
+        kind = self._dtypes.get(t.dtype, floats)
+        st = t.stride() if t.dim() == 3 else None
+        if kind >= floats or not t.is_cuda or st is None or tuple(t.shape[1:]) != heads or st[2] != 1 or \
+                (heads[0] > 1 and st[1] != heads[1]):
+            raise ValueError(f"{name}: a device tensor [rows, {heads[0]}, {heads[1]}] with dense rows in "
+                             f"{'bf16 or fp16' if floats == 2 else 'bf16, fp16 or fp32'} is needed, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        width = heads[0] * heads[1]
+        return (st[0] if t.shape[0] > 1 else max(st[0], width)), kind
+
+    def _index(self, page_table, row_off, base, B):
+        _vector(page_table, B * self.pages_per_seq, "page_table", "int32")
+        _vector(row_off, B + 1, "row_off", "int32")
+        _vector(base, B, "base", "int32")
+
+    def write(self, layer, k, v, page_table, row_off, base, B, max_span, stream=None):
+        """Quantise rows k, v [R, n_kv_heads, head_dim] (bf16, fp16 or fp32) at positions base[b] + i."""
+        ks, kind = self._rows(k, self._kv, "k")
+        vs, same = self._rows(v, self._kv, "v")
+        if kind != same or k.shape[0] != v.shape[0]:
+            raise ValueError("k and v: one type and the same rows are needed")
+        self._index(page_table, row_off, base, B)
+        _check(lib().sdv_qcache_write(self.cache, layer, _ptr(k), ks, _ptr(v), vs, kind, _ptr(page_table),
+                                      _ptr(row_off), _ptr(base), B, max_span, _stream(stream)), "qcache_write")
+
+    def read(self, layer, page_table, row_off, base, B, max_span, k, v, stream=None):
+        """Read the rows at positions base[b] + i back into k, v [R, n_kv_heads, head_dim]."""
+        ks, kind = self._rows(k, self._kv, "k")
+        vs, same = self._rows(v, self._kv, "v")
+        if kind != same or k.shape[0] != v.shape[0]:
+            raise ValueError("k and v: one type and the same rows are needed")
+        self._index(page_table, row_off, base, B)
+        _check(lib().sdv_qcache_read(self.cache, layer, _ptr(page_table), _ptr(row_off), _ptr(base), B, max_span,
+                                     _ptr(k), ks, _ptr(v), vs, kind, _stream(stream)), "qcache_read")
+
+    def attention(self, layer, q, page_table, row_off, base, B, max_span, out, window=0, stream=None):
+        """Attention of the rows q [R, n_q_heads, head_dim] (bf16 or fp16) at positions base[b] + i over
+        their sequence's cache, into out of the same type."""
+        qs, kind = self._rows(q, self._q, "q", 2)
+        os_, same = self._rows(out, self._q, "out", 2)
+        if kind != same or q.shape[0] != out.shape[0]:
+            raise ValueError("q and out: one type and the same rows are needed")
+        self._index(page_table, row_off, base, B)
+        _check(lib().sdv_qcache_attention(self.cache, layer, _ptr(q), qs, kind, _ptr(page_table), _ptr(row_off),
+                                          _ptr(base), B, max_span, window, _ptr(out), os_, _stream(stream)),
+               "qcache_attention")
+
+    def get_status(self) -> int:
+        v = ctypes.c_int32()
+        _check(lib().sdv_qcache_get_status(self.cache, ctypes.byref(v)), "qcache_get_status")
+        return v.value

@@ -6,6 +6,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = [os.path.join(PKG, "csrc", "sdv_api.cu"), os.path.join(PKG, "csrc", "noalloc.cu"),
+       os.path.join(PKG, "csrc", "qcache.cu"),
        os.path.join(PKG, "csrc", "governor.cpp")]
 DEPS = [os.path.join(PKG, "csrc", f) for f in os.listdir(os.path.join(PKG, "csrc"))] + \
        [os.path.join(ROOT, "include", "sdv.h")]
@@ -31,7 +32,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "--threads", "4", "-std=c++17", "--shared", "-Xcompiler", "-fPIC",
            "-cudart", "shared", "-I", os.path.join(ROOT, "include"),
            *os.environ.get("SDV_NVCC_EXTRA", "").split(), *SRC, "-o", tmp]
     if verbose:

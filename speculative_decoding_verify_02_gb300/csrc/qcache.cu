@@ -1,0 +1,248 @@
+// C ABI of the 8-bit KV cache: quantising rows as they are written, reading them back, and attention
+// over the codes.
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "qcache_attention.cuh"
+
+using namespace sdv;
+
+struct sdv_qcache {
+    sdv_qcache_cfg c{};
+    int device = 0, sm_count = 0, pages_per_seq = 0;
+    uint8_t *codes = nullptr;
+    float *scales = nullptr;
+    uint8_t *ws = nullptr;
+    size_t layer_codes = 0, layer_scales = 0;
+};
+
+namespace {
+
+int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+int check_cfg(const sdv_qcache_cfg *c) {
+    if (!c) return SDV_ERR_ARG;
+    if (c->n_layers <= 0 || c->n_q_heads <= 0 || c->n_kv_heads <= 0 || c->n_q_heads % c->n_kv_heads) return SDV_ERR_ARG;
+    if (c->page_size <= 0 || c->n_pages <= 0 || c->scale_block <= 0 || c->page_size % c->scale_block)
+        return SDV_ERR_ARG;
+    if (c->max_batch <= 0 || c->max_batch > 256 || c->max_rows <= 0 || c->max_span <= 0 ||
+        c->max_span > c->max_rows || c->max_context < c->max_span)
+        return SDV_ERR_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return SDV_ERR_UNSUPPORTED;
+    if (c->n_q_heads > 1024 || c->max_rows > (1 << 20) || c->max_context > (1 << 30) || c->page_size > (1 << 20))
+        return SDV_ERR_UNSUPPORTED;
+    return SDV_OK;
+}
+
+size_t layer_codes(const sdv_qcache_cfg &c) {
+    return static_cast<size_t>(c.n_pages) * 2 * c.n_kv_heads * c.page_size * c.head_dim;
+}
+size_t layer_scales(const sdv_qcache_cfg &c) {
+    return static_cast<size_t>(c.n_pages) * 2 * c.n_kv_heads * (c.page_size / c.scale_block);
+}
+
+template <typename... KArgs, typename... Args>
+int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, void *stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? SDV_OK : SDV_ERR_CUDA;
+}
+
+// Arguments that every call shares, checked; SDV_OK and the kernels' block, or the error.
+int common_args(const sdv_qcache *q, int layer, const int32_t *table, const int32_t *row_off, const int32_t *base, int B,
+                int max_span, QCacheArgs *a) {
+    if (!q || !table || !row_off || !base || layer < 0 || layer >= q->c.n_layers || B <= 0 || B > q->c.max_batch ||
+        max_span <= 0 || max_span > q->c.max_span)
+        return SDV_ERR_ARG;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != q->device) return SDV_ERR_ARG;
+    a->codes = q->codes + q->layer_codes * layer;
+    a->scales = q->scales + q->layer_scales * layer;
+    a->status = reinterpret_cast<int *>(q->ws);
+    a->page_table = table;
+    a->row_off = row_off;
+    a->base = base;
+    a->pages_per_seq = q->pages_per_seq;
+    a->page_size = q->c.page_size;
+    a->n_pages = q->c.n_pages;
+    a->scale_block = q->c.scale_block;
+    a->nkv = q->c.n_kv_heads;
+    a->B = B;
+    a->max_span = max_span;
+    a->max_rows = q->c.max_rows;
+    a->max_context = q->c.max_context;
+    return SDV_OK;
+}
+
+size_t dtype_size(int dtype) { return dtype == SDV_FP32 ? 4 : 2; }
+bool aligned16(const void *p, int64_t stride, int dtype) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * static_cast<int64_t>(dtype_size(dtype)) % 16 == 0;
+}
+bool element_aligned(const void *p, int dtype) { return reinterpret_cast<uintptr_t>(p) % dtype_size(dtype) == 0; }
+
+template <typename T, int D>
+int write_rows(const QCacheArgs &a, const void *k, int64_t ks, const void *v, int64_t vs, bool vec, void *stream) {
+    const int blocks = (a.max_span + a.scale_block - 2) / a.scale_block + 1;  // a span touches at most
+    const dim3 grid(cdiv(static_cast<long long>(blocks) * 2 * a.nkv, kQWriteThreads / 32), a.B);
+    const T *kp = static_cast<const T *>(k), *vp = static_cast<const T *>(v);
+    const long long k_stride = ks, v_stride = vs;
+    return vec ? launch(qcache_write_kernel<T, D, true>, grid, kQWriteThreads, 0, stream, a, kp, vp, k_stride, v_stride)
+               : launch(qcache_write_kernel<T, D, false>, grid, kQWriteThreads, 0, stream, a, kp, vp, k_stride, v_stride);
+}
+
+template <typename T, int D>
+int read_rows(const QCacheArgs &a, void *k, int64_t ks, void *v, int64_t vs, bool vec, void *stream) {
+    const dim3 grid(cdiv(a.max_span, kQReadThreads / (D / 8)), a.B, 2 * a.nkv);
+    T *kp = static_cast<T *>(k), *vp = static_cast<T *>(v);
+    const long long k_stride = ks, v_stride = vs;
+    return vec ? launch(qcache_read_kernel<T, D, true>, grid, kQReadThreads, 0, stream, a, kp, vp, k_stride, v_stride)
+               : launch(qcache_read_kernel<T, D, false>, grid, kQReadThreads, 0, stream, a, kp, vp, k_stride, v_stride);
+}
+
+}  // namespace
+
+extern "C" {
+
+int sdv_qcache_bytes(const sdv_qcache_cfg *cfg, size_t *codes, size_t *scales, size_t *workspace) {
+    const int r = check_cfg(cfg);
+    if (r) return r;
+    if (!codes || !scales || !workspace) return SDV_ERR_ARG;
+    *codes = layer_codes(*cfg) * cfg->n_layers;
+    *scales = layer_scales(*cfg) * cfg->n_layers * sizeof(float);
+    *workspace = 256;
+    return SDV_OK;
+}
+
+int sdv_qcache_create(const sdv_qcache_cfg *cfg, void *d_codes, void *d_scales, void *d_workspace, void *stream,
+                      sdv_qcache **out) {
+    const int r = check_cfg(cfg);
+    if (r) return r;
+    if (!d_codes || !d_scales || !d_workspace || !out) return SDV_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(d_codes) % 16 || reinterpret_cast<uintptr_t>(d_scales) % 16 ||
+        reinterpret_cast<uintptr_t>(d_workspace) % 256)
+        return SDV_ERR_ARG;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SDV_ERR_CUDA;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, qcache_write_kernel<bf16, 128, true>) != cudaSuccess) {
+        cudaGetLastError();
+        return SDV_ERR_UNSUPPORTED;  // no sm_103a image for this device
+    }
+    sdv_qcache *q = new (std::nothrow) sdv_qcache();
+    if (!q) return SDV_ERR_ARG;
+    q->c = *cfg;
+    q->device = dev;
+    q->sm_count = sms;
+    q->pages_per_seq = cdiv(cfg->max_context, cfg->page_size);
+    q->codes = static_cast<uint8_t *>(d_codes);
+    q->scales = static_cast<float *>(d_scales);
+    q->ws = static_cast<uint8_t *>(d_workspace);
+    q->layer_codes = layer_codes(*cfg);
+    q->layer_scales = layer_scales(*cfg);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(q->codes, 0, q->layer_codes * cfg->n_layers, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(q->scales, 0, q->layer_scales * cfg->n_layers * sizeof(float), st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(q->ws, 0, 256, st);
+    if (e != cudaSuccess) {
+        delete q;
+        return SDV_ERR_CUDA;
+    }
+    *out = q;
+    return SDV_OK;
+}
+
+int sdv_qcache_destroy(sdv_qcache *cache) {
+    delete cache;
+    return SDV_OK;
+}
+
+int sdv_qcache_write(sdv_qcache *cache, int layer, const void *d_k, int64_t k_stride, const void *d_v, int64_t v_stride,
+                     int dtype, const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
+                     int max_span, void *stream) {
+    QCacheArgs a{};
+    const int r = common_args(cache, layer, d_page_table, d_row_off, d_base, B, max_span, &a);
+    if (r) return r;
+    const int D = cache->c.head_dim, width = cache->c.n_kv_heads * D;
+    if (dtype != SDV_BF16 && dtype != SDV_FP16 && dtype != SDV_FP32) return SDV_ERR_UNSUPPORTED;
+    if (!d_k || !d_v || k_stride < width || v_stride < width || !element_aligned(d_k, dtype) ||
+        !element_aligned(d_v, dtype))
+        return SDV_ERR_ARG;
+    const bool vec = aligned16(d_k, k_stride, dtype) && aligned16(d_v, v_stride, dtype);
+#define SDV_QWRITE(T)                                                                     \
+    return D == 128 ? write_rows<T, 128>(a, d_k, k_stride, d_v, v_stride, vec, stream) \
+                    : write_rows<T, 64>(a, d_k, k_stride, d_v, v_stride, vec, stream)
+    if (dtype == SDV_BF16) SDV_QWRITE(bf16);
+    if (dtype == SDV_FP16) SDV_QWRITE(__half);
+    SDV_QWRITE(float);
+#undef SDV_QWRITE
+}
+
+int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, const int32_t *d_row_off,
+                    const int32_t *d_base, int B, int max_span, void *d_k, int64_t k_stride, void *d_v,
+                    int64_t v_stride, int dtype, void *stream) {
+    QCacheArgs a{};
+    const int r = common_args(cache, layer, d_page_table, d_row_off, d_base, B, max_span, &a);
+    if (r) return r;
+    const int D = cache->c.head_dim, width = cache->c.n_kv_heads * D;
+    if (dtype != SDV_BF16 && dtype != SDV_FP16 && dtype != SDV_FP32) return SDV_ERR_UNSUPPORTED;
+    if (!d_k || !d_v || k_stride < width || v_stride < width || !element_aligned(d_k, dtype) ||
+        !element_aligned(d_v, dtype))
+        return SDV_ERR_ARG;
+    const bool vec = aligned16(d_k, k_stride, dtype) && aligned16(d_v, v_stride, dtype);
+#define SDV_QREAD(T)                                                                     \
+    return D == 128 ? read_rows<T, 128>(a, d_k, k_stride, d_v, v_stride, vec, stream) \
+                    : read_rows<T, 64>(a, d_k, k_stride, d_v, v_stride, vec, stream)
+    if (dtype == SDV_BF16) SDV_QREAD(bf16);
+    if (dtype == SDV_FP16) SDV_QREAD(__half);
+    SDV_QREAD(float);
+#undef SDV_QREAD
+}
+
+int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t q_stride, int dtype,
+                         const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
+                         int max_span, int window, void *d_out, int64_t out_stride, void *stream) {
+    QAttnArgs a{};
+    const int r = common_args(cache, layer, d_page_table, d_row_off, d_base, B, max_span, &a.c);
+    if (r) return r;
+    const int D = cache->c.head_dim, width = cache->c.n_q_heads * D;
+    if (dtype != SDV_BF16 && dtype != SDV_FP16) return SDV_ERR_UNSUPPORTED;
+    if (!d_q || !d_out || window < 0 || q_stride < width || out_stride < width || !element_aligned(d_q, dtype) ||
+        !element_aligned(d_out, dtype))
+        return SDV_ERR_ARG;
+    a.q = d_q;
+    a.out = d_out;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.nq = cache->c.n_q_heads;
+    a.window = window;
+    a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(D));
+    const dim3 grid(max_span, a.nq, B);
+    if (dtype == SDV_BF16)
+        return D == 128 ? launch(qcache_attn_simple_kernel<bf16, 128>, grid, kQSimpleThreads, 0, stream, a)
+                        : launch(qcache_attn_simple_kernel<bf16, 64>, grid, kQSimpleThreads, 0, stream, a);
+    return D == 128 ? launch(qcache_attn_simple_kernel<__half, 128>, grid, kQSimpleThreads, 0, stream, a)
+                    : launch(qcache_attn_simple_kernel<__half, 64>, grid, kQSimpleThreads, 0, stream, a);
+}
+
+int sdv_qcache_get_status(sdv_qcache *cache, int32_t *h_status) {
+    if (!cache || !h_status) return SDV_ERR_ARG;
+    if (cudaDeviceSynchronize() != cudaSuccess) return SDV_ERR_CUDA;
+    int v = 0;
+    const int zero = 0;
+    if (cudaMemcpy(&v, cache->ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return SDV_ERR_CUDA;
+    if (cudaMemcpy(cache->ws, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return SDV_ERR_CUDA;
+    *h_status = v;
+    return SDV_OK;
+}
+
+}  // extern "C"

@@ -9,6 +9,7 @@
 #include <new>
 #include <vector>
 
+#include "accept_sampled.cuh"
 #include "attention.cuh"
 #include "attention_group.cuh"
 #include "common.cuh"
@@ -118,6 +119,7 @@ struct sdv_ctx {
     float *attn_po = nullptr;
     float2 *attn_pml = nullptr;
     int *attn_cnt = nullptr;
+    float2 *accept_part = nullptr;  // sampled acceptance: chunk statistics of the logit rows
     int attn_splits = 1;
     int attn_group = kAttnGroup;  // key positions per attention group (1024, or 2048 for long sequences)
     int attn_lo = 1;  // attention products with hi/lo pairs (queries and probabilities)
@@ -306,8 +308,10 @@ size_t carve(const sdv_model_cfg &m, const sdv_cache_cfg &c, sdv_ctx *ctx, uint8
     float *apo = reinterpret_cast<float *>(take(sizeof(float) * nslots * D));
     float2 *apml = reinterpret_cast<float2 *>(take(sizeof(float2) * nslots));
     int *acnt = reinterpret_cast<int *>(take(sizeof(int) * static_cast<size_t>(B) * m.n_kv_heads * kAttnCluster));
+    auto *apart = reinterpret_cast<float2 *>(take(sizeof(float2) * kRowsCap * ceil_div(m.vocab, kAcceptChunk)));
 
     if (ctx) {
+        ctx->accept_part = apart;
         ctx->st = s;
         ctx->x = x;
         ctx->xb = xb;
@@ -1006,6 +1010,49 @@ int sdv_accept_greedy(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_ro
     p.n_commit = d_n_commit;
     p.new_len = d_new_len;
     return rc(launch(ctx, accept_kernel, dim3(ceil_div(B, 128)), dim3(128), 0, static_cast<cudaStream_t>(stream), p));
+}
+
+int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_row_off, const float *d_logits,
+                       int64_t logits_stride, const float *d_temperature, const float *d_uniform,
+                       const float *d_noise, int64_t noise_stride, const float *d_draft_probs, int64_t probs_stride,
+                       int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
+                       int32_t *d_new_len, void *stream) {
+    if (!ctx || !d_tokens || !d_row_off || !d_logits || !d_temperature || !d_uniform || !d_noise || !d_n_accept ||
+        !d_committed || !d_n_commit || !d_new_len)
+        return SDV_ERR_ARG;
+    if (B <= 0 || B > ctx->c.max_batch || max_commit <= 0 || logits_stride < ctx->m.vocab ||
+        noise_stride < ctx->m.vocab || (d_draft_probs && probs_stride < ctx->m.vocab))
+        return SDV_ERR_ARG;
+    AcceptSampledArgs p{};
+    p.s = ctx->st;
+    p.tokens = d_tokens;
+    p.row_off = d_row_off;
+    p.logits = d_logits;
+    p.temperature = d_temperature;
+    p.uniform = d_uniform;
+    p.noise = d_noise;
+    p.probs = d_draft_probs;
+    p.logits_stride = logits_stride;
+    p.noise_stride = noise_stride;
+    p.probs_stride = probs_stride;
+    p.B = B;
+    p.max_span = std::min(max_commit, ctx->c.max_span);
+    p.max_commit = max_commit;
+    p.vocab = ctx->m.vocab;
+    p.n_chunks = ceil_div(ctx->m.vocab, kAcceptChunk);
+    p.rows_cap = kRowsCap;
+    p.adaptive = ctx->gen_adaptive;
+    p.k_max = ctx->gen_kmax;
+    p.part = ctx->accept_part;
+    p.n_accept = d_n_accept;
+    p.committed = d_committed;
+    p.n_commit = d_n_commit;
+    p.new_len = d_new_len;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch(ctx, accept_stats_kernel, dim3(p.n_chunks, B * p.max_span), dim3(kAcceptThreads), 0, st, p);
+    if (e == cudaSuccess)
+        e = launch_cluster(ctx, accept_draw_kernel, dim3(B * kDrawCluster), dim3(kDrawThreads), 0, st, kDrawCluster, p);
+    return rc(e);
 }
 
 int sdv_rewind_cache(sdv_ctx *ctx, const int32_t *d_length, int B, void *stream) {

@@ -98,19 +98,35 @@ class SpecLoop:
 
     # ------------------------------------------------------------------ one step
     def step(self, drafter=SDV_DRAFT_NGRAM, table=None, table_stride=0, logits=None, ngram=True, temperature=None,
-             seed: int = 0):
+             seed: int = 0, uniforms=None, noise=None, draft_probs=None):
         """One transaction: propose, reserve, verify (greedy, or sampled at `temperature`, a float32
-        device tensor [B]), accept, rewind, and commit to the n-gram index."""
+        device tensor [B]), accept, rewind, and commit to the n-gram index. With `uniforms` (float32
+        [max_rows] in [0, 1)) and `noise` (float32 [B, vocab], exponential) the drafts are accepted
+        against the target's probabilities at `temperature` instead of matched by token;
+        `draft_probs` [max_rows, vocab] is the drafter's distribution (None: certain drafts). Both
+        are read on the device, so a captured step takes what they hold when it is replayed."""
         v, B = self.v, self.B
+        if uniforms is not None:
+            if temperature is None or noise is None:
+                raise ValueError("acceptance against probabilities needs temperature, uniforms and noise")
+            if logits is None:
+                if self.logits is None:
+                    import torch
+                    self.logits = torch.empty(self.max_rows, v.mcfg.vocab, dtype=torch.float32, device="cuda")
+                logits = self.logits
         v.propose(drafter, table, table_stride, B, self.max_span, self.tokens, self.row_off, self.required)
         v.ensure_capacity(self.required, B)
-        if temperature is None:
+        if temperature is None or uniforms is not None:
             v.spec_forward(self.tokens, self.row_off, B, self.max_rows, self.max_span, self.argmax, logits)
         else:
             v.spec_forward_sampled(self.tokens, self.row_off, B, self.max_rows, self.max_span, temperature, seed,
                                    self.argmax, logits)
-        v.accept_greedy(self.tokens, self.row_off, self.argmax, B, self.max_span, self.n_accept, self.committed,
-                        self.n_commit, self.new_len)
+        if uniforms is not None:
+            v.accept_sampled(self.tokens, self.row_off, logits, temperature, uniforms, noise, B, self.max_span,
+                             self.n_accept, self.committed, self.n_commit, self.new_len, draft_probs=draft_probs)
+        else:
+            v.accept_greedy(self.tokens, self.row_off, self.argmax, B, self.max_span, self.n_accept, self.committed,
+                            self.n_commit, self.new_len)
         v.rewind_cache(self.new_len, B)
         if ngram:
             v.ngram_commit(self.committed, self.n_commit, B, self.max_span)
