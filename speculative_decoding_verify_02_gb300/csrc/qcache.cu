@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 
 #include "qcache_attention.cuh"
 
@@ -19,6 +20,10 @@ struct sdv_qcache {
 
 namespace {
 
+// Attention of a batch is cut into this many times the CTAs that fit at once (two per SM), so that sequences of
+// different lengths even out; a single sequence into just as many as fit.
+constexpr int kQWaves = 3;
+
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 int check_cfg(const sdv_qcache_cfg *c) {
@@ -30,6 +35,8 @@ int check_cfg(const sdv_qcache_cfg *c) {
         c->max_span > c->max_rows || c->max_context < c->max_span)
         return SDV_ERR_ARG;
     if (c->head_dim != 64 && c->head_dim != 128) return SDV_ERR_UNSUPPORTED;
+    // a row of the layer's pool is indexed in 32 bits
+    if (static_cast<double>(c->n_pages) * 2 * c->n_kv_heads * c->page_size > 4294967294.0) return SDV_ERR_UNSUPPORTED;
     if (c->n_q_heads > 1024 || c->max_rows > (1 << 20) || c->max_context > (1 << 30) || c->page_size > (1 << 20))
         return SDV_ERR_UNSUPPORTED;
     return SDV_OK;
@@ -89,6 +96,67 @@ bool aligned16(const void *p, int64_t stride, int dtype) {
 }
 bool element_aligned(const void *p, int dtype) { return reinterpret_cast<uintptr_t>(p) % dtype_size(dtype) == 0; }
 
+// ---- attention: tile rows, parts of a sequence and workspace
+// Rows of a tile: 16, 32 or (bf16) 64, the smallest that holds a span's rows of one kv head. Only wide bf16
+// spans take 64: three planes of an fp16 query beside two of p would not leave two CTAs room in TMEM.
+int attn_rows(int span_rows, int dtype) { return span_rows <= 16 ? 16 : span_rows <= 32 || dtype == SDV_FP16 ? 32 : 64; }
+
+struct AttnPlan {
+    int rows, tiles, splits;
+};
+AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int dtype) {
+    AttnPlan p;
+    const int span_rows = max_span * (q->c.n_q_heads / q->c.n_kv_heads);
+    p.rows = attn_rows(span_rows, dtype);
+    p.tiles = cdiv(span_rows, p.rows);
+    const long long units = static_cast<long long>(B) * q->c.n_kv_heads * p.tiles;
+    const int waves = B > 1 ? kQWaves : 1;
+    const long long s = 2LL * q->sm_count * waves / units;
+    p.splits = static_cast<int>(std::max(1LL, std::min<long long>(s, cdiv(q->c.max_context, kQKeys))));
+    return p;
+}
+
+// Floats of attention's partial results: rows x heads x splits of the largest call, D + 2 each. splits >= 2 only
+// while B nkv tiles splits <= 2 SMs x waves, and a tile holds at most 64 rows.
+size_t attn_partials(const sdv_qcache_cfg &c, int sm_count) {
+    const size_t all = static_cast<size_t>(c.max_batch) * c.max_span * c.n_q_heads * cdiv(c.max_context, kQKeys);
+    const size_t cut = static_cast<size_t>(2) * sm_count * kQWaves * 64;
+    return std::min(all, cut);
+}
+
+template <typename T, int D, int ROWS>
+int launch_attn_rows(const QAttnArgs &a, const AttnPlan &p, void *stream) {
+    typedef QTile<T, D, ROWS> Q;
+    const dim3 grid(static_cast<unsigned>(p.tiles) * a.c.nkv * p.splits, 1, a.c.B);
+    int r = launch(qcache_attn_kernel<T, D, ROWS>, grid, Q::THREADS, Q::SMEM, stream, a);
+    if (r == SDV_OK && p.splits > 1)
+        r = launch(qcache_merge_kernel<T, D>,
+                   dim3(cdiv(static_cast<long long>(a.c.max_span) * a.nq, kQMergeThreads / 32), a.c.B), kQMergeThreads, 0,
+                   stream, a);
+    return r;
+}
+template <typename T, int D>
+int launch_attn(const QAttnArgs &a, const AttnPlan &p, void *stream) {
+    if (p.rows == 16) return launch_attn_rows<T, D, 16>(a, p, stream);
+    if constexpr (!std::is_same<T, __half>::value)
+        if (p.rows == 64) return launch_attn_rows<T, D, 64>(a, p, stream);
+    return launch_attn_rows<T, D, 32>(a, p, stream);
+}
+
+template <typename T, int D, int ROWS>
+cudaError_t set_attn() {
+    return cudaFuncSetAttribute(qcache_attn_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                QTile<T, D, ROWS>::SMEM);
+}
+template <typename T, int D>
+cudaError_t set_attn_all() {
+    cudaError_t e = set_attn<T, D, 16>();
+    if (e == cudaSuccess) e = set_attn<T, D, 32>();
+    if constexpr (!std::is_same<T, __half>::value)
+        if (e == cudaSuccess) e = set_attn<T, D, 64>();
+    return e;
+}
+
 template <typename T, int D>
 int write_rows(const QCacheArgs &a, const void *k, int64_t ks, const void *v, int64_t vs, bool vec, void *stream) {
     const int blocks = (a.max_span + a.scale_block - 2) / a.scale_block + 1;  // a span touches at most
@@ -118,7 +186,13 @@ int sdv_qcache_bytes(const sdv_qcache_cfg *cfg, size_t *codes, size_t *scales, s
     if (!codes || !scales || !workspace) return SDV_ERR_ARG;
     *codes = layer_codes(*cfg) * cfg->n_layers;
     *scales = layer_scales(*cfg) * cfg->n_layers * sizeof(float);
-    *workspace = 256;
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    else
+        cudaGetLastError();  // no device to ask: the part's 152
+    const size_t slots = attn_partials(*cfg, sms);
+    *workspace = 256 + slots * sizeof(float2) / 256 * 256 + 256 + slots * cfg->head_dim * sizeof(float);
     return SDV_OK;
 }
 
@@ -138,6 +212,9 @@ int sdv_qcache_create(const sdv_qcache_cfg *cfg, void *d_codes, void *d_scales, 
         cudaGetLastError();
         return SDV_ERR_UNSUPPORTED;  // no sm_103a image for this device
     }
+    if (set_attn_all<bf16, 128>() != cudaSuccess || set_attn_all<bf16, 64>() != cudaSuccess ||
+        set_attn_all<__half, 128>() != cudaSuccess || set_attn_all<__half, 64>() != cudaSuccess)
+        return SDV_ERR_CUDA;
     sdv_qcache *q = new (std::nothrow) sdv_qcache();
     if (!q) return SDV_ERR_ARG;
     q->c = *cfg;
@@ -225,13 +302,16 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     a.out_stride = out_stride;
     a.nq = cache->c.n_q_heads;
     a.window = window;
+    a.q_vec = aligned16(d_q, q_stride, dtype);
     a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(D));
-    const dim3 grid(max_span, a.nq, B);
-    if (dtype == SDV_BF16)
-        return D == 128 ? launch(qcache_attn_simple_kernel<bf16, 128>, grid, kQSimpleThreads, 0, stream, a)
-                        : launch(qcache_attn_simple_kernel<bf16, 64>, grid, kQSimpleThreads, 0, stream, a);
-    return D == 128 ? launch(qcache_attn_simple_kernel<__half, 128>, grid, kQSimpleThreads, 0, stream, a)
-                    : launch(qcache_attn_simple_kernel<__half, 64>, grid, kQSimpleThreads, 0, stream, a);
+    const AttnPlan p = attn_plan(cache, B, max_span, dtype);
+    const size_t slots = attn_partials(cache->c, cache->sm_count);
+    a.splits = p.splits;
+    a.tiles = p.tiles;
+    a.part_ml = reinterpret_cast<float2 *>(cache->ws + 256);
+    a.part_o = reinterpret_cast<float *>(cache->ws + 512 + slots * sizeof(float2) / 256 * 256);
+    if (dtype == SDV_BF16) return D == 128 ? launch_attn<bf16, 128>(a, p, stream) : launch_attn<bf16, 64>(a, p, stream);
+    return D == 128 ? launch_attn<__half, 128>(a, p, stream) : launch_attn<__half, 64>(a, p, stream);
 }
 
 int sdv_qcache_get_status(sdv_qcache *cache, int32_t *h_status) {

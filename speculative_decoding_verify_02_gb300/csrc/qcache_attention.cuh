@@ -1,4 +1,27 @@
-// Attention over the 8-bit cache.
+// Attention over the 8-bit cache on the fp8 tensor cores.
+//
+// For one kv head, ROWS query rows (span row x head of the group) against 128 keys at a time:
+//     S^T [128 keys x rows] = K . Q^T          (A = the K codes as they lie in the cache, B = Q)
+//     O^T [dims x rows]     = V^T . P^T        (A = the V codes read along the other axis, B = P)
+// so K and V enter the tensor cores as the bytes they are, a key (then a dim) to a TMEM lane, and the
+// few query rows of a verify step are the narrow operand: an MMA of 128 lanes costs 45 clocks for any
+// width up to 64 (measured), 365 for the eight of a chunk, against the 1,370 that the chunk's 32 KB take
+// at this SM's share of HBM.
+//
+// The 16-bit operand of each product is split into e4m3 planes laid side by side along the width:
+//   q = 2^-e (q0 + 2^-5 q1 + 2^-10 q2), e from the tile's largest |q|: two planes hold a bf16's eight
+//       bits exactly, three an fp16's eleven (what lies 2^-20 below the largest rounds away). Tiles of 64
+//       rows (bf16) add the two planes' products in the accumulator instead, with q1 at q0's own scale:
+//       half the columns, exact to 2^-18 of the largest;
+//   p = x0 + 2^-6 x1 + 2^-11 x2, x = 64 p in (0, 128]: p is rounded to fp16's eleven bits and the planes hold
+//       them down to 2^-26 (two planes lost the tail under one large p: 2% off at p = 2^-16).
+// The planes' products are otherwise added in fp32 afterwards.
+//
+// A key's V scale is not applied to V: it joins the exponent. With s_t the score in log2 units and
+// w_t = s_t + log2 vs_t, x_t = 2^(w_t - M) multiplies the bare codes, M being a row's running maximum of w,
+// and the sum l takes 2^(s_t - M); o / l is the result, precise relative to the largest contribution
+// however far the scales lie apart. M follows the maximum only when that has grown by more than one
+// (hence x up to 2 . 64), so the accumulators are rarely rescaled.
 #pragma once
 
 #include "qcache.cuh"
@@ -11,96 +34,580 @@ struct QAttnArgs {
     void *out;
     long long q_stride, out_stride;  // elements between rows
     int nq, window;                  // window: positions a row sees, its own the last (0: all)
+    int splits;                      // parts a sequence's keys are cut into at most
+    int tiles;                       // row tiles of a span of max_span rows
+    int q_vec;                       // q rows are 16-byte aligned
     float scale_log2;                // log2(e) / sqrt(D)
+    float *part_o;                   // [sequence][span row][q head][splits][D]
+    float2 *part_ml;                 // [sequence][span row][q head][splits]: (M, l)
 };
 
-constexpr int kQSimpleThreads = 128;
+constexpr int kQKeys = 128;     // keys of a chunk
+constexpr int kQStages = 2;     // chunks in shared memory
 
-// One CTA per (span row, q head, sequence): its warps take 32 keys at a time, a lane one key, with a
-// running maximum and sum a warp, joined at the end.
-template <typename T, int D>
-__global__ void __launch_bounds__(kQSimpleThreads) qcache_attn_simple_kernel(QAttnArgs a) {
+template <typename T, int D_, int ROWS_>
+struct QTile {
+    static constexpr int D = D_, ROWS = ROWS_;
+    static constexpr int PQ = sizeof(T) == 2 && !__is_same(T, __half) ? 2 : 3;  // planes of q
+    static constexpr int PP = 3;                                                  // planes of p
+    static constexpr bool FOLD = ROWS == 64;                                      // q planes share S's columns
+    static constexpr int WG = ROWS == 64 ? 2 : 1;                                 // softmax warpgroups
+    static constexpr int CW = ROWS / WG;                                          // columns of one
+    static constexpr int NQ = PQ * ROWS, NP = PP * ROWS;                          // widths of the two products
+    static constexpr int W = ROWS == 32 ? 128 : 64;  // bytes of a key's P line: every plane, or (64 rows) one
+    static constexpr int P_LINES = (NP + W - 1) / W;
+    static constexpr int TILE = kQKeys * D;                                       // bytes of a K or V chunk
+    static constexpr int Q_BYTES = (NQ * D + 1023) / 1024 * 1024, P_BYTES = kQKeys * W * P_LINES;
+    static constexpr int SMEM = 1024 + kQStages * 2 * TILE + Q_BYTES + P_BYTES;
+    static constexpr int NS = FOLD ? ROWS : NQ;                                   // columns of S^T
+    static constexpr int O_COL = (NS + 31) / 32 * 32;                             // TMEM column of O^T
+    static constexpr int COLS = O_COL + NP <= 128 ? 128 : 256;
+    static constexpr int THREADS = WG * 128 + 64;
+    static_assert(ROWS == 16 || ROWS == 32 || (ROWS == 64 && PQ == 2), "tile rows");
+    static_assert(O_COL + NP <= COLS, "TMEM columns");
+    static_assert(NQ % 16 == 0 && NP % 16 == 0, "MMA widths");
+    static_assert(2 * (SMEM + 4096) <= 227 * 1024, "two CTAs per SM");
+};
+
+// ------------------------------------------------------------------ PTX
+// D[tmem] (+)= A . B^T, kind::f8f6f4 (e4m3 operands, fp32 accumulate), one CTA.
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: fp32 D, e4m3 A and B; mn: both operands run along M / N in memory.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn) {
+    return (1u << 4) | (mn ? 3u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+// Matrix descriptor over lines of `width` bytes (64 or 128) with that width's swizzle, eight lines to an
+// atom; `beside` bytes on lie the atoms that continue the lines (0: the same atom again, so that the 64
+// dims of V at D = 64 fill both halves of the 128 lanes, of which the upper is not read).
+__device__ __forceinline__ uint64_t line_desc(uint32_t addr, int width, uint32_t beside = 0) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(beside >> 4) << 16 | static_cast<uint64_t>(8 * width >> 4) << 32 |
+           static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(width == 128 ? 2 : 4) << 61;
+}
+// Byte offset of (line, byte) under that swizzle, in a buffer aligned to 1024 bytes.
+__device__ __forceinline__ uint32_t line_offset(uint32_t line, uint32_t byte, int width) {
+    const uint32_t off = line * width + byte;
+    return off ^ ((off >> 7 & (width == 128 ? 7 : 3)) << 4);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+// Arrive on `bar` once all of this thread's earlier cp.async have landed (counted at init).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float redux_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Barrier of `threads` threads that also tells each whether any of them brought true.
+__device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(v ? 1 : 0)
+        : "memory");
+    return r != 0;
+}
+// Sixteen TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Two fp16 values as e4m3 codes, and back.
+__device__ __forceinline__ uint32_t e4m3_of_f16x2(uint32_t h) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+    return c;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+    return h;
+}
+__device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t hscale2_u(uint32_t a, float s) {
+    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), __float2half2_rn(s));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// ------------------------------------------------------------------ the work of a CTA
+// Grid ((split, kv head, row tile), 1, sequence): the tiles that read the same keys run side by side. A
+// sequence of L keys is cut into parts of ceil(L / splits) keys, rounded up to whole chunks: the cut
+// depends on the sequence's own length and the call's B and max_span only.
+__device__ __forceinline__ int qattn_part_keys(int L, int splits) {
+    const int per = (L + splits - 1) / splits;
+    return (per + kQKeys - 1) / kQKeys * kQKeys;
+}
+// First partial result of span row i of sequence b (by its place in the span, which max_span bounds).
+__device__ __forceinline__ size_t qattn_slot(const QAttnArgs &a, int b, int i, int hq) {
+    return ((static_cast<size_t>(b) * a.c.max_span + i) * a.nq + hq) * a.splits;
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_kernel(QAttnArgs a) {
+    typedef QTile<T, D, ROWS> Q;
+    constexpr int CW = Q::CW;
     pdl_trigger();
     pdl_wait();
     const QCacheArgs &c = a.c;
-    const int i = blockIdx.x, hq = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int grp = a.nq / c.nkv, tile = blockIdx.x % a.tiles, b = blockIdx.z;
+    const int h = blockIdx.x / a.tiles % c.nkv, split = blockIdx.x / a.tiles / c.nkv;
     const QSpan s = qcache_span(c, b);
     T *out = static_cast<T *>(a.out);
     if (s.S == 0) {
-        if (s.code != SDV_OK && i == 0 && hq == 0 && tid == 0) set_status(c.status, s.code);
-        for (int r = i; r < s.rows; r += gridDim.x)  // refused: NaN rather than stale memory
-            for (int d = tid; d < D; d += kQSimpleThreads)
-                out[(s.r0 + r) * a.out_stride + hq * D + d] = from_f32<T>(NAN);
+        if (split == 0 && s.code != SDV_OK) {
+            if (blockIdx.x == 0 && tid == 0) set_status(c.status, s.code);
+            // refused: NaN rather than stale memory, this kv head's q heads shared over the tiles
+            for (int r = tile; r < s.rows; r += a.tiles)
+                for (int d = tid; d < grp * D; d += Q::THREADS)
+                    out[(s.r0 + r) * a.out_stride + h * grp * D + d] = from_f32<T>(NAN);
+        }
         return;
     }
-    if (i >= s.S) return;
-    __shared__ float q_s[D], o_s[4][D], m_s[4], l_s[4];
-    const T *q = static_cast<const T *>(a.q) + (s.r0 + i) * a.q_stride + hq * D;
-    for (int d = tid; d < D; d += kQSimpleThreads) q_s[d] = to_f32(q[d]) * a.scale_log2;
+    const int row0 = tile * ROWS, n_rows = min(ROWS, s.S * grp - row0);  // flattened (span row, head) rows
+    const int L = s.p0 + s.S, keys = qattn_part_keys(L, a.splits), parts = (L + keys - 1) / keys;
+    if (n_rows <= 0 || split >= parts) return;
+    const int pos_lo = s.p0 + row0 / grp, pos_hi = s.p0 + (row0 + n_rows - 1) / grp;
+    int first = split * keys;
+    const int last = min(first + keys, pos_hi + 1);
+    if (a.window > 0) first = max(first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
+    const int n_chunks = max(0, (last - first + kQKeys - 1) / kQKeys);
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t kv_s = smem, q_s = smem + kQStages * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
+    __shared__ uint64_t full[kQStages], empty[kQStages], s_full, p_full, o_full;
+    __shared__ uint32_t tmem_s;
+    __shared__ __align__(16) float m_ref[ROWS], m_use[ROWS];  // a row's reference maximum; the same with 0 for -inf
+    __shared__ uint32_t m_key[ROWS];
+    __shared__ int pos_s[ROWS];
+    __shared__ float l_s[4][ROWS], amax_s[Q::WG * 4];
+    __shared__ float kv_scale[kQStages][2][kQKeys];
+    __shared__ uint32_t row_s[kQKeys];
+
+    if (tid == 0) {
+        for (int i = 0; i < kQStages; ++i) {
+            mbar_init(&full[i], 32);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&s_full, 1);
+        mbar_init(&p_full, Q::WG * 128);
+        mbar_init(&o_full, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_s, Q::COLS);
+        tmem_relinquish();
+    }
+    for (int r = tid; r < ROWS; r += Q::THREADS) {
+        m_ref[r] = -INFINITY;
+        m_use[r] = 0.f;
+        m_key[r] = 0;
+        pos_s[r] = r < n_rows ? s.p0 + (row0 + r) / grp : -1;
+    }
+    // Q: the tile's rows as e4m3 planes [plane x ROWS + row][D], eight values a thread at a time
+    float q_unit = 1.f;  // 2^-e: what the planes' products are multiplied by
+    constexpr int QN = ROWS * D / 8 / (Q::WG * 128);
+    if (warp < Q::WG * 4) {
+        float x[QN][8], amax = 0.f;
+#pragma unroll
+        for (int n = 0; n < QN; ++n) {
+            const int e = n * Q::WG * 128 + tid, r = e / (D / 8), col = e % (D / 8) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
+            if (r < n_rows) {
+                const int fr = row0 + r;
+                const T *src = static_cast<const T *>(a.q) + (s.r0 + fr / grp) * a.q_stride +
+                               (h * grp + fr % grp) * D + col;
+                if (a.q_vec)
+                    load8<T, true>(src, x[n]);
+                else
+                    load8<T, false>(src, x[n]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (fabsf(x[n][j]) < INFINITY)
+                    amax = fmaxf(amax, fabsf(x[n][j]));
+                else
+                    x[n][j] = NAN;  // spoils its own row
+            }
+        }
+        amax = redux_max(amax);
+        if (lane == 0) amax_s[warp] = amax;
+        named_bar_sync(3, Q::WG * 128);
+#pragma unroll
+        for (int w = 0; w < Q::WG * 4; ++w) amax = fmaxf(amax, amax_s[w]);
+        // 2^e with amax 2^e in [128, 256); bounded so that both powers stay normal
+        const int ex = amax > 0.f ? min(max(7 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), -120), 120) : 0;
+        const float up = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+        q_unit = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+        for (int n = 0; n < QN; ++n) {
+            const int e = n * Q::WG * 128 + tid, r = e / (D / 8), col = e % (D / 8) * 8;
+            float rest[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rest[j] = x[n][j] * up;
+#pragma unroll
+            for (int p = 0; p < Q::PQ; ++p) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = e4m3x2(rest[2 * j], rest[2 * j + 1]);
+                    const float2 f = e4m3x2_f32(w[j]);
+                    rest[2 * j] = (rest[2 * j] - f.x) * (Q::FOLD ? 1.f : 32.f);
+                    rest[2 * j + 1] = (rest[2 * j + 1] - f.y) * (Q::FOLD ? 1.f : 32.f);
+                }
+                const uint32_t dst = q_s + line_offset(p * ROWS + r, col, D);
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[0] | w[1] << 16),
+                             "r"(w[2] | w[3] << 16)
+                             : "memory");
+            }
+        }
+        fence_async_smem();
+    }
+    tc_fence_before();
     __syncthreads();
-    const int pos = s.p0 + i, h = hq / (a.nq / c.nkv), first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    const int nblk = c.page_size / c.scale_block;
-    float m = -INFINITY, l = 0.f, o[D / 32];
+    tc_fence_after();
+    const uint32_t tmem = tmem_s;
+    bool ok = true;  // false once a wait gave up: the rest runs without waiting, and the status word says so
+
+    if (warp == Q::WG * 4) {
+        // ---- producer: 16-byte pieces of K and V rows and the rows' scales, a chunk ahead
+        constexpr int PPR = D / 16, RPI = 32 / PPR;
+        const int nblk = c.page_size / c.scale_block;
+        const int *table = c.page_table + static_cast<size_t>(b) * c.pages_per_seq;
+        const size_t v_off = static_cast<size_t>(c.nkv) * c.page_size * D;
+        int page[4];
+        auto look = [&](int ch) {
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) o[d] = 0.f;
-    for (int t0 = first + warp * 32; t0 <= pos; t0 += 128) {
-        const int t = t0 + lane;
-        float sc = -INFINITY, vs = 0.f;
-        size_t vrow = 0;
-        if (t <= pos) {
-            const int page = qcache_page(c, b, t / c.page_size), slot = t % c.page_size;
-            sc = 0.f;
-            if (page >= 0) {
-                const size_t ph = (static_cast<size_t>(page) * 2) * c.nkv + h;
-                const uint2 *kc = reinterpret_cast<const uint2 *>(c.codes + (ph * c.page_size + slot) * D);
-                for (int d = 0; d < D / 8; ++d) {
-                    const uint2 w = kc[d];
-                    const uint32_t r[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+            for (int j = 0; j < 4; ++j) {
+                const int t = first + ch * kQKeys + j * 32 + lane;
+                page[j] = t < last ? table[t / c.page_size] : -1;
+            }
+        };
+        look(0);
+        for (int ch = 0; ch < n_chunks; ++ch) {
+            const int st = ch % kQStages;
+            if (ch >= kQStages && ok) ok = mbar_wait(&empty[st], (ch / kQStages - 1) & 1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = e4m3x2_f32(r[j]);
-                        sc = fmaf(f.x, q_s[8 * d + 2 * j], fmaf(f.y, q_s[8 * d + 2 * j + 1], sc));
+            for (int j = 0; j < 4; ++j) {
+                const int t = first + ch * kQKeys + j * 32 + lane, slot = t % c.page_size;
+                const bool in = page[j] >= 0 && page[j] < c.n_pages;
+                if (!in && t < last) set_status(c.status, SDV_ERR_CAPACITY);
+                const size_t ph = in ? static_cast<size_t>(page[j]) * 2 * c.nkv + h : 0;
+                row_s[j * 32 + lane] = in ? static_cast<uint32_t>(ph * c.page_size + slot) : 0xffffffffu;
+                const float *sc = c.scales + (in ? ph * nblk + slot / c.scale_block : 0);
+                cp_async4(smem_u32(&kv_scale[st][0][j * 32 + lane]), sc, in);
+                cp_async4(smem_u32(&kv_scale[st][1][j * 32 + lane]), in ? sc + static_cast<size_t>(c.nkv) * nblk : sc, in);
+            }
+            __syncwarp();
+            const uint32_t k_s = kv_s + st * 2 * Q::TILE;
+#pragma unroll 4
+            for (int j = 0; j < kQKeys / RPI; ++j) {
+                const int r = j * RPI + lane / PPR;
+                const uint32_t row = row_s[r];
+                const bool in = row != 0xffffffffu;
+                const uint8_t *src = c.codes + (in ? static_cast<size_t>(row) * D : 0) + lane % PPR * 16;
+                const uint32_t dst = k_s + line_offset(r, lane % PPR * 16, D);
+                cp_async16(dst, src, in);
+                cp_async16(dst + Q::TILE, src + (in ? v_off : 0), in);
+            }
+            cp_async_arrive(&full[st]);
+            __syncwarp();
+            look(ch + 1);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == Q::WG * 4 + 1) {
+        // ---- MMA issue
+        if (lane == 0) {
+            const uint32_t id_s = idesc_e4m3(128, Q::NS, false), id_o = idesc_e4m3(128, Q::NP, true);
+            for (int ch = 0; ch < n_chunks; ++ch) {
+                const int st = ch % kQStages;
+                const uint32_t k_s = kv_s + st * 2 * Q::TILE, v_s = k_s + Q::TILE;
+                if (ok) ok = mbar_wait(&full[st], (ch / kQStages) & 1);
+                fence_async_smem();  // the copies were generic writes; the tensor cores read through the async proxy
+#pragma unroll
+                for (int k = 0; k < D / 32 * (Q::FOLD ? Q::PQ : 1); ++k)
+                    umma_e4m3(tmem, line_desc(k_s + k % (D / 32) * 32, D),
+                              line_desc(q_s + k / (D / 32) * ROWS * D + k % (D / 32) * 32, D), id_s, k > 0);
+                umma_commit(&s_full);
+                if (ok) ok = mbar_wait(&p_full, ch & 1);
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kQKeys / 32; ++k)
+                    umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k * D, D), line_desc(p_s + 32 * k * Q::W, Q::W, kQKeys * Q::W), id_o,
+                              k > 0);
+                umma_commit(&o_full);
+                umma_commit(&empty[st]);
+            }
+            if (!ok) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax and accumulation: a thread is key (then dim) `tid % 128` of the chunk
+        const int g = warp / 4, col0 = g * CW, key = tid % 128;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        const float unit = q_unit * a.scale_log2;
+        float acc[CW], l[CW];
+#pragma unroll
+        for (int r = 0; r < CW; ++r) acc[r] = l[r] = 0.f;
+        for (int ch = 0; ch < n_chunks; ++ch) {
+            const int st = ch % kQStages, t0 = first + ch * kQKeys, t = t0 + key;
+            if (ok) ok = mbar_wait(&full[st], (ch / kQStages) & 1);  // the scales' own arrival
+            const float ks = kv_scale[st][0][key] * unit, vs = kv_scale[st][1][key], lv = __log2f(vs);
+            const bool masked = t0 + kQKeys - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window);
+            if (ok) ok = mbar_wait(&s_full, ch & 1);
+            tc_fence_after();
+            // sixteen rows' scores of this key in log2 units, -inf where a row does not see it
+            auto scores = [&](int r0, float *sc) {
+                tmem_ld16(tmem + lanes + col0 + r0, sc);
+                if constexpr (Q::FOLD) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[r] *= ks;
+                } else {
+                    float v[16];
+                    tmem_ld16(tmem + lanes + ROWS + col0 + r0, v);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[r] = fmaf(v[r], 0x1p-5f, sc[r]);
+                    if constexpr (Q::PQ == 3) {
+                        tmem_ld16(tmem + lanes + 2 * ROWS + col0 + r0, v);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) sc[r] = fmaf(v[r], 0x1p-10f, sc[r]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[r] *= ks;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int pos = pos_s[col0 + r0 + r];
+                        if (t > pos || (a.window > 0 && t <= pos - a.window)) sc[r] = -INFINITY;
                     }
                 }
-                sc *= c.scales[ph * nblk + slot / c.scale_block];
-                vs = c.scales[(ph + c.nkv) * nblk + slot / c.scale_block];
-                vrow = ((ph + c.nkv) * c.page_size + slot) * D;
+            };
+            // 64-row tiles read the scores from TMEM twice rather than hold them
+            float kept[Q::FOLD ? 1 : CW];
+            bool grow = false;  // does a row's maximum leave the range that its reference covers?
+            const float lv1 = lv - 1.f;
+#pragma unroll
+            for (int r0 = 0; r0 < CW; r0 += 16) {
+                float sc[16];
+                scores(r0, sc);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    grow |= redux_max(sc[r] + lv1) > m_ref[col0 + r0 + r];
+                    if constexpr (!Q::FOLD) kept[r0 + r] = sc[r];
+                }
+            }
+            if (bar_or(1 + g, 128, grow)) {
+#pragma unroll
+                for (int r0 = 0; r0 < CW; r0 += 16) {
+                    float sc[16];
+                    if constexpr (Q::FOLD) scores(r0, sc);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float m = redux_max((Q::FOLD ? sc[r] : kept[Q::FOLD ? 0 : r0 + r]) + lv);
+                        if (lane == r) top = m;
+                    }
+                    if (lane < 16 && top > m_ref[col0 + r0 + lane] + 1.f) atomicMax(&m_key[col0 + r0 + lane], orderable(top));
+                }
+                named_bar_sync(1 + g, 128);
+                // the new reference of row r, or the old one
+                auto reference = [&](int r) {
+                    const uint32_t k = m_key[r];
+                    const float m = __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+                    return k != 0 && m > m_ref[r] + 1.f ? m : m_ref[r];
+                };
+#pragma unroll
+                for (int r = 0; r < CW; ++r) {
+                    const float m = reference(col0 + r);
+                    if (m != m_ref[col0 + r]) {
+                        // m_use is 0 for -inf: all that l holds then are keys of scale 0
+                        const float f = ex2(fminf(m_use[col0 + r] - m, 120.f));
+                        acc[r] *= f;
+                        l[r] *= f;
+                    }
+                }
+                named_bar_sync(1 + g, 128);
+                if (key < CW) {
+                    const float m = reference(col0 + key);
+                    m_ref[col0 + key] = m;
+                    m_use[col0 + key] = m == -INFINITY ? 0.f : m;
+                }
+                named_bar_sync(1 + g, 128);
+            }
+            // x = 64 p as planes; a line of P holds this key's values of every row and plane. l takes x / (64 vs); keys
+            // whose scale is 0 or so small that x may vanish beside it (2^-60) send their warp to the exponential.
+            const float lv6 = lv + 6.f;
+            const bool small = __any_sync(0xffffffffu, !(vs >= 0x1p-60f));
+            const float to_l = small ? 0.f : 0x1p-6f / vs;
+#pragma unroll
+            for (int r0 = 0; r0 < CW; r0 += 16) {
+                float sc[16];
+                if constexpr (Q::FOLD) {
+                    scores(r0, sc);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[r] = kept[Q::FOLD ? 0 : r0 + r];
+                }
+                if (small) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) l[r0 + r] += ex2(sc[r] - m_use[col0 + r0 + r]);
+                }
+                uint32_t w[Q::PP][8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 m = *reinterpret_cast<const float2 *>(&m_use[col0 + r0 + 2 * j]);
+                    const float x0 = ex2(sc[2 * j] + lv6 - m.x), x1 = ex2(sc[2 * j + 1] + lv6 - m.y);
+                    l[r0 + 2 * j] = fmaf(x0, to_l, l[r0 + 2 * j]);
+                    l[r0 + 2 * j + 1] = fmaf(x1, to_l, l[r0 + 2 * j + 1]);
+                    uint32_t x = f16x2(x0, x1);
+#pragma unroll
+                    for (int p = 0; p < Q::PP; ++p) {
+                        w[p][j] = e4m3_of_f16x2(x);
+                        if (p + 1 < Q::PP) x = hscale2_u(hsub2_u(x, f16x2_of_e4m3(w[p][j])), p == 0 ? 64.f : 32.f);
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < Q::PP; ++p) {
+                    const int byte = p * ROWS + col0 + r0;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     p_s + byte / Q::W * (kQKeys * Q::W) + line_offset(key, byte % Q::W, Q::W)),
+                                 "r"(w[p][0] | w[p][1] << 16), "r"(w[p][2] | w[p][3] << 16), "r"(w[p][4] | w[p][5] << 16),
+                                 "r"(w[p][6] | w[p][7] << 16)
+                                 : "memory");
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(&p_full);
+            if (ok) ok = mbar_wait(&o_full, ch & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int p = 0; p < Q::PP; ++p)
+#pragma unroll
+                for (int r0 = 0; r0 < CW; r0 += 16) {
+                    float v[16];
+                    tmem_ld16(tmem + lanes + Q::O_COL + p * ROWS + col0 + r0, v);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        acc[r0 + r] = fmaf(v[r], p == 0 ? 0x1p-6f : p == 1 ? 0x1p-12f : 0x1p-17f, acc[r0 + r]);
+                }
+        }
+        if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
+        // ---- sums over the keys, and the rows out
+        float sum[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) sum[r] = r < CW ? l[r < CW ? r : 0] : 0.f;
+        const float mine = transpose_sum32(sum, lane);
+        if (lane < CW) l_s[warp % 4][col0 + lane] = mine;
+        named_bar_sync(1 + g, 128);
+#pragma unroll
+        for (int r = 0; r < CW; ++r) {
+            const int fr = row0 + col0 + r;
+            if (col0 + r >= n_rows) break;
+            const float total = (l_s[0][col0 + r] + l_s[1][col0 + r]) + (l_s[2][col0 + r] + l_s[3][col0 + r]);
+            const int row = s.r0 + fr / grp, hq = h * grp + fr % grp;
+            if (key < D) {
+                if (parts == 1) {
+                    out[row * a.out_stride + hq * D + key] = from_f32<T>(total == 0.f ? 0.f : acc[r] / total);
+                } else {
+                    const size_t slot = qattn_slot(a, b, fr / grp, hq) + split;
+                    a.part_o[slot * D + key] = acc[r];
+                    if (key == 0) a.part_ml[slot] = make_float2(m_ref[col0 + r], total);
+                }
             }
         }
-        float mn = sc;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-        mn = fmaxf(mn, m);
-        const float alpha = exp2f(m - mn), p = exp2f(sc - mn);
-        m = mn;
-        l = l * alpha + warp_sum(p);
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) o[d] *= alpha;
-        for (int j = 0; j < 32; ++j) {
-            const float pv = __shfl_sync(0xffffffffu, p, j) * __shfl_sync(0xffffffffu, vs, j);
-            const size_t row = __shfl_sync(0xffffffffu, vrow, j);
-            if (pv == 0.f) continue;
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-                const uint32_t code = c.codes[row + d * 32 + lane];
-                o[d] = fmaf(pv, e4m3x2_f32(code).x, o[d]);
-            }
-        }
+        tc_fence_before();
     }
-    if (lane == 0) m_s[warp] = m, l_s[warp] = l;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) o_s[warp][d * 32 + lane] = o[d];
     __syncthreads();
-    const float mx = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
-    for (int d = tid; d < D; d += kQSimpleThreads) {
-        float num = 0.f, den = 0.f;
-        for (int w = 0; w < 4; ++w) {
-            const float f = exp2f(m_s[w] - mx);
-            num += f * o_s[w][d];
-            den += f * l_s[w];
-        }
-        out[(s.r0 + i) * a.out_stride + hq * D + d] = from_f32<T>(num / den);
+    if (warp == 0) tmem_dealloc(tmem, Q::COLS);
+}
+
+constexpr int kQMergeThreads = 128;
+
+// A warp joins the parts of one (row, q head): o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i, in part order.
+template <typename T, int D>
+__global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.y, item = blockIdx.x * (kQMergeThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
+    const QSpan s = qcache_span(a.c, b);
+    const int i = item / a.nq, hq = item % a.nq;
+    if (i >= s.S) return;
+    const int L = s.p0 + s.S, keys = qattn_part_keys(L, a.splits), parts = (L + keys - 1) / keys;
+    if (parts == 1) return;
+    const int row = s.r0 + i;
+    const size_t slot = qattn_slot(a, b, i, hq);
+    // parts without a key of this row hold M = -inf, l = 0, o = 0
+    float m = -INFINITY;
+    for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[slot + p].x);
+    m = redux_max(m);
+    if (m == -INFINITY) m = 0.f;
+    constexpr int V = D / 32;
+    float o[V], l = 0.f;
+#pragma unroll
+    for (int d = 0; d < V; ++d) o[d] = 0.f;
+    for (int p = 0; p < parts; ++p) {
+        const float2 ml = a.part_ml[slot + p];
+        if (ml.y == 0.f) continue;
+        const float f = ex2(fminf((ml.x == -INFINITY ? 0.f : ml.x) - m, 120.f));
+        l = fmaf(f, ml.y, l);
+        float v[V];
+        if constexpr (V == 4)
+            *reinterpret_cast<float4 *>(v) = reinterpret_cast<const float4 *>(a.part_o + (slot + p) * D)[lane];
+        else
+            *reinterpret_cast<float2 *>(v) = reinterpret_cast<const float2 *>(a.part_o + (slot + p) * D)[lane];
+#pragma unroll
+        for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[d], o[d]);
     }
+    T *dst = static_cast<T *>(a.out) + row * a.out_stride + hq * D + lane * V;
+#pragma unroll
+    for (int d = 0; d < V; ++d) dst[d] = from_f32<T>(l == 0.f ? 0.f : o[d] / l);
 }
 
 }  // namespace sdv
