@@ -16,6 +16,7 @@ struct sdv_qcache {
     float *scales = nullptr;
     uint8_t *ws = nullptr;
     size_t layer_codes = 0, layer_scales = 0;
+    FastDiv by_page{}, by_block{};
 };
 
 namespace {
@@ -87,6 +88,8 @@ int common_args(const sdv_qcache *q, int layer, const int32_t *table, const int3
     a->max_span = max_span;
     a->max_rows = q->c.max_rows;
     a->max_context = q->c.max_context;
+    a->by_page = q->by_page;
+    a->by_block = q->by_block;
     return SDV_OK;
 }
 
@@ -226,6 +229,8 @@ int sdv_qcache_create(const sdv_qcache_cfg *cfg, void *d_codes, void *d_scales, 
     q->ws = static_cast<uint8_t *>(d_workspace);
     q->layer_codes = layer_codes(*cfg);
     q->layer_scales = layer_scales(*cfg);
+    q->by_page = FastDiv::of(cfg->page_size);
+    q->by_block = FastDiv::of(cfg->scale_block);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemsetAsync(q->codes, 0, q->layer_codes * cfg->n_layers, st);
     if (e == cudaSuccess) e = cudaMemsetAsync(q->scales, 0, q->layer_scales * cfg->n_layers * sizeof(float), st);
@@ -303,11 +308,13 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     a.nq = cache->c.n_q_heads;
     a.window = window;
     a.q_vec = aligned16(d_q, q_stride, dtype);
+    a.grp_mul = ((1u << 22) + a.nq / a.c.nkv - 1) / (a.nq / a.c.nkv);
     a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(D));
     const AttnPlan p = attn_plan(cache, B, max_span, dtype);
     const size_t slots = attn_partials(cache->c, cache->sm_count);
     a.splits = p.splits;
     a.tiles = p.tiles;
+    a.blocks = cache->c.page_size / cache->c.scale_block;
     a.part_ml = reinterpret_cast<float2 *>(cache->ws + 256);
     a.part_o = reinterpret_cast<float *>(cache->ws + 512 + slots * sizeof(float2) / 256 * 256);
     if (dtype == SDV_BF16) return D == 128 ? launch_attn<bf16, 128>(a, p, stream) : launch_attn<bf16, 64>(a, p, stream);

@@ -15,12 +15,30 @@
 
 namespace sdv {
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication: floor(n m / 2^(31 + l)) with
+// l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1 < 2^32. m d exceeds 2^(31 + l) by at most d <= 2^l, so the
+// quotient is off by less than n / 2^31 / d < 1 / d: never across a whole number.
+struct FastDiv {
+    uint32_t m;
+    int shift;
+    static FastDiv of(uint32_t d) {
+        int l = 0;
+        while ((1ull << l) < d) ++l;
+        return {static_cast<uint32_t>((1ull << (31 + l)) / d + 1), 31 + l};
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return static_cast<int>(static_cast<unsigned long long>(static_cast<uint32_t>(n)) * m >> shift);
+    }
+    __device__ __forceinline__ int mod(int n, int d) const { return n - div(n) * d; }
+};
+
 struct QCacheArgs {
     uint8_t *codes;   // the layer's [n_pages][2][nkv][page_size][D]
     float *scales;    // the layer's [n_pages][2][nkv][page_size / scale_block]
     int *status;
     const int *page_table, *row_off, *base;
     int pages_per_seq, page_size, n_pages, scale_block, nkv, B, max_span, max_rows, max_context;
+    FastDiv by_page, by_block;  // page_size and scale_block
 };
 
 // One sequence's span: rows r0 .. r0 + S - 1 at positions p0 .. p0 + S - 1. S = 0 where it is empty or

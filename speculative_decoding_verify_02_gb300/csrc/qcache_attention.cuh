@@ -36,7 +36,9 @@ struct QAttnArgs {
     int nq, window;                  // window: positions a row sees, its own the last (0: all)
     int splits;                      // parts a sequence's keys are cut into at most
     int tiles;                       // row tiles of a span of max_span rows
+    int blocks;                      // scale blocks of a page
     int q_vec;                       // q rows are 16-byte aligned
+    uint32_t grp_mul;                // ceil(2^22 / q heads a kv head)
     float scale_log2;                // log2(e) / sqrt(D)
     float *part_o;                   // [sequence][span row][q head][splits][D]
     float2 *part_ml;                 // [sequence][span row][q head][splits]: (M, l)
@@ -44,14 +46,13 @@ struct QAttnArgs {
 
 constexpr int kQKeys = 128;     // keys of a chunk
 constexpr int kQStages = 2;     // chunks in shared memory
-
 template <typename T, int D_, int ROWS_>
 struct QTile {
     static constexpr int D = D_, ROWS = ROWS_;
     static constexpr int PQ = sizeof(T) == 2 && !__is_same(T, __half) ? 2 : 3;  // planes of q
     static constexpr int PP = 3;                                                  // planes of p
     static constexpr bool FOLD = ROWS == 64;                                      // q planes share S's columns
-    static constexpr int WG = ROWS == 64 ? 2 : 1;                                 // softmax warpgroups
+    static constexpr int WG = ROWS == 16 ? 1 : 2;                                 // softmax warpgroups
     static constexpr int CW = ROWS / WG;                                          // columns of one
     static constexpr int NQ = PQ * ROWS, NP = PP * ROWS;                          // widths of the two products
     static constexpr int W = ROWS == 32 ? 128 : 64;  // bytes of a key's P line: every plane, or (64 rows) one
@@ -62,11 +63,11 @@ struct QTile {
     static constexpr int NS = FOLD ? ROWS : NQ;                                   // columns of S^T
     static constexpr int O_COL = (NS + 31) / 32 * 32;                             // TMEM column of O^T
     static constexpr int COLS = O_COL + NP <= 128 ? 128 : 256;
-    static constexpr int THREADS = WG * 128 + 64;
+    static constexpr int THREADS = WG * 128 + 32;  // softmax warps, which also load, and the MMA warp
     static_assert(ROWS == 16 || ROWS == 32 || (ROWS == 64 && PQ == 2), "tile rows");
     static_assert(O_COL + NP <= COLS, "TMEM columns");
     static_assert(NQ % 16 == 0 && NP % 16 == 0, "MMA widths");
-    static_assert(2 * (SMEM + 4096) <= 227 * 1024, "two CTAs per SM");
+    static_assert(2 * (SMEM + 6144 + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 // ------------------------------------------------------------------ PTX
@@ -134,19 +135,26 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
         : "memory");
     return r != 0;
 }
-// Sixteen TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
-    uint32_t r[16];
+// Sixteen TMEM columns of this thread's lane; tmem_ld_wait before the values are used.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Waits for this thread's TMEM loads; the values pass through, so that no use of them moves above it.
+__device__ __forceinline__ void tmem_ld_pass(float (&v)[16]) {
+    asm volatile(""
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+template <typename... V>
+__device__ __forceinline__ void tmem_ld_wait(V &...v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    (tmem_ld_pass(v), ...);
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -185,12 +193,17 @@ __device__ __forceinline__ size_t qattn_slot(const QAttnArgs &a, int b, int i, i
     return ((static_cast<size_t>(b) * a.c.max_span + i) * a.nq + hq) * a.splits;
 }
 
+// A row of the tile: its row of the call, its q head and its place in the span.
+struct QRow {
+    int row, hq, i;
+};
+
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_kernel(QAttnArgs a) {
     typedef QTile<T, D, ROWS> Q;
     constexpr int CW = Q::CW;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // after the wait: what starts behind this kernel may read what came before it
     const QCacheArgs &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int grp = a.nq / c.nkv, tile = blockIdx.x % a.tiles, b = blockIdx.z;
@@ -210,7 +223,13 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     const int row0 = tile * ROWS, n_rows = min(ROWS, s.S * grp - row0);  // flattened (span row, head) rows
     const int L = s.p0 + s.S, keys = qattn_part_keys(L, a.splits), parts = (L + keys - 1) / keys;
     if (n_rows <= 0 || split >= parts) return;
-    const int pos_lo = s.p0 + row0 / grp, pos_hi = s.p0 + (row0 + n_rows - 1) / grp;
+    const int i0 = row0 / grp, h0 = row0 - i0 * grp;
+    // row r of the tile is head (h0 + r) % grp of span row i0 + (h0 + r) / grp; h0 + r < grp + 64 <= 1088
+    auto row_of = [&](int r) {
+        const int q = static_cast<int>((h0 + r) * a.grp_mul >> 22);
+        return QRow{s.r0 + i0 + q, h * grp + h0 + r - q * grp, i0 + q};
+    };
+    const int pos_lo = s.p0 + i0, pos_hi = s.p0 + (row0 + n_rows - 1) / grp;
     int first = split * keys;
     const int last = min(first + keys, pos_hi + 1);
     if (a.window > 0) first = max(first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
@@ -219,39 +238,91 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     extern __shared__ uint8_t smem_raw[];
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t kv_s = smem, q_s = smem + kQStages * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
-    __shared__ uint64_t full[kQStages], empty[kQStages], s_full, p_full, o_full;
+    __shared__ uint64_t k_full[kQStages], v_full[kQStages], s_full, p_full, o_full;
     __shared__ uint32_t tmem_s;
-    __shared__ __align__(16) float m_ref[ROWS], m_use[ROWS];  // a row's reference maximum; the same with 0 for -inf
+    // a row's reference maximum, the same with 0 for -inf, and the factor by which it last moved
+    __shared__ __align__(16) float m_ref[ROWS], m_use[ROWS], m_step[ROWS];
     __shared__ uint32_t m_key[ROWS];
     __shared__ int pos_s[ROWS];
     __shared__ float l_s[4][ROWS], amax_s[Q::WG * 4];
-    __shared__ float kv_scale[kQStages][2][kQKeys];
-    __shared__ uint32_t row_s[kQKeys];
+    __shared__ float kv_scale[4][2][kQKeys];  // four chunks deep: softmax may still read the one two back
 
-    if (tid == 0) {
-        for (int i = 0; i < kQStages; ++i) {
-            mbar_init(&full[i], 32);
-            mbar_init(&empty[i], 1);
+    // ---- loads: a softmax warp brings LW keys of each chunk in 16-byte pieces, K with both scales, then V
+    const bool is_mma = warp == Q::WG * 4;
+    constexpr int LW = kQKeys / (Q::WG * 4), PPR = D / 16, RPI = 32 / PPR;  // keys a warp, pieces a row, rows a copy
+    const int my_key = warp * LW + lane;                                     // lanes below LW: the key looked up
+    const int *table = c.page_table + static_cast<size_t>(b) * c.pages_per_seq;
+    auto look = [&](int ch) {  // page of this lane's key, or -1
+        const int t = first + ch * kQKeys + my_key;
+        return lane < LW && t < last ? table[c.by_page.div(t)] : -1;
+    };
+    auto load_rows = [&](uint32_t dst, uint32_t rows, size_t off) {
+        const uint8_t *codes = c.codes + off + lane % PPR * 16;
+#pragma unroll
+        for (int j = 0; j < LW / RPI; ++j) {
+            const int r = j * RPI + lane / PPR;
+            const uint32_t row = __shfl_sync(0xffffffffu, rows, r);
+            const bool in = row != 0xffffffffu;
+            cp_async16(dst + line_offset(warp * LW + r, lane % PPR * 16, D), codes + (in ? static_cast<size_t>(row) * D : 0),
+                       in);
         }
-        mbar_init(&s_full, 1);
-        mbar_init(&p_full, Q::WG * 128);
-        mbar_init(&o_full, 1);
-        fence_mbar_init();
-    }
-    if (warp == 0) {
+    };
+    // K rows and scales of chunk ch; returns the pool row of this lane's key for the V rows
+    auto load_k = [&](int ch, int page) {
+        const int t = first + ch * kQKeys + my_key;
+        const bool in = page >= 0 && page < c.n_pages;
+        uint32_t row = 0xffffffffu;
+        if (lane < LW) {
+            if (!in && t < last) set_status(c.status, SDV_ERR_CAPACITY);
+            const int slot = c.by_page.mod(t, c.page_size), nblk = a.blocks;
+            const size_t ph = in ? static_cast<size_t>(page) * 2 * c.nkv + h : 0;
+            if (in) row = static_cast<uint32_t>(ph * c.page_size + slot);
+            const float *sc = c.scales + (in ? ph * nblk + c.by_block.div(slot) : 0);
+            cp_async4(smem_u32(&kv_scale[ch % 4][0][my_key]), sc, in);
+            cp_async4(smem_u32(&kv_scale[ch % 4][1][my_key]), in ? sc + c.nkv * nblk : sc, in);
+        }
+        load_rows(kv_s + ch % kQStages * 2 * Q::TILE, row, 0);
+        cp_async_arrive(&k_full[ch % kQStages]);
+        return row;
+    };
+    const size_t v_off = static_cast<size_t>(c.nkv) * c.page_size * D;
+    auto load_v = [&](int ch, uint32_t row) {
+        load_rows(kv_s + (ch % kQStages * 2 + 1) * Q::TILE, row, v_off);
+        cp_async_arrive(&v_full[ch % kQStages]);
+    };
+    int page = -1;           // of the next chunk whose K is to be loaded
+    uint32_t v_row = 0;      // of the next chunk whose V is to be loaded
+    if (!is_mma) {
+        const int page0 = look(0), page1 = look(1);
+        page = look(2);
+        if (tid == 0) {
+            for (int i = 0; i < kQStages; ++i) {
+                mbar_init(&k_full[i], Q::WG * 128);
+                mbar_init(&v_full[i], Q::WG * 128);
+            }
+            mbar_init(&s_full, 2);
+            mbar_init(&p_full, Q::WG * 128);
+            mbar_init(&o_full, 1);
+            fence_mbar_init();
+        }
+        named_bar_sync(7, Q::WG * 128);
+        // the first chunks are on their way while the queries are prepared
+        if (n_chunks > 0) load_v(0, load_k(0, page0));
+        if (n_chunks > 1) load_v(1, load_k(1, page1));
+    } else {
         tmem_alloc(&tmem_s, Q::COLS);
         tmem_relinquish();
-    }
-    for (int r = tid; r < ROWS; r += Q::THREADS) {
-        m_ref[r] = -INFINITY;
-        m_use[r] = 0.f;
-        m_key[r] = 0;
-        pos_s[r] = r < n_rows ? s.p0 + (row0 + r) / grp : -1;
+        for (int r = lane; r < ROWS; r += 32) {
+            m_ref[r] = -INFINITY;
+            m_use[r] = 0.f;
+            m_key[r] = 0;
+            pos_s[r] = r < n_rows ? s.p0 + row_of(r).i : -1;
+        }
     }
     // Q: the tile's rows as e4m3 planes [plane x ROWS + row][D], eight values a thread at a time
     float q_unit = 1.f;  // 2^-e: what the planes' products are multiplied by
     constexpr int QN = ROWS * D / 8 / (Q::WG * 128);
-    if (warp < Q::WG * 4) {
+    if (!is_mma) {
         float x[QN][8], amax = 0.f;
 #pragma unroll
         for (int n = 0; n < QN; ++n) {
@@ -259,14 +330,16 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
             if (r < n_rows) {
-                const int fr = row0 + r;
-                const T *src = static_cast<const T *>(a.q) + (s.r0 + fr / grp) * a.q_stride +
-                               (h * grp + fr % grp) * D + col;
+                const QRow w = row_of(r);
+                const T *src = static_cast<const T *>(a.q) + w.row * a.q_stride + w.hq * D + col;
                 if (a.q_vec)
                     load8<T, true>(src, x[n]);
                 else
                     load8<T, false>(src, x[n]);
             }
+        }
+#pragma unroll
+        for (int n = 0; n < QN; ++n)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (fabsf(x[n][j]) < INFINITY)
@@ -274,10 +347,9 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                 else
                     x[n][j] = NAN;  // spoils its own row
             }
-        }
         amax = redux_max(amax);
         if (lane == 0) amax_s[warp] = amax;
-        named_bar_sync(3, Q::WG * 128);
+        named_bar_sync(7, Q::WG * 128);
 #pragma unroll
         for (int w = 0; w < Q::WG * 4; ++w) amax = fmaxf(amax, amax_s[w]);
         // 2^e with amax 2^e in [128, 256); bounded so that both powers stay normal
@@ -314,74 +386,36 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     const uint32_t tmem = tmem_s;
     bool ok = true;  // false once a wait gave up: the rest runs without waiting, and the status word says so
 
-    if (warp == Q::WG * 4) {
-        // ---- producer: 16-byte pieces of K and V rows and the rows' scales, a chunk ahead
-        constexpr int PPR = D / 16, RPI = 32 / PPR;
-        const int nblk = c.page_size / c.scale_block;
-        const int *table = c.page_table + static_cast<size_t>(b) * c.pages_per_seq;
-        const size_t v_off = static_cast<size_t>(c.nkv) * c.page_size * D;
-        int page[4];
-        auto look = [&](int ch) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = first + ch * kQKeys + j * 32 + lane;
-                page[j] = t < last ? table[t / c.page_size] : -1;
-            }
-        };
-        look(0);
-        for (int ch = 0; ch < n_chunks; ++ch) {
-            const int st = ch % kQStages;
-            if (ch >= kQStages && ok) ok = mbar_wait(&empty[st], (ch / kQStages - 1) & 1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = first + ch * kQKeys + j * 32 + lane, slot = t % c.page_size;
-                const bool in = page[j] >= 0 && page[j] < c.n_pages;
-                if (!in && t < last) set_status(c.status, SDV_ERR_CAPACITY);
-                const size_t ph = in ? static_cast<size_t>(page[j]) * 2 * c.nkv + h : 0;
-                row_s[j * 32 + lane] = in ? static_cast<uint32_t>(ph * c.page_size + slot) : 0xffffffffu;
-                const float *sc = c.scales + (in ? ph * nblk + slot / c.scale_block : 0);
-                cp_async4(smem_u32(&kv_scale[st][0][j * 32 + lane]), sc, in);
-                cp_async4(smem_u32(&kv_scale[st][1][j * 32 + lane]), in ? sc + static_cast<size_t>(c.nkv) * nblk : sc, in);
-            }
-            __syncwarp();
-            const uint32_t k_s = kv_s + st * 2 * Q::TILE;
-#pragma unroll 4
-            for (int j = 0; j < kQKeys / RPI; ++j) {
-                const int r = j * RPI + lane / PPR;
-                const uint32_t row = row_s[r];
-                const bool in = row != 0xffffffffu;
-                const uint8_t *src = c.codes + (in ? static_cast<size_t>(row) * D : 0) + lane % PPR * 16;
-                const uint32_t dst = k_s + line_offset(r, lane % PPR * 16, D);
-                cp_async16(dst, src, in);
-                cp_async16(dst + Q::TILE, src + (in ? v_off : 0), in);
-            }
-            cp_async_arrive(&full[st]);
-            __syncwarp();
-            look(ch + 1);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == Q::WG * 4 + 1) {
-        // ---- MMA issue
+    if (is_mma) {
+        // ---- MMA issue: the scores of a chunk go out as soon as the previous chunk's are read
         if (lane == 0) {
             const uint32_t id_s = idesc_e4m3(128, Q::NS, false), id_o = idesc_e4m3(128, Q::NP, true);
-            for (int ch = 0; ch < n_chunks; ++ch) {
+            auto issue_scores = [&](int ch) {
                 const int st = ch % kQStages;
-                const uint32_t k_s = kv_s + st * 2 * Q::TILE, v_s = k_s + Q::TILE;
-                if (ok) ok = mbar_wait(&full[st], (ch / kQStages) & 1);
+                const uint32_t k_s = kv_s + st * 2 * Q::TILE;
+                if (ok) ok = mbar_wait(&k_full[st], (ch / kQStages) & 1);
                 fence_async_smem();  // the copies were generic writes; the tensor cores read through the async proxy
 #pragma unroll
                 for (int k = 0; k < D / 32 * (Q::FOLD ? Q::PQ : 1); ++k)
                     umma_e4m3(tmem, line_desc(k_s + k % (D / 32) * 32, D),
                               line_desc(q_s + k / (D / 32) * ROWS * D + k % (D / 32) * 32, D), id_s, k > 0);
                 umma_commit(&s_full);
+                mbar_arrive(&s_full);  // passes on the scales' arrival, too
+            };
+            if (n_chunks > 0) issue_scores(0);
+            for (int ch = 0; ch < n_chunks; ++ch) {
+                const int st = ch % kQStages;
+                const uint32_t v_s = kv_s + (st * 2 + 1) * Q::TILE;
                 if (ok) ok = mbar_wait(&p_full, ch & 1);
                 tc_fence_after();
+                if (ch + 1 < n_chunks) issue_scores(ch + 1);
+                if (ok) ok = mbar_wait(&v_full[st], (ch / kQStages) & 1);
+                fence_async_smem();
 #pragma unroll
                 for (int k = 0; k < kQKeys / 32; ++k)
-                    umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k * D, D), line_desc(p_s + 32 * k * Q::W, Q::W, kQKeys * Q::W), id_o,
-                              k > 0);
+                    umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k * D, D),
+                              line_desc(p_s + 32 * k * Q::W, Q::W, kQKeys * Q::W), id_o, k > 0);
                 umma_commit(&o_full);
-                umma_commit(&empty[st]);
             }
             if (!ok) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         }
@@ -394,31 +428,47 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         float acc[CW], l[CW];
 #pragma unroll
         for (int r = 0; r < CW; ++r) acc[r] = l[r] = 0.f;
+        // adds the product of the chunk last sent to the tensor cores
+        auto accumulate = [&](int ch) {
+            if (ok) ok = mbar_wait(&o_full, ch & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int r0 = 0; r0 < CW; r0 += 16) {
+                float v[3][16];
+#pragma unroll
+                for (int p = 0; p < 3; ++p) tmem_ld16(tmem + lanes + Q::O_COL + p * ROWS + col0 + r0, v[p]);
+                tmem_ld_wait(v[0], v[1], v[2]);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[r0 + r] += fmaf(v[2][r], 0x1p-17f, fmaf(v[1][r], 0x1p-12f, v[0][r] * 0x1p-6f));
+            }
+        };
         for (int ch = 0; ch < n_chunks; ++ch) {
-            const int st = ch % kQStages, t0 = first + ch * kQKeys, t = t0 + key;
-            if (ok) ok = mbar_wait(&full[st], (ch / kQStages) & 1);  // the scales' own arrival
-            const float ks = kv_scale[st][0][key] * unit, vs = kv_scale[st][1][key], lv = __log2f(vs);
+            const int t0 = first + ch * kQKeys, t = t0 + key;
             const bool masked = t0 + kQKeys - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window);
             if (ok) ok = mbar_wait(&s_full, ch & 1);
             tc_fence_after();
+            const float ks = kv_scale[ch % 4][0][key] * unit, vs = kv_scale[ch % 4][1][key], lv = __log2f(vs);
             // sixteen rows' scores of this key in log2 units, -inf where a row does not see it
-            auto scores = [&](int r0, float *sc) {
+            auto scores = [&](int r0, float (&sc)[16]) {
                 tmem_ld16(tmem + lanes + col0 + r0, sc);
                 if constexpr (Q::FOLD) {
+                    tmem_ld_wait(sc);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) sc[r] *= ks;
-                } else {
+                } else if constexpr (Q::PQ == 2) {
                     float v[16];
                     tmem_ld16(tmem + lanes + ROWS + col0 + r0, v);
+                    tmem_ld_wait(sc, v);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[r] = fmaf(v[r], 0x1p-5f, sc[r]);
-                    if constexpr (Q::PQ == 3) {
-                        tmem_ld16(tmem + lanes + 2 * ROWS + col0 + r0, v);
+                    for (int r = 0; r < 16; ++r) sc[r] = fmaf(v[r], 0x1p-5f, sc[r]) * ks;
+                } else {
+                    float v[16], u[16];
+                    tmem_ld16(tmem + lanes + ROWS + col0 + r0, v);
+                    tmem_ld16(tmem + lanes + 2 * ROWS + col0 + r0, u);
+                    tmem_ld_wait(sc, v, u);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) sc[r] = fmaf(v[r], 0x1p-10f, sc[r]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[r] *= ks;
+                    for (int r = 0; r < 16; ++r) sc[r] = fmaf(u[r], 0x1p-10f, fmaf(v[r], 0x1p-5f, sc[r])) * ks;
                 }
                 if (masked) {
 #pragma unroll
@@ -429,71 +479,50 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                 }
             };
             // 64-row tiles read the scores from TMEM twice rather than hold them
-            float kept[Q::FOLD ? 1 : CW];
-            bool grow = false;  // does a row's maximum leave the range that its reference covers?
-            const float lv1 = lv - 1.f;
+            float kept[16];
+            float top = -INFINITY;  // lane r: the warp's maximum of row r
 #pragma unroll
             for (int r0 = 0; r0 < CW; r0 += 16) {
-                float sc[16];
-                scores(r0, sc);
+                scores(r0, kept);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    grow |= redux_max(sc[r] + lv1) > m_ref[col0 + r0 + r];
-                    if constexpr (!Q::FOLD) kept[r0 + r] = sc[r];
+                    const float m = redux_max(kept[r] + lv);
+                    if (lane == r0 + r) top = m;
                 }
             }
+            if (ch > 0) {
+                accumulate(ch - 1);
+                if (ch + 1 < n_chunks && ch + 1 >= kQStages) load_v(ch + 1, v_row);  // its stage's V has been used
+            }
+            // does a row's maximum leave the range that its reference covers?
+            const bool grow = lane < CW && top > m_ref[col0 + lane] + 1.f;
+            if (grow) atomicMax(&m_key[col0 + lane], orderable(top));
             if (bar_or(1 + g, 128, grow)) {
-#pragma unroll
-                for (int r0 = 0; r0 < CW; r0 += 16) {
-                    float sc[16];
-                    if constexpr (Q::FOLD) scores(r0, sc);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float m = redux_max((Q::FOLD ? sc[r] : kept[Q::FOLD ? 0 : r0 + r]) + lv);
-                        if (lane == r) top = m;
-                    }
-                    if (lane < 16 && top > m_ref[col0 + r0 + lane] + 1.f) atomicMax(&m_key[col0 + r0 + lane], orderable(top));
-                }
-                named_bar_sync(1 + g, 128);
-                // the new reference of row r, or the old one
-                auto reference = [&](int r) {
-                    const uint32_t k = m_key[r];
-                    const float m = __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-                    return k != 0 && m > m_ref[r] + 1.f ? m : m_ref[r];
-                };
-#pragma unroll
-                for (int r = 0; r < CW; ++r) {
-                    const float m = reference(col0 + r);
-                    if (m != m_ref[col0 + r]) {
-                        // m_use is 0 for -inf: all that l holds then are keys of scale 0
-                        const float f = ex2(fminf(m_use[col0 + r] - m, 120.f));
-                        acc[r] *= f;
-                        l[r] *= f;
-                    }
-                }
-                named_bar_sync(1 + g, 128);
                 if (key < CW) {
-                    const float m = reference(col0 + key);
-                    m_ref[col0 + key] = m;
-                    m_use[col0 + key] = m == -INFINITY ? 0.f : m;
+                    const uint32_t k = m_key[col0 + key];
+                    const float now = __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), was = m_ref[col0 + key];
+                    const bool moves = k != 0 && now > was + 1.f;
+                    // m_use is 0 for -inf: all that l holds then are keys of scale 0
+                    m_step[col0 + key] = moves ? ex2(fminf(m_use[col0 + key] - now, 120.f)) : 1.f;
+                    if (moves) m_ref[col0 + key] = m_use[col0 + key] = now;
                 }
                 named_bar_sync(1 + g, 128);
+#pragma unroll
+                for (int r = 0; r < CW; r += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&m_step[col0 + r]);
+                    acc[r] *= f.x, acc[r + 1] *= f.y, acc[r + 2] *= f.z, acc[r + 3] *= f.w;
+                    l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+                }
             }
             // x = 64 p as planes; a line of P holds this key's values of every row and plane. l takes x / (64 vs); keys
             // whose scale is 0 or so small that x may vanish beside it (2^-60) send their warp to the exponential.
             const float lv6 = lv + 6.f;
             const bool small = __any_sync(0xffffffffu, !(vs >= 0x1p-60f));
-            const float to_l = small ? 0.f : 0x1p-6f / vs;
+            const float to_l = small ? 0.f : __fdividef(0x1p-6f, vs);
 #pragma unroll
             for (int r0 = 0; r0 < CW; r0 += 16) {
-                float sc[16];
-                if constexpr (Q::FOLD) {
-                    scores(r0, sc);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[r] = kept[Q::FOLD ? 0 : r0 + r];
-                }
+                float (&sc)[16] = kept;
+                if constexpr (Q::FOLD) scores(r0, sc);
                 if (small) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) l[r0 + r] += ex2(sc[r] - m_use[col0 + r0 + r]);
@@ -525,19 +554,13 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(&p_full);
-            if (ok) ok = mbar_wait(&o_full, ch & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int p = 0; p < Q::PP; ++p)
-#pragma unroll
-                for (int r0 = 0; r0 < CW; r0 += 16) {
-                    float v[16];
-                    tmem_ld16(tmem + lanes + Q::O_COL + p * ROWS + col0 + r0, v);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        acc[r0 + r] = fmaf(v[r], p == 0 ? 0x1p-6f : p == 1 ? 0x1p-12f : 0x1p-17f, acc[r0 + r]);
-                }
+            if (ch + kQStages < n_chunks) {  // this chunk's K has been used
+                v_row = load_k(ch + kQStages, page);
+                page = look(ch + kQStages + 1);
+            }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (n_chunks > 0) accumulate(n_chunks - 1);
         if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         // ---- sums over the keys, and the rows out
         float sum[32];
@@ -546,26 +569,28 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         const float mine = transpose_sum32(sum, lane);
         if (lane < CW) l_s[warp % 4][col0 + lane] = mine;
         named_bar_sync(1 + g, 128);
+        if (key < D) {
+            const size_t o_step = static_cast<size_t>(a.splits) * D, part0 = qattn_slot(a, b, 0, h * grp) + split;
 #pragma unroll
-        for (int r = 0; r < CW; ++r) {
-            const int fr = row0 + col0 + r;
-            if (col0 + r >= n_rows) break;
-            const float total = (l_s[0][col0 + r] + l_s[1][col0 + r]) + (l_s[2][col0 + r] + l_s[3][col0 + r]);
-            const int row = s.r0 + fr / grp, hq = h * grp + fr % grp;
-            if (key < D) {
-                if (parts == 1) {
-                    out[row * a.out_stride + hq * D + key] = from_f32<T>(total == 0.f ? 0.f : acc[r] / total);
-                } else {
-                    const size_t slot = qattn_slot(a, b, fr / grp, hq) + split;
-                    a.part_o[slot * D + key] = acc[r];
-                    if (key == 0) a.part_ml[slot] = make_float2(m_ref[col0 + r], total);
+            for (int r = 0; r < CW; ++r) {
+                if (col0 + r < n_rows) {
+                    const int q = static_cast<int>((h0 + col0 + r) * a.grp_mul >> 22), head = h0 + col0 + r - q * grp;
+                    const float total = (l_s[0][col0 + r] + l_s[1][col0 + r]) + (l_s[2][col0 + r] + l_s[3][col0 + r]);
+                    if (parts == 1) {
+                        out[(s.r0 + i0 + q) * a.out_stride + (h * grp + head) * D + key] =
+                            from_f32<T>(total == 0.f ? 0.f : __fdividef(acc[r], total));
+                    } else {
+                        const uint32_t at = (i0 + q) * a.nq + head;  // rows x heads of a call: below 2^31
+                        a.part_o[part0 * D + at * o_step + key] = acc[r];
+                        if (key == 0) a.part_ml[part0 + static_cast<size_t>(at) * a.splits] = make_float2(m_ref[col0 + r], total);
+                    }
                 }
             }
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, Q::COLS);
+    if (is_mma) tmem_dealloc(tmem, Q::COLS);
 }
 
 constexpr int kQMergeThreads = 128;
@@ -573,14 +598,15 @@ constexpr int kQMergeThreads = 128;
 // A warp joins the parts of one (row, q head): o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i, in part order.
 template <typename T, int D>
 __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs a) {
-    pdl_trigger();
-    pdl_wait();
+    // the spans are no results of the attention before it, which started after whatever wrote them
     const int b = blockIdx.y, item = blockIdx.x * (kQMergeThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
     const QSpan s = qcache_span(a.c, b);
     const int i = item / a.nq, hq = item % a.nq;
     if (i >= s.S) return;
     const int L = s.p0 + s.S, keys = qattn_part_keys(L, a.splits), parts = (L + keys - 1) / keys;
     if (parts == 1) return;
+    pdl_wait();
+    pdl_trigger();
     const int row = s.r0 + i;
     const size_t slot = qattn_slot(a, b, i, hq);
     // parts without a key of this row hold M = -inf, l = 0, o = 0
