@@ -130,11 +130,10 @@ size_t attn_partials(const sdv_qcache_cfg &c, int sm_count) {
 template <typename T, int D, int ROWS>
 int launch_attn_rows(const QAttnArgs &a, const AttnPlan &p, void *stream) {
     typedef QTile<T, D, ROWS> Q;
-    const dim3 grid(static_cast<unsigned>(p.tiles) * a.c.nkv * p.splits, 1, a.c.B);
+    const dim3 grid(static_cast<unsigned>(p.tiles) * a.c.nkv, p.splits, a.c.B);
     int r = launch(qcache_attn_kernel<T, D, ROWS>, grid, Q::THREADS, Q::SMEM, stream, a);
     if (r == SDV_OK && p.splits > 1)
-        r = launch(qcache_merge_kernel<T, D>,
-                   dim3(cdiv(static_cast<long long>(a.c.max_span) * a.nq, kQMergeThreads / 32), a.c.B), kQMergeThreads, 0,
+        r = launch(qcache_merge_kernel<T, D>, dim3(static_cast<unsigned>(a.c.max_span) * a.nq, a.c.B), kQMergeThreads, 0,
                    stream, a);
     return r;
 }
@@ -308,13 +307,17 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     a.nq = cache->c.n_q_heads;
     a.window = window;
     a.q_vec = aligned16(d_q, q_stride, dtype);
-    a.grp_mul = ((1u << 22) + a.nq / a.c.nkv - 1) / (a.nq / a.c.nkv);
     a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(D));
     const AttnPlan p = attn_plan(cache, B, max_span, dtype);
     const size_t slots = attn_partials(cache->c, cache->sm_count);
     a.splits = p.splits;
     a.tiles = p.tiles;
     a.blocks = cache->c.page_size / cache->c.scale_block;
+    a.grp = a.nq / a.c.nkv;
+    a.by_tiles = FastDiv::of(a.tiles);
+    a.by_splits = FastDiv::of(a.splits);
+    a.by_grp = FastDiv::of(a.grp);
+    a.by_nq = FastDiv::of(a.nq);
     a.part_ml = reinterpret_cast<float2 *>(cache->ws + 256);
     a.part_o = reinterpret_cast<float *>(cache->ws + 512 + slots * sizeof(float2) / 256 * 256);
     if (dtype == SDV_BF16) return D == 128 ? launch_attn<bf16, 128>(a, p, stream) : launch_attn<bf16, 64>(a, p, stream);

@@ -37,8 +37,9 @@ struct QAttnArgs {
     int splits;                      // parts a sequence's keys are cut into at most
     int tiles;                       // row tiles of a span of max_span rows
     int blocks;                      // scale blocks of a page
+    int grp;                         // q heads a kv head
     int q_vec;                       // q rows are 16-byte aligned
-    uint32_t grp_mul;                // ceil(2^22 / q heads a kv head)
+    FastDiv by_tiles, by_splits, by_grp, by_nq;
     float scale_log2;                // log2(e) / sqrt(D)
     float *part_o;                   // [sequence][span row][q head][splits][D]
     float2 *part_ml;                 // [sequence][span row][q head][splits]: (M, l)
@@ -156,6 +157,19 @@ __device__ __forceinline__ void tmem_ld_wait(V &...v) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     (tmem_ld_pass(v), ...);
 }
+// Lanes j and j + 16 receive the sum over all 32 lanes of v[j].
+__device__ __forceinline__ float transpose_sum16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int s = 8; s >= 1; s >>= 1) {
+        const bool upper = (lane & s) != 0;
+#pragma unroll
+        for (int i = 0; i < s; ++i) {
+            const float send = upper ? v[i] : v[i + s], keep = upper ? v[i + s] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -181,11 +195,11 @@ __device__ __forceinline__ uint32_t hscale2_u(uint32_t a, float s) {
 }
 
 // ------------------------------------------------------------------ the work of a CTA
-// Grid ((split, kv head, row tile), 1, sequence): the tiles that read the same keys run side by side. A
+// Grid ((kv head, row tile), split, sequence): the tiles that read the same keys run side by side. A
 // sequence of L keys is cut into parts of ceil(L / splits) keys, rounded up to whole chunks: the cut
 // depends on the sequence's own length and the call's B and max_span only.
-__device__ __forceinline__ int qattn_part_keys(int L, int splits) {
-    const int per = (L + splits - 1) / splits;
+__device__ __forceinline__ int qattn_part_keys(const QAttnArgs &a, int L) {
+    const int per = a.by_splits.div(L + a.splits - 1);
     return (per + kQKeys - 1) / kQKeys * kQKeys;
 }
 // First partial result of span row i of sequence b (by its place in the span, which max_span bounds).
@@ -206,8 +220,8 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     pdl_trigger();  // after the wait: what starts behind this kernel may read what came before it
     const QCacheArgs &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int grp = a.nq / c.nkv, tile = blockIdx.x % a.tiles, b = blockIdx.z;
-    const int h = blockIdx.x / a.tiles % c.nkv, split = blockIdx.x / a.tiles / c.nkv;
+    const int grp = a.grp, split = blockIdx.y, b = blockIdx.z;
+    const int h = a.by_tiles.div(blockIdx.x), tile = blockIdx.x - h * a.tiles;
     const QSpan s = qcache_span(c, b);
     T *out = static_cast<T *>(a.out);
     if (s.S == 0) {
@@ -221,15 +235,14 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         return;
     }
     const int row0 = tile * ROWS, n_rows = min(ROWS, s.S * grp - row0);  // flattened (span row, head) rows
-    const int L = s.p0 + s.S, keys = qattn_part_keys(L, a.splits), parts = (L + keys - 1) / keys;
-    if (n_rows <= 0 || split >= parts) return;
-    const int i0 = row0 / grp, h0 = row0 - i0 * grp;
-    // row r of the tile is head (h0 + r) % grp of span row i0 + (h0 + r) / grp; h0 + r < grp + 64 <= 1088
+    const int L = s.p0 + s.S, keys = qattn_part_keys(a, L);
+    if (n_rows <= 0 || split * static_cast<long long>(keys) >= L) return;
+    const bool whole = keys >= L;  // the sequence has one part
     auto row_of = [&](int r) {
-        const int q = static_cast<int>((h0 + r) * a.grp_mul >> 22);
-        return QRow{s.r0 + i0 + q, h * grp + h0 + r - q * grp, i0 + q};
+        const int i = a.by_grp.div(row0 + r);
+        return QRow{s.r0 + i, h * grp + row0 + r - i * grp, i};
     };
-    const int pos_lo = s.p0 + i0, pos_hi = s.p0 + (row0 + n_rows - 1) / grp;
+    const int pos_lo = s.p0 + a.by_grp.div(row0), pos_hi = s.p0 + a.by_grp.div(row0 + n_rows - 1);
     int first = split * keys;
     const int last = min(first + keys, pos_hi + 1);
     if (a.window > 0) first = max(first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
@@ -563,28 +576,49 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         if (n_chunks > 0) accumulate(n_chunks - 1);
         if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         // ---- sums over the keys, and the rows out
-        float sum[32];
 #pragma unroll
-        for (int r = 0; r < 32; ++r) sum[r] = r < CW ? l[r < CW ? r : 0] : 0.f;
-        const float mine = transpose_sum32(sum, lane);
-        if (lane < CW) l_s[warp % 4][col0 + lane] = mine;
+        for (int r0 = 0; r0 < CW; r0 += 16) {
+            float sum[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum[r] = l[r0 + r];
+            const float mine = transpose_sum16(sum, lane);
+            if (lane < 16) l_s[warp % 4][col0 + r0 + lane] = mine;
+        }
         named_bar_sync(1 + g, 128);
-        if (key < D) {
-            const size_t o_step = static_cast<size_t>(a.splits) * D, part0 = qattn_slot(a, b, 0, h * grp) + split;
+        const int rows = min(CW, n_rows - col0);
+        QRow w = row_of(col0);
+        if (whole) {
+            if (key < D) {
+                T *dst = out + w.row * a.out_stride + w.hq * D + key;
+                const long long next = a.out_stride - grp * D;  // from past a row's last head to the next row's first
+                int left = grp - (w.hq - h * grp);
 #pragma unroll
-            for (int r = 0; r < CW; ++r) {
-                if (col0 + r < n_rows) {
-                    const int q = static_cast<int>((h0 + col0 + r) * a.grp_mul >> 22), head = h0 + col0 + r - q * grp;
-                    const float total = (l_s[0][col0 + r] + l_s[1][col0 + r]) + (l_s[2][col0 + r] + l_s[3][col0 + r]);
-                    if (parts == 1) {
-                        out[(s.r0 + i0 + q) * a.out_stride + (h * grp + head) * D + key] =
-                            from_f32<T>(total == 0.f ? 0.f : __fdividef(acc[r], total));
-                    } else {
-                        const uint32_t at = (i0 + q) * a.nq + head;  // rows x heads of a call: below 2^31
-                        a.part_o[part0 * D + at * o_step + key] = acc[r];
-                        if (key == 0) a.part_ml[part0 + static_cast<size_t>(at) * a.splits] = make_float2(m_ref[col0 + r], total);
-                    }
+                for (int r = 0; r < CW; ++r) {
+                    const int k = col0 + r;
+                    const float total = (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]);
+                    if (r < rows) *dst = from_f32<T>(total == 0.f ? 0.f : __fdividef(acc[r], total));
+                    dst += D;
+                    if (--left == 0) dst += next, left = grp;
                 }
+            }
+        } else {
+            if (key < D) {
+                const size_t step = static_cast<size_t>(a.splits) * D;
+                float *dst = a.part_o + (qattn_slot(a, b, w.i, w.hq) + split) * D + key;
+                const size_t next = (a.nq - grp) * step;
+                int left = grp - (w.hq - h * grp);
+#pragma unroll
+                for (int r = 0; r < CW; ++r) {
+                    if (r < rows) *dst = acc[r];
+                    dst += step;
+                    if (--left == 0) dst += next, left = grp;
+                }
+            }
+            if (key < rows) {
+                const int k = col0 + key;
+                w = row_of(k);
+                a.part_ml[qattn_slot(a, b, w.i, w.hq) + split] =
+                    make_float2(m_ref[k], (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]));
             }
         }
         tc_fence_before();
@@ -595,45 +629,53 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
 
 constexpr int kQMergeThreads = 128;
 
-// A warp joins the parts of one (row, q head): o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i, in part order.
+// A CTA joins the parts of one (row, q head): o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i, every fourth part a
+// warp, the four in order. Grid (span row x head, sequence).
 template <typename T, int D>
 __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs a) {
+    constexpr int V = D / 32, NW = kQMergeThreads / 32;
+    const int b = blockIdx.y, i = a.by_nq.div(blockIdx.x), hq = blockIdx.x - i * a.nq;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // the spans are no results of the attention before it, which started after whatever wrote them
-    const int b = blockIdx.y, item = blockIdx.x * (kQMergeThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
     const QSpan s = qcache_span(a.c, b);
-    const int i = item / a.nq, hq = item % a.nq;
-    if (i >= s.S) return;
-    const int L = s.p0 + s.S, keys = qattn_part_keys(L, a.splits), parts = (L + keys - 1) / keys;
-    if (parts == 1) return;
-    pdl_wait();
+    const int L = s.p0 + s.S, keys = qattn_part_keys(a, max(L, 1));
+    const int parts = (L + keys - 1) / keys;
+    __shared__ float o_s[NW][D], l_s[NW];
+    pdl_wait();  // in every CTA: this kernel's end stands for the attention's, too
     pdl_trigger();
-    const int row = s.r0 + i;
+    if (i >= s.S || keys >= L) return;
     const size_t slot = qattn_slot(a, b, i, hq);
     // parts without a key of this row hold M = -inf, l = 0, o = 0
     float m = -INFINITY;
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[slot + p].x);
     m = redux_max(m);
     if (m == -INFINITY) m = 0.f;
-    constexpr int V = D / 32;
     float o[V], l = 0.f;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] = 0.f;
-    for (int p = 0; p < parts; ++p) {
+#pragma unroll 8
+    for (int p = warp; p < parts; p += NW) {
         const float2 ml = a.part_ml[slot + p];
-        if (ml.y == 0.f) continue;
-        const float f = ex2(fminf((ml.x == -INFINITY ? 0.f : ml.x) - m, 120.f));
-        l = fmaf(f, ml.y, l);
         float v[V];
         if constexpr (V == 4)
             *reinterpret_cast<float4 *>(v) = reinterpret_cast<const float4 *>(a.part_o + (slot + p) * D)[lane];
         else
             *reinterpret_cast<float2 *>(v) = reinterpret_cast<const float2 *>(a.part_o + (slot + p) * D)[lane];
+        // M = -inf with l > 0: keys of scale 0 alone, counted from 0
+        const float f = ml.y == 0.f ? 0.f : ex2(fminf((ml.x == -INFINITY ? 0.f : ml.x) - m, 120.f));
+        l = fmaf(f, ml.y, l);
 #pragma unroll
         for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[d], o[d]);
     }
-    T *dst = static_cast<T *>(a.out) + row * a.out_stride + hq * D + lane * V;
 #pragma unroll
-    for (int d = 0; d < V; ++d) dst[d] = from_f32<T>(l == 0.f ? 0.f : o[d] / l);
+    for (int d = 0; d < V; ++d) o_s[warp][lane * V + d] = o[d];
+    if (lane == 0) l_s[warp] = l;
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d < D) {
+        const float num = (o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d]), den = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
+        static_cast<T *>(a.out)[(s.r0 + i) * a.out_stride + hq * D + d] = from_f32<T>(den == 0.f ? 0.f : num / den);
+    }
 }
 
 }  // namespace sdv
