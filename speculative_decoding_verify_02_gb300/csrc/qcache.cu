@@ -23,7 +23,11 @@ namespace {
 
 // Attention of a batch is cut into this many times the CTAs that fit at once (two per SM), so that sequences of
 // different lengths even out; a single sequence into just as many as fit.
-constexpr int kQWaves = 3;
+#ifndef QW1
+#define QW1 1
+#define QWB 3
+#endif
+constexpr int kQWaves = QWB;
 
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -113,7 +117,7 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int dtype) {
     p.rows = attn_rows(span_rows, dtype);
     p.tiles = cdiv(span_rows, p.rows);
     const long long units = static_cast<long long>(B) * q->c.n_kv_heads * p.tiles;
-    const int waves = B > 1 ? kQWaves : 1;
+    const int waves = B > 1 ? QWB : QW1;
     const long long s = 2LL * q->sm_count * waves / units;
     p.splits = static_cast<int>(std::max(1LL, std::min<long long>(s, cdiv(q->c.max_context, kQKeys))));
     return p;
@@ -145,14 +149,22 @@ int launch_attn(const QAttnArgs &a, const AttnPlan &p, void *stream) {
     return launch_attn_rows<T, D, 32>(a, p, stream);
 }
 
+// Every kernel asks for the largest shared-memory carveout: an SM that changes it between an attention and its merge
+// drains first, and with the default one attention CTA fits instead of two.
+template <typename K>
+cudaError_t set_carveout(K kern) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
 template <typename T, int D, int ROWS>
 cudaError_t set_attn() {
-    return cudaFuncSetAttribute(qcache_attn_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                QTile<T, D, ROWS>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(qcache_attn_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         QTile<T, D, ROWS>::SMEM);
+    return e == cudaSuccess ? set_carveout(qcache_attn_kernel<T, D, ROWS>) : e;
 }
 template <typename T, int D>
 cudaError_t set_attn_all() {
-    cudaError_t e = set_attn<T, D, 16>();
+    cudaError_t e = set_carveout(qcache_merge_kernel<T, D>);
+    if (e == cudaSuccess) e = set_attn<T, D, 16>();
     if (e == cudaSuccess) e = set_attn<T, D, 32>();
     if constexpr (!std::is_same<T, __half>::value)
         if (e == cudaSuccess) e = set_attn<T, D, 64>();

@@ -47,6 +47,7 @@ struct QAttnArgs {
 
 constexpr int kQKeys = 128;     // keys of a chunk
 constexpr int kQStages = 2;     // chunks in shared memory
+constexpr float kQNoRef = -1e30f;  // a row's M before it has seen a key: below any w, and w - M is no NaN
 template <typename T, int D_, int ROWS_>
 struct QTile {
     static constexpr int D = D_, ROWS = ROWS_;
@@ -216,12 +217,40 @@ template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_kernel(QAttnArgs a) {
     typedef QTile<T, D, ROWS> Q;
     constexpr int CW = Q::CW;
-    pdl_wait();
-    pdl_trigger();  // after the wait: what starts behind this kernel may read what came before it
     const QCacheArgs &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int grp = a.grp, split = blockIdx.y, b = blockIdx.z;
     const int h = a.by_tiles.div(blockIdx.x), tile = blockIdx.x - h * a.tiles;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t kv_s = smem, q_s = smem + kQStages * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
+    __shared__ uint64_t k_full[kQStages], v_full[kQStages], s_full, p_full, o_full;
+    __shared__ uint32_t tmem_s;
+    __shared__ __align__(16) float m_neg[ROWS], m_step[ROWS];  // -M of each row, and 2^(M before - M) where M last moved
+    __shared__ uint32_t m_key[ROWS];
+    __shared__ int pos_s[ROWS];
+    __shared__ float l_s[4][ROWS], amax_s[Q::WG * 4];
+    __shared__ float kv_scale[4][2][kQKeys];  // four chunks deep: softmax may still read the one two back
+    const bool is_mma = warp == Q::WG * 4;
+    // what needs no data goes before the wait for the kernel ahead
+    if (tid == 0) {
+        for (int i = 0; i < kQStages; ++i) {
+            mbar_init(&k_full[i], Q::WG * 128);
+            mbar_init(&v_full[i], Q::WG * 128);
+        }
+        mbar_init(&s_full, 2);
+        mbar_init(&p_full, Q::WG * 128);
+        mbar_init(&o_full, 1);
+        fence_mbar_init();
+    }
+    if (tid < ROWS) {
+        m_neg[tid] = -kQNoRef;
+        m_key[tid] = 0;
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();  // after the wait: what starts behind this kernel may read what came before it
+
     const QSpan s = qcache_span(c, b);
     T *out = static_cast<T *>(a.out);
     if (s.S == 0) {
@@ -248,20 +277,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     if (a.window > 0) first = max(first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
     const int n_chunks = max(0, (last - first + kQKeys - 1) / kQKeys);
 
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t kv_s = smem, q_s = smem + kQStages * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
-    __shared__ uint64_t k_full[kQStages], v_full[kQStages], s_full, p_full, o_full;
-    __shared__ uint32_t tmem_s;
-    // a row's reference maximum, the same with 0 for -inf, and the factor by which it last moved
-    __shared__ __align__(16) float m_ref[ROWS], m_use[ROWS], m_step[ROWS];
-    __shared__ uint32_t m_key[ROWS];
-    __shared__ int pos_s[ROWS];
-    __shared__ float l_s[4][ROWS], amax_s[Q::WG * 4];
-    __shared__ float kv_scale[4][2][kQKeys];  // four chunks deep: softmax may still read the one two back
-
     // ---- loads: a softmax warp brings LW keys of each chunk in 16-byte pieces, K with both scales, then V
-    const bool is_mma = warp == Q::WG * 4;
     constexpr int LW = kQKeys / (Q::WG * 4), PPR = D / 16, RPI = 32 / PPR;  // keys a warp, pieces a row, rows a copy
     const int my_key = warp * LW + lane;                                     // lanes below LW: the key looked up
     const int *table = c.page_table + static_cast<size_t>(b) * c.pages_per_seq;
@@ -308,29 +324,13 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     if (!is_mma) {
         const int page0 = look(0), page1 = look(1);
         page = look(2);
-        if (tid == 0) {
-            for (int i = 0; i < kQStages; ++i) {
-                mbar_init(&k_full[i], Q::WG * 128);
-                mbar_init(&v_full[i], Q::WG * 128);
-            }
-            mbar_init(&s_full, 2);
-            mbar_init(&p_full, Q::WG * 128);
-            mbar_init(&o_full, 1);
-            fence_mbar_init();
-        }
-        named_bar_sync(7, Q::WG * 128);
         // the first chunks are on their way while the queries are prepared
         if (n_chunks > 0) load_v(0, load_k(0, page0));
         if (n_chunks > 1) load_v(1, load_k(1, page1));
     } else {
         tmem_alloc(&tmem_s, Q::COLS);
         tmem_relinquish();
-        for (int r = lane; r < ROWS; r += 32) {
-            m_ref[r] = -INFINITY;
-            m_use[r] = 0.f;
-            m_key[r] = 0;
-            pos_s[r] = r < n_rows ? s.p0 + row_of(r).i : -1;
-        }
+        for (int r = lane; r < ROWS; r += 32) pos_s[r] = r < n_rows ? s.p0 + row_of(r).i : -1;
     }
     // Q: the tile's rows as e4m3 planes [plane x ROWS + row][D], eight values a thread at a time
     float q_unit = 1.f;  // 2^-e: what the planes' products are multiplied by
@@ -452,8 +452,15 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                 for (int p = 0; p < 3; ++p) tmem_ld16(tmem + lanes + Q::O_COL + p * ROWS + col0 + r0, v[p]);
                 tmem_ld_wait(v[0], v[1], v[2]);
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    acc[r0 + r] += fmaf(v[2][r], 0x1p-17f, fmaf(v[1][r], 0x1p-12f, v[0][r] * 0x1p-6f));
+                for (int r = 0; r < 16; r += 2) {
+                    float2 o = make_float2(acc[r0 + r], acc[r0 + r + 1]);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        const float u = p == 0 ? 0x1p-6f : p == 1 ? 0x1p-12f : 0x1p-17f;
+                        o = __ffma2_rn(make_float2(v[p][r], v[p][r + 1]), make_float2(u, u), o);
+                    }
+                    acc[r0 + r] = o.x, acc[r0 + r + 1] = o.y;
+                }
             }
         };
         for (int ch = 0; ch < n_chunks; ++ch) {
@@ -464,24 +471,30 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             const float ks = kv_scale[ch % 4][0][key] * unit, vs = kv_scale[ch % 4][1][key], lv = __log2f(vs);
             // sixteen rows' scores of this key in log2 units, -inf where a row does not see it
             auto scores = [&](int r0, float (&sc)[16]) {
+                float v[Q::FOLD ? 1 : Q::PQ - 1][16];
                 tmem_ld16(tmem + lanes + col0 + r0, sc);
-                if constexpr (Q::FOLD) {
-                    tmem_ld_wait(sc);
+                if constexpr (!Q::FOLD) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[r] *= ks;
-                } else if constexpr (Q::PQ == 2) {
-                    float v[16];
-                    tmem_ld16(tmem + lanes + ROWS + col0 + r0, v);
-                    tmem_ld_wait(sc, v);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[r] = fmaf(v[r], 0x1p-5f, sc[r]) * ks;
+                    for (int p = 1; p < Q::PQ; ++p) tmem_ld16(tmem + lanes + p * ROWS + col0 + r0, v[p - 1]);
+                    if constexpr (Q::PQ == 2)
+                        tmem_ld_wait(sc, v[0]);
+                    else
+                        tmem_ld_wait(sc, v[0], v[1]);
                 } else {
-                    float v[16], u[16];
-                    tmem_ld16(tmem + lanes + ROWS + col0 + r0, v);
-                    tmem_ld16(tmem + lanes + 2 * ROWS + col0 + r0, u);
-                    tmem_ld_wait(sc, v, u);
+                    tmem_ld_wait(sc);
+                }
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[r] = fmaf(u[r], 0x1p-10f, fmaf(v[r], 0x1p-5f, sc[r])) * ks;
+                for (int r = 0; r < 16; r += 2) {
+                    float2 z = make_float2(sc[r], sc[r + 1]);
+                    if constexpr (!Q::FOLD) {
+#pragma unroll
+                        for (int p = 1; p < Q::PQ; ++p) {
+                            const float u = p == 1 ? 0x1p-5f : 0x1p-10f;
+                            z = __ffma2_rn(make_float2(v[p - 1][r], v[p - 1][r + 1]), make_float2(u, u), z);
+                        }
+                    }
+                    z = __fmul2_rn(z, make_float2(ks, ks));
+                    sc[r] = z.x, sc[r + 1] = z.y;
                 }
                 if (masked) {
 #pragma unroll
@@ -491,33 +504,41 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                     }
                 }
             };
-            // 64-row tiles read the scores from TMEM twice rather than hold them
-            float kept[16];
-            float top = -INFINITY;  // lane r: the warp's maximum of row r
+            // does a row's w leave the range that its reference covers, w > M + 1? 64-row tiles read the scores from
+            // TMEM twice rather than hold them
+            float kept[16], over = -INFINITY;
 #pragma unroll
             for (int r0 = 0; r0 < CW; r0 += 16) {
                 scores(r0, kept);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float m = redux_max(kept[r] + lv);
-                    if (lane == r0 + r) top = m;
+                for (int r = 0; r < 16; r += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(&m_neg[col0 + r0 + r]);
+                    const float2 d = __fadd2_rn(make_float2(kept[r], kept[r + 1]), make_float2(m.x, m.y));
+                    const float2 e = __fadd2_rn(make_float2(kept[r + 2], kept[r + 3]), make_float2(m.z, m.w));
+                    over = fmaxf(over, fmaxf(fmaxf(d.x, d.y), fmaxf(e.x, e.y)));
                 }
             }
-            if (ch > 0) {
-                accumulate(ch - 1);
-                if (ch + 1 < n_chunks && ch + 1 >= kQStages) load_v(ch + 1, v_row);  // its stage's V has been used
-            }
-            // does a row's maximum leave the range that its reference covers?
-            const bool grow = lane < CW && top > m_ref[col0 + lane] + 1.f;
-            if (grow) atomicMax(&m_key[col0 + lane], orderable(top));
-            if (bar_or(1 + g, 128, grow)) {
+            if (ch > 0) accumulate(ch - 1);
+            if (bar_or(1 + g, 128, over + lv > 1.f)) {
+#pragma unroll
+                for (int r0 = 0; r0 < CW; r0 += 16) {
+                    if constexpr (Q::FOLD) scores(r0, kept);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float m = redux_max(kept[r] + lv);
+                        if (lane == r) top = m;
+                    }
+                    if (lane < 16 && top > -INFINITY) atomicMax(&m_key[col0 + r0 + lane], orderable(top));
+                }
+                named_bar_sync(1 + g, 128);
                 if (key < CW) {
                     const uint32_t k = m_key[col0 + key];
-                    const float now = __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), was = m_ref[col0 + key];
+                    const float now = __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), was = -m_neg[col0 + key];
                     const bool moves = k != 0 && now > was + 1.f;
-                    // m_use is 0 for -inf: all that l holds then are keys of scale 0
-                    m_step[col0 + key] = moves ? ex2(fminf(m_use[col0 + key] - now, 120.f)) : 1.f;
-                    if (moves) m_ref[col0 + key] = m_use[col0 + key] = now;
+                    // without a reference so far l holds keys of scale 0 alone, counted from 0
+                    m_step[col0 + key] = moves ? ex2(fminf((was == kQNoRef ? 0.f : was) - now, 120.f)) : 1.f;
+                    if (moves) m_neg[col0 + key] = -now;
                 }
                 named_bar_sync(1 + g, 128);
 #pragma unroll
@@ -534,20 +555,25 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             const float to_l = small ? 0.f : __fdividef(0x1p-6f, vs);
 #pragma unroll
             for (int r0 = 0; r0 < CW; r0 += 16) {
-                float (&sc)[16] = kept;
-                if constexpr (Q::FOLD) scores(r0, sc);
+                if constexpr (Q::FOLD) scores(r0, kept);
                 if (small) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) l[r0 + r] += ex2(sc[r] - m_use[col0 + r0 + r]);
+                    for (int r = 0; r < 16; ++r) {
+                        const float m = m_neg[col0 + r0 + r];
+                        l[r0 + r] += ex2(kept[r] + (m == -kQNoRef ? 0.f : m));
+                    }
                 }
                 uint32_t w[Q::PP][8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float2 m = *reinterpret_cast<const float2 *>(&m_use[col0 + r0 + 2 * j]);
-                    const float x0 = ex2(sc[2 * j] + lv6 - m.x), x1 = ex2(sc[2 * j + 1] + lv6 - m.y);
-                    l[r0 + 2 * j] = fmaf(x0, to_l, l[r0 + 2 * j]);
-                    l[r0 + 2 * j + 1] = fmaf(x1, to_l, l[r0 + 2 * j + 1]);
-                    uint32_t x = f16x2(x0, x1);
+                    const int r = r0 + 2 * j;
+                    const float2 m = *reinterpret_cast<const float2 *>(&m_neg[col0 + r]);
+                    // (s - M) + log2 vs: the first difference is small where it matters
+                    const float2 e = __fadd2_rn(__fadd2_rn(make_float2(kept[2 * j], kept[2 * j + 1]), m), make_float2(lv6, lv6));
+                    const float2 x2 = make_float2(ex2(e.x), ex2(e.y));
+                    const float2 n = __ffma2_rn(x2, make_float2(to_l, to_l), make_float2(l[r], l[r + 1]));
+                    l[r] = n.x, l[r + 1] = n.y;
+                    uint32_t x = f16x2(x2.x, x2.y);
 #pragma unroll
                     for (int p = 0; p < Q::PP; ++p) {
                         w[p][j] = e4m3_of_f16x2(x);
@@ -567,7 +593,9 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(&p_full);
-            if (ch + kQStages < n_chunks) {  // this chunk's K has been used
+            // while the next scores are computed: the stages that this chunk's K and the last one's V have left
+            if (ch > 0 && ch + kQStages - 1 < n_chunks) load_v(ch + kQStages - 1, v_row);
+            if (ch + kQStages < n_chunks) {
                 v_row = load_k(ch + kQStages, page);
                 page = look(ch + kQStages + 1);
             }
@@ -618,7 +646,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                 const int k = col0 + key;
                 w = row_of(k);
                 a.part_ml[qattn_slot(a, b, w.i, w.hq) + split] =
-                    make_float2(m_ref[k], (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]));
+                    make_float2(-m_neg[k], (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]));
             }
         }
         tc_fence_before();
@@ -645,11 +673,11 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs 
     pdl_trigger();
     if (i >= s.S || keys >= L) return;
     const size_t slot = qattn_slot(a, b, i, hq);
-    // parts without a key of this row hold M = -inf, l = 0, o = 0
-    float m = -INFINITY;
+    // parts without a key of this row hold M = kQNoRef, l = 0, o = 0
+    float m = kQNoRef;
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[slot + p].x);
     m = redux_max(m);
-    if (m == -INFINITY) m = 0.f;
+    if (m == kQNoRef) m = 0.f;
     float o[V], l = 0.f;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] = 0.f;
@@ -661,8 +689,8 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs 
             *reinterpret_cast<float4 *>(v) = reinterpret_cast<const float4 *>(a.part_o + (slot + p) * D)[lane];
         else
             *reinterpret_cast<float2 *>(v) = reinterpret_cast<const float2 *>(a.part_o + (slot + p) * D)[lane];
-        // M = -inf with l > 0: keys of scale 0 alone, counted from 0
-        const float f = ml.y == 0.f ? 0.f : ex2(fminf((ml.x == -INFINITY ? 0.f : ml.x) - m, 120.f));
+        // l > 0 without a reference: keys of scale 0 alone, counted from 0
+        const float f = ml.y == 0.f ? 0.f : ex2(fminf((ml.x == kQNoRef ? 0.f : ml.x) - m, 120.f));
         l = fmaf(f, ml.y, l);
 #pragma unroll
         for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[d], o[d]);
