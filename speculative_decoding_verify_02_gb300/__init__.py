@@ -179,32 +179,48 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+_raw_stream = _device = None
+
+
 def _stream(stream) -> int:
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    """The given stream's handle, or the current stream's (read without making a Stream object, which
+    costs about as much as a launch)."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    global _raw_stream, _device
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _raw_stream(_device())
 
 
 # Argument checks of the calls that take strides and types from their tensors. Plain comparisons of
 # attributes: they cost about as much as the ctypes call itself.
-def _expect(t, name, rows):
-    if t.shape[0] < rows:
-        raise ValueError(f"{name}: {t.shape[0]} rows, {rows} are needed")
+_types = {}
+
+
+def _dtype(name):
+    t = _types.get(name)
+    if t is None:
+        import torch
+        t = _types[name] = getattr(torch, name)
+    return t
 
 
 def _vector(t, n, name, dtype):
-    """A contiguous device tensor of at least n elements."""
-    import torch
-    if t.dtype is not getattr(torch, dtype) or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+    """A contiguous device tensor of at least n elements; returns its address."""
+    if t.dtype is not dtype or not t.is_cuda or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} device tensor of at least {n} elements is needed, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _f32_rows(t, cols, name):
-    """Row stride of a device matrix of float32 rows of at least `cols` elements."""
-    import torch
-    if t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[1] < cols or t.stride(1) != 1:
-        raise ValueError(f"{name}: a float32 device matrix of rows of {cols} is needed, got {t.dtype} "
+def _f32_rows(t, rows, cols, name):
+    """Row stride of a device matrix of at least `rows` float32 rows of at least `cols` elements."""
+    if t.dtype is not _dtype("float32") or not t.is_cuda or t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols \
+            or t.stride(1) != 1:
+        raise ValueError(f"{name}: a float32 device matrix of {rows} rows of {cols} is needed, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
 
@@ -343,21 +359,17 @@ class Verifier:
         with the given random numbers: uniforms [R] in [0, 1) and exponential noise [B, vocab].
         draft_probs [R, vocab]: the distribution each draft was drawn from, row r for the draft in
         row r + 1; None: every draft was certain. All float32; the outputs as accept_greedy."""
-        V = self.mcfg.vocab
-        rows = _f32_rows(logits, V, "logits"), _f32_rows(noise, V, "noise")
-        q_stride = 0 if draft_probs is None else _f32_rows(draft_probs, V, "draft_probs")
-        _expect(noise, "noise", B)
-        if draft_probs is not None:
-            _expect(draft_probs, "draft_probs", min(logits.shape[0], self.ccfg.max_rows))
-        _vector(temperature, B, "temperature", "float32")
-        _vector(uniforms, min(logits.shape[0], self.ccfg.max_rows), "uniforms", "float32")
-        for t, n, name in ((row_off, B + 1, "row_off"), (n_accept, B, "n_accept"), (n_commit, B, "n_commit"),
-                           (new_len, B, "new_len"), (committed, B * max_commit, "committed"), (tokens, 1, "tokens")):
-            _vector(t, n, name, "int32")
-        _check(lib().sdv_accept_sampled(self.ctx, _ptr(tokens), _ptr(row_off), _ptr(logits), rows[0],
-                                        _ptr(temperature), _ptr(uniforms), _ptr(noise), rows[1], _ptr(draft_probs),
-                                        q_stride, B, max_commit, _ptr(n_accept), _ptr(committed), _ptr(n_commit),
-                                        _ptr(new_len), _stream(stream)), "accept_sampled")
+        V, R = self.mcfg.vocab, min(logits.shape[0], self.ccfg.max_rows)
+        f32, i32 = _dtype("float32"), _dtype("int32")
+        l_stride, e_stride = _f32_rows(logits, 1, V, "logits"), _f32_rows(noise, B, V, "noise")
+        q_stride = 0 if draft_probs is None else _f32_rows(draft_probs, R, V, "draft_probs")
+        _check(lib().sdv_accept_sampled(
+            self.ctx, _vector(tokens, 1, "tokens", i32), _vector(row_off, B + 1, "row_off", i32), logits.data_ptr(),
+            l_stride, _vector(temperature, B, "temperature", f32), _vector(uniforms, R, "uniforms", f32),
+            noise.data_ptr(), e_stride, _ptr(draft_probs), q_stride, B, max_commit,
+            _vector(n_accept, B, "n_accept", i32), _vector(committed, B * max_commit, "committed", i32),
+            _vector(n_commit, B, "n_commit", i32), _vector(new_len, B, "new_len", i32), _stream(stream)),
+            "accept_sampled")
 
     def rewind_cache(self, length, B, stream=None):
         _check(lib().sdv_rewind_cache(self.ctx, _ptr(length), B, _stream(stream)), "rewind_cache")
@@ -439,7 +451,7 @@ class QuantCache:
         self.cache = c
         self.pages_per_seq = -(-max_context // page_size)
         self._dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-        self._kv, self._q = (n_kv_heads, head_dim), (n_q_heads, head_dim)
+        self._kv_heads, self._q_heads, self._dim = n_kv_heads, n_q_heads, head_dim
 
     def close(self):
         if self.cache:
@@ -453,53 +465,49 @@ class QuantCache:
             pass
 
     def _rows(self, t, heads, name, floats=3):
-        """(row stride, type) of a device tensor [R, heads, dim] with dense rows."""
-        kind = self._dtypes.get(t.dtype, floats)
-        st = t.stride() if t.dim() == 3 else None
-        if kind >= floats or not t.is_cuda or st is None or tuple(t.shape[1:]) != heads or st[2] != 1 or \
-                (heads[0] > 1 and st[1] != heads[1]):
-            raise ValueError(f"{name}: a device tensor [rows, {heads[0]}, {heads[1]}] with dense rows in "
-                             f"{'bf16 or fp16' if floats == 2 else 'bf16, fp16 or fp32'} is needed, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        width = heads[0] * heads[1]
-        return (st[0] if t.shape[0] > 1 else max(st[0], width)), kind
+        """(address, rows, row stride, type) of a device tensor [R, heads, dim] with dense rows."""
+        kind, shape = self._dtypes.get(t.dtype, floats), t.shape
+        if kind < floats and len(shape) == 3 and t.is_cuda and shape[1] == heads and shape[2] == self._dim:
+            st = t.stride()
+            if st[2] == 1 and (st[1] == self._dim or heads == 1):
+                return t.data_ptr(), shape[0], (st[0] if shape[0] > 1 else max(st[0], heads * self._dim)), kind
+        raise ValueError(f"{name}: a device tensor [rows, {heads}, {self._dim}] with dense rows in "
+                         f"{'bf16 or fp16' if floats == 2 else 'bf16, fp16 or fp32'} is needed, got {t.dtype} "
+                         f"{tuple(shape)} on {t.device}")
 
     def _index(self, page_table, row_off, base, B):
-        _vector(page_table, B * self.pages_per_seq, "page_table", "int32")
-        _vector(row_off, B + 1, "row_off", "int32")
-        _vector(base, B, "base", "int32")
+        i32 = _dtype("int32")
+        return (_vector(page_table, B * self.pages_per_seq, "page_table", i32),
+                _vector(row_off, B + 1, "row_off", i32), _vector(base, B, "base", i32))
 
     def write(self, layer, k, v, page_table, row_off, base, B, max_span, stream=None):
         """Quantise rows k, v [R, n_kv_heads, head_dim] (bf16, fp16 or fp32) at positions base[b] + i."""
-        ks, kind = self._rows(k, self._kv, "k")
-        vs, same = self._rows(v, self._kv, "v")
-        if kind != same or k.shape[0] != v.shape[0]:
+        kp, kr, ks, kind = self._rows(k, self._kv_heads, "k")
+        vp, vr, vs, same = self._rows(v, self._kv_heads, "v")
+        if kind != same or kr != vr:
             raise ValueError("k and v: one type and the same rows are needed")
-        self._index(page_table, row_off, base, B)
-        _check(lib().sdv_qcache_write(self.cache, layer, _ptr(k), ks, _ptr(v), vs, kind, _ptr(page_table),
-                                      _ptr(row_off), _ptr(base), B, max_span, _stream(stream)), "qcache_write")
+        _check(lib().sdv_qcache_write(self.cache, layer, kp, ks, vp, vs, kind,
+                                      *self._index(page_table, row_off, base, B), B, max_span, _stream(stream)),
+               "qcache_write")
 
     def read(self, layer, page_table, row_off, base, B, max_span, k, v, stream=None):
         """Read the rows at positions base[b] + i back into k, v [R, n_kv_heads, head_dim]."""
-        ks, kind = self._rows(k, self._kv, "k")
-        vs, same = self._rows(v, self._kv, "v")
-        if kind != same or k.shape[0] != v.shape[0]:
+        kp, kr, ks, kind = self._rows(k, self._kv_heads, "k")
+        vp, vr, vs, same = self._rows(v, self._kv_heads, "v")
+        if kind != same or kr != vr:
             raise ValueError("k and v: one type and the same rows are needed")
-        self._index(page_table, row_off, base, B)
-        _check(lib().sdv_qcache_read(self.cache, layer, _ptr(page_table), _ptr(row_off), _ptr(base), B, max_span,
-                                     _ptr(k), ks, _ptr(v), vs, kind, _stream(stream)), "qcache_read")
+        _check(lib().sdv_qcache_read(self.cache, layer, *self._index(page_table, row_off, base, B), B, max_span, kp, ks,
+                                     vp, vs, kind, _stream(stream)), "qcache_read")
 
     def attention(self, layer, q, page_table, row_off, base, B, max_span, out, window=0, stream=None):
         """Attention of the rows q [R, n_q_heads, head_dim] (bf16 or fp16) at positions base[b] + i over
         their sequence's cache, into out of the same type."""
-        qs, kind = self._rows(q, self._q, "q", 2)
-        os_, same = self._rows(out, self._q, "out", 2)
-        if kind != same or q.shape[0] != out.shape[0]:
+        qp, qr, qs, kind = self._rows(q, self._q_heads, "q", 2)
+        op, orows, os_, same = self._rows(out, self._q_heads, "out", 2)
+        if kind != same or qr != orows:
             raise ValueError("q and out: one type and the same rows are needed")
-        self._index(page_table, row_off, base, B)
-        _check(lib().sdv_qcache_attention(self.cache, layer, _ptr(q), qs, kind, _ptr(page_table), _ptr(row_off),
-                                          _ptr(base), B, max_span, window, _ptr(out), os_, _stream(stream)),
-               "qcache_attention")
+        _check(lib().sdv_qcache_attention(self.cache, layer, qp, qs, kind, *self._index(page_table, row_off, base, B), B,
+                                          max_span, window, op, os_, _stream(stream)), "qcache_attention")
 
     def get_status(self) -> int:
         v = ctypes.c_int32()

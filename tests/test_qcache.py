@@ -58,15 +58,16 @@ def test_null_arguments(sdv):
 
 def test_binding_refuses_host_tensors_types_and_shapes(sdv):
     q = object.__new__(sdv.QuantCache)
+    q._dim = 64
     q._dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
     for t in (torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.float64),
               torch.zeros(2, 128, dtype=torch.bfloat16)):
         with pytest.raises(ValueError, match="k: a device tensor"):
-            q._rows(t, (2, 64), "k")
+            q._rows(t, 2, "k")
     with pytest.raises(ValueError, match="base"):
-        sdv._vector(torch.zeros(2, dtype=torch.int64), 2, "base", "int32")
+        sdv._vector(torch.zeros(2, dtype=torch.int64), 2, "base", torch.int32)
     with pytest.raises(ValueError, match="logits"):
-        sdv._f32_rows(torch.zeros(2, 8), 8, "logits")
+        sdv._f32_rows(torch.zeros(2, 8), 2, 8, "logits")
 
 
 def test_loop_refuses_uniforms_without_temperature(sdv):
