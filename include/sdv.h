@@ -222,6 +222,8 @@ int sdv_accept_greedy(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_ro
  *                 exponential distribution, fresh for every call.
  *   d_draft_probs [R] rows of fp32, probs_stride floats apart, or NULL (the
  *                 stride is then ignored). The last row of a span is not read.
+ *   rows          rows that d_tokens, d_logits, d_uniform and d_draft_probs hold;
+ *                 at most the context's 128 are used. A span past them is refused.
  *   max_commit    row stride of d_committed; a span longer than it is refused.
  * Device errors: a refused span (SDV_ERR_ARG; outputs as for an empty one); a
  * draft outside [0, vocab) counts as refused and a row without a logit above
@@ -229,7 +231,7 @@ int sdv_accept_greedy(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_ro
 int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_row_off, const float *d_logits,
                        int64_t logits_stride, const float *d_temperature, const float *d_uniform,
                        const float *d_noise, int64_t noise_stride, const float *d_draft_probs, int64_t probs_stride,
-                       int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
+                       int rows, int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
                        int32_t *d_new_len, void *stream);
 
 /* [TS] SpecRewindCache; [PI] LIFO drop; [CA] rollback == do not advance.
@@ -404,8 +406,9 @@ int sdv_noalloc_status(int32_t *h_status);
  * masked position would reach the rows that do not see it. sdv_qcache_write
  * stores none.
  * Spans are packed as everywhere: row row_off[b] + i is position base[b] + i of
- * sequence b. A span longer than max_span or outside [0, max_rows) sets
- * SDV_ERR_ARG, one past max_context SDV_ERR_CAPACITY: its rows are not written
+ * sequence b; `rows` is how many the call's row tensors hold (at most the
+ * cache's max_rows are used). A span longer than max_span or outside
+ * [0, rows) sets SDV_ERR_ARG, one past max_context SDV_ERR_CAPACITY: its rows are not written
  * or read, and come back from attention as NaN. A page id outside
  * [0, n_pages) sets SDV_ERR_CAPACITY and is not accessed; it reads as zeros. */
 #define SDV_BF16 0
@@ -447,7 +450,7 @@ int sdv_qcache_destroy(sdv_qcache *cache);
  * +-448 scale and a NaN as zero, neither counts for the scale, and either sets
  * SDV_ERR_DEVICE. Spans of one call must not share pages that they write. */
 int sdv_qcache_write(sdv_qcache *cache, int layer, const void *d_k, int64_t k_stride, const void *d_v, int64_t v_stride,
-                     int dtype, const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
+                     int dtype, int rows, const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
                      int max_span, void *stream);
 
 /* Read the rows of each span back: d_k, d_v as in sdv_qcache_write, as outputs.
@@ -455,7 +458,7 @@ int sdv_qcache_write(sdv_qcache *cache, int layer, const void *d_k, int64_t k_st
  * held. */
 int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, const int32_t *d_row_off,
                     const int32_t *d_base, int B, int max_span, void *d_k, int64_t k_stride, void *d_v,
-                    int64_t v_stride, int dtype, void *stream);
+                    int64_t v_stride, int dtype, int rows, void *stream);
 
 /* Paged attention over the codes, as sdv_op_attention over 16 bits: the row at
  * position p attends positions 0..p, or max(0, p - window + 1)..p for
@@ -464,7 +467,7 @@ int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, c
  * out_stride elements apart; q after RoPE; scores are q.k / sqrt(head_dim).
  * A row's result depends on its own sequence, B, max_span and window only, not
  * on the other sequences. */
-int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t q_stride, int dtype,
+int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t q_stride, int dtype, int rows,
                          const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
                          int max_span, int window, void *d_out, int64_t out_stride, void *stream);
 

@@ -110,13 +110,13 @@ def lib():
     L.sdv_spec_forward_sampled.argtypes = [vp, vp, vp, i32, i32, i32, vp, ctypes.c_uint64, vp, vp, vp]
     L.sdv_accept_greedy.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]
     i64 = ctypes.c_int64
-    L.sdv_accept_sampled.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp]
+    L.sdv_accept_sampled.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp]
     L.sdv_qcache_bytes.argtypes = [P(QCacheCfg), P(sz), P(sz), P(sz)]
     L.sdv_qcache_create.argtypes = [P(QCacheCfg), vp, vp, vp, vp, P(vp)]
     L.sdv_qcache_destroy.argtypes = [vp]
-    L.sdv_qcache_write.argtypes = [vp, i32, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, vp]
-    L.sdv_qcache_read.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp]
-    L.sdv_qcache_attention.argtypes = [vp, i32, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp]
+    L.sdv_qcache_write.argtypes = [vp, i32, vp, i64, vp, i64, i32, i32, vp, vp, vp, i32, i32, vp]
+    L.sdv_qcache_read.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, i32, vp]
+    L.sdv_qcache_attention.argtypes = [vp, i32, vp, i64, i32, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp]
     L.sdv_qcache_get_status.argtypes = [vp, P(ctypes.c_int32)]
     L.sdv_rewind_cache.argtypes = [vp, vp, i32, vp]
     L.sdv_cache_seq_len.argtypes = [vp, vp, vp]
@@ -361,12 +361,12 @@ class Verifier:
         row r + 1; None: every draft was certain. All float32; the outputs as accept_greedy."""
         V, R = self.mcfg.vocab, min(logits.shape[0], self.ccfg.max_rows)
         f32, i32 = _dtype("float32"), _dtype("int32")
-        l_stride, e_stride = _f32_rows(logits, 1, V, "logits"), _f32_rows(noise, B, V, "noise")
+        l_stride, e_stride = _f32_rows(logits, 0, V, "logits"), _f32_rows(noise, B, V, "noise")
         q_stride = 0 if draft_probs is None else _f32_rows(draft_probs, R, V, "draft_probs")
         _check(lib().sdv_accept_sampled(
-            self.ctx, _vector(tokens, 1, "tokens", i32), _vector(row_off, B + 1, "row_off", i32), logits.data_ptr(),
+            self.ctx, _vector(tokens, R, "tokens", i32), _vector(row_off, B + 1, "row_off", i32), logits.data_ptr(),
             l_stride, _vector(temperature, B, "temperature", f32), _vector(uniforms, R, "uniforms", f32),
-            noise.data_ptr(), e_stride, _ptr(draft_probs), q_stride, B, max_commit,
+            noise.data_ptr(), e_stride, _ptr(draft_probs), q_stride, R, B, max_commit,
             _vector(n_accept, B, "n_accept", i32), _vector(committed, B * max_commit, "committed", i32),
             _vector(n_commit, B, "n_commit", i32), _vector(new_len, B, "new_len", i32), _stream(stream)),
             "accept_sampled")
@@ -486,7 +486,7 @@ class QuantCache:
         vp, vr, vs, same = self._rows(v, self._kv_heads, "v")
         if kind != same or kr != vr:
             raise ValueError("k and v: one type and the same rows are needed")
-        _check(lib().sdv_qcache_write(self.cache, layer, kp, ks, vp, vs, kind,
+        _check(lib().sdv_qcache_write(self.cache, layer, kp, ks, vp, vs, kind, kr,
                                       *self._index(page_table, row_off, base, B), B, max_span, _stream(stream)),
                "qcache_write")
 
@@ -497,7 +497,7 @@ class QuantCache:
         if kind != same or kr != vr:
             raise ValueError("k and v: one type and the same rows are needed")
         _check(lib().sdv_qcache_read(self.cache, layer, *self._index(page_table, row_off, base, B), B, max_span, kp, ks,
-                                     vp, vs, kind, _stream(stream)), "qcache_read")
+                                     vp, vs, kind, kr, _stream(stream)), "qcache_read")
 
     def attention(self, layer, q, page_table, row_off, base, B, max_span, out, window=0, stream=None):
         """Attention of the rows q [R, n_q_heads, head_dim] (bf16 or fp16) at positions base[b] + i over
@@ -506,7 +506,7 @@ class QuantCache:
         op, orows, os_, same = self._rows(out, self._q_heads, "out", 2)
         if kind != same or qr != orows:
             raise ValueError("q and out: one type and the same rows are needed")
-        _check(lib().sdv_qcache_attention(self.cache, layer, qp, qs, kind, *self._index(page_table, row_off, base, B), B,
+        _check(lib().sdv_qcache_attention(self.cache, layer, qp, qs, kind, qr, *self._index(page_table, row_off, base, B), B,
                                           max_span, window, op, os_, _stream(stream)), "qcache_attention")
 
     def get_status(self) -> int:

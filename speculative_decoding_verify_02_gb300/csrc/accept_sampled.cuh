@@ -19,8 +19,6 @@ namespace sdv {
 constexpr int kAcceptThreads = 256;
 constexpr int kAcceptPer = 16;                               // logits a thread holds
 constexpr int kAcceptChunk = kAcceptThreads * kAcceptPer;    // logits of one statistics CTA
-constexpr int kDrawThreads = 512;
-constexpr int kDrawCluster = 8;                              // CTAs that share a sequence's draw
 constexpr int kAcceptMaxSpan = 128;
 
 struct AcceptSampledArgs {
@@ -30,6 +28,8 @@ struct AcceptSampledArgs {
     long long logits_stride, noise_stride, probs_stride;  // floats between rows
     int B, max_span, max_commit, vocab, n_chunks, rows_cap, adaptive, k_max;
     float2 *part;  // [rows_cap][n_chunks]: (max, sum) of a chunk, or (max, index of the max) of a greedy row
+    unsigned long long *keys;  // [max_batch][2]: best score so far, over max(p - q, 0) and over p
+    int *arrived;              // [max_batch]: chunks that have put in theirs
     int *n_accept, *committed, *n_commit, *new_len;
 };
 
@@ -61,10 +61,30 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
     return v;
 }
 
+// Sixteen values a thread of a chunk of a row: four groups of four, coalesced, `fill` past the vocabulary.
+__device__ __forceinline__ void load_chunk(const float *row, int v0, int vocab, float fill, float (&x)[kAcceptPer]) {
+    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0 && v0 + kAcceptChunk <= vocab;
+#pragma unroll
+    for (int j = 0; j < kAcceptPer / 4; ++j) {
+        const int v = v0 + (j * kAcceptThreads + threadIdx.x) * 4;
+        if (vec) {
+            const float4 f = *reinterpret_cast<const float4 *>(row + v);
+            x[4 * j] = f.x, x[4 * j + 1] = f.y, x[4 * j + 2] = f.z, x[4 * j + 3] = f.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[4 * j + k] = v + k < vocab ? row[v + k] : fill;
+        }
+    }
+}
+// Vocabulary index of value j of this thread.
+__device__ __forceinline__ int chunk_index(int v0, int j) {
+    return v0 + ((j / 4) * kAcceptThreads + threadIdx.x) * 4 + (j & 3);
+}
+
 // Statistics of one chunk of one row: grid (chunks, B * max_span).
 __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSampledArgs p) {
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     const int b = blockIdx.y / p.max_span, i = blockIdx.y % p.max_span;
     const int2 sp = accept_span(p, b);
     if (i >= sp.y) return;
@@ -72,19 +92,12 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSamp
     const float T = p.temperature[b];
     const float *row = p.logits + r * p.logits_stride;
     const int v0 = blockIdx.x * kAcceptChunk, tid = threadIdx.x;
-    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0 && v0 + kAcceptChunk <= p.vocab;
-    float x[kAcceptPer];
-#pragma unroll
-    for (int j = 0; j < kAcceptPer / 4; ++j) {
-        const int v = v0 + (j * kAcceptThreads + tid) * 4;
-        if (vec) {
-            const float4 f = *reinterpret_cast<const float4 *>(row + v);
-            x[4 * j] = f.x, x[4 * j + 1] = f.y, x[4 * j + 2] = f.z, x[4 * j + 3] = f.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[4 * j + k] = v + k < p.vocab ? row[v + k] : -INFINITY;
-        }
+    if (blockIdx.x == 0 && i == 0 && tid < 2) {  // for the draw that follows
+        p.keys[2 * b + tid] = 0;
+        if (tid == 0) p.arrived[b] = 0;
     }
+    float x[kAcceptPer];
+    load_chunk(row, v0, p.vocab, -INFINITY, x);
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kAcceptPer; ++j) m = fmaxf(m, x[j]);  // fmaxf passes over NaN
@@ -103,7 +116,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSamp
         if (m > -INFINITY) {
 #pragma unroll
             for (int j = 0; j < kAcceptPer; ++j)
-                if (x[j] == m) atomicMin(&best, v0 + ((j / 4) * kAcceptThreads + tid) * 4 + (j & 3));
+                if (x[j] == m) atomicMin(&best, chunk_index(v0, j));
         }
         __syncthreads();
         if (tid == 0) *out = make_float2(m, __int_as_float(best));
@@ -125,19 +138,18 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSamp
     }
 }
 
-// One cluster per sequence: the accepted prefix (each CTA finds it from the chunk statistics), the
-// race over the vocabulary split over the CTAs, and the outputs and loop state as accept_kernel
-// writes them.
-__global__ void __launch_bounds__(kDrawThreads) accept_draw_kernel(AcceptSampledArgs p) {
-    pdl_trigger();
+// The accepted prefix of a sequence (every CTA finds it from the chunk statistics), the race over one
+// chunk of the vocabulary at its last row, and, in the CTA that comes last, the outputs and loop state as
+// accept_kernel writes them. Grid (chunks, B). The best key is the same in any order of arrival.
+__global__ void __launch_bounds__(kAcceptThreads) accept_draw_kernel(AcceptSampledArgs p) {
     pdl_wait();
-    const int b = blockIdx.x / kDrawCluster;
-    const uint32_t rank = cluster_ctarank();
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    pdl_trigger();
+    constexpr int NW = kAcceptThreads / 32;
+    const int b = blockIdx.y, v0 = blockIdx.x * kAcceptChunk, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int2 sp = accept_span(p, b);
     const int r0 = sp.x, S = sp.y;
-    if (S == 0) {  // the whole cluster leaves together
-        if (rank == 0 && tid == 0) {
+    if (S == 0) {
+        if (blockIdx.x == 0 && tid == 0) {
             if (p.row_off[b + 1] != r0) set_status(p.s.status, SDV_ERR_ARG);
             p.n_accept[b] = -1;
             p.n_commit[b] = 0;
@@ -146,13 +158,20 @@ __global__ void __launch_bounds__(kDrawThreads) accept_draw_kernel(AcceptSampled
         return;
     }
     __shared__ float row_m[kAcceptMaxSpan], row_l[kAcceptMaxSpan];
-    __shared__ int row_best[kAcceptMaxSpan], row_ok[kAcceptMaxSpan], m_s;
-    __shared__ unsigned long long keys[2][kDrawThreads / 32], cta_key[2];
+    __shared__ int row_best[kAcceptMaxSpan], row_ok[kAcceptMaxSpan], m_s, last_s;
+    __shared__ unsigned long long keys[2][NW];
     const float T = p.temperature[b];
     const bool greedy = !(T > 0.f);
+    if (greedy && blockIdx.x > 0) return;  // the statistics hold the answer
     const float c = 1.4426950408889634f / T;
-    for (int i = warp; i < S; i += kDrawThreads / 32) {
-        const int r = r0 + i;
+    float e[kAcceptPer];
+    if (!greedy) load_chunk(p.noise + b * p.noise_stride, v0, p.vocab, 1.f, e);
+    for (int i = warp; i < S; i += NW) {
+        const int r = r0 + i, d = i + 1 < S ? p.tokens[r + 1] : -1;
+        const bool draft = d >= 0 && d < p.vocab;
+        // asked for ahead of the sums
+        const float q = draft && p.probs ? p.probs[r * p.probs_stride + d] : 1.f, u = p.uniform[r];
+        const float x = draft ? p.logits[r * p.logits_stride + d] : 0.f;
         const float2 *part = p.part + static_cast<size_t>(r) * p.n_chunks;
         float m = -INFINITY, l = 0.f;
         int best = 0x7fffffff;
@@ -172,23 +191,21 @@ __global__ void __launch_bounds__(kDrawThreads) accept_draw_kernel(AcceptSampled
             row_m[i] = m;
             row_l[i] = l;
             row_best[i] = best;
-            int ok = 0;
-            if (i + 1 < S && m > -INFINITY) {
-                const int d = p.tokens[r + 1];
-                if (d >= 0 && d < p.vocab) {
-                    const float q = p.probs ? p.probs[r * p.probs_stride + d] : 1.f;
-                    // the draft's own weight in 64 bits: one value a row, and the one that decides
-                    const float x = p.logits[r * p.logits_stride + d];
-                    double pd;
-                    if (greedy)
-                        pd = d == best ? 1.0 : 0.0;
-                    else if (x == m)
-                        pd = 1.0 / l;
-                    else
-                        pd = x > -INFINITY && x < m
-                                 ? exp((static_cast<double>(x) - static_cast<double>(m)) / static_cast<double>(T)) / l
-                                 : 0.0;
-                    ok = static_cast<double>(p.uniform[r]) * static_cast<double>(q) < pd;
+            bool ok = false;
+            if (draft && m > -INFINITY) {
+                if (greedy) {
+                    ok = d == best && u * q < 1.f;
+                } else {
+                    const float uq = u * q, pd = logit_weight(x, m, c) / l;
+                    ok = uq < pd;
+                    // next to the border the draft's own weight is taken in 64 bits: fp32's is off by |x - m| / T 2^-23
+                    // and a few 2^-24 at most, 2^-15 up to 100 units below the maximum
+                    if (fabsf(uq - pd) <= 0x1p-15f * pd) {
+                        const double w = x == m ? 1.0
+                                                : exp((static_cast<double>(x) - static_cast<double>(m)) /
+                                                      static_cast<double>(T));
+                        ok = static_cast<double>(u) * static_cast<double>(q) < w / l;
+                    }
                 }
             }
             row_ok[i] = ok;
@@ -209,32 +226,26 @@ __global__ void __launch_bounds__(kDrawThreads) accept_draw_kernel(AcceptSampled
         token = xm > -INFINITY ? row_best[m] : 0;
     } else {
         const float inv_l = 1.f / row_l[m];
-        const float *x = p.logits + r * p.logits_stride, *e = p.noise + b * p.noise_stride;
-        const float *q = rejected && p.probs ? p.probs + r * p.probs_stride : nullptr;
         const int drop = rejected && !p.probs ? p.tokens[r + 1] : -1;  // a certain draft leaves no weight
-        // best score over max(p - q, 0), and over p in case nothing is left of it
+        float x[kAcceptPer], q[kAcceptPer];
+        load_chunk(p.logits + r * p.logits_stride, v0, p.vocab, -INFINITY, x);
+        if (rejected && p.probs) {
+            load_chunk(p.probs + r * p.probs_stride, v0, p.vocab, 0.f, q);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kAcceptPer; ++j) q[j] = 0.f;
+        }
+        // best score over max(p - q, 0), and over p in case nothing is left of it; a thread's indexes ascend
         float s0 = -1.f, s1 = -1.f;
         int i0 = 0, i1 = 0;
-        auto consider = [&](int v, float xv, float qv, float ev) {
-            const float pv = logit_weight(xv, xm, c) * inv_l;
-            const float w = v == drop ? 0.f : pv - qv;
-            const float t0 = w > 0.f ? w / ev : -1.f, t1 = pv > 0.f ? pv / ev : -1.f;
+#pragma unroll
+        for (int j = 0; j < kAcceptPer; ++j) {
+            const int v = chunk_index(v0, j);
+            const float pv = logit_weight(x[j], xm, c) * inv_l, w = v == drop ? 0.f : pv - q[j];
+            const float t0 = w > 0.f ? w / e[j] : -1.f, t1 = pv > 0.f ? pv / e[j] : -1.f;
             if (t0 > s0) s0 = t0, i0 = v;
             if (t1 > s1) s1 = t1, i1 = v;
-        };
-        const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(e) |
-                           reinterpret_cast<uintptr_t>(q)) & 15) == 0;
-        const int nvec = vec ? p.vocab / 4 : 0;
-        for (int k = rank * kDrawThreads + tid; k < nvec; k += kDrawCluster * kDrawThreads) {
-            const float4 xv = reinterpret_cast<const float4 *>(x)[k], ev = reinterpret_cast<const float4 *>(e)[k];
-            const float4 qv = q ? reinterpret_cast<const float4 *>(q)[k] : make_float4(0.f, 0.f, 0.f, 0.f);
-            consider(4 * k, xv.x, qv.x, ev.x);
-            consider(4 * k + 1, xv.y, qv.y, ev.y);
-            consider(4 * k + 2, xv.z, qv.z, ev.z);
-            consider(4 * k + 3, xv.w, qv.w, ev.w);
         }
-        for (int v = 4 * nvec + rank * kDrawThreads + tid; v < p.vocab; v += kDrawCluster * kDrawThreads)
-            consider(v, x[v], q ? q[v] : 0.f, e[v]);
         // scores are >= 0, so their bits order them; the complement of the index breaks ties low
         auto pack = [](float s, int v) {
             return s < 0.f ? 0ull
@@ -243,28 +254,28 @@ __global__ void __launch_bounds__(kDrawThreads) accept_draw_kernel(AcceptSampled
         const unsigned long long k0 = warp_max_u64(pack(s0, i0)), k1 = warp_max_u64(pack(s1, i1));
         if (lane == 0) keys[0][warp] = k0, keys[1][warp] = k1;
         __syncthreads();
-        if (warp < 2) {
-            const unsigned long long k = warp_max_u64(lane < kDrawThreads / 32 ? keys[warp][lane] : 0ull);
-            if (lane == 0) cta_key[warp] = k;
-        }
-        cluster_sync();
-        if (rank == 0 && warp == 0) {
-            unsigned long long k[2];
+        if (tid == 0) {
+            unsigned long long best[2] = {0, 0};
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                k[t] = 0;
-                if (lane < kDrawCluster) {
-                    const float2 f = ld_dsmem_f2(mapa_shared(smem_u32(&cta_key[t]), lane));
-                    k[t] = static_cast<unsigned long long>(__float_as_uint(f.y)) << 32 | __float_as_uint(f.x);
-                }
-                k[t] = warp_max_u64(k[t]);
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) best[t] = keys[t][w] > best[t] ? keys[t][w] : best[t];
+            if (best[0]) atomicMax(&p.keys[2 * b], best[0]);
+            if (best[1]) atomicMax(&p.keys[2 * b + 1], best[1]);
+            __threadfence();
+            last_s = atomicAdd(&p.arrived[b], 1) == p.n_chunks - 1;
+            if (last_s) {
+                __threadfence();
+                const unsigned long long a0 = atomicMax(&p.keys[2 * b], 0ull), a1 = atomicMax(&p.keys[2 * b + 1], 0ull);
+                const unsigned long long won = a0 ? a0 : a1;
+                m_s = won ? static_cast<int>(~static_cast<uint32_t>(won)) : 0;
             }
-            const unsigned long long won = k[0] ? k[0] : k[1];
-            token = won ? static_cast<int>(~static_cast<uint32_t>(won)) : 0;
         }
-        cluster_sync();  // no CTA leaves while its key may still be read
+        __syncthreads();
+        if (!last_s) return;
+        token = m_s;
     }
-    if (rank != 0 || warp != 0) return;
+    if (warp != 0) return;
     for (int i = lane; i < m; i += 32) p.committed[static_cast<size_t>(b) * p.max_commit + i] = p.tokens[r0 + 1 + i];
     if (lane != 0) return;
     if (xm == -INFINITY) set_status(p.s.status, SDV_ERR_DEVICE);  // a row without a logit to draw

@@ -16,7 +16,7 @@ struct sdv_qcache {
     float *scales = nullptr;
     uint8_t *ws = nullptr;
     size_t layer_codes = 0, layer_scales = 0;
-    FastDiv by_page{}, by_block{};
+    FastDiv by_page{}, by_block{}, by_heads{};
 };
 
 namespace {
@@ -70,9 +70,9 @@ int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, void *str
 }
 
 // Arguments that every call shares, checked; SDV_OK and the kernels' block, or the error.
-int common_args(const sdv_qcache *q, int layer, const int32_t *table, const int32_t *row_off, const int32_t *base, int B,
-                int max_span, QCacheArgs *a) {
-    if (!q || !table || !row_off || !base || layer < 0 || layer >= q->c.n_layers || B <= 0 || B > q->c.max_batch ||
+int common_args(const sdv_qcache *q, int layer, int rows, const int32_t *table, const int32_t *row_off,
+                const int32_t *base, int B, int max_span, QCacheArgs *a) {
+    if (!q || !table || !row_off || !base || layer < 0 || layer >= q->c.n_layers || rows <= 0 || B <= 0 || B > q->c.max_batch ||
         max_span <= 0 || max_span > q->c.max_span)
         return SDV_ERR_ARG;
     int dev = -1;
@@ -90,10 +90,12 @@ int common_args(const sdv_qcache *q, int layer, const int32_t *table, const int3
     a->nkv = q->c.n_kv_heads;
     a->B = B;
     a->max_span = max_span;
-    a->max_rows = q->c.max_rows;
+    a->max_rows = std::min(rows, q->c.max_rows);
     a->max_context = q->c.max_context;
     a->by_page = q->by_page;
     a->by_block = q->by_block;
+    a->by_heads = q->by_heads;
+    a->blocks = q->c.page_size / q->c.scale_block;
     return SDV_OK;
 }
 
@@ -183,7 +185,7 @@ int write_rows(const QCacheArgs &a, const void *k, int64_t ks, const void *v, in
 
 template <typename T, int D>
 int read_rows(const QCacheArgs &a, void *k, int64_t ks, void *v, int64_t vs, bool vec, void *stream) {
-    const dim3 grid(cdiv(a.max_span, kQReadThreads / (D / 8)), a.B, 2 * a.nkv);
+    const dim3 grid(2 * a.nkv, cdiv(a.max_span, kQReadThreads / (D / 8) * kQReadRows), a.B);
     T *kp = static_cast<T *>(k), *vp = static_cast<T *>(v);
     const long long k_stride = ks, v_stride = vs;
     return vec ? launch(qcache_read_kernel<T, D, true>, grid, kQReadThreads, 0, stream, a, kp, vp, k_stride, v_stride)
@@ -242,6 +244,7 @@ int sdv_qcache_create(const sdv_qcache_cfg *cfg, void *d_codes, void *d_scales, 
     q->layer_scales = layer_scales(*cfg);
     q->by_page = FastDiv::of(cfg->page_size);
     q->by_block = FastDiv::of(cfg->scale_block);
+    q->by_heads = FastDiv::of(2 * cfg->n_kv_heads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemsetAsync(q->codes, 0, q->layer_codes * cfg->n_layers, st);
     if (e == cudaSuccess) e = cudaMemsetAsync(q->scales, 0, q->layer_scales * cfg->n_layers * sizeof(float), st);
@@ -260,10 +263,10 @@ int sdv_qcache_destroy(sdv_qcache *cache) {
 }
 
 int sdv_qcache_write(sdv_qcache *cache, int layer, const void *d_k, int64_t k_stride, const void *d_v, int64_t v_stride,
-                     int dtype, const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
+                     int dtype, int rows, const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
                      int max_span, void *stream) {
     QCacheArgs a{};
-    const int r = common_args(cache, layer, d_page_table, d_row_off, d_base, B, max_span, &a);
+    const int r = common_args(cache, layer, rows, d_page_table, d_row_off, d_base, B, max_span, &a);
     if (r) return r;
     const int D = cache->c.head_dim, width = cache->c.n_kv_heads * D;
     if (dtype != SDV_BF16 && dtype != SDV_FP16 && dtype != SDV_FP32) return SDV_ERR_UNSUPPORTED;
@@ -282,9 +285,9 @@ int sdv_qcache_write(sdv_qcache *cache, int layer, const void *d_k, int64_t k_st
 
 int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, const int32_t *d_row_off,
                     const int32_t *d_base, int B, int max_span, void *d_k, int64_t k_stride, void *d_v,
-                    int64_t v_stride, int dtype, void *stream) {
+                    int64_t v_stride, int dtype, int rows, void *stream) {
     QCacheArgs a{};
-    const int r = common_args(cache, layer, d_page_table, d_row_off, d_base, B, max_span, &a);
+    const int r = common_args(cache, layer, rows, d_page_table, d_row_off, d_base, B, max_span, &a);
     if (r) return r;
     const int D = cache->c.head_dim, width = cache->c.n_kv_heads * D;
     if (dtype != SDV_BF16 && dtype != SDV_FP16 && dtype != SDV_FP32) return SDV_ERR_UNSUPPORTED;
@@ -301,11 +304,11 @@ int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, c
 #undef SDV_QREAD
 }
 
-int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t q_stride, int dtype,
+int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t q_stride, int dtype, int rows,
                          const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
                          int max_span, int window, void *d_out, int64_t out_stride, void *stream) {
     QAttnArgs a{};
-    const int r = common_args(cache, layer, d_page_table, d_row_off, d_base, B, max_span, &a.c);
+    const int r = common_args(cache, layer, rows, d_page_table, d_row_off, d_base, B, max_span, &a.c);
     if (r) return r;
     const int D = cache->c.head_dim, width = cache->c.n_q_heads * D;
     if (dtype != SDV_BF16 && dtype != SDV_FP16) return SDV_ERR_UNSUPPORTED;
@@ -324,7 +327,6 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     const size_t slots = attn_partials(cache->c, cache->sm_count);
     a.splits = p.splits;
     a.tiles = p.tiles;
-    a.blocks = cache->c.page_size / cache->c.scale_block;
     a.grp = a.nq / a.c.nkv;
     a.by_tiles = FastDiv::of(a.tiles);
     a.by_splits = FastDiv::of(a.splits);

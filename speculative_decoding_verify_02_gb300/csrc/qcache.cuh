@@ -38,7 +38,8 @@ struct QCacheArgs {
     int *status;
     const int *page_table, *row_off, *base;
     int pages_per_seq, page_size, n_pages, scale_block, nkv, B, max_span, max_rows, max_context;
-    FastDiv by_page, by_block;  // page_size and scale_block
+    int blocks;                           // scale blocks of a page
+    FastDiv by_page, by_block, by_heads;  // page_size, scale_block, 2 nkv
 };
 
 // One sequence's span: rows r0 .. r0 + S - 1 at positions p0 .. p0 + S - 1. S = 0 where it is empty or
@@ -87,21 +88,29 @@ __device__ __forceinline__ bf16 from_f32<bf16>(float x) { return __float2bfloat1
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half(x); }
 
-// Eight values of a row in registers, from a row that is 16-byte aligned or (VEC false) not.
+// Eight values of a row as they lie in memory, from a row that is 16-byte aligned or (VEC false) not.
+template <typename T>
+struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ float at(int k) const { return to_f32(reinterpret_cast<const T *>(u)[k]); }
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *src, float (&x)[8]) {
+__device__ __forceinline__ Raw8<T> load_raw8(const T *src) {
+    Raw8<T> r;
     if constexpr (VEC) {
-        constexpr int W = sizeof(T) * 8 / 16;
-        uint4 u[W];
 #pragma unroll
-        for (int w = 0; w < W; ++w) u[w] = __ldg(reinterpret_cast<const uint4 *>(src) + w);
-        const T *t = reinterpret_cast<const T *>(u);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = to_f32(t[k]);
+        for (int w = 0; w < static_cast<int>(sizeof(T)) / 2; ++w) r.u[w] = __ldg(reinterpret_cast<const uint4 *>(src) + w);
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = to_f32(src[k]);
+        for (int k = 0; k < 8; ++k) reinterpret_cast<T *>(r.u)[k] = src[k];
     }
+    return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T *src, float (&x)[8]) {
+    const Raw8<T> r = load_raw8<T, VEC>(src);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = r.at(k);
 }
 
 // Two fp32 values as e4m3 codes (round to nearest even, clamped to +-448): lo in bits 0-7.
@@ -121,54 +130,65 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
 }
 
 constexpr int kQWriteThreads = 256;
+constexpr int kQHold = 8;  // rows a lane holds between finding the scale and rounding: 16 rows a block at D = 128
 
 // A warp quantises one block: (sequence, block of its span, K or V, kv head). Lanes hold eight values
-// each, 32 / (D / 8) rows at a time. A block that the span starts inside keeps its scale or a larger
-// one, and its rows below the span are rounded again by the ratio of the two.
+// each, 32 / (D / 8) rows at a time; the first kQHold of a lane's rows stay in registers, those of longer
+// blocks are read twice. A block that the span starts inside keeps its scale or a larger one, and its rows
+// below the span are rounded again by the ratio of the two. Warps of a CTA take K and V of neighbouring
+// heads, whose rows lie side by side.
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kQWriteThreads) qcache_write_kernel(QCacheArgs a, const T *k, const T *v,
                                                                       long long k_stride, long long v_stride) {
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     constexpr int LPR = D / 8, RPI = 32 / LPR;
     const int item = blockIdx.x * (kQWriteThreads / 32) + threadIdx.x / 32;
     const int b = blockIdx.y, lane = threadIdx.x % 32;
-    const int kv = item % (2 * a.nkv) / a.nkv, h = item % a.nkv;
+    const int blk = a.by_heads.div(item), kvh = item - blk * 2 * a.nkv, kv = kvh >= a.nkv, h = kvh - kv * a.nkv;
     const QSpan s = qcache_span(a, b);
     if (s.S == 0) {
         if (s.code != SDV_OK && item == 0 && lane == 0) set_status(a.status, s.code);
         return;
     }
-    const int tok0 = (s.p0 / a.scale_block + item / (2 * a.nkv)) * a.scale_block;
+    const int tok0 = (a.by_block.div(s.p0) + blk) * a.scale_block;
     if (tok0 >= s.p0 + s.S) return;
     const int lo = max(tok0, s.p0), hi = min(tok0 + a.scale_block, s.p0 + s.S);
-    const int page = qcache_page(a, b, tok0 / a.page_size);
+    const int col = lane % LPR * 8, sub = lane / LPR;
+    const long long stride = kv ? v_stride : k_stride;
+    const T *src = (kv ? v : k) + (s.r0 + (lo + sub - s.p0)) * stride + h * D + col;
+    Raw8<T> x[kQHold];
+#pragma unroll
+    for (int n = 0; n < kQHold; ++n)
+        if (lo + sub + n * RPI < hi) x[n] = load_raw8<T, VEC>(src + n * RPI * stride);
+    const int slots = a.by_page.div(tok0), slot0 = tok0 - slots * a.page_size, page = qcache_page(a, b, slots);
     if (page < 0) return;
     const size_t ph = (static_cast<size_t>(page) * 2 + kv) * a.nkv + h;
-    uint8_t *dst = a.codes + (ph * a.page_size + tok0 % a.page_size) * D;  // the block's first slot
-    float *scale = a.scales + ph * (a.page_size / a.scale_block) + tok0 % a.page_size / a.scale_block;
-    const int col = lane % LPR * 8, sub = lane / LPR;
-    const T *src = (kv ? v + (s.r0 - s.p0) * v_stride : k + (s.r0 - s.p0) * k_stride) + h * D + col;
-    const long long stride = kv ? v_stride : k_stride;
+    uint8_t *dst = a.codes + (ph * a.page_size + slot0) * D;  // the block's first slot
+    float *scale = a.scales + ph * a.blocks + a.by_block.div(slot0);
+    const float was = lo > tok0 ? *scale : 0.f;
     float amax = 0.f;
     bool bad = false;
-    for (int t = lo + sub; t < hi; t += RPI) {
-        float x[8];
-        load8<T, VEC>(src + t * stride, x);
+    auto look = [&](const Raw8<T> &r) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float m = fabsf(x[j]);
-            if (m < INFINITY) amax = fmaxf(amax, m);
-            else bad = true;
+            const float m = fabsf(r.at(j));
+            if (m < INFINITY)
+                amax = fmaxf(amax, m);
+            else
+                bad = true;
         }
-    }
+    };
+#pragma unroll
+    for (int n = 0; n < kQHold; ++n)
+        if (lo + sub + n * RPI < hi) look(x[n]);
+    for (int t = lo + sub + kQHold * RPI; t < hi; t += RPI) look(load_raw8<T, VEC>(src + (t - lo - sub) * stride));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (bad) set_status(a.status, SDV_ERR_DEVICE);
     float now = e4m3_scale(amax);
     if (lo > tok0) {
-        float old = *scale;
-        if (!(old > 0.f && old < INFINITY)) old = 0.f;  // never written: nothing below the span counts
+        const float old = was > 0.f && was < INFINITY ? was : 0.f;  // 0: never written, nothing below the span counts
         now = fmaxf(now, old);
         const float ratio = old / now;
         if (ratio != 1.f)
@@ -184,65 +204,82 @@ __global__ void __launch_bounds__(kQWriteThreads) qcache_write_kernel(QCacheArgs
                 *c = make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
             }
     }
-    const float inv = 1.f / now;  // exact: a power of two from 2^-120 to 2^126
-    for (int t = lo + sub; t < hi; t += RPI) {
-        float x[8];
-        load8<T, VEC>(src + t * stride, x);
+    const float inv = 1.f / now;  // exact: a power of two from 2^-127 to 2^126
+    auto put = [&](int t, const Raw8<T> &r) {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] == x[j] ? x[j] * inv : 0.f;
-        *reinterpret_cast<uint2 *>(dst + (t - tok0) * D + col) =
-            make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16, e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
-    }
+        for (int j = 0; j < 4; ++j) {
+            const float f = r.at(2 * j), g = r.at(2 * j + 1);
+            w[j] = e4m3x2(f == f ? f * inv : 0.f, g == g ? g * inv : 0.f);
+        }
+        *reinterpret_cast<uint2 *>(dst + (t - tok0) * D + col) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    };
+#pragma unroll
+    for (int n = 0; n < kQHold; ++n)
+        if (lo + sub + n * RPI < hi) put(lo + sub + n * RPI, x[n]);
+    for (int t = lo + sub + kQHold * RPI; t < hi; t += RPI) put(t, load_raw8<T, VEC>(src + (t - lo - sub) * stride));
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale = now;
 }
 
 constexpr int kQReadThreads = 256;
+constexpr int kQReadRows = 4;  // rows a thread reads, so that many loads are under way
 
-// Eight codes a thread: code * scale (exact in fp32 but where it leaves fp32's range), rounded once.
-// Grid (span rows in groups, sequences, K|V x heads).
+// Eight codes of a row a thread and kQReadRows rows: code * scale (exact in fp32 but where it leaves
+// fp32's range), rounded once. Grid (K|V x heads, span rows in groups, sequences): neighbouring CTAs fill
+// neighbouring parts of the same output rows.
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kQReadThreads) qcache_read_kernel(QCacheArgs a, T *k, T *v, long long k_stride,
                                                                     long long v_stride) {
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     constexpr int LPR = D / 8, RPB = kQReadThreads / LPR;
-    const int b = blockIdx.y, kv = blockIdx.z / a.nkv, h = blockIdx.z % a.nkv;
+    const int b = blockIdx.z, kv = blockIdx.x >= a.nkv, h = blockIdx.x - kv * a.nkv;
     const QSpan s = qcache_span(a, b);
     if (s.S == 0) {
-        if (s.code != SDV_OK && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) set_status(a.status, s.code);
+        if (s.code != SDV_OK && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, s.code);
         return;
     }
-    const int i = blockIdx.x * RPB + threadIdx.x / LPR, col = threadIdx.x % LPR * 8;
-    if (i >= s.S) return;
-    const int p = s.p0 + i, page = qcache_page(a, b, p / a.page_size), slot = p % a.page_size;
-    float x[8];
-    if (page >= 0) {
-        const size_t ph = (static_cast<size_t>(page) * 2 + kv) * a.nkv + h;
-        const uint2 w = *reinterpret_cast<const uint2 *>(a.codes + (ph * a.page_size + slot) * D + col);
-        const float sc = a.scales[ph * (a.page_size / a.scale_block) + slot / a.scale_block];
-        const uint32_t r[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+    const int i0 = blockIdx.y * RPB * kQReadRows + threadIdx.x / LPR, col = threadIdx.x % LPR * 8;
+    if (i0 >= s.S) return;
+    uint2 w[kQReadRows];
+    float sc[kQReadRows];
+#pragma unroll
+    for (int n = 0; n < kQReadRows; ++n) {
+        const int i = i0 + n * RPB, p = s.p0 + i;
+        w[n] = make_uint2(0, 0);
+        sc[n] = 0.f;
+        if (i < s.S) {
+            const int at = a.by_page.div(p), slot = p - at * a.page_size, page = qcache_page(a, b, at);
+            if (page >= 0) {
+                const size_t ph = (static_cast<size_t>(page) * 2 + kv) * a.nkv + h;
+                w[n] = *reinterpret_cast<const uint2 *>(a.codes + (ph * a.page_size + slot) * D + col);
+                sc[n] = a.scales[ph * a.blocks + a.by_block.div(slot)];
+            }
+        }
+    }
+    T *dst = (kv ? v : k) + s.r0 * (kv ? v_stride : k_stride) + h * D + col;
+    const long long stride = kv ? v_stride : k_stride;
+#pragma unroll
+    for (int n = 0; n < kQReadRows; ++n) {
+        const int i = i0 + n * RPB;
+        if (i >= s.S) break;
+        const uint32_t r[4] = {w[n].x & 0xffffu, w[n].x >> 16, w[n].y & 0xffffu, w[n].y >> 16};
+        alignas(16) T y[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f = e4m3x2_f32(r[j]);
-            x[2 * j] = f.x * sc;
-            x[2 * j + 1] = f.y * sc;
+            y[2 * j] = from_f32<T>(f.x * sc[n]);
+            y[2 * j + 1] = from_f32<T>(f.y * sc[n]);
         }
-    } else {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = 0.f;
-    }
-    T *dst = (kv ? v + (s.r0 + i) * v_stride : k + (s.r0 + i) * k_stride) + h * D + col;
-    alignas(16) T y[8];
+            for (int u = 0; u < static_cast<int>(sizeof(T)) / 2; ++u)
+                reinterpret_cast<uint4 *>(dst + i * stride)[u] = reinterpret_cast<const uint4 *>(y)[u];
+        } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = from_f32<T>(x[j]);
-    if constexpr (VEC) {
-#pragma unroll
-        for (int w = 0; w < static_cast<int>(sizeof(T)) / 2; ++w)
-            reinterpret_cast<uint4 *>(dst)[w] = reinterpret_cast<const uint4 *>(y)[w];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dst[j] = y[j];
+            for (int j = 0; j < 8; ++j) dst[i * stride + j] = y[j];
+        }
     }
 }
 

@@ -36,7 +36,6 @@ struct QAttnArgs {
     int nq, window;                  // window: positions a row sees, its own the last (0: all)
     int splits;                      // parts a sequence's keys are cut into at most
     int tiles;                       // row tiles of a span of max_span rows
-    int blocks;                      // scale blocks of a page
     int grp;                         // q heads a kv head
     int q_vec;                       // q rows are 16-byte aligned
     FastDiv by_tiles, by_splits, by_grp, by_nq;
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         uint32_t row = 0xffffffffu;
         if (lane < LW) {
             if (!in && t < last) set_status(c.status, SDV_ERR_CAPACITY);
-            const int slot = c.by_page.mod(t, c.page_size), nblk = a.blocks;
+            const int slot = c.by_page.mod(t, c.page_size), nblk = c.blocks;
             const size_t ph = in ? static_cast<size_t>(page) * 2 * c.nkv + h : 0;
             if (in) row = static_cast<uint32_t>(ph * c.page_size + slot);
             const float *sc = c.scales + (in ? ph * nblk + c.by_block.div(slot) : 0);

@@ -119,7 +119,9 @@ struct sdv_ctx {
     float *attn_po = nullptr;
     float2 *attn_pml = nullptr;
     int *attn_cnt = nullptr;
-    float2 *accept_part = nullptr;  // sampled acceptance: chunk statistics of the logit rows
+    float2 *accept_part = nullptr;  // sampled acceptance: chunk statistics of the logit rows, best scores, arrivals
+    unsigned long long *accept_keys = nullptr;
+    int *accept_arrived = nullptr;
     int attn_splits = 1;
     int attn_group = kAttnGroup;  // key positions per attention group (1024, or 2048 for long sequences)
     int attn_lo = 1;  // attention products with hi/lo pairs (queries and probabilities)
@@ -309,9 +311,13 @@ size_t carve(const sdv_model_cfg &m, const sdv_cache_cfg &c, sdv_ctx *ctx, uint8
     float2 *apml = reinterpret_cast<float2 *>(take(sizeof(float2) * nslots));
     int *acnt = reinterpret_cast<int *>(take(sizeof(int) * static_cast<size_t>(B) * m.n_kv_heads * kAttnCluster));
     auto *apart = reinterpret_cast<float2 *>(take(sizeof(float2) * kRowsCap * ceil_div(m.vocab, kAcceptChunk)));
+    auto *akeys = reinterpret_cast<unsigned long long *>(take(sizeof(unsigned long long) * 2 * B));
+    int *aarrived = reinterpret_cast<int *>(take(sizeof(int) * B));
 
     if (ctx) {
         ctx->accept_part = apart;
+        ctx->accept_keys = akeys;
+        ctx->accept_arrived = aarrived;
         ctx->st = s;
         ctx->x = x;
         ctx->xb = xb;
@@ -1015,12 +1021,12 @@ int sdv_accept_greedy(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_ro
 int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_row_off, const float *d_logits,
                        int64_t logits_stride, const float *d_temperature, const float *d_uniform,
                        const float *d_noise, int64_t noise_stride, const float *d_draft_probs, int64_t probs_stride,
-                       int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
+                       int rows, int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
                        int32_t *d_new_len, void *stream) {
     if (!ctx || !d_tokens || !d_row_off || !d_logits || !d_temperature || !d_uniform || !d_noise || !d_n_accept ||
         !d_committed || !d_n_commit || !d_new_len)
         return SDV_ERR_ARG;
-    if (B <= 0 || B > ctx->c.max_batch || max_commit <= 0 || logits_stride < ctx->m.vocab ||
+    if (B <= 0 || B > ctx->c.max_batch || rows <= 0 || max_commit <= 0 || logits_stride < ctx->m.vocab ||
         noise_stride < ctx->m.vocab || (d_draft_probs && probs_stride < ctx->m.vocab))
         return SDV_ERR_ARG;
     AcceptSampledArgs p{};
@@ -1040,10 +1046,12 @@ int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_r
     p.max_commit = max_commit;
     p.vocab = ctx->m.vocab;
     p.n_chunks = ceil_div(ctx->m.vocab, kAcceptChunk);
-    p.rows_cap = kRowsCap;
+    p.rows_cap = std::min(rows, kRowsCap);
     p.adaptive = ctx->gen_adaptive;
     p.k_max = ctx->gen_kmax;
     p.part = ctx->accept_part;
+    p.keys = ctx->accept_keys;
+    p.arrived = ctx->accept_arrived;
     p.n_accept = d_n_accept;
     p.committed = d_committed;
     p.n_commit = d_n_commit;
@@ -1051,7 +1059,7 @@ int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_r
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch(ctx, accept_stats_kernel, dim3(p.n_chunks, B * p.max_span), dim3(kAcceptThreads), 0, st, p);
     if (e == cudaSuccess)
-        e = launch_cluster(ctx, accept_draw_kernel, dim3(B * kDrawCluster), dim3(kDrawThreads), 0, st, kDrawCluster, p);
+        e = launch(ctx, accept_draw_kernel, dim3(p.n_chunks, B), dim3(kAcceptThreads), 0, st, p);
     return rc(e);
 }
 

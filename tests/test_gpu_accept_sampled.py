@@ -195,6 +195,11 @@ def test_refused_spans():
     for b in (0, 2):
         for a, r in zip(got, ref):
             np.testing.assert_array_equal(a[b], r[b])
+    short = dict(x, logits=x["logits"][:10])                          # fewer rows than the offsets name: the last span
+    got = _run(v, short)                                              # is refused
+    assert v.get_status() == -1 and got[0].tolist()[2] == -1
+    for a, r in zip(got, _ref(x, lengths)):
+        np.testing.assert_array_equal(a[:2], r[:2])
     z = torch.zeros
     f, i = dict(device="cuda"), dict(device="cuda", dtype=torch.int32)
     good = dict(tokens=z(11, **i), row_off=z(4, **i), logits=z(11, 700, **f), temperature=z(3, **f), uniforms=z(11, **f),

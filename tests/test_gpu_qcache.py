@@ -363,6 +363,9 @@ def test_device_errors_are_caught_and_bounded():
     assert s.cache.get_status() == -1
     bad = s.d_table.clone()
     bad[1, 1], bad[1, 3] = s.n_pages, -5
+    # row tensors that hold fewer rows than the offsets name: the second span is refused, nothing past them is touched
+    s.cache.attention(1, qt[:5], s.d_table, s.d_off, s.d_base, 2, 4, out[:5])
+    assert s.cache.get_status() == -1
     s.cache.codes.copy_(codes)                                        # what the first of those spans wrote, taken back
     s.cache.scales.copy_(scales)
     s.cache.read(1, bad, s.d_off, s.d_base, 2, 4, kt, kt.clone())

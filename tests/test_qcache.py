@@ -47,12 +47,12 @@ def test_null_arguments(sdv):
     assert L.sdv_qcache_bytes(ctypes.byref(_cfg(sdv)), None, None, None) == err
     out = ctypes.c_void_p()
     assert L.sdv_qcache_create(ctypes.byref(_cfg(sdv)), None, None, None, None, ctypes.byref(out)) == err
-    assert L.sdv_qcache_write(None, 0, None, 0, None, 0, 0, None, None, None, 1, 1, None) == err
-    assert L.sdv_qcache_read(None, 0, None, None, None, 1, 1, None, 0, None, 0, 0, None) == err
-    assert L.sdv_qcache_attention(None, 0, None, 0, 0, None, None, None, 1, 1, 0, None, 0, None) == err
+    assert L.sdv_qcache_write(None, 0, None, 0, None, 0, 0, 1, None, None, None, 1, 1, None) == err
+    assert L.sdv_qcache_read(None, 0, None, None, None, 1, 1, None, 0, None, 0, 0, 1, None) == err
+    assert L.sdv_qcache_attention(None, 0, None, 0, 0, 1, None, None, None, 1, 1, 0, None, 0, None) == err
     assert L.sdv_qcache_get_status(None, None) == err
     assert L.sdv_qcache_destroy(None) == 0
-    assert L.sdv_accept_sampled(None, None, None, None, 0, None, None, None, 0, None, 0, 1, 1, None, None, None, None,
+    assert L.sdv_accept_sampled(None, None, None, None, 0, None, None, None, 0, None, 0, 1, 1, 1, None, None, None, None,
                                 None) == err
 
 
