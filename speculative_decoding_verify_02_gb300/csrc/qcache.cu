@@ -175,12 +175,16 @@ cudaError_t set_attn_all() {
 
 template <typename T, int D>
 int write_rows(const QCacheArgs &a, const void *k, int64_t ks, const void *v, int64_t vs, bool vec, void *stream) {
-    const int blocks = (a.max_span + a.scale_block - 2) / a.scale_block + 1;  // a span touches at most
-    const dim3 grid(cdiv(static_cast<long long>(blocks) * 2 * a.nkv, kQWriteThreads / 32), a.B);
+    constexpr int kWindow = kQHold * 32 / (D / 8);
+    const bool small = a.scale_block < 16 && (a.scale_block & (a.scale_block - 1)) == 0;
+    const int unit = small ? kWindow : a.scale_block;  // tokens of a warp
+    const int units = (a.max_span + unit - 2) / unit + 1;  // a span touches at most
+    const dim3 grid(cdiv(static_cast<long long>(units) * 2 * a.nkv, kQWriteThreads / 32), a.B);
     const T *kp = static_cast<const T *>(k), *vp = static_cast<const T *>(v);
     const long long k_stride = ks, v_stride = vs;
-    return vec ? launch(qcache_write_kernel<T, D, true>, grid, kQWriteThreads, 0, stream, a, kp, vp, k_stride, v_stride)
-               : launch(qcache_write_kernel<T, D, false>, grid, kQWriteThreads, 0, stream, a, kp, vp, k_stride, v_stride);
+    auto *kern = small ? (vec ? qcache_write_small_kernel<T, D, true> : qcache_write_small_kernel<T, D, false>)
+                       : (vec ? qcache_write_kernel<T, D, true> : qcache_write_kernel<T, D, false>);
+    return launch(kern, grid, kQWriteThreads, 0, stream, a, kp, vp, k_stride, v_stride);
 }
 
 template <typename T, int D>

@@ -93,6 +93,25 @@ template <typename T>
 struct Raw8 {
     uint4 u[sizeof(T) / 2];
     __device__ __forceinline__ float at(int k) const { return to_f32(reinterpret_cast<const T *>(u)[k]); }
+    // The larger of `m` and the values' magnitudes; not below infinity where one of them is not finite. Magnitudes of a
+    // type order like their bits, and so above infinity do NaNs.
+    __device__ __forceinline__ uint32_t top(uint32_t m) const {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(u)) / 4; ++k) {
+            if constexpr (sizeof(T) == 4)
+                m = max(m, w[k] & 0x7fffffffu);
+            else
+                m = __vmaxu2(m, w[k] & 0x7fff7fffu);
+        }
+        return m;
+    }
+    static __device__ __forceinline__ float top_value(uint32_t m) {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(m);
+        const unsigned short h = static_cast<unsigned short>(max(m & 0xffffu, m >> 16));
+        if constexpr (sizeof(T) == 2) return to_f32(*reinterpret_cast<const T *>(&h));
+        return 0.f;
+    }
 };
 template <typename T, bool VEC>
 __device__ __forceinline__ Raw8<T> load_raw8(const T *src) {
@@ -138,7 +157,7 @@ constexpr int kQHold = 8;  // rows a lane holds between finding the scale and ro
 // below the span are rounded again by the ratio of the two. Warps of a CTA take K and V of neighbouring
 // heads, whose rows lie side by side.
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(kQWriteThreads) qcache_write_kernel(QCacheArgs a, const T *k, const T *v,
+__global__ void __launch_bounds__(kQWriteThreads, VEC && sizeof(T) == 2 ? 4 : 2) qcache_write_kernel(QCacheArgs a, const T *k, const T *v,
                                                                       long long k_stride, long long v_stride) {
     pdl_wait();
     pdl_trigger();
@@ -167,25 +186,23 @@ __global__ void __launch_bounds__(kQWriteThreads) qcache_write_kernel(QCacheArgs
     uint8_t *dst = a.codes + (ph * a.page_size + slot0) * D;  // the block's first slot
     float *scale = a.scales + ph * a.blocks + a.by_block.div(slot0);
     const float was = lo > tok0 ? *scale : 0.f;
-    float amax = 0.f;
-    bool bad = false;
-    auto look = [&](const Raw8<T> &r) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float m = fabsf(r.at(j));
-            if (m < INFINITY)
-                amax = fmaxf(amax, m);
-            else
-                bad = true;
-        }
-    };
+    uint32_t m = 0;
 #pragma unroll
     for (int n = 0; n < kQHold; ++n)
-        if (lo + sub + n * RPI < hi) look(x[n]);
-    for (int t = lo + sub + kQHold * RPI; t < hi; t += RPI) look(load_raw8<T, VEC>(src + (t - lo - sub) * stride));
+        if (lo + sub + n * RPI < hi) m = x[n].top(m);
+    for (int t = lo + sub + kQHold * RPI; t < hi; t += RPI) m = load_raw8<T, VEC>(src + (t - lo - sub) * stride).top(m);
+    float amax = Raw8<T>::top_value(m);
+    if (__any_sync(0xffffffffu, !(amax < INFINITY))) {  // values that are not finite do not count
+        amax = 0.f;
+        for (int t = lo + sub; t < hi; t += RPI) {
+            const Raw8<T> r = load_raw8<T, VEC>(src + (t - lo - sub) * stride);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(r.at(j)) < INFINITY ? fabsf(r.at(j)) : 0.f);
+        }
+        if (lane == 0) set_status(a.status, SDV_ERR_DEVICE);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (bad) set_status(a.status, SDV_ERR_DEVICE);
     float now = e4m3_scale(amax);
     if (lo > tok0) {
         const float old = was > 0.f && was < INFINITY ? was : 0.f;  // 0: never written, nothing below the span counts
@@ -220,6 +237,114 @@ __global__ void __launch_bounds__(kQWriteThreads) qcache_write_kernel(QCacheArgs
     for (int t = lo + sub + kQHold * RPI; t < hi; t += RPI) put(t, load_raw8<T, VEC>(src + (t - lo - sub) * stride));
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale = now;
+}
+
+// Blocks of 1, 2, 4 or 8 tokens: a warp takes a window of kQHold * (32 / (D / 8)) tokens (16 at D = 128),
+// whole blocks of it, so that a lane still has kQHold rows under way (one block a warp wrote 65,536 rows of one
+// token a block in 8 times the time). Each row finds its page; the rows of a block agree on its maximum by
+// shuffles and, past a warp's width of rows, across the rows a lane holds.
+template <typename T, int D, bool VEC>
+__global__ void __launch_bounds__(kQWriteThreads, VEC && sizeof(T) == 2 ? 3 : 2) qcache_write_small_kernel(
+    QCacheArgs a, const T *k, const T *v, long long k_stride, long long v_stride) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int LPR = D / 8, RPI = 32 / LPR, WIN = kQHold * RPI;
+    const int item = blockIdx.x * (kQWriteThreads / 32) + threadIdx.x / 32;
+    const int b = blockIdx.y, lane = threadIdx.x % 32;
+    const int win = a.by_heads.div(item), kvh = item - win * 2 * a.nkv, kv = kvh >= a.nkv, h = kvh - kv * a.nkv;
+    const QSpan s = qcache_span(a, b);
+    if (s.S == 0) {
+        if (s.code != SDV_OK && item == 0 && lane == 0) set_status(a.status, s.code);
+        return;
+    }
+    const int t0 = (s.p0 / WIN + win) * WIN, sb = a.scale_block;
+    if (t0 >= s.p0 + s.S) return;
+    const int lo = max(t0, s.p0), hi = min(t0 + WIN, s.p0 + s.S), live0 = lo & ~(sb - 1);  // sb is a power of two
+    const int col = lane % LPR * 8, sub = lane / LPR;
+    const long long stride = kv ? v_stride : k_stride;
+    const T *src = (kv ? v : k) + h * D + col;
+    Raw8<T> x[kQHold];
+    uint8_t *dst[kQHold];
+    float *scale[kQHold], was[kQHold];
+#pragma unroll
+    for (int n = 0; n < kQHold; ++n) {
+        const int t = t0 + sub + n * RPI;
+        if (t >= lo && t < hi) x[n] = load_raw8<T, VEC>(src + (s.r0 + (t - s.p0)) * stride);
+    }
+#pragma unroll
+    for (int n = 0; n < kQHold; ++n) {
+        const int t = t0 + sub + n * RPI;
+        dst[n] = nullptr;
+        was[n] = 0.f;
+        scale[n] = nullptr;
+        if (t >= live0 && t < hi) {
+            const int at = a.by_page.div(t), slot = t - at * a.page_size, page = qcache_page(a, b, at);
+            if (page >= 0) {
+                const size_t ph = (static_cast<size_t>(page) * 2 + kv) * a.nkv + h;
+                dst[n] = a.codes + (ph * a.page_size + slot) * D + col;
+                scale[n] = a.scales + ph * a.blocks + a.by_block.div(slot);
+                if (live0 < lo && (t & ~(sb - 1)) == live0) was[n] = *scale[n];
+            }
+        }
+    }
+    float peak[kQHold];
+#pragma unroll
+    for (int n = 0; n < kQHold; ++n) {
+        const int t = t0 + sub + n * RPI;
+        const bool mine = t >= lo && t < hi;
+        float m = mine ? Raw8<T>::top_value(x[n].top(0)) : 0.f;
+        if (mine && !(m < INFINITY)) {  // values that are not finite do not count
+            m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[n].at(j)) < INFINITY ? fabsf(x[n].at(j)) : 0.f);
+            set_status(a.status, SDV_ERR_DEVICE);
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+        for (int r = 1; r < RPI; r <<= 1)
+            if (r < sb) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, r * LPR));
+        peak[n] = m;
+    }
+#pragma unroll
+    for (int g = 2; g <= kQHold / 2; g <<= 1)  // blocks that go on in the next rows of a lane
+        if (sb >= g * RPI) {
+#pragma unroll
+            for (int n = 0; n < kQHold; n += g) {
+                const float m = fmaxf(peak[n], peak[n + g / 2]);
+#pragma unroll
+                for (int j = 0; j < g; ++j) peak[n + j] = m;
+            }
+        }
+    __syncwarp();  // the old scales are read
+#pragma unroll
+    for (int n = 0; n < kQHold; ++n) {
+        const int t = t0 + sub + n * RPI;
+        if (!dst[n]) continue;
+        const float old = was[n] > 0.f && was[n] < INFINITY ? was[n] : 0.f;
+        const float now = fmaxf(e4m3_scale(peak[n]), old);
+        uint32_t w[4];
+        if (t >= lo) {
+            const float inv = 1.f / now;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float f = x[n].at(2 * j), g = x[n].at(2 * j + 1);
+                w[j] = e4m3x2(f == f ? f * inv : 0.f, g == g ? g * inv : 0.f);
+            }
+        } else {  // a row below the span in the block that it starts inside
+            const float ratio = old / now;
+            if (ratio == 1.f) continue;
+            const uint2 c = *reinterpret_cast<const uint2 *>(dst[n]);
+            const uint32_t r[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = e4m3x2_f32(r[j]);
+                w[j] = e4m3x2(f.x * ratio, f.y * ratio);
+            }
+        }
+        *reinterpret_cast<uint2 *>(dst[n]) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        if (t >= lo && col == 0 && (t == lo || (t & (sb - 1)) == 0)) *scale[n] = now;
+    }
 }
 
 constexpr int kQReadThreads = 256;

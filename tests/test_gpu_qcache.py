@@ -76,6 +76,12 @@ WRITES = [
     (2, 64, 1, 1, [3, 0], [9, 4]),
     (5, 128, 128, 128, [60, 127], [130, 1]),
     (1, 128, 7, 7, [6, 2], [20, 3]),
+    (2, 64, 16, 2, [31, 7, 100], [70, 1, 33]),
+    (2, 128, 4, 2, [13, 6], [37, 2]),
+    (1, 64, 8, 8, [5, 35], [45, 60]),
+    (2, 128, 24, 8, [13, 22], [30, 5]),
+    (1, 128, 12, 4, [6, 2], [40, 3]),
+    (1, 64, 12, 12, [6, 30], [40, 7]),
 ]
 
 
@@ -87,9 +93,11 @@ def test_write_and_read_back(nkv, D, ps, sb, lengths, spans, dtype):
     import torch
     s = Setup(nkv, nkv, D, ps, sb, lengths, spans, seed=len(spans) + sb, room=max(spans))
     s.fill()
+    finite = True
     for again in range(2):
         kt, k = s.values((s.rows, nkv, D), dtype)
         vt, v = s.values((s.rows, nkv, D), dtype, 3.0)
+        finite = finite and bool(np.isfinite(v).all())                # fp16 may overflow at this spread
         s.cache.write(s.layer, kt, vt, *s.args())
         for b in range(s.B):
             r = slice(s.off[b], s.off[b + 1])
@@ -106,7 +114,7 @@ def test_write_and_read_back(nkv, D, ps, sb, lengths, spans, dtype):
         # the next write begins one row into this one: lower rows live, later rows overwritten
         s.lengths = [l + 1 if n > 1 else l for l, n in zip(s.lengths, spans)]
         s.d_base = _i32(s.lengths)
-    assert s.cache.get_status() == 0
+    assert s.cache.get_status() == (0 if finite else -4)
     assert int(s.cache.codes[0].sum()) == 0 and float(s.cache.scales[0].sum()) == 0  # the other layer
 
 
