@@ -81,23 +81,29 @@ __device__ __forceinline__ int chunk_index(int v0, int j) {
     return v0 + ((j / 4) * kAcceptThreads + threadIdx.x) * 4 + (j & 3);
 }
 
-// Statistics of one chunk of one row: grid (chunks, B * max_span).
+// Statistics of one chunk of one row: grid (chunks, rows). The row's logits are asked for before its
+// sequence is known: 78 MB of them keep 4 waves of CTAs busy, and every latency in a CTA's chain counts in each.
 __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSampledArgs p) {
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.y / p.max_span, i = blockIdx.y % p.max_span;
-    const int2 sp = accept_span(p, b);
-    if (i >= sp.y) return;
-    const int r = sp.x + i;
+    const int r = blockIdx.y, v0 = blockIdx.x * kAcceptChunk, tid = threadIdx.x;
+    float x[kAcceptPer];
+    load_chunk(p.logits + r * p.logits_stride, v0, p.vocab, -INFINITY, x);
+    __shared__ int seq_s;
+    if (tid == 0) seq_s = -1;
+    __syncthreads();
+    if (tid < p.B) {  // B <= 256 threads
+        const int2 sp = accept_span(p, tid);
+        if (r >= sp.x && r < sp.x + sp.y) seq_s = tid;
+    }
+    __syncthreads();
+    const int b = seq_s;
+    if (b < 0) return;  // a row of no span
     const float T = p.temperature[b];
-    const float *row = p.logits + r * p.logits_stride;
-    const int v0 = blockIdx.x * kAcceptChunk, tid = threadIdx.x;
-    if (blockIdx.x == 0 && i == 0 && tid < 2) {  // for the draw that follows
+    if (blockIdx.x == 0 && r == p.row_off[b] && tid < 2) {  // for the draw that follows
         p.keys[2 * b + tid] = 0;
         if (tid == 0) p.arrived[b] = 0;
     }
-    float x[kAcceptPer];
-    load_chunk(row, v0, p.vocab, -INFINITY, x);
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kAcceptPer; ++j) m = fmaxf(m, x[j]);  // fmaxf passes over NaN
@@ -141,7 +147,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSamp
 // The accepted prefix of a sequence (every CTA finds it from the chunk statistics), the race over one
 // chunk of the vocabulary at its last row, and, in the CTA that comes last, the outputs and loop state as
 // accept_kernel writes them. Grid (chunks, B). The best key is the same in any order of arrival.
-__global__ void __launch_bounds__(kAcceptThreads) accept_draw_kernel(AcceptSampledArgs p) {
+__global__ void __launch_bounds__(kAcceptThreads, 4) accept_draw_kernel(AcceptSampledArgs p) {
     pdl_wait();
     pdl_trigger();
     constexpr int NW = kAcceptThreads / 32;
@@ -164,6 +170,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_draw_kernel(AcceptSampl
     const bool greedy = !(T > 0.f);
     if (greedy && blockIdx.x > 0) return;  // the statistics hold the answer
     const float c = 1.4426950408889634f / T;
+    // what the last CTA will need, asked for early
+    const int length = p.s.seq_len[b], done = p.s.generated[b], kcur = p.s.kcur[b];
     float e[kAcceptPer];
     if (!greedy) load_chunk(p.noise + b * p.noise_stride, v0, p.vocab, 1.f, e);
     for (int i = warp; i < S; i += NW) {
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_draw_kernel(AcceptSampl
         for (int j = 0; j < kAcceptPer; ++j) {
             const int v = chunk_index(v0, j);
             const float pv = logit_weight(x[j], xm, c) * inv_l, w = v == drop ? 0.f : pv - q[j];
-            const float t0 = w > 0.f ? w / e[j] : -1.f, t1 = pv > 0.f ? pv / e[j] : -1.f;
+            const float inv = __frcp_rn(e[j]), t0 = w > 0.f ? w * inv : -1.f, t1 = pv > 0.f ? pv * inv : -1.f;
             if (t0 > s0) s0 = t0, i0 = v;
             if (t1 > s1) s1 = t1, i1 = v;
         }
@@ -286,12 +294,12 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_draw_kernel(AcceptSampl
     p.committed[static_cast<size_t>(b) * p.max_commit + m] = token;
     p.n_accept[b] = m;
     p.n_commit[b] = m + 1;
-    p.new_len[b] = p.s.seq_len[b] - S + m + 1;
+    p.new_len[b] = length - S + m + 1;
     // loop state: next current token, tokens generated, adaptive draft length
     const int k = S - 1;
     p.s.cur_tok[b] = token;
-    p.s.generated[b] += m + 1;
-    if (p.adaptive && k > 0) p.s.kcur[b] = (m == k) ? min(p.s.kcur[b] + 2, p.k_max) : max(p.s.kcur[b] - 1, 1);
+    p.s.generated[b] = done + m + 1;
+    if (p.adaptive && k > 0) p.s.kcur[b] = (m == k) ? min(kcur + 2, p.k_max) : max(kcur - 1, 1);
 }
 
 }  // namespace sdv

@@ -1046,7 +1046,7 @@ int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_r
     p.max_commit = max_commit;
     p.vocab = ctx->m.vocab;
     p.n_chunks = ceil_div(ctx->m.vocab, kAcceptChunk);
-    p.rows_cap = std::min(rows, kRowsCap);
+    p.rows_cap = std::min({rows, kRowsCap, B * std::min(max_commit, ctx->c.max_span)});  // packed spans end there
     p.adaptive = ctx->gen_adaptive;
     p.k_max = ctx->gen_kmax;
     p.part = ctx->accept_part;
@@ -1057,7 +1057,7 @@ int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_r
     p.n_commit = d_n_commit;
     p.new_len = d_new_len;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(ctx, accept_stats_kernel, dim3(p.n_chunks, B * p.max_span), dim3(kAcceptThreads), 0, st, p);
+    cudaError_t e = launch(ctx, accept_stats_kernel, dim3(p.n_chunks, p.rows_cap), dim3(kAcceptThreads), 0, st, p);
     if (e == cudaSuccess)
         e = launch(ctx, accept_draw_kernel, dim3(p.n_chunks, B), dim3(kAcceptThreads), 0, st, p);
     return rc(e);
