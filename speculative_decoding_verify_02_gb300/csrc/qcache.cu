@@ -4,6 +4,7 @@
 #include <cmath>
 #include <new>
 #include <type_traits>
+#include <vector>
 
 #include "qcache_attention.cuh"
 
@@ -17,6 +18,8 @@ struct sdv_qcache {
     uint8_t *ws = nullptr;
     size_t layer_codes = 0, layer_scales = 0;
     FastDiv by_page{}, by_block{}, by_heads{};
+    int box_rows = 0;                 // pool rows of a TMA box (0: the page size fits none)
+    std::vector<CUtensorMap> pools;   // one map a layer over its pool rows
 };
 
 namespace {
@@ -52,6 +55,34 @@ size_t layer_codes(const sdv_qcache_cfg &c) {
 }
 size_t layer_scales(const sdv_qcache_cfg &c) {
     return static_cast<size_t>(c.n_pages) * 2 * c.n_kv_heads * (c.page_size / c.scale_block);
+}
+
+// Rows of a TMA box: the largest power of two up to a chunk that divides the page size, from eight (a swizzle atom).
+int box_rows_of(const sdv_qcache_cfg &c) {
+    if (static_cast<long long>(c.n_pages) * 2 * c.n_kv_heads * c.page_size >= (1ll << 31)) return 0;  // box rows are int
+    int r = 1;
+    while (r < kQKeys && c.page_size % (2 * r) == 0) r *= 2;
+    return r >= 8 ? r : 0;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// A layer's pool as [row][D] bytes; a box is box_rows rows, with the swizzle of their width.
+bool encode_pool_rows(CUtensorMap *tm, void *codes, const sdv_qcache_cfg &c, int box_rows) {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return false;
+    const cuuint64_t D = c.head_dim;
+    cuuint64_t dims[2] = {D, static_cast<cuuint64_t>(c.n_pages) * 2 * c.n_kv_heads * c.page_size}, strides[1] = {D};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+    return reinterpret_cast<EncodeTiledFn>(fn)(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, es,
+                                               CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename... KArgs, typename... Args>
@@ -134,21 +165,21 @@ size_t attn_partials(const sdv_qcache_cfg &c, int sm_count) {
 }
 
 template <typename T, int D, int ROWS>
-int launch_attn_rows(const QAttnArgs &a, const AttnPlan &p, void *stream) {
+int launch_attn_rows(const CUtensorMap &pool, const QAttnArgs &a, const AttnPlan &p, void *stream) {
     typedef QTile<T, D, ROWS> Q;
     const dim3 grid(static_cast<unsigned>(p.tiles) * a.c.nkv, p.splits, a.c.B);
-    int r = launch(qcache_attn_kernel<T, D, ROWS>, grid, Q::THREADS, Q::SMEM, stream, a);
+    int r = launch(qcache_attn_kernel<T, D, ROWS>, grid, Q::THREADS, Q::SMEM, stream, pool, a);
     if (r == SDV_OK && p.splits > 1)
         r = launch(qcache_merge_kernel<T, D>, dim3(static_cast<unsigned>(a.c.max_span) * a.nq, a.c.B), kQMergeThreads, 0,
                    stream, a);
     return r;
 }
 template <typename T, int D>
-int launch_attn(const QAttnArgs &a, const AttnPlan &p, void *stream) {
-    if (p.rows == 16) return launch_attn_rows<T, D, 16>(a, p, stream);
+int launch_attn(const CUtensorMap &pool, const QAttnArgs &a, const AttnPlan &p, void *stream) {
+    if (p.rows == 16) return launch_attn_rows<T, D, 16>(pool, a, p, stream);
     if constexpr (!std::is_same<T, __half>::value)
-        if (p.rows == 64) return launch_attn_rows<T, D, 64>(a, p, stream);
-    return launch_attn_rows<T, D, 32>(a, p, stream);
+        if (p.rows == 64) return launch_attn_rows<T, D, 64>(pool, a, p, stream);
+    return launch_attn_rows<T, D, 32>(pool, a, p, stream);
 }
 
 // Every kernel asks for the largest shared-memory carveout: an SM that changes it between an attention and its merge
@@ -249,6 +280,19 @@ int sdv_qcache_create(const sdv_qcache_cfg *cfg, void *d_codes, void *d_scales, 
     q->by_page = FastDiv::of(cfg->page_size);
     q->by_block = FastDiv::of(cfg->scale_block);
     q->by_heads = FastDiv::of(2 * cfg->n_kv_heads);
+    q->box_rows = box_rows_of(*cfg);
+    bool maps = true;
+    try {
+        q->pools.resize(cfg->n_layers);
+        for (int l = 0; l < cfg->n_layers && q->box_rows && maps; ++l)
+            maps = encode_pool_rows(&q->pools[l], q->codes + q->layer_codes * l, *cfg, q->box_rows);
+    } catch (const std::bad_alloc &) {
+        maps = false;
+    }
+    if (!maps) {
+        delete q;
+        return SDV_ERR_CUDA;
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemsetAsync(q->codes, 0, q->layer_codes * cfg->n_layers, st);
     if (e == cudaSuccess) e = cudaMemsetAsync(q->scales, 0, q->layer_scales * cfg->n_layers * sizeof(float), st);
@@ -338,8 +382,12 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     a.by_nq = FastDiv::of(a.nq);
     a.part_ml = reinterpret_cast<float2 *>(cache->ws + 256);
     a.part_o = reinterpret_cast<float *>(cache->ws + 512 + slots * sizeof(float2) / 256 * 256);
-    if (dtype == SDV_BF16) return D == 128 ? launch_attn<bf16, 128>(a, p, stream) : launch_attn<bf16, 64>(a, p, stream);
-    return D == 128 ? launch_attn<__half, 128>(a, p, stream) : launch_attn<__half, 64>(a, p, stream);
+    a.box_rows = cache->box_rows;
+    a.pool_rows = cache->box_rows ? cache->c.n_pages * 2 * a.c.nkv * a.c.page_size : 0;
+    const CUtensorMap &pool = cache->pools[layer];
+    if (dtype == SDV_BF16)
+        return D == 128 ? launch_attn<bf16, 128>(pool, a, p, stream) : launch_attn<bf16, 64>(pool, a, p, stream);
+    return D == 128 ? launch_attn<__half, 128>(pool, a, p, stream) : launch_attn<__half, 64>(pool, a, p, stream);
 }
 
 int sdv_qcache_get_status(sdv_qcache *cache, int32_t *h_status) {

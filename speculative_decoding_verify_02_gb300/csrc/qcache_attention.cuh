@@ -41,6 +41,8 @@ struct QAttnArgs {
     FastDiv by_tiles, by_splits, by_grp, by_nq;
     float scale_log2;                // log2(e) / sqrt(D)
     float *part_o;                   // [sequence][span row][q head][splits][D]
+    int box_rows;                    // pool rows of a TMA box; 0: pages that no box fits, copied in 16-byte pieces
+    int pool_rows;                   // rows of the layer's pool: a box there reads zeros
     float2 *part_ml;                 // [sequence][span row][q head][splits]: (M, l)
 };
 
@@ -62,9 +64,10 @@ struct QTile {
     static constexpr int Q_BYTES = (NQ * D + 1023) / 1024 * 1024, P_BYTES = kQKeys * W * P_LINES;
     static constexpr int SMEM = 1024 + kQStages * 2 * TILE + Q_BYTES + P_BYTES;
     static constexpr int NS = FOLD ? ROWS : NQ;                                   // columns of S^T
-    static constexpr int O_COL = (NS + 31) / 32 * 32;                             // TMEM column of O^T
+    static constexpr int NSB = 2 * NS + NP <= 256 ? 2 : 1;                        // S^T of the next chunk beside this one's
+    static constexpr int O_COL = (NSB * NS + 31) / 32 * 32;                       // TMEM column of O^T
     static constexpr int COLS = O_COL + NP <= 128 ? 128 : 256;
-    static constexpr int THREADS = WG * 128 + 32;  // softmax warps, which also load, and the MMA warp
+    static constexpr int THREADS = WG * 128 + 64;  // softmax warps, the load warp, the MMA warp
     static_assert(ROWS == 16 || ROWS == 32 || (ROWS == 64 && PQ == 2), "tile rows");
     static_assert(O_COL + NP <= COLS, "TMEM columns");
     static_assert(NQ % 16 == 0 && NP % 16 == 0, "MMA widths");
@@ -109,8 +112,27 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool va
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// A box of pool rows into shared memory, completion counted on `bar`.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *tm, uint64_t *bar, int row) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(0), "r"(row)
+        : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Whether the phase of the given parity is over, without waiting.
+__device__ __forceinline__ bool mbar_done(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
@@ -213,7 +235,8 @@ struct QRow {
 };
 
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_kernel(QAttnArgs a) {
+__global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_kernel(
+    const __grid_constant__ CUtensorMap pool, const __grid_constant__ QAttnArgs a) {
     typedef QTile<T, D, ROWS> Q;
     constexpr int CW = Q::CW;
     const QCacheArgs &c = a.c;
@@ -223,21 +246,23 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     extern __shared__ uint8_t smem_raw[];
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t kv_s = smem, q_s = smem + kQStages * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
-    __shared__ uint64_t k_full[kQStages], v_full[kQStages], s_full, p_full, o_full;
+    __shared__ uint64_t k_full[kQStages], k_empty[kQStages], v_full[kQStages], v_empty[kQStages], s_full[2], p_full, o_full;
     __shared__ uint32_t tmem_s;
     __shared__ __align__(16) float m_neg[ROWS], m_step[ROWS];  // -M of each row, and 2^(M before - M) where M last moved
     __shared__ uint32_t m_key[ROWS];
     __shared__ int pos_s[ROWS];
     __shared__ float l_s[4][ROWS], amax_s[Q::WG * 4];
     __shared__ float kv_scale[4][2][kQKeys];  // four chunks deep: softmax may still read the one two back
-    const bool is_mma = warp == Q::WG * 4;
+    const bool is_load = warp == Q::WG * 4, is_mma = warp == Q::WG * 4 + 1;
     // what needs no data goes before the wait for the kernel ahead
     if (tid == 0) {
         for (int i = 0; i < kQStages; ++i) {
-            mbar_init(&k_full[i], Q::WG * 128);
-            mbar_init(&v_full[i], Q::WG * 128);
+            mbar_init(&k_full[i], 33);
+            mbar_init(&v_full[i], 33);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 2);
         }
-        mbar_init(&s_full, 2);
         mbar_init(&p_full, Q::WG * 128);
         mbar_init(&o_full, 1);
         fence_mbar_init();
@@ -276,57 +301,87 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     if (a.window > 0) first = max(first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
     const int n_chunks = max(0, (last - first + kQKeys - 1) / kQKeys);
 
-    // ---- loads: a softmax warp brings LW keys of each chunk in 16-byte pieces, K with both scales, then V
-    constexpr int LW = kQKeys / (Q::WG * 4), PPR = D / 16, RPI = 32 / PPR;  // keys a warp, pieces a row, rows a copy
-    const int my_key = warp * LW + lane;                                     // lanes below LW: the key looked up
+    bool ok = true;  // false once a wait gave up: the rest runs without waiting, and the status word says so
+    // ---- the load warp: a chunk's K rows with both scales, then its V rows. Pages of a multiple of eight tokens come in
+    // TMA boxes, a lane a box (a box past the pool is zeros); others in 16-byte pieces.
     const int *table = c.page_table + static_cast<size_t>(b) * c.pages_per_seq;
-    auto look = [&](int ch) {  // page of this lane's key, or -1
-        const int t = first + ch * kQKeys + my_key;
-        return lane < LW && t < last ? table[c.by_page.div(t)] : -1;
-    };
-    auto load_rows = [&](uint32_t dst, uint32_t rows, size_t off) {
-        const uint8_t *codes = c.codes + off + lane % PPR * 16;
+    uint32_t rows[4], sc_at[4];  // pool rows and scales of this lane's four keys of a chunk
+    int box = 0;                 // pool row of its box
+    auto look = [&](int ch) {
+        // the five page-table entries first, so that their latencies pass together; keys past the last read its entry
+        const int t0 = first + ch * kQKeys, tb = t0 + lane % 16 * a.box_rows;
+        const bool has_box = lane % 16 * a.box_rows < kQKeys && tb < last;
+        int at[5], page[5];
 #pragma unroll
-        for (int j = 0; j < LW / RPI; ++j) {
-            const int r = j * RPI + lane / PPR;
-            const uint32_t row = __shfl_sync(0xffffffffu, rows, r);
-            const bool in = row != 0xffffffffu;
-            cp_async16(dst + line_offset(warp * LW + r, lane % PPR * 16, D), codes + (in ? static_cast<size_t>(row) * D : 0),
-                       in);
+        for (int j = 0; j < 5; ++j) {
+            at[j] = c.by_page.div(min(j < 4 ? t0 + j * 32 + lane : tb, last - 1));
+            page[j] = table[at[j]];
+        }
+        box = a.pool_rows;
+        if (has_box && page[4] >= 0 && page[4] < c.n_pages) box = (page[4] * 2 * c.nkv + h) * c.page_size + tb - at[4] * c.page_size;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = t0 + j * 32 + lane;
+            rows[j] = 0xffffffffu;
+            if (t < last) {
+                if (page[j] >= 0 && page[j] < c.n_pages) {
+                    const uint32_t ph = static_cast<uint32_t>(page[j]) * 2 * c.nkv + h, slot = t - at[j] * c.page_size;
+                    rows[j] = ph * c.page_size + slot;
+                    sc_at[j] = ph * c.blocks + c.by_block.div(slot);
+                } else {
+                    set_status(c.status, SDV_ERR_CAPACITY);
+                }
+            }
         }
     };
-    // K rows and scales of chunk ch; returns the pool row of this lane's key for the V rows
-    auto load_k = [&](int ch, int page) {
-        const int t = first + ch * kQKeys + my_key;
-        const bool in = page >= 0 && page < c.n_pages;
-        uint32_t row = 0xffffffffu;
-        if (lane < LW) {
-            if (!in && t < last) set_status(c.status, SDV_ERR_CAPACITY);
-            const int slot = c.by_page.mod(t, c.page_size), nblk = c.blocks;
-            const size_t ph = in ? static_cast<size_t>(page) * 2 * c.nkv + h : 0;
-            if (in) row = static_cast<uint32_t>(ph * c.page_size + slot);
-            const float *sc = c.scales + (in ? ph * nblk + c.by_block.div(slot) : 0);
-            cp_async4(smem_u32(&kv_scale[ch % 4][0][my_key]), sc, in);
-            cp_async4(smem_u32(&kv_scale[ch % 4][1][my_key]), in ? sc + c.nkv * nblk : sc, in);
+    const int v_rows = c.nkv * c.page_size;
+    // lanes 0 to 15 bring K's boxes, 16 to 31 V's
+    auto load_half = [&](int ch, bool v) {
+        const int st = ch % kQStages;
+        const uint32_t dst = kv_s + (st * 2 + (v ? 1 : 0)) * Q::TILE;
+        uint64_t *full = v ? &v_full[st] : &k_full[st];
+        if (ch >= kQStages && ok) ok = mbar_wait(v ? &v_empty[st] : &k_empty[st], (ch / kQStages - 1) & 1);
+        if (a.box_rows) {
+            if (lane == 0) mbar_arrive_expect_tx(full, Q::TILE);
+            __syncwarp();
+            const int n = lane % 16;
+            if (lane / 16 == (v ? 1 : 0) && n * a.box_rows < kQKeys)
+                load_box(dst + n * a.box_rows * D, &pool, full, box + (v && box < a.pool_rows ? v_rows : 0));
+        } else {
+            constexpr int PPR = D / 16, RPI = 32 / PPR;  // pieces a row, rows a copy
+            const uint8_t *codes = c.codes + lane % PPR * 16 + (v ? static_cast<size_t>(v_rows) * D : 0);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                for (int j = 0; j < 32 / RPI; ++j) {
+                    const int r = j * RPI + lane / PPR;
+                    const uint32_t row = __shfl_sync(0xffffffffu, rows[g], r);
+                    const bool in = row != 0xffffffffu;
+                    cp_async16(dst + line_offset(g * 32 + r, lane % PPR * 16, D),
+                               in ? codes + static_cast<size_t>(row) * D : c.codes, in);
+                }
+            if (lane == 0) mbar_arrive(full);
         }
-        load_rows(kv_s + ch % kQStages * 2 * Q::TILE, row, 0);
-        cp_async_arrive(&k_full[ch % kQStages]);
-        return row;
+        if (!v) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = rows[j] != 0xffffffffu;
+                const float *sc = c.scales + (in ? sc_at[j] : 0);
+                cp_async4(smem_u32(&kv_scale[ch % 4][0][j * 32 + lane]), sc, in);
+                cp_async4(smem_u32(&kv_scale[ch % 4][1][j * 32 + lane]), in ? sc + c.nkv * c.blocks : sc, in);
+            }
+        }
+        cp_async_arrive(full);
     };
-    const size_t v_off = static_cast<size_t>(c.nkv) * c.page_size * D;
-    auto load_v = [&](int ch, uint32_t row) {
-        load_rows(kv_s + (ch % kQStages * 2 + 1) * Q::TILE, row, v_off);
-        cp_async_arrive(&v_full[ch % kQStages]);
-    };
-    int page = -1;           // of the next chunk whose K is to be loaded
-    uint32_t v_row = 0;      // of the next chunk whose V is to be loaded
-    if (!is_mma) {
-        const int page0 = look(0), page1 = look(1);
-        page = look(2);
-        // the first chunks are on their way while the queries are prepared
-        if (n_chunks > 0) load_v(0, load_k(0, page0));
-        if (n_chunks > 1) load_v(1, load_k(1, page1));
-    } else {
+    if (is_load) {
+        // on its own from here on: the first chunks are on their way while the queries are prepared
+        for (int ch = 0; ch < n_chunks; ++ch) {
+            look(ch);
+            load_half(ch, false);
+            load_half(ch, true);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
+    } else if (is_mma) {
         tmem_alloc(&tmem_s, Q::COLS);
         tmem_relinquish();
         for (int r = lane; r < ROWS; r += 32) pos_s[r] = r < n_rows ? s.p0 + row_of(r).i : -1;
@@ -334,7 +389,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     // Q: the tile's rows as e4m3 planes [plane x ROWS + row][D], eight values a thread at a time
     float q_unit = 1.f;  // 2^-e: what the planes' products are multiplied by
     constexpr int QN = ROWS * D / 8 / (Q::WG * 128);
-    if (!is_mma) {
+    if (!is_load && !is_mma) {
         float x[QN][8], amax = 0.f;
 #pragma unroll
         for (int n = 0; n < QN; ++n) {
@@ -393,34 +448,38 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         fence_async_smem();
     }
     tc_fence_before();
-    __syncthreads();
+    if (!is_load) named_bar_sync(6, Q::WG * 128 + 32);  // the queries and the TMEM address are there
     tc_fence_after();
-    const uint32_t tmem = tmem_s;
-    bool ok = true;  // false once a wait gave up: the rest runs without waiting, and the status word says so
+    const uint32_t tmem = is_load ? 0 : tmem_s;
 
     if (is_mma) {
-        // ---- MMA issue: the scores of a chunk go out as soon as the previous chunk's are read
+        // ---- MMA issue
         if (lane == 0) {
             const uint32_t id_s = idesc_e4m3(128, Q::NS, false), id_o = idesc_e4m3(128, Q::NP, true);
-            auto issue_scores = [&](int ch) {
-                const int st = ch % kQStages;
-                const uint32_t k_s = kv_s + st * 2 * Q::TILE;
+            int asked = 0;  // chunks whose scores have been issued
+            auto issue_scores = [&]() {
+                const int ch = asked++, st = ch % kQStages;
+                const uint32_t k_s = kv_s + st * 2 * Q::TILE, d = tmem + ch % Q::NSB * Q::NS;
                 if (ok) ok = mbar_wait(&k_full[st], (ch / kQStages) & 1);
-                fence_async_smem();  // the copies were generic writes; the tensor cores read through the async proxy
+                fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
 #pragma unroll
                 for (int k = 0; k < D / 32 * (Q::FOLD ? Q::PQ : 1); ++k)
-                    umma_e4m3(tmem, line_desc(k_s + k % (D / 32) * 32, D),
+                    umma_e4m3(d, line_desc(k_s + k % (D / 32) * 32, D),
                               line_desc(q_s + k / (D / 32) * ROWS * D + k % (D / 32) * 32, D), id_s, k > 0);
-                umma_commit(&s_full);
-                mbar_arrive(&s_full);  // passes on the scales' arrival, too
+                umma_commit(&s_full[ch % Q::NSB]);
+                umma_commit(&k_empty[st]);
+                mbar_arrive(&s_full[ch % Q::NSB]);  // passes on the scales' arrival, too
             };
-            if (n_chunks > 0) issue_scores(0);
+            if (n_chunks > 0) issue_scores();
             for (int ch = 0; ch < n_chunks; ++ch) {
                 const int st = ch % kQStages;
                 const uint32_t v_s = kv_s + (st * 2 + 1) * Q::TILE;
+                // with room for two, the next scores go out before this chunk's probabilities are there if its keys are
+                if (Q::NSB == 2 && asked < n_chunks && mbar_done(&k_full[asked % kQStages], (asked / kQStages) & 1))
+                    issue_scores();
                 if (ok) ok = mbar_wait(&p_full, ch & 1);
                 tc_fence_after();
-                if (ch + 1 < n_chunks) issue_scores(ch + 1);
+                if (Q::NSB == 1 && asked < n_chunks) issue_scores();
                 if (ok) ok = mbar_wait(&v_full[st], (ch / kQStages) & 1);
                 fence_async_smem();
 #pragma unroll
@@ -428,11 +487,13 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                     umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k * D, D),
                               line_desc(p_s + 32 * k * Q::W, Q::W, kQKeys * Q::W), id_o, k > 0);
                 umma_commit(&o_full);
+                umma_commit(&v_empty[st]);
+                if (Q::NSB == 2 && asked == ch + 1 && asked < n_chunks) issue_scores();
             }
             if (!ok) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         }
         __syncwarp();
-    } else {
+    } else if (!is_load) {
         // ---- softmax and accumulation: a thread is key (then dim) `tid % 128` of the chunk
         const int g = warp / 4, col0 = g * CW, key = tid % 128;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
@@ -465,16 +526,17 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         for (int ch = 0; ch < n_chunks; ++ch) {
             const int t0 = first + ch * kQKeys, t = t0 + key;
             const bool masked = t0 + kQKeys - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window);
-            if (ok) ok = mbar_wait(&s_full, ch & 1);
+            if (ok) ok = mbar_wait(&s_full[ch % Q::NSB], (ch / Q::NSB) & 1);
             tc_fence_after();
-            const float ks = kv_scale[ch % 4][0][key] * unit, vs = kv_scale[ch % 4][1][key], lv = __log2f(vs);
+            const uint32_t s_col = tmem + lanes + ch % Q::NSB * Q::NS + col0;
+            const float ks = kv_scale[ch % 4][0][key] * unit, vs = t < last ? kv_scale[ch % 4][1][key] : 1.f, lv = __log2f(vs);
             // sixteen rows' scores of this key in log2 units, -inf where a row does not see it
             auto scores = [&](int r0, float (&sc)[16]) {
                 float v[Q::FOLD ? 1 : Q::PQ - 1][16];
-                tmem_ld16(tmem + lanes + col0 + r0, sc);
+                tmem_ld16(s_col + r0, sc);
                 if constexpr (!Q::FOLD) {
 #pragma unroll
-                    for (int p = 1; p < Q::PQ; ++p) tmem_ld16(tmem + lanes + p * ROWS + col0 + r0, v[p - 1]);
+                    for (int p = 1; p < Q::PQ; ++p) tmem_ld16(s_col + p * ROWS + r0, v[p - 1]);
                     if constexpr (Q::PQ == 2)
                         tmem_ld_wait(sc, v[0]);
                     else
@@ -589,17 +651,19 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                                  : "memory");
                 }
             }
+            if (t0 + kQKeys > last) {  // slots behind the sequence may hold anything, and 0 times a NaN is none
+                const int st = ch % kQStages;
+                if (ok) ok = mbar_wait(&v_full[st], (ch / kQStages) & 1);
+                if (t >= last)
+                    for (int j = g; j < D / 16; j += Q::WG)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(kv_s + (st * 2 + 1) * Q::TILE + key * D + j * 16),
+                                     "r"(0)
+                                     : "memory");
+            }
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(&p_full);
-            // while the next scores are computed: the stages that this chunk's K and the last one's V have left
-            if (ch > 0 && ch + kQStages - 1 < n_chunks) load_v(ch + kQStages - 1, v_row);
-            if (ch + kQStages < n_chunks) {
-                v_row = load_k(ch + kQStages, page);
-                page = look(ch + kQStages + 1);
-            }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
         if (n_chunks > 0) accumulate(n_chunks - 1);
         if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         // ---- sums over the keys, and the rows out
@@ -667,7 +731,7 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs 
     const QSpan s = qcache_span(a.c, b);
     const int L = s.p0 + s.S, keys = qattn_part_keys(a, max(L, 1));
     const int parts = (L + keys - 1) / keys;
-    __shared__ float o_s[NW][D], l_s[NW];
+    __shared__ float o_s[NW][D], l_s;
     pdl_wait();  // in every CTA: this kernel's end stands for the attention's, too
     pdl_trigger();
     if (i >= s.S || keys >= L) return;
@@ -680,27 +744,40 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs 
     float o[V], l = 0.f;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] = 0.f;
-#pragma unroll 8
-    for (int p = warp; p < parts; p += NW) {
-        const float2 ml = a.part_ml[slot + p];
-        float v[V];
-        if constexpr (V == 4)
-            *reinterpret_cast<float4 *>(v) = reinterpret_cast<const float4 *>(a.part_o + (slot + p) * D)[lane];
-        else
-            *reinterpret_cast<float2 *>(v) = reinterpret_cast<const float2 *>(a.part_o + (slot + p) * D)[lane];
+    // 32 parts at a time: a lane weighs one, the warp's eight are read at once
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+        const float2 ml = p0 + lane < parts ? a.part_ml[slot + p0 + lane] : make_float2(kQNoRef, 0.f);
         // l > 0 without a reference: keys of scale 0 alone, counted from 0
-        const float f = ml.y == 0.f ? 0.f : ex2(fminf((ml.x == kQNoRef ? 0.f : ml.x) - m, 120.f));
-        l = fmaf(f, ml.y, l);
+        const float mine = ml.y == 0.f ? 0.f : ex2(fminf((ml.x == kQNoRef ? 0.f : ml.x) - m, 120.f));
+        float v[32 / NW][V];
 #pragma unroll
-        for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[d], o[d]);
+        for (int j = 0; j < 32 / NW; ++j) {
+            const int p = p0 + warp + j * NW;
+#pragma unroll
+            for (int d = 0; d < V; ++d) v[j][d] = 0.f;
+            if (p < parts) {
+                const float *src = a.part_o + (slot + p) * D + lane * V;
+                if constexpr (V == 4)
+                    *reinterpret_cast<float4 *>(v[j]) = *reinterpret_cast<const float4 *>(src);
+                else
+                    *reinterpret_cast<float2 *>(v[j]) = *reinterpret_cast<const float2 *>(src);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 32 / NW; ++j) {
+            const float f = __shfl_sync(0xffffffffu, mine, warp + j * NW);
+#pragma unroll
+            for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[j][d], o[d]);
+        }
+        if (warp == 0) l += warp_sum(mine * ml.y);
     }
 #pragma unroll
     for (int d = 0; d < V; ++d) o_s[warp][lane * V + d] = o[d];
-    if (lane == 0) l_s[warp] = l;
+    if (threadIdx.x == 0) l_s = l;
     __syncthreads();
     const int d = threadIdx.x;
     if (d < D) {
-        const float num = (o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d]), den = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
+        const float num = (o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d]), den = l_s;
         static_cast<T *>(a.out)[(s.r0 + i) * a.out_stride + hq * D + d] = from_f32<T>(den == 0.f ? 0.f : num / den);
     }
 }
