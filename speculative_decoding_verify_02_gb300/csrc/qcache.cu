@@ -3,7 +3,6 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
-#include <type_traits>
 #include <vector>
 
 #include "qcache_attention.cuh"
@@ -28,7 +27,7 @@ namespace {
 // different lengths even out; a single sequence into just as many as fit.
 #ifndef QW1
 #define QW1 1
-#define QWB 3
+#define QWB 2
 #endif
 constexpr int kQWaves = QWB;
 
@@ -137,18 +136,19 @@ bool aligned16(const void *p, int64_t stride, int dtype) {
 bool element_aligned(const void *p, int dtype) { return reinterpret_cast<uintptr_t>(p) % dtype_size(dtype) == 0; }
 
 // ---- attention: tile rows, parts of a sequence and workspace
-// Rows of a tile: 16, 32 or (bf16) 64, the smallest that holds a span's rows of one kv head. Only wide bf16
-// spans take 64: three planes of an fp16 query beside two of p would not leave two CTAs room in TMEM.
-int attn_rows(int span_rows, int dtype) { return span_rows <= 16 ? 16 : span_rows <= 32 || dtype == SDV_FP16 ? 32 : 64; }
+// Rows of a tile: 16 or 32, the smaller that holds a span's rows of one kv head. Tiles of 64 rows halved the reads of
+// long spans' keys, but their two-fold rows a thread spilled: 128 rows at 32K took 288 us against 240.
+int attn_rows(int span_rows) { return span_rows <= 16 ? 16 : 32; }
 
 struct AttnPlan {
-    int rows, tiles, splits;
+    int rows, tiles, splits, ctas;
 };
-AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int dtype) {
+AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span) {
     AttnPlan p;
     const int span_rows = max_span * (q->c.n_q_heads / q->c.n_kv_heads);
-    p.rows = attn_rows(span_rows, dtype);
+    p.rows = attn_rows(span_rows);
     p.tiles = cdiv(span_rows, p.rows);
+    p.ctas = 2 * q->sm_count;
     const long long units = static_cast<long long>(B) * q->c.n_kv_heads * p.tiles;
     const int waves = B > 1 ? QWB : QW1;
     const long long s = 2LL * q->sm_count * waves / units;
@@ -157,28 +157,27 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int dtype) {
 }
 
 // Floats of attention's partial results: rows x heads x splits of the largest call, D + 2 each. splits >= 2 only
-// while B nkv tiles splits <= 2 SMs x waves, and a tile holds at most 64 rows.
+// while B nkv tiles splits <= 2 SMs x waves, and a tile holds at most 32 rows.
 size_t attn_partials(const sdv_qcache_cfg &c, int sm_count) {
     const size_t all = static_cast<size_t>(c.max_batch) * c.max_span * c.n_q_heads * cdiv(c.max_context, kQKeys);
-    const size_t cut = static_cast<size_t>(2) * sm_count * kQWaves * 64;
+    const size_t cut = static_cast<size_t>(2) * sm_count * kQWaves * 32;
     return std::min(all, cut);
 }
 
 template <typename T, int D, int ROWS>
 int launch_attn_rows(const CUtensorMap &pool, const QAttnArgs &a, const AttnPlan &p, void *stream) {
     typedef QTile<T, D, ROWS> Q;
-    const dim3 grid(static_cast<unsigned>(p.tiles) * a.c.nkv, p.splits, a.c.B);
-    int r = launch(qcache_attn_kernel<T, D, ROWS>, grid, Q::THREADS, Q::SMEM, stream, pool, a);
-    if (r == SDV_OK && p.splits > 1)
-        r = launch(qcache_merge_kernel<T, D>, dim3(static_cast<unsigned>(a.c.max_span) * a.nq, a.c.B), kQMergeThreads, 0,
-                   stream, a);
-    return r;
+    const dim3 grid(static_cast<unsigned>(std::min(a.units, p.ctas)));
+    const int r = launch(qcache_attn_kernel<T, D, ROWS>, grid, Q::THREADS, Q::SMEM, stream, pool, a);
+    if (r != SDV_OK || p.splits == 1) return r;
+    const long long items = static_cast<long long>(a.c.max_span) * a.nq;
+    if (p.splits <= 8 && items * a.c.B > 1024)  // few items: four warps each are done sooner (848 keys: 1.2 against 1.9 us)
+        return launch(qcache_merge_kernel<T, D, 1>, dim3(cdiv(items, 4), a.c.B), kQMergeThreads, 0, stream, a);
+    return launch(qcache_merge_kernel<T, D, 4>, dim3(static_cast<unsigned>(items), a.c.B), kQMergeThreads, 0, stream, a);
 }
 template <typename T, int D>
 int launch_attn(const CUtensorMap &pool, const QAttnArgs &a, const AttnPlan &p, void *stream) {
     if (p.rows == 16) return launch_attn_rows<T, D, 16>(pool, a, p, stream);
-    if constexpr (!std::is_same<T, __half>::value)
-        if (p.rows == 64) return launch_attn_rows<T, D, 64>(pool, a, p, stream);
     return launch_attn_rows<T, D, 32>(pool, a, p, stream);
 }
 
@@ -196,11 +195,10 @@ cudaError_t set_attn() {
 }
 template <typename T, int D>
 cudaError_t set_attn_all() {
-    cudaError_t e = set_carveout(qcache_merge_kernel<T, D>);
+    cudaError_t e = set_carveout(qcache_merge_kernel<T, D, 1>);
+    if (e == cudaSuccess) e = set_carveout(qcache_merge_kernel<T, D, 4>);
     if (e == cudaSuccess) e = set_attn<T, D, 16>();
     if (e == cudaSuccess) e = set_attn<T, D, 32>();
-    if constexpr (!std::is_same<T, __half>::value)
-        if (e == cudaSuccess) e = set_attn<T, D, 64>();
     return e;
 }
 
@@ -371,12 +369,17 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     a.window = window;
     a.q_vec = aligned16(d_q, q_stride, dtype);
     a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(D));
-    const AttnPlan p = attn_plan(cache, B, max_span, dtype);
+    const AttnPlan p = attn_plan(cache, B, max_span);
     const size_t slots = attn_partials(cache->c, cache->sm_count);
     a.splits = p.splits;
     a.tiles = p.tiles;
     a.grp = a.nq / a.c.nkv;
+    const long long units = static_cast<long long>(B) * p.splits * a.c.nkv * p.tiles;
+    if (units > (1 << 30)) return SDV_ERR_UNSUPPORTED;
+    a.units = static_cast<int>(units);
+    a.counter = reinterpret_cast<int *>(cache->ws) + 1;
     a.by_tiles = FastDiv::of(a.tiles);
+    a.by_kv = FastDiv::of(a.c.nkv);
     a.by_splits = FastDiv::of(a.splits);
     a.by_grp = FastDiv::of(a.grp);
     a.by_nq = FastDiv::of(a.nq);

@@ -10,12 +10,10 @@
 //
 // The 16-bit operand of each product is split into e4m3 planes laid side by side along the width:
 //   q = 2^-e (q0 + 2^-5 q1 + 2^-10 q2), e from the tile's largest |q|: two planes hold a bf16's eight
-//       bits exactly, three an fp16's eleven (what lies 2^-20 below the largest rounds away). Tiles of 64
-//       rows (bf16) add the two planes' products in the accumulator instead, with q1 at q0's own scale:
-//       half the columns, exact to 2^-18 of the largest;
+//       bits exactly, three an fp16's eleven (what lies 2^-20 below the largest rounds away);
 //   p = x0 + 2^-6 x1 + 2^-11 x2, x = 64 p in (0, 128]: p is rounded to fp16's eleven bits and the planes hold
 //       them down to 2^-26 (two planes lost the tail under one large p: 2% off at p = 2^-16).
-// The planes' products are otherwise added in fp32 afterwards.
+// The planes' products are added in fp32 afterwards.
 //
 // A key's V scale is not applied to V: it joins the exponent. With s_t the score in log2 units and
 // w_t = s_t + log2 vs_t, x_t = 2^(w_t - M) multiplies the bare codes, M being a row's running maximum of w,
@@ -34,11 +32,13 @@ struct QAttnArgs {
     void *out;
     long long q_stride, out_stride;  // elements between rows
     int nq, window;                  // window: positions a row sees, its own the last (0: all)
+    int units;                       // B x splits x nkv x tiles
+    int *counter;                    // units taken beyond the first of each CTA, CTAs done; both zero between calls
     int splits;                      // parts a sequence's keys are cut into at most
     int tiles;                       // row tiles of a span of max_span rows
     int grp;                         // q heads a kv head
     int q_vec;                       // q rows are 16-byte aligned
-    FastDiv by_tiles, by_splits, by_grp, by_nq;
+    FastDiv by_tiles, by_kv, by_splits, by_grp, by_nq;
     float scale_log2;                // log2(e) / sqrt(D)
     float *part_o;                   // [sequence][span row][q head][splits][D]
     int box_rows;                    // pool rows of a TMA box; 0: pages that no box fits, copied in 16-byte pieces
@@ -54,21 +54,17 @@ struct QTile {
     static constexpr int D = D_, ROWS = ROWS_;
     static constexpr int PQ = sizeof(T) == 2 && !__is_same(T, __half) ? 2 : 3;  // planes of q
     static constexpr int PP = 3;                                                  // planes of p
-    static constexpr bool FOLD = ROWS == 64;                                      // q planes share S's columns
-    static constexpr int WG = ROWS == 16 ? 1 : 2;                                 // softmax warpgroups
-    static constexpr int CW = ROWS / WG;                                          // columns of one
+    static constexpr int CW = 16, WG = ROWS / CW;                                 // columns of a softmax warpgroup
     static constexpr int NQ = PQ * ROWS, NP = PP * ROWS;                          // widths of the two products
-    static constexpr int W = ROWS == 32 ? 128 : 64;  // bytes of a key's P line: every plane, or (64 rows) one
-    static constexpr int P_LINES = (NP + W - 1) / W;
+    static constexpr int W = NP <= 64 ? 64 : 128;                                 // bytes of a key's P line
     static constexpr int TILE = kQKeys * D;                                       // bytes of a K or V chunk
-    static constexpr int Q_BYTES = (NQ * D + 1023) / 1024 * 1024, P_BYTES = kQKeys * W * P_LINES;
+    static constexpr int Q_BYTES = (NQ * D + 1023) / 1024 * 1024, P_BYTES = kQKeys * W;
     static constexpr int SMEM = 1024 + kQStages * 2 * TILE + Q_BYTES + P_BYTES;
-    static constexpr int NS = FOLD ? ROWS : NQ;                                   // columns of S^T
-    static constexpr int NSB = 2 * NS + NP <= 256 ? 2 : 1;                        // S^T of the next chunk beside this one's
-    static constexpr int O_COL = (NSB * NS + 31) / 32 * 32;                       // TMEM column of O^T
+    static constexpr int NSB = 2 * NQ + NP <= 256 ? 2 : 1;                        // S^T of the next chunk beside this one's
+    static constexpr int O_COL = (NSB * NQ + 31) / 32 * 32;                       // TMEM column of O^T
     static constexpr int COLS = O_COL + NP <= 128 ? 128 : 256;
     static constexpr int THREADS = WG * 128 + 64;  // softmax warps, the load warp, the MMA warp
-    static_assert(ROWS == 16 || ROWS == 32 || (ROWS == 64 && PQ == 2), "tile rows");
+    static_assert(ROWS == 16 || ROWS == 32, "tile rows");
     static_assert(O_COL + NP <= COLS, "TMEM columns");
     static_assert(NQ % 16 == 0 && NP % 16 == 0, "MMA widths");
     static_assert(2 * (SMEM + 6144 + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -91,10 +87,10 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn) {
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 // Matrix descriptor over lines of `width` bytes (64 or 128) with that width's swizzle, eight lines to an
-// atom; `beside` bytes on lie the atoms that continue the lines (0: the same atom again, so that the 64
-// dims of V at D = 64 fill both halves of the 128 lanes, of which the upper is not read).
-__device__ __forceinline__ uint64_t line_desc(uint32_t addr, int width, uint32_t beside = 0) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(beside >> 4) << 16 | static_cast<uint64_t>(8 * width >> 4) << 32 |
+// atom. The offset between atoms side by side is 0: operands are one atom wide, but for V at D = 64, whose
+// dims so fill both halves of the 128 lanes (the upper half is not read).
+__device__ __forceinline__ uint64_t line_desc(uint32_t addr, int width) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(8 * width >> 4) << 32 |
            static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(width == 128 ? 2 : 4) << 61;
 }
 // Byte offset of (line, byte) under that swizzle, in a buffer aligned to 1024 bytes.
@@ -121,6 +117,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *tm, ui
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// mbar_wait with a limit of its own.
+__device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer() - t0 > limit_ns) return false;
+    return true;
 }
 // Whether the phase of the given parity is over, without waiting.
 __device__ __forceinline__ bool mbar_done(uint64_t *bar, uint32_t parity) {
@@ -196,16 +200,30 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// Two fp16 values as e4m3 codes, and back.
-__device__ __forceinline__ uint32_t e4m3_of_f16x2(uint32_t h) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+// Four fp16 values as e4m3 codes in a word, and back. Both halves in one statement: codes that pass through 16-bit
+// values of their own are widened and joined again.
+__device__ __forceinline__ uint32_t e4m3_of_f16x4(uint32_t lo, uint32_t hi) {
+    uint32_t c;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(c)
+        : "r"(lo), "r"(hi));
     return c;
 }
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
-    return h;
+__device__ __forceinline__ void f16x4_of_e4m3(uint32_t c, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
 }
 __device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
     const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
@@ -217,12 +235,22 @@ __device__ __forceinline__ uint32_t hscale2_u(uint32_t a, float s) {
 }
 
 // ------------------------------------------------------------------ the work of a CTA
-// Grid ((kv head, row tile), split, sequence): the tiles that read the same keys run side by side. A
-// sequence of L keys is cut into parts of ceil(L / splits) keys, rounded up to whole chunks: the cut
-// depends on the sequence's own length and the call's B and max_span only.
-__device__ __forceinline__ int qattn_part_keys(const QAttnArgs &a, int L) {
-    const int per = a.by_splits.div(L + a.splits - 1);
-    return (per + kQKeys - 1) / kQKeys * kQKeys;
+// A unit is (sequence, part, kv head, row tile), in that order, so that the tiles that read the same keys run
+// side by side. A sequence of L keys is cut into parts of ceil(L / splits) keys, rounded up to whole chunks:
+// the cut depends on the sequence's own length and the call's B and max_span only. A CTA starts with the unit
+// of its number and takes the next one from a counter; the order changes no result. Its load warp is
+// ahead of the others by up to two units, so that only the first one's page tables and keys are waited for.
+// With a window the cut starts at the chunk of the first key that any row of the span sees.
+struct QCut {
+    int origin, keys, parts;  // parts of `keys` keys from `origin` to the sequence's end
+};
+__device__ __forceinline__ QCut qattn_cut(const QAttnArgs &a, int p0, int S) {
+    QCut c;
+    c.origin = a.window > 0 ? max(0, p0 - a.window + 1) / kQKeys * kQKeys : 0;
+    const int n = p0 + S - c.origin, per = a.by_splits.div(n + a.splits - 1);
+    c.keys = (per + kQKeys - 1) / kQKeys * kQKeys;
+    c.parts = (n + c.keys - 1) / c.keys;
+    return c;
 }
 // First partial result of span row i of sequence b (by its place in the span, which max_span bounds).
 __device__ __forceinline__ size_t qattn_slot(const QAttnArgs &a, int b, int i, int hq) {
@@ -233,6 +261,11 @@ __device__ __forceinline__ size_t qattn_slot(const QAttnArgs &a, int b, int i, i
 struct QRow {
     int row, hq, i;
 };
+enum { kUnitEnd, kUnitRows, kUnitRefused };
+struct QUnit {
+    int state, b, h, split, row0, n_rows, r0, S, p0, first, last, whole;  // whole: the sequence has one part
+};
+constexpr uint64_t kQUnitWaitNs = 10 * kWaitLimitNs;  // above any sum of the waits that a unit's end depends on
 
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_kernel(
@@ -241,17 +274,18 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     constexpr int CW = Q::CW;
     const QCacheArgs &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int grp = a.grp, split = blockIdx.y, b = blockIdx.z;
-    const int h = a.by_tiles.div(blockIdx.x), tile = blockIdx.x - h * a.tiles;
+    const int grp = a.grp;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t kv_s = smem, q_s = smem + kQStages * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
     __shared__ uint64_t k_full[kQStages], k_empty[kQStages], v_full[kQStages], v_empty[kQStages], s_full[2], p_full, o_full;
     __shared__ uint32_t tmem_s;
     __shared__ __align__(16) float m_neg[ROWS], m_step[ROWS];  // -M of each row, and 2^(M before - M) where M last moved
-    __shared__ uint32_t m_key[ROWS];
     __shared__ int pos_s[ROWS];
-    __shared__ float l_s[4][ROWS], amax_s[Q::WG * 4];
+    __shared__ long long to_s[ROWS];  // where a row's result begins: in `out`, or of its part in part_o
+    __shared__ float top_s[4][ROWS], l_s[4][ROWS], amax_s[2][Q::WG * 4];
+    __shared__ uint64_t unit_full[2], unit_empty[2], q_full;
+    __shared__ QUnit unit_s[2];
     __shared__ float kv_scale[4][2][kQKeys];  // four chunks deep: softmax may still read the one two back
     const bool is_load = warp == Q::WG * 4, is_mma = warp == Q::WG * 4 + 1;
     // what needs no data goes before the wait for the kernel ahead
@@ -263,53 +297,47 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 2);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&unit_full[i], 1);
+            mbar_init(&unit_empty[i], Q::WG * 128 + 1);
+        }
+        mbar_init(&q_full, Q::WG * 128);
         mbar_init(&p_full, Q::WG * 128);
         mbar_init(&o_full, 1);
         fence_mbar_init();
-    }
-    if (tid < ROWS) {
-        m_neg[tid] = -kQNoRef;
-        m_key[tid] = 0;
     }
     __syncthreads();
     pdl_wait();
     pdl_trigger();  // after the wait: what starts behind this kernel may read what came before it
 
-    const QSpan s = qcache_span(c, b);
     T *out = static_cast<T *>(a.out);
-    if (s.S == 0) {
-        if (split == 0 && s.code != SDV_OK) {
-            if (blockIdx.x == 0 && tid == 0) set_status(c.status, s.code);
-            // refused: NaN rather than stale memory, this kv head's q heads shared over the tiles
-            for (int r = tile; r < s.rows; r += a.tiles)
-                for (int d = tid; d < grp * D; d += Q::THREADS)
-                    out[(s.r0 + r) * a.out_stride + h * grp * D + d] = from_f32<T>(NAN);
-        }
-        return;
-    }
-    const int row0 = tile * ROWS, n_rows = min(ROWS, s.S * grp - row0);  // flattened (span row, head) rows
-    const int L = s.p0 + s.S, keys = qattn_part_keys(a, L);
-    if (n_rows <= 0 || split * static_cast<long long>(keys) >= L) return;
-    const bool whole = keys >= L;  // the sequence has one part
-    auto row_of = [&](int r) {
-        const int i = a.by_grp.div(row0 + r);
-        return QRow{s.r0 + i, h * grp + row0 + r - i * grp, i};
-    };
-    const int pos_lo = s.p0 + a.by_grp.div(row0), pos_hi = s.p0 + a.by_grp.div(row0 + n_rows - 1);
-    int first = split * keys;
-    const int last = min(first + keys, pos_hi + 1);
-    if (a.window > 0) first = max(first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
-    const int n_chunks = max(0, (last - first + kQKeys - 1) / kQKeys);
-
     bool ok = true;  // false once a wait gave up: the rest runs without waiting, and the status word says so
+    // The k-th unit of this CTA, as the load warp leaves it.
+    auto take_unit = [&](int k) {
+        QUnit u;
+        u.state = kUnitEnd;
+        if (mbar_wait_for(&unit_full[k % 2], k / 2 & 1, kQUnitWaitNs)) {
+            u = unit_s[k % 2];
+            mbar_arrive(&unit_empty[k % 2]);
+        } else {
+            set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
+        }
+        return u;
+    };
+    auto row_of = [&](const QUnit &u, int r) {
+        const int i = a.by_grp.div(u.row0 + r);
+        return QRow{u.r0 + i, u.h * grp + u.row0 + r - i * grp, i};
+    };
+    auto chunks_of = [&](const QUnit &u) { return max(0, (u.last - u.first + kQKeys - 1) / kQKeys); };
+
     // ---- the load warp: a chunk's K rows with both scales, then its V rows. Pages of a multiple of eight tokens come in
     // TMA boxes, a lane a box (a box past the pool is zeros); others in 16-byte pieces.
-    const int *table = c.page_table + static_cast<size_t>(b) * c.pages_per_seq;
     uint32_t rows[4], sc_at[4];  // pool rows and scales of this lane's four keys of a chunk
     int box = 0;                 // pool row of its box
-    auto look = [&](int ch) {
+    auto look = [&](const QUnit &u, int ch) {
         // the five page-table entries first, so that their latencies pass together; keys past the last read its entry
-        const int t0 = first + ch * kQKeys, tb = t0 + lane % 16 * a.box_rows;
+        const int *table = c.page_table + static_cast<size_t>(u.b) * c.pages_per_seq;
+        const int h = u.h, last = u.last, t0 = u.first + ch * kQKeys, tb = t0 + lane % 16 * a.box_rows;
         const bool has_box = lane % 16 * a.box_rows < kQKeys && tb < last;
         int at[5], page[5];
 #pragma unroll
@@ -373,56 +401,219 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         cp_async_arrive(full);
     };
     if (is_load) {
-        // on its own from here on: the first chunks are on their way while the queries are prepared
-        for (int ch = 0; ch < n_chunks; ++ch) {
-            look(ch);
-            load_half(ch, false);
-            load_half(ch, true);
+        int n = blockIdx.x, chunk = 0, k = 0;
+        // With more units than CTAs the long sequences' go first, so that what is left for the end is short: lane r holds
+        // the sequence of rank r by length (up to 32 sequences; more of them even out by their number).
+        int ranked = lane;
+        const bool by_length = static_cast<int>(gridDim.x) < a.units && c.B > 1 && c.B <= 32;
+        if (by_length) {
+            const QSpan s = qcache_span(c, min(lane, c.B - 1));
+            const int mine = lane < c.B ? (s.S ? s.p0 + s.S : 0) : -1;
+            int rank = 0;
+#pragma unroll
+            for (int o = 0; o < 32; ++o) {
+                const int other = __shfl_sync(0xffffffffu, mine, o);
+                rank += other > mine || (other == mine && o < lane);
+            }
+#pragma unroll
+            for (int o = 0; o < 32; ++o)
+                if (__shfl_sync(0xffffffffu, rank, o) == lane) ranked = o;
+        }
+        while (n < a.units) {
+            // the next unit's number is on its way while this one's keys are asked for
+            int next = a.units;
+            if (static_cast<int>(gridDim.x) < a.units) {
+                if (lane == 0) next = gridDim.x + atomicAdd(&a.counter[0], 1);
+            }
+            QUnit u;
+            const int nt = a.by_tiles.div(n), ns = a.by_kv.div(nt);
+            const int tile = n - nt * a.tiles;
+            u.h = nt - ns * c.nkv;
+            u.b = a.by_splits.div(ns);
+            u.split = ns - u.b * a.splits;
+            if (by_length) u.b = __shfl_sync(0xffffffffu, ranked, u.b);
+            const QSpan s = qcache_span(c, u.b);
+            u.r0 = s.r0, u.S = s.S, u.p0 = s.p0;
+            u.row0 = tile * ROWS;
+            u.n_rows = min(ROWS, s.S * grp - u.row0);
+            const QCut cut = qattn_cut(a, s.p0, max(s.S, 1));
+            u.state = kUnitEnd;
+            if (s.S == 0) {
+                if (s.code != SDV_OK && u.split == 0) {
+                    u.state = kUnitRefused;
+                    u.S = s.rows;
+                    u.n_rows = tile;
+                    if (u.h == 0 && tile == 0 && lane == 0) set_status(c.status, s.code);
+                }
+            } else if (u.n_rows > 0 && u.split < cut.parts) {
+                u.state = kUnitRows;
+            }
+            if (u.state != kUnitEnd) {
+                const int pos_lo = s.p0 + a.by_grp.div(u.row0), pos_hi = s.p0 + a.by_grp.div(u.row0 + max(u.n_rows, 1) - 1);
+                u.whole = cut.parts == 1;
+                u.first = cut.origin + u.split * cut.keys;
+                u.last = min(u.first + cut.keys, pos_hi + 1);
+                if (a.window > 0) u.first = max(u.first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
+                if (k >= 2 && !mbar_wait_for(&unit_empty[k % 2], (k / 2 - 1) & 1, kQUnitWaitNs)) ok = false;
+                if (lane == 0) {
+                    unit_s[k % 2] = u;
+                    mbar_arrive(&unit_full[k % 2]);
+                }
+                ++k;
+                if (u.state == kUnitRows) {
+                    const int n_chunks = chunks_of(u);
+                    for (int ch = 0; ch < n_chunks; ++ch, ++chunk) {
+                        look(u, ch);
+                        load_half(chunk, false);
+                        load_half(chunk, true);
+                    }
+                }
+            }
+            n = __shfl_sync(0xffffffffu, next, 0);
+        }
+        if (k >= 2 && !mbar_wait_for(&unit_empty[k % 2], (k / 2 - 1) & 1, kQUnitWaitNs)) ok = false;
+        if (lane == 0) {
+            unit_s[k % 2].state = kUnitEnd;
+            mbar_arrive(&unit_full[k % 2]);
+            // the last CTA to take its leave sets the counter back for the next call
+            if (static_cast<int>(gridDim.x) < a.units && atomicAdd(&a.counter[1], 1) == static_cast<int>(gridDim.x) - 1) {
+                a.counter[0] = 0;
+                a.counter[1] = 0;
+            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
+        if (!ok) {  // no copy may land after this CTA's shared memory is someone else's
+            for (int i = max(0, chunk - kQStages); i < chunk; ++i) {
+                mbar_wait(&k_full[i % kQStages], (i / kQStages) & 1);
+                mbar_wait(&v_full[i % kQStages], (i / kQStages) & 1);
+            }
+            if (lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
+        }
     } else if (is_mma) {
         tmem_alloc(&tmem_s, Q::COLS);
         tmem_relinquish();
-        for (int r = lane; r < ROWS; r += 32) pos_s[r] = r < n_rows ? s.p0 + row_of(r).i : -1;
     }
-    // Q: the tile's rows as e4m3 planes [plane x ROWS + row][D], eight values a thread at a time
-    float q_unit = 1.f;  // 2^-e: what the planes' products are multiplied by
-    constexpr int QN = ROWS * D / 8 / (Q::WG * 128);
-    if (!is_load && !is_mma) {
-        float x[QN][8], amax = 0.f;
+    if (!is_load) {
+        tc_fence_before();
+        named_bar_sync(6, Q::WG * 128 + 32);  // the TMEM address is there
+        tc_fence_after();
+    }
+    const uint32_t tmem = is_load ? 0 : tmem_s;
+
+    if (is_mma) {
+        // ---- MMA issue
+        if (lane == 0) {
+            const uint32_t id_s = idesc_e4m3(128, Q::NQ, false), id_o = idesc_e4m3(128, Q::NP, true);
+            int asked = 0, base = 0;  // chunks whose scores have been issued; chunks of the units before
+            auto issue_scores = [&]() {
+                const int ch = asked++, st = ch % kQStages;
+                const uint32_t k_s = kv_s + st * 2 * Q::TILE, d = tmem + ch % Q::NSB * Q::NQ;
+                if (ok) ok = mbar_wait(&k_full[st], (ch / kQStages) & 1);
+                fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
 #pragma unroll
-        for (int n = 0; n < QN; ++n) {
-            const int e = n * Q::WG * 128 + tid, r = e / (D / 8), col = e % (D / 8) * 8;
+                for (int k = 0; k < D / 32; ++k)
+                    umma_e4m3(d, line_desc(k_s + 32 * k, D), line_desc(q_s + 32 * k, D), id_s, k > 0);
+                umma_commit(&s_full[ch % Q::NSB]);
+                umma_commit(&k_empty[st]);
+                mbar_arrive(&s_full[ch % Q::NSB]);  // passes on the scales' arrival, too
+            };
+            int queries = 0;
+            for (int k = 0;; ++k) {
+                const QUnit u = take_unit(k);
+                if (u.state == kUnitEnd) break;
+                if (u.state != kUnitRows) continue;
+                const int end = base + chunks_of(u);
+                if (base == end) continue;  // the softmax warps prepare no queries then, either
+                if (ok) ok = mbar_wait(&q_full, queries++ & 1);
+                tc_fence_after();
+                issue_scores();
+                for (int ch = base; ch < end; ++ch) {
+                    const int st = ch % kQStages;
+                    const uint32_t v_s = kv_s + (st * 2 + 1) * Q::TILE;
+                    // with room for two, the next scores go out before this chunk's probabilities are there if its keys are
+                    if (Q::NSB == 2 && asked < end && mbar_done(&k_full[asked % kQStages], (asked / kQStages) & 1))
+                        issue_scores();
+                    if (ok) ok = mbar_wait(&p_full, ch & 1);
+                    tc_fence_after();
+                    if (Q::NSB == 1 && asked < end) issue_scores();
+                    if (ok) ok = mbar_wait(&v_full[st], (ch / kQStages) & 1);
+                    fence_async_smem();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
-            if (r < n_rows) {
-                const QRow w = row_of(r);
-                const T *src = static_cast<const T *>(a.q) + w.row * a.q_stride + w.hq * D + col;
-                if (a.q_vec)
-                    load8<T, true>(src, x[n]);
-                else
-                    load8<T, false>(src, x[n]);
+                    for (int k4 = 0; k4 < kQKeys / 32; ++k4)
+                        umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k4 * D, D),
+                                  line_desc(p_s + 32 * k4 * Q::W, Q::W), id_o, k4 > 0);
+                    umma_commit(&o_full);
+                    umma_commit(&v_empty[st]);
+                    if (Q::NSB == 2 && asked == ch + 1 && asked < end) issue_scores();
+                }
+                base = end;
             }
+            if (!ok) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         }
+        __syncwarp();
+    } else if (!is_load) {
+        // ---- softmax and accumulation: a thread is key (then dim) `tid % 128` of the chunk
+        const int g = warp / 4, col0 = g * CW, key = tid % 128;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        int base = 0;  // chunks of the units before
+        constexpr int QN = ROWS * D / 8 / (Q::WG * 128);
+        Raw8<T> raw[QN];  // this thread's share of a tile's queries
+        bool asked_q = false;
+        auto ask_q = [&](const QUnit &u) {
+#pragma unroll
+            for (int n = 0; n < QN; ++n) {
+                const int e = n * Q::WG * 128 + tid, r = e / (D / 8), col = e % (D / 8) * 8;
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) raw[n].u[j] = make_uint4(0, 0, 0, 0);
+                if (r < u.n_rows) {
+                    const QRow w = row_of(u, r);
+                    const T *src = static_cast<const T *>(a.q) + w.row * a.q_stride + w.hq * D + col;
+                    raw[n] = a.q_vec ? load_raw8<T, true>(src) : load_raw8<T, false>(src);
+                }
+            }
+        };
+        for (int unit_no = 0;; ++unit_no) {
+        const QUnit u = take_unit(unit_no);
+        if (u.state == kUnitEnd) break;
+        if (u.state == kUnitRefused) {  // NaN rather than stale memory, this kv head's q heads shared over the tiles
+            for (int r = u.n_rows; r < u.S; r += a.tiles)
+                for (int d = tid; d < grp * D; d += Q::WG * 128)
+                    out[(u.r0 + r) * a.out_stride + u.h * grp * D + d] = from_f32<T>(NAN);
+            continue;
+        }
+        const int n_rows = u.n_rows, n_chunks = chunks_of(u), first = u.first, last = u.last;
+        const int pos_lo = u.p0 + a.by_grp.div(u.row0), pos_hi = u.p0 + a.by_grp.div(u.row0 + n_rows - 1);
+        // the queries' planes [plane x ROWS + row][D], eight values a thread at a time; the scores that read the last
+        // unit's have been waited for
+        named_bar_sync(5, Q::WG * 128);  // nobody reads the last unit's rows any more
+        if (tid < ROWS) {
+            const QRow w = row_of(u, min(tid, n_rows - 1));
+            m_neg[tid] = -kQNoRef;
+            pos_s[tid] = tid < n_rows ? u.p0 + w.i : -1;
+            to_s[tid] = u.whole ? w.row * a.out_stride + w.hq * D
+                                : static_cast<long long>(qattn_slot(a, u.b, w.i, w.hq) + u.split) * D;
+        }
+        if (!asked_q) ask_q(u);
+        float x[QN][8], amax = 0.f;
 #pragma unroll
         for (int n = 0; n < QN; ++n)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                x[n][j] = raw[n].at(j);
                 if (fabsf(x[n][j]) < INFINITY)
                     amax = fmaxf(amax, fabsf(x[n][j]));
                 else
                     x[n][j] = NAN;  // spoils its own row
             }
         amax = redux_max(amax);
-        if (lane == 0) amax_s[warp] = amax;
+        if (lane == 0) amax_s[unit_no & 1][warp] = amax;
         named_bar_sync(7, Q::WG * 128);
 #pragma unroll
-        for (int w = 0; w < Q::WG * 4; ++w) amax = fmaxf(amax, amax_s[w]);
+        for (int w = 0; w < Q::WG * 4; ++w) amax = fmaxf(amax, amax_s[unit_no & 1][w]);
         // 2^e with amax 2^e in [128, 256); bounded so that both powers stay normal
         const int ex = amax > 0.f ? min(max(7 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), -120), 120) : 0;
         const float up = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
-        q_unit = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        const float unit = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll
         for (int n = 0; n < QN; ++n) {
             const int e = n * Q::WG * 128 + tid, r = e / (D / 8), col = e % (D / 8) * 8;
@@ -436,8 +627,8 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                 for (int j = 0; j < 4; ++j) {
                     w[j] = e4m3x2(rest[2 * j], rest[2 * j + 1]);
                     const float2 f = e4m3x2_f32(w[j]);
-                    rest[2 * j] = (rest[2 * j] - f.x) * (Q::FOLD ? 1.f : 32.f);
-                    rest[2 * j + 1] = (rest[2 * j + 1] - f.y) * (Q::FOLD ? 1.f : 32.f);
+                    rest[2 * j] = (rest[2 * j] - f.x) * 32.f;
+                    rest[2 * j + 1] = (rest[2 * j + 1] - f.y) * 32.f;
                 }
                 const uint32_t dst = q_s + line_offset(p * ROWS + r, col, D);
                 asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[0] | w[1] << 16),
@@ -446,167 +637,105 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             }
         }
         fence_async_smem();
-    }
-    tc_fence_before();
-    if (!is_load) named_bar_sync(6, Q::WG * 128 + 32);  // the queries and the TMEM address are there
-    tc_fence_after();
-    const uint32_t tmem = is_load ? 0 : tmem_s;
-
-    if (is_mma) {
-        // ---- MMA issue
-        if (lane == 0) {
-            const uint32_t id_s = idesc_e4m3(128, Q::NS, false), id_o = idesc_e4m3(128, Q::NP, true);
-            int asked = 0;  // chunks whose scores have been issued
-            auto issue_scores = [&]() {
-                const int ch = asked++, st = ch % kQStages;
-                const uint32_t k_s = kv_s + st * 2 * Q::TILE, d = tmem + ch % Q::NSB * Q::NS;
-                if (ok) ok = mbar_wait(&k_full[st], (ch / kQStages) & 1);
-                fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
-#pragma unroll
-                for (int k = 0; k < D / 32 * (Q::FOLD ? Q::PQ : 1); ++k)
-                    umma_e4m3(d, line_desc(k_s + k % (D / 32) * 32, D),
-                              line_desc(q_s + k / (D / 32) * ROWS * D + k % (D / 32) * 32, D), id_s, k > 0);
-                umma_commit(&s_full[ch % Q::NSB]);
-                umma_commit(&k_empty[st]);
-                mbar_arrive(&s_full[ch % Q::NSB]);  // passes on the scales' arrival, too
-            };
-            if (n_chunks > 0) issue_scores();
-            for (int ch = 0; ch < n_chunks; ++ch) {
-                const int st = ch % kQStages;
-                const uint32_t v_s = kv_s + (st * 2 + 1) * Q::TILE;
-                // with room for two, the next scores go out before this chunk's probabilities are there if its keys are
-                if (Q::NSB == 2 && asked < n_chunks && mbar_done(&k_full[asked % kQStages], (asked / kQStages) & 1))
-                    issue_scores();
-                if (ok) ok = mbar_wait(&p_full, ch & 1);
-                tc_fence_after();
-                if (Q::NSB == 1 && asked < n_chunks) issue_scores();
-                if (ok) ok = mbar_wait(&v_full[st], (ch / kQStages) & 1);
-                fence_async_smem();
-#pragma unroll
-                for (int k = 0; k < kQKeys / 32; ++k)
-                    umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k * D, D),
-                              line_desc(p_s + 32 * k * Q::W, Q::W, kQKeys * Q::W), id_o, k > 0);
-                umma_commit(&o_full);
-                umma_commit(&v_empty[st]);
-                if (Q::NSB == 2 && asked == ch + 1 && asked < n_chunks) issue_scores();
-            }
-            if (!ok) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
+        if (n_chunks > 0) {
+            tc_fence_before();
+            mbar_arrive(&q_full);
         }
-        __syncwarp();
-    } else if (!is_load) {
-        // ---- softmax and accumulation: a thread is key (then dim) `tid % 128` of the chunk
-        const int g = warp / 4, col0 = g * CW, key = tid % 128;
-        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
-        const float unit = q_unit * a.scale_log2;
         float acc[CW], l[CW];
 #pragma unroll
         for (int r = 0; r < CW; ++r) acc[r] = l[r] = 0.f;
         // adds the product of the chunk last sent to the tensor cores
         auto accumulate = [&](int ch) {
-            if (ok) ok = mbar_wait(&o_full, ch & 1);
+            if (ok) ok = mbar_wait(&o_full, (base + ch) & 1);
             tc_fence_after();
+            float v[3][16];
 #pragma unroll
-            for (int r0 = 0; r0 < CW; r0 += 16) {
-                float v[3][16];
+            for (int p = 0; p < 3; ++p) tmem_ld16(tmem + lanes + Q::O_COL + p * ROWS + col0, v[p]);
+            tmem_ld_wait(v[0], v[1], v[2]);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) tmem_ld16(tmem + lanes + Q::O_COL + p * ROWS + col0 + r0, v[p]);
-                tmem_ld_wait(v[0], v[1], v[2]);
+            for (int r = 0; r < 16; r += 2) {
+                float2 o = make_float2(acc[r], acc[r + 1]);
 #pragma unroll
-                for (int r = 0; r < 16; r += 2) {
-                    float2 o = make_float2(acc[r0 + r], acc[r0 + r + 1]);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        const float u = p == 0 ? 0x1p-6f : p == 1 ? 0x1p-12f : 0x1p-17f;
-                        o = __ffma2_rn(make_float2(v[p][r], v[p][r + 1]), make_float2(u, u), o);
-                    }
-                    acc[r0 + r] = o.x, acc[r0 + r + 1] = o.y;
+                for (int p = 0; p < 3; ++p) {
+                    const float u = p == 0 ? 0x1p-6f : p == 1 ? 0x1p-12f : 0x1p-17f;
+                    o = __ffma2_rn(make_float2(v[p][r], v[p][r + 1]), make_float2(u, u), o);
                 }
+                acc[r] = o.x, acc[r + 1] = o.y;
             }
         };
         for (int ch = 0; ch < n_chunks; ++ch) {
             const int t0 = first + ch * kQKeys, t = t0 + key;
             const bool masked = t0 + kQKeys - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window);
-            if (ok) ok = mbar_wait(&s_full[ch % Q::NSB], (ch / Q::NSB) & 1);
+            const int gc = base + ch;
+            if (ok) ok = mbar_wait(&s_full[gc % Q::NSB], (gc / Q::NSB) & 1);
             tc_fence_after();
-            const uint32_t s_col = tmem + lanes + ch % Q::NSB * Q::NS + col0;
-            const float ks = kv_scale[ch % 4][0][key] * unit, vs = t < last ? kv_scale[ch % 4][1][key] : 1.f, lv = __log2f(vs);
+            const uint32_t s_col = tmem + lanes + gc % Q::NSB * Q::NQ + col0;
+            const float ks = kv_scale[gc % 4][0][key] * unit, vs = t < last ? kv_scale[gc % 4][1][key] : 1.f, lv = __log2f(vs);
             // sixteen rows' scores of this key in log2 units, -inf where a row does not see it
-            auto scores = [&](int r0, float (&sc)[16]) {
-                float v[Q::FOLD ? 1 : Q::PQ - 1][16];
-                tmem_ld16(s_col + r0, sc);
-                if constexpr (!Q::FOLD) {
+            float sc[16];
+            {
+                float v[Q::PQ - 1][16];
+                tmem_ld16(s_col, sc);
 #pragma unroll
-                    for (int p = 1; p < Q::PQ; ++p) tmem_ld16(s_col + p * ROWS + r0, v[p - 1]);
-                    if constexpr (Q::PQ == 2)
-                        tmem_ld_wait(sc, v[0]);
-                    else
-                        tmem_ld_wait(sc, v[0], v[1]);
-                } else {
-                    tmem_ld_wait(sc);
-                }
+                for (int p = 1; p < Q::PQ; ++p) tmem_ld16(s_col + p * ROWS, v[p - 1]);
+                if constexpr (Q::PQ == 2)
+                    tmem_ld_wait(sc, v[0]);
+                else
+                    tmem_ld_wait(sc, v[0], v[1]);
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) {
                     float2 z = make_float2(sc[r], sc[r + 1]);
-                    if constexpr (!Q::FOLD) {
 #pragma unroll
-                        for (int p = 1; p < Q::PQ; ++p) {
-                            const float u = p == 1 ? 0x1p-5f : 0x1p-10f;
-                            z = __ffma2_rn(make_float2(v[p - 1][r], v[p - 1][r + 1]), make_float2(u, u), z);
-                        }
+                    for (int p = 1; p < Q::PQ; ++p) {
+                        const float u = p == 1 ? 0x1p-5f : 0x1p-10f;
+                        z = __ffma2_rn(make_float2(v[p - 1][r], v[p - 1][r + 1]), make_float2(u, u), z);
                     }
                     z = __fmul2_rn(z, make_float2(ks, ks));
                     sc[r] = z.x, sc[r + 1] = z.y;
                 }
-                if (masked) {
+            }
+            if (masked) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int pos = pos_s[col0 + r0 + r];
-                        if (t > pos || (a.window > 0 && t <= pos - a.window)) sc[r] = -INFINITY;
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    const int pos = pos_s[col0 + r];
+                    if (t > pos || (a.window > 0 && t <= pos - a.window)) sc[r] = -INFINITY;
                 }
-            };
-            // does a row's w leave the range that its reference covers, w > M + 1? 64-row tiles read the scores from
-            // TMEM twice rather than hold them
-            float kept[16], over = -INFINITY;
+            }
+            // does a row's w leave the range that its reference covers, w > M + 1?
+            float over = -INFINITY;
 #pragma unroll
-            for (int r0 = 0; r0 < CW; r0 += 16) {
-                scores(r0, kept);
-#pragma unroll
-                for (int r = 0; r < 16; r += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(&m_neg[col0 + r0 + r]);
-                    const float2 d = __fadd2_rn(make_float2(kept[r], kept[r + 1]), make_float2(m.x, m.y));
-                    const float2 e = __fadd2_rn(make_float2(kept[r + 2], kept[r + 3]), make_float2(m.z, m.w));
-                    over = fmaxf(over, fmaxf(fmaxf(d.x, d.y), fmaxf(e.x, e.y)));
-                }
+            for (int r = 0; r < 16; r += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(&m_neg[col0 + r]);
+                const float2 d = __fadd2_rn(make_float2(sc[r], sc[r + 1]), make_float2(m.x, m.y));
+                const float2 e = __fadd2_rn(make_float2(sc[r + 2], sc[r + 3]), make_float2(m.z, m.w));
+                over = max3(max3(over, d.x, d.y), e.x, e.y);
             }
             if (ch > 0) accumulate(ch - 1);
             if (bar_or(1 + g, 128, over + lv > 1.f)) {
+                float top = -INFINITY;
 #pragma unroll
-                for (int r0 = 0; r0 < CW; r0 += 16) {
-                    if constexpr (Q::FOLD) scores(r0, kept);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float m = redux_max(kept[r] + lv);
-                        if (lane == r) top = m;
-                    }
-                    if (lane < 16 && top > -INFINITY) atomicMax(&m_key[col0 + r0 + lane], orderable(top));
+                for (int r = 0; r < 16; ++r) {
+                    const float m = redux_max(sc[r] + lv);
+                    if (lane == r) top = m;
                 }
+                if (lane < 16) top_s[warp % 4][col0 + lane] = top;
                 named_bar_sync(1 + g, 128);
                 if (key < CW) {
-                    const uint32_t k = m_key[col0 + key];
-                    const float now = __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), was = -m_neg[col0 + key];
-                    const bool moves = k != 0 && now > was + 1.f;
+                    const int k = col0 + key;
+                    const float now = fmaxf(fmaxf(top_s[0][k], top_s[1][k]), fmaxf(top_s[2][k], top_s[3][k])), was = -m_neg[k];
+                    const bool moves = now > was + 1.f;
                     // without a reference so far l holds keys of scale 0 alone, counted from 0
-                    m_step[col0 + key] = moves ? ex2(fminf((was == kQNoRef ? 0.f : was) - now, 120.f)) : 1.f;
-                    if (moves) m_neg[col0 + key] = -now;
+                    m_step[k] = moves ? ex2(fminf((was == kQNoRef ? 0.f : was) - now, 120.f)) : 1.f;
+                    if (moves) m_neg[k] = -now;
                 }
                 named_bar_sync(1 + g, 128);
+                if (ch > 0) {
 #pragma unroll
-                for (int r = 0; r < CW; r += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(&m_step[col0 + r]);
-                    acc[r] *= f.x, acc[r + 1] *= f.y, acc[r + 2] *= f.z, acc[r + 3] *= f.w;
-                    l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+                    for (int r = 0; r < 16; r += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&m_step[col0 + r]);
+                        acc[r] *= f.x, acc[r + 1] *= f.y, acc[r + 2] *= f.z, acc[r + 3] *= f.w;
+                        l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+                    }
                 }
             }
             // x = 64 p as planes; a line of P holds this key's values of every row and plane. l takes x / (64 vs); keys
@@ -614,46 +743,47 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             const float lv6 = lv + 6.f;
             const bool small = __any_sync(0xffffffffu, !(vs >= 0x1p-60f));
             const float to_l = small ? 0.f : __fdividef(0x1p-6f, vs);
+            if (small) {
 #pragma unroll
-            for (int r0 = 0; r0 < CW; r0 += 16) {
-                if constexpr (Q::FOLD) scores(r0, kept);
-                if (small) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float m = m_neg[col0 + r0 + r];
-                        l[r0 + r] += ex2(kept[r] + (m == -kQNoRef ? 0.f : m));
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    const float m = m_neg[col0 + r];
+                    l[r] += ex2(sc[r] + (m == -kQNoRef ? 0.f : m));
                 }
-                uint32_t w[Q::PP][8];
+            }
+            uint32_t w[Q::PP][4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int r = r0 + 2 * j;
-                    const float2 m = *reinterpret_cast<const float2 *>(&m_neg[col0 + r]);
+            for (int j = 0; j < 4; ++j) {
+                const float4 m = *reinterpret_cast<const float4 *>(&m_neg[col0 + 4 * j]);
+                uint32_t x[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 4 * j + 2 * i;
                     // (s - M) + log2 vs: the first difference is small where it matters
-                    const float2 e = __fadd2_rn(__fadd2_rn(make_float2(kept[2 * j], kept[2 * j + 1]), m), make_float2(lv6, lv6));
-                    const float2 x2 = make_float2(ex2(e.x), ex2(e.y));
+                    const float2 d = __fadd2_rn(make_float2(sc[r], sc[r + 1]), i ? make_float2(m.z, m.w) : make_float2(m.x, m.y));
+                    const float2 e = __fadd2_rn(d, make_float2(lv6, lv6)), x2 = make_float2(ex2(e.x), ex2(e.y));
                     const float2 n = __ffma2_rn(x2, make_float2(to_l, to_l), make_float2(l[r], l[r + 1]));
                     l[r] = n.x, l[r + 1] = n.y;
-                    uint32_t x = f16x2(x2.x, x2.y);
-#pragma unroll
-                    for (int p = 0; p < Q::PP; ++p) {
-                        w[p][j] = e4m3_of_f16x2(x);
-                        if (p + 1 < Q::PP) x = hscale2_u(hsub2_u(x, f16x2_of_e4m3(w[p][j])), p == 0 ? 64.f : 32.f);
-                    }
+                    x[i] = f16x2(x2.x, x2.y);
                 }
 #pragma unroll
                 for (int p = 0; p < Q::PP; ++p) {
-                    const int byte = p * ROWS + col0 + r0;
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     p_s + byte / Q::W * (kQKeys * Q::W) + line_offset(key, byte % Q::W, Q::W)),
-                                 "r"(w[p][0] | w[p][1] << 16), "r"(w[p][2] | w[p][3] << 16), "r"(w[p][4] | w[p][5] << 16),
-                                 "r"(w[p][6] | w[p][7] << 16)
-                                 : "memory");
+                    w[p][j] = e4m3_of_f16x4(x[0], x[1]);
+                    if (p + 1 < Q::PP) {
+                        uint32_t lo, hi;
+                        f16x4_of_e4m3(w[p][j], lo, hi);
+                        x[0] = hscale2_u(hsub2_u(x[0], lo), p == 0 ? 64.f : 32.f);
+                        x[1] = hscale2_u(hsub2_u(x[1], hi), p == 0 ? 64.f : 32.f);
+                    }
                 }
             }
+#pragma unroll
+            for (int p = 0; p < Q::PP; ++p)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_s + line_offset(key, p * ROWS + col0, Q::W)),
+                             "r"(w[p][0]), "r"(w[p][1]), "r"(w[p][2]), "r"(w[p][3])
+                             : "memory");
             if (t0 + kQKeys > last) {  // slots behind the sequence may hold anything, and 0 times a NaN is none
-                const int st = ch % kQStages;
-                if (ok) ok = mbar_wait(&v_full[st], (ch / kQStages) & 1);
+                const int st = gc % kQStages;
+                if (ok) ok = mbar_wait(&v_full[st], (gc / kQStages) & 1);
                 if (t >= last)
                     for (int j = g; j < D / 16; j += Q::WG)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(kv_s + (st * 2 + 1) * Q::TILE + key * D + j * 16),
@@ -664,53 +794,41 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             tc_fence_before();
             mbar_arrive(&p_full);
         }
+        // the next unit's queries are asked for before this one's last product is in
+        asked_q = false;
+        if (mbar_done(&unit_full[(unit_no + 1) % 2], (unit_no + 1) / 2 & 1)) {
+            const QUnit &next = unit_s[(unit_no + 1) % 2];
+            if (next.state == kUnitRows) {
+                ask_q(next);
+                asked_q = true;
+            }
+        }
         if (n_chunks > 0) accumulate(n_chunks - 1);
         if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         // ---- sums over the keys, and the rows out
-#pragma unroll
-        for (int r0 = 0; r0 < CW; r0 += 16) {
-            float sum[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sum[r] = l[r0 + r];
-            const float mine = transpose_sum16(sum, lane);
-            if (lane < 16) l_s[warp % 4][col0 + r0 + lane] = mine;
-        }
+        const float mine = transpose_sum16(l, lane);
+        if (lane < 16) l_s[warp % 4][col0 + lane] = mine;
         named_bar_sync(1 + g, 128);
         const int rows = min(CW, n_rows - col0);
-        QRow w = row_of(col0);
-        if (whole) {
-            if (key < D) {
-                T *dst = out + w.row * a.out_stride + w.hq * D + key;
-                const long long next = a.out_stride - grp * D;  // from past a row's last head to the next row's first
-                int left = grp - (w.hq - h * grp);
+        if (key < D) {
+            if (u.whole) {
 #pragma unroll
                 for (int r = 0; r < CW; ++r) {
                     const int k = col0 + r;
                     const float total = (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]);
-                    if (r < rows) *dst = from_f32<T>(total == 0.f ? 0.f : __fdividef(acc[r], total));
-                    dst += D;
-                    if (--left == 0) dst += next, left = grp;
+                    if (r < rows) out[to_s[k] + key] = from_f32<T>(total == 0.f ? 0.f : __fdividef(acc[r], total));
                 }
-            }
-        } else {
-            if (key < D) {
-                const size_t step = static_cast<size_t>(a.splits) * D;
-                float *dst = a.part_o + (qattn_slot(a, b, w.i, w.hq) + split) * D + key;
-                const size_t next = (a.nq - grp) * step;
-                int left = grp - (w.hq - h * grp);
+            } else {
 #pragma unroll
-                for (int r = 0; r < CW; ++r) {
-                    if (r < rows) *dst = acc[r];
-                    dst += step;
-                    if (--left == 0) dst += next, left = grp;
-                }
+                for (int r = 0; r < CW; ++r)
+                    if (r < rows) a.part_o[to_s[col0 + r] + key] = acc[r];
             }
-            if (key < rows) {
-                const int k = col0 + key;
-                w = row_of(k);
-                a.part_ml[qattn_slot(a, b, w.i, w.hq) + split] =
-                    make_float2(-m_neg[k], (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]));
-            }
+        }
+        if (!u.whole && key < rows) {
+            const int k = col0 + key;
+            a.part_ml[to_s[k] / D] = make_float2(-m_neg[k], (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]));
+        }
+        base += n_chunks;
         }
         tc_fence_before();
     }
@@ -720,21 +838,22 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
 
 constexpr int kQMergeThreads = 128;
 
-// A CTA joins the parts of one (row, q head): o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i, every fourth part a
-// warp, the four in order. Grid (span row x head, sequence).
-template <typename T, int D>
-__global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs a) {
-    constexpr int V = D / 32, NW = kQMergeThreads / 32;
-    const int b = blockIdx.y, i = a.by_nq.div(blockIdx.x), hq = blockIdx.x - i * a.nq;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+// NW warps join the parts of one (row, q head): o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i, every NW-th part a
+// warp, the warps in order. NW = 1 up to eight parts (the loads that a warp has under way), else 4.
+// Grid (span row x head in groups of 4 / NW, sequence).
+template <typename T, int D, int NW>
+__global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(const __grid_constant__ QAttnArgs a) {
+    constexpr int V = D / 32;
+    const int warp = threadIdx.x / 32 % NW, lane = threadIdx.x % 32;
+    const int b = blockIdx.y, item = blockIdx.x * (kQMergeThreads / 32 / NW) + threadIdx.x / 32 / NW;
+    const int i = a.by_nq.div(item), hq = item - i * a.nq;
     // the spans are no results of the attention before it, which started after whatever wrote them
     const QSpan s = qcache_span(a.c, b);
-    const int L = s.p0 + s.S, keys = qattn_part_keys(a, max(L, 1));
-    const int parts = (L + keys - 1) / keys;
+    const int parts = qattn_cut(a, s.p0, max(s.S, 1)).parts;
     __shared__ float o_s[NW][D], l_s;
     pdl_wait();  // in every CTA: this kernel's end stands for the attention's, too
     pdl_trigger();
-    if (i >= s.S || keys >= L) return;
+    if (i >= s.S || parts == 1) return;
     const size_t slot = qattn_slot(a, b, i, hq);
     // parts without a key of this row hold M = kQNoRef, l = 0, o = 0
     float m = kQNoRef;
@@ -744,14 +863,15 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs 
     float o[V], l = 0.f;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] = 0.f;
-    // 32 parts at a time: a lane weighs one, the warp's eight are read at once
-    for (int p0 = 0; p0 < parts; p0 += 32) {
-        const float2 ml = p0 + lane < parts ? a.part_ml[slot + p0 + lane] : make_float2(kQNoRef, 0.f);
+    // 32 parts (8 for one warp) at a time: a lane weighs one, the warp's eight are read at once
+    constexpr int P = 8 * NW;
+    for (int p0 = 0; p0 < parts; p0 += P) {
+        const float2 ml = lane < P && p0 + lane < parts ? a.part_ml[slot + p0 + lane] : make_float2(kQNoRef, 0.f);
         // l > 0 without a reference: keys of scale 0 alone, counted from 0
         const float mine = ml.y == 0.f ? 0.f : ex2(fminf((ml.x == kQNoRef ? 0.f : ml.x) - m, 120.f));
-        float v[32 / NW][V];
+        float v[8][V];
 #pragma unroll
-        for (int j = 0; j < 32 / NW; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const int p = p0 + warp + j * NW;
 #pragma unroll
             for (int d = 0; d < V; ++d) v[j][d] = 0.f;
@@ -764,21 +884,27 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(QAttnArgs 
             }
         }
 #pragma unroll
-        for (int j = 0; j < 32 / NW; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const float f = __shfl_sync(0xffffffffu, mine, warp + j * NW);
 #pragma unroll
             for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[j][d], o[d]);
         }
         if (warp == 0) l += warp_sum(mine * ml.y);
     }
+    T *dst = static_cast<T *>(a.out) + (s.r0 + i) * a.out_stride + hq * D;
+    if constexpr (NW == 1) {
 #pragma unroll
-    for (int d = 0; d < V; ++d) o_s[warp][lane * V + d] = o[d];
-    if (threadIdx.x == 0) l_s = l;
-    __syncthreads();
-    const int d = threadIdx.x;
-    if (d < D) {
-        const float num = (o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d]), den = l_s;
-        static_cast<T *>(a.out)[(s.r0 + i) * a.out_stride + hq * D + d] = from_f32<T>(den == 0.f ? 0.f : num / den);
+        for (int d = 0; d < V; ++d) dst[lane * V + d] = from_f32<T>(l == 0.f ? 0.f : o[d] / l);
+    } else {
+#pragma unroll
+        for (int d = 0; d < V; ++d) o_s[warp][lane * V + d] = o[d];
+        if (threadIdx.x == 0) l_s = l;
+        __syncthreads();
+        const int d = threadIdx.x;
+        if (d < D) {
+            const float num = (o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d]);
+            dst[d] = from_f32<T>(l_s == 0.f ? 0.f : num / l_s);
+        }
     }
 }
 
