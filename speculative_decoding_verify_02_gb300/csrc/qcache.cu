@@ -136,9 +136,9 @@ bool aligned16(const void *p, int64_t stride, int dtype) {
 bool element_aligned(const void *p, int dtype) { return reinterpret_cast<uintptr_t>(p) % dtype_size(dtype) == 0; }
 
 // ---- attention: tile rows, parts of a sequence and workspace
-// Rows of a tile: 16 or 32, the smaller that holds a span's rows of one kv head. Tiles of 64 rows halved the reads of
-// long spans' keys, but their two-fold rows a thread spilled: 128 rows at 32K took 288 us against 240.
-int attn_rows(int span_rows) { return span_rows <= 16 ? 16 : 32; }
+// Rows of a tile: 16, 32 or 64, the smallest that holds a span's rows of one kv head. Long spans read every key once a
+// tile, out of L2: with tiles of 32 rows, two CTAs an SM waited for keys a third of the time (128 rows at 32K: 225 us).
+int attn_rows(int span_rows) { return span_rows <= 16 ? 16 : span_rows <= 32 ? 32 : 64; }
 
 struct AttnPlan {
     int rows, tiles, splits, ctas;
@@ -148,16 +148,16 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span) {
     const int span_rows = max_span * (q->c.n_q_heads / q->c.n_kv_heads);
     p.rows = attn_rows(span_rows);
     p.tiles = cdiv(span_rows, p.rows);
-    p.ctas = 2 * q->sm_count;
+    p.ctas = (p.rows == 64 ? 1 : 2) * q->sm_count;
     const long long units = static_cast<long long>(B) * q->c.n_kv_heads * p.tiles;
     const int waves = B > 1 ? QWB : QW1;
-    const long long s = 2LL * q->sm_count * waves / units;
+    const long long s = static_cast<long long>(p.ctas) * waves / units;
     p.splits = static_cast<int>(std::max(1LL, std::min<long long>(s, cdiv(q->c.max_context, kQKeys))));
     return p;
 }
 
 // Floats of attention's partial results: rows x heads x splits of the largest call, D + 2 each. splits >= 2 only
-// while B nkv tiles splits <= 2 SMs x waves, and a tile holds at most 32 rows.
+// while B nkv tiles splits <= 2 SMs x waves, and a tile holds at most 64 rows (of half as many CTAs).
 size_t attn_partials(const sdv_qcache_cfg &c, int sm_count) {
     const size_t all = static_cast<size_t>(c.max_batch) * c.max_span * c.n_q_heads * cdiv(c.max_context, kQKeys);
     const size_t cut = static_cast<size_t>(2) * sm_count * kQWaves * 32;
@@ -178,6 +178,7 @@ int launch_attn_rows(const CUtensorMap &pool, const QAttnArgs &a, const AttnPlan
 template <typename T, int D>
 int launch_attn(const CUtensorMap &pool, const QAttnArgs &a, const AttnPlan &p, void *stream) {
     if (p.rows == 16) return launch_attn_rows<T, D, 16>(pool, a, p, stream);
+    if (p.rows == 64) return launch_attn_rows<T, D, 64>(pool, a, p, stream);
     return launch_attn_rows<T, D, 32>(pool, a, p, stream);
 }
 
@@ -199,6 +200,7 @@ cudaError_t set_attn_all() {
     if (e == cudaSuccess) e = set_carveout(qcache_merge_kernel<T, D, 4>);
     if (e == cudaSuccess) e = set_attn<T, D, 16>();
     if (e == cudaSuccess) e = set_attn<T, D, 32>();
+    if (e == cudaSuccess) e = set_attn<T, D, 64>();
     return e;
 }
 

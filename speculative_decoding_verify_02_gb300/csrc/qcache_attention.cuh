@@ -47,7 +47,6 @@ struct QAttnArgs {
 };
 
 constexpr int kQKeys = 128;     // keys of a chunk
-constexpr int kQStages = 2;     // chunks in shared memory
 constexpr float kQNoRef = -1e30f;  // a row's M before it has seen a key: below any w, and w - M is no NaN
 template <typename T, int D_, int ROWS_>
 struct QTile {
@@ -56,18 +55,21 @@ struct QTile {
     static constexpr int PP = 3;                                                  // planes of p
     static constexpr int CW = 16, WG = ROWS / CW;                                 // columns of a softmax warpgroup
     static constexpr int NQ = PQ * ROWS, NP = PP * ROWS;                          // widths of the two products
-    static constexpr int W = NP <= 64 ? 64 : 128;                                 // bytes of a key's P line
+    static constexpr int CTAS = ROWS == 64 ? 1 : 2, STAGES = ROWS == 64 ? 4 : 2;  // CTAs an SM, chunks in a CTA's memory
+    static constexpr int W = ROWS == 32 ? 128 : 64, P_ATOMS = (NP + W - 1) / W;   // bytes of a key's P line, lines a key
     static constexpr int TILE = kQKeys * D;                                       // bytes of a K or V chunk
-    static constexpr int Q_BYTES = (NQ * D + 1023) / 1024 * 1024, P_BYTES = kQKeys * W;
-    static constexpr int SMEM = 1024 + kQStages * 2 * TILE + Q_BYTES + P_BYTES;
-    static constexpr int NSB = 2 * NQ + NP <= 256 ? 2 : 1;                        // S^T of the next chunk beside this one's
+    static constexpr int Q_BYTES = (NQ * D + 1023) / 1024 * 1024, P_BYTES = kQKeys * W * P_ATOMS;
+    static constexpr int SMEM = 1024 + STAGES * 2 * TILE + Q_BYTES + P_BYTES;
+    static constexpr int SCALES = 2 * STAGES;  // chunks of scales: loads run STAGES ahead of the scores, those two of softmax
+    static constexpr int TMEM = 512 / CTAS;
+    static constexpr int NSB = 2 * NQ + NP <= TMEM ? 2 : 1;                       // S^T of the next chunk beside this one's
     static constexpr int O_COL = (NSB * NQ + 31) / 32 * 32;                       // TMEM column of O^T
-    static constexpr int COLS = O_COL + NP <= 128 ? 128 : 256;
+    static constexpr int COLS = O_COL + NP <= 128 ? 128 : O_COL + NP <= 256 ? 256 : 512;
     static constexpr int THREADS = WG * 128 + 64;  // softmax warps, the load warp, the MMA warp
-    static_assert(ROWS == 16 || ROWS == 32, "tile rows");
-    static_assert(O_COL + NP <= COLS, "TMEM columns");
+    static_assert(ROWS == 16 || ROWS == 32 || ROWS == 64, "tile rows");
+    static_assert(COLS <= TMEM && O_COL + NP <= COLS, "TMEM columns");
     static_assert(NQ % 16 == 0 && NP % 16 == 0, "MMA widths");
-    static_assert(2 * (SMEM + 6144 + 1024) <= 228 * 1024, "two CTAs per SM");
+    static_assert(CTAS * (SMEM + 6400 + (SCALES - 4) * 1024 + 1024) <= 228 * 1024, "CTAs per SM");
 };
 
 // ------------------------------------------------------------------ PTX
@@ -87,10 +89,10 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn) {
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 // Matrix descriptor over lines of `width` bytes (64 or 128) with that width's swizzle, eight lines to an
-// atom. The offset between atoms side by side is 0: operands are one atom wide, but for V at D = 64, whose
-// dims so fill both halves of the 128 lanes (the upper half is not read).
-__device__ __forceinline__ uint64_t line_desc(uint32_t addr, int width) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(8 * width >> 4) << 32 |
+// atom; `beside` bytes on lie the atoms that continue the lines (0: the same atom again, so that the 64
+// dims of V at D = 64 fill both halves of the 128 lanes, of which the upper is not read).
+__device__ __forceinline__ uint64_t line_desc(uint32_t addr, int width, uint32_t beside = 0) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(beside >> 4) << 16 | static_cast<uint64_t>(8 * width >> 4) << 32 |
            static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(width == 128 ? 2 : 4) << 61;
 }
 // Byte offset of (line, byte) under that swizzle, in a buffer aligned to 1024 bytes.
@@ -268,7 +270,7 @@ struct QUnit {
 constexpr uint64_t kQUnitWaitNs = 10 * kWaitLimitNs;  // above any sum of the waits that a unit's end depends on
 
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_kernel(
+__global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>::CTAS) qcache_attn_kernel(
     const __grid_constant__ CUtensorMap pool, const __grid_constant__ QAttnArgs a) {
     typedef QTile<T, D, ROWS> Q;
     constexpr int CW = Q::CW;
@@ -277,8 +279,8 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     const int grp = a.grp;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t kv_s = smem, q_s = smem + kQStages * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
-    __shared__ uint64_t k_full[kQStages], k_empty[kQStages], v_full[kQStages], v_empty[kQStages], s_full[2], p_full, o_full;
+    const uint32_t kv_s = smem, q_s = smem + Q::STAGES * 2 * Q::TILE, p_s = q_s + Q::Q_BYTES;
+    __shared__ uint64_t k_full[Q::STAGES], k_empty[Q::STAGES], v_full[Q::STAGES], v_empty[Q::STAGES], s_full[2], p_full, o_full;
     __shared__ uint32_t tmem_s;
     __shared__ __align__(16) float m_neg[ROWS], m_step[ROWS];  // -M of each row, and 2^(M before - M) where M last moved
     __shared__ int pos_s[ROWS];
@@ -286,18 +288,18 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
     __shared__ float top_s[4][ROWS], l_s[4][ROWS], amax_s[2][Q::WG * 4];
     __shared__ uint64_t unit_full[2], unit_empty[2], q_full;
     __shared__ QUnit unit_s[2];
-    __shared__ float kv_scale[4][2][kQKeys];  // four chunks deep: softmax may still read the one two back
+    __shared__ float kv_scale[Q::SCALES][2][kQKeys];
     const bool is_load = warp == Q::WG * 4, is_mma = warp == Q::WG * 4 + 1;
     // what needs no data goes before the wait for the kernel ahead
     if (tid == 0) {
-        for (int i = 0; i < kQStages; ++i) {
+        for (int i = 0; i < Q::STAGES; ++i) {
             mbar_init(&k_full[i], 33);
             mbar_init(&v_full[i], 33);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_empty[i], 1);
-            mbar_init(&s_full[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 2);
             mbar_init(&unit_full[i], 1);
             mbar_init(&unit_empty[i], Q::WG * 128 + 1);
         }
@@ -332,28 +334,30 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
 
     // ---- the load warp: a chunk's K rows with both scales, then its V rows. Pages of a multiple of eight tokens come in
     // TMA boxes, a lane a box (a box past the pool is zeros); others in 16-byte pieces.
-    uint32_t rows[4], sc_at[4];  // pool rows and scales of this lane's four keys of a chunk
-    int box = 0;                 // pool row of its box
-    auto look = [&](const QUnit &u, int ch) {
-        // the five page-table entries first, so that their latencies pass together; keys past the last read its entry
+    int at[5], page[5];          // page-table slots and entries of this lane's four keys of a chunk and of its box
+    uint32_t rows[4], sc_at[4];  // pool rows and scales of the keys
+    int box = 0;                 // pool row of the box
+    auto ask = [&](const QUnit &u, int ch) {  // keys past the last read its entry
         const int *table = c.page_table + static_cast<size_t>(u.b) * c.pages_per_seq;
-        const int h = u.h, last = u.last, t0 = u.first + ch * kQKeys, tb = t0 + lane % 16 * a.box_rows;
-        const bool has_box = lane % 16 * a.box_rows < kQKeys && tb < last;
-        int at[5], page[5];
+        const int t0 = u.first + ch * kQKeys;
 #pragma unroll
         for (int j = 0; j < 5; ++j) {
-            at[j] = c.by_page.div(min(j < 4 ? t0 + j * 32 + lane : tb, last - 1));
+            at[j] = c.by_page.div(min(t0 + (j < 4 ? j * 32 + lane : lane % 16 * a.box_rows), u.last - 1));
             page[j] = table[at[j]];
         }
+    };
+    auto place = [&](const QUnit &u, int ch) {
+        const int t0 = u.first + ch * kQKeys, tb = t0 + lane % 16 * a.box_rows;
         box = a.pool_rows;
-        if (has_box && page[4] >= 0 && page[4] < c.n_pages) box = (page[4] * 2 * c.nkv + h) * c.page_size + tb - at[4] * c.page_size;
+        if (lane % 16 * a.box_rows < kQKeys && tb < u.last && page[4] >= 0 && page[4] < c.n_pages)
+            box = (page[4] * 2 * c.nkv + u.h) * c.page_size + tb - at[4] * c.page_size;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t = t0 + j * 32 + lane;
             rows[j] = 0xffffffffu;
-            if (t < last) {
+            if (t < u.last) {
                 if (page[j] >= 0 && page[j] < c.n_pages) {
-                    const uint32_t ph = static_cast<uint32_t>(page[j]) * 2 * c.nkv + h, slot = t - at[j] * c.page_size;
+                    const uint32_t ph = static_cast<uint32_t>(page[j]) * 2 * c.nkv + u.h, slot = t - at[j] * c.page_size;
                     rows[j] = ph * c.page_size + slot;
                     sc_at[j] = ph * c.blocks + c.by_block.div(slot);
                 } else {
@@ -363,18 +367,14 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         }
     };
     const int v_rows = c.nkv * c.page_size;
-    // lanes 0 to 15 bring K's boxes, 16 to 31 V's
-    auto load_half = [&](int ch, bool v) {
-        const int st = ch % kQStages;
-        const uint32_t dst = kv_s + (st * 2 + (v ? 1 : 0)) * Q::TILE;
-        uint64_t *full = v ? &v_full[st] : &k_full[st];
-        if (ch >= kQStages && ok) ok = mbar_wait(v ? &v_empty[st] : &k_empty[st], (ch / kQStages - 1) & 1);
+    // the K (or V) rows of a chunk into its stage: lanes 0 to 15 bring K's boxes, 16 to 31 V's
+    auto copy = [&](uint32_t dst, uint64_t *full, bool v, int box_row, const uint32_t (&row)[4]) {
         if (a.box_rows) {
             if (lane == 0) mbar_arrive_expect_tx(full, Q::TILE);
             __syncwarp();
             const int n = lane % 16;
             if (lane / 16 == (v ? 1 : 0) && n * a.box_rows < kQKeys)
-                load_box(dst + n * a.box_rows * D, &pool, full, box + (v && box < a.pool_rows ? v_rows : 0));
+                load_box(dst + n * a.box_rows * D, &pool, full, box_row + (v && box_row < a.pool_rows ? v_rows : 0));
         } else {
             constexpr int PPR = D / 16, RPI = 32 / PPR;  // pieces a row, rows a copy
             const uint8_t *codes = c.codes + lane % PPR * 16 + (v ? static_cast<size_t>(v_rows) * D : 0);
@@ -382,23 +382,32 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             for (int g = 0; g < 4; ++g)
                 for (int j = 0; j < 32 / RPI; ++j) {
                     const int r = j * RPI + lane / PPR;
-                    const uint32_t row = __shfl_sync(0xffffffffu, rows[g], r);
-                    const bool in = row != 0xffffffffu;
+                    const uint32_t from = __shfl_sync(0xffffffffu, row[g], r);
+                    const bool in = from != 0xffffffffu;
                     cp_async16(dst + line_offset(g * 32 + r, lane % PPR * 16, D),
-                               in ? codes + static_cast<size_t>(row) * D : c.codes, in);
+                               in ? codes + static_cast<size_t>(from) * D : c.codes, in);
                 }
             if (lane == 0) mbar_arrive(full);
         }
-        if (!v) {
+    };
+    auto load_k = [&](int chunk) {
+        const int st = chunk % Q::STAGES;
+        if (chunk >= Q::STAGES && ok) ok = mbar_wait(&k_empty[st], (chunk / Q::STAGES - 1) & 1);
+        copy(kv_s + st * 2 * Q::TILE, &k_full[st], false, box, rows);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = rows[j] != 0xffffffffu;
-                const float *sc = c.scales + (in ? sc_at[j] : 0);
-                cp_async4(smem_u32(&kv_scale[ch % 4][0][j * 32 + lane]), sc, in);
-                cp_async4(smem_u32(&kv_scale[ch % 4][1][j * 32 + lane]), in ? sc + c.nkv * c.blocks : sc, in);
-            }
+        for (int j = 0; j < 4; ++j) {
+            const bool in = rows[j] != 0xffffffffu;
+            const float *sc = c.scales + (in ? sc_at[j] : 0);
+            cp_async4(smem_u32(&kv_scale[chunk % Q::SCALES][0][j * 32 + lane]), sc, in);
+            cp_async4(smem_u32(&kv_scale[chunk % Q::SCALES][1][j * 32 + lane]), in ? sc + c.nkv * c.blocks : sc, in);
         }
-        cp_async_arrive(full);
+        cp_async_arrive(&k_full[st]);
+    };
+    auto load_v = [&](int chunk, int box_row, const uint32_t (&row)[4]) {
+        const int st = chunk % Q::STAGES;
+        if (chunk >= Q::STAGES && ok) ok = mbar_wait(&v_empty[st], (chunk / Q::STAGES - 1) & 1);
+        copy(kv_s + (st * 2 + 1) * Q::TILE, &v_full[st], true, box_row, row);
+        cp_async_arrive(&v_full[st]);
     };
     if (is_load) {
         int n = blockIdx.x, chunk = 0, k = 0;
@@ -461,11 +470,23 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                 }
                 ++k;
                 if (u.state == kUnitRows) {
+                    // K a chunk ahead of V (its stages free up sooner), page-table entries a chunk ahead of K
                     const int n_chunks = chunks_of(u);
+                    if (n_chunks > 0) {
+                        ask(u, 0);
+                        place(u, 0);
+                        if (n_chunks > 1) ask(u, 1);
+                        load_k(chunk);
+                    }
                     for (int ch = 0; ch < n_chunks; ++ch, ++chunk) {
-                        look(u, ch);
-                        load_half(chunk, false);
-                        load_half(chunk, true);
+                        const int box_v = box;
+                        const uint32_t rows_v[4] = {rows[0], rows[1], rows[2], rows[3]};
+                        if (ch + 1 < n_chunks) {
+                            place(u, ch + 1);
+                            if (ch + 2 < n_chunks) ask(u, ch + 2);
+                            load_k(chunk + 1);
+                        }
+                        load_v(chunk, box_v, rows_v);
                     }
                 }
             }
@@ -483,9 +504,9 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (!ok) {  // no copy may land after this CTA's shared memory is someone else's
-            for (int i = max(0, chunk - kQStages); i < chunk; ++i) {
-                mbar_wait(&k_full[i % kQStages], (i / kQStages) & 1);
-                mbar_wait(&v_full[i % kQStages], (i / kQStages) & 1);
+            for (int i = max(0, chunk - Q::STAGES); i < chunk; ++i) {
+                mbar_wait(&k_full[i % Q::STAGES], (i / Q::STAGES) & 1);
+                mbar_wait(&v_full[i % Q::STAGES], (i / Q::STAGES) & 1);
             }
             if (lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         }
@@ -506,9 +527,9 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             const uint32_t id_s = idesc_e4m3(128, Q::NQ, false), id_o = idesc_e4m3(128, Q::NP, true);
             int asked = 0, base = 0;  // chunks whose scores have been issued; chunks of the units before
             auto issue_scores = [&]() {
-                const int ch = asked++, st = ch % kQStages;
+                const int ch = asked++, st = ch % Q::STAGES;
                 const uint32_t k_s = kv_s + st * 2 * Q::TILE, d = tmem + ch % Q::NSB * Q::NQ;
-                if (ok) ok = mbar_wait(&k_full[st], (ch / kQStages) & 1);
+                if (ok) ok = mbar_wait(&k_full[st], (ch / Q::STAGES) & 1);
                 fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
@@ -528,20 +549,30 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
                 tc_fence_after();
                 issue_scores();
                 for (int ch = base; ch < end; ++ch) {
-                    const int st = ch % kQStages;
+                    const int st = ch % Q::STAGES;
                     const uint32_t v_s = kv_s + (st * 2 + 1) * Q::TILE;
-                    // with room for two, the next scores go out before this chunk's probabilities are there if its keys are
-                    if (Q::NSB == 2 && asked < end && mbar_done(&k_full[asked % kQStages], (asked / kQStages) & 1))
-                        issue_scores();
-                    if (ok) ok = mbar_wait(&p_full, ch & 1);
+                    // with room for two, the next scores go out while this chunk's probabilities are awaited, as soon as
+                    // their keys are there (asking once only missed them by a little every time)
+                    if (ok) {
+                        const uint64_t since = globaltimer();
+                        while (!mbar_done(&p_full, ch & 1)) {
+                            if (Q::NSB == 2 && asked == ch + 1 && asked < end &&
+                                mbar_done(&k_full[asked % Q::STAGES], (asked / Q::STAGES) & 1))
+                                issue_scores();
+                            if (globaltimer() - since > kWaitLimitNs) {
+                                ok = false;
+                                break;
+                            }
+                        }
+                    }
                     tc_fence_after();
                     if (Q::NSB == 1 && asked < end) issue_scores();
-                    if (ok) ok = mbar_wait(&v_full[st], (ch / kQStages) & 1);
+                    if (ok) ok = mbar_wait(&v_full[st], (ch / Q::STAGES) & 1);
                     fence_async_smem();
 #pragma unroll
                     for (int k4 = 0; k4 < kQKeys / 32; ++k4)
                         umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k4 * D, D),
-                                  line_desc(p_s + 32 * k4 * Q::W, Q::W), id_o, k4 > 0);
+                                  line_desc(p_s + 32 * k4 * Q::W, Q::W, kQKeys * Q::W), id_o, k4 > 0);
                     umma_commit(&o_full);
                     umma_commit(&v_empty[st]);
                     if (Q::NSB == 2 && asked == ch + 1 && asked < end) issue_scores();
@@ -670,7 +701,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             if (ok) ok = mbar_wait(&s_full[gc % Q::NSB], (gc / Q::NSB) & 1);
             tc_fence_after();
             const uint32_t s_col = tmem + lanes + gc % Q::NSB * Q::NQ + col0;
-            const float ks = kv_scale[gc % 4][0][key] * unit, vs = t < last ? kv_scale[gc % 4][1][key] : 1.f, lv = __log2f(vs);
+            const float ks = kv_scale[gc % Q::SCALES][0][key] * unit, vs = t < last ? kv_scale[gc % Q::SCALES][1][key] : 1.f, lv = __log2f(vs);
             // sixteen rows' scores of this key in log2 units, -inf where a row does not see it
             float sc[16];
             {
@@ -778,12 +809,14 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, 2) qcache_attn_ker
             }
 #pragma unroll
             for (int p = 0; p < Q::PP; ++p)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_s + line_offset(key, p * ROWS + col0, Q::W)),
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 p_s + (p * ROWS + col0) / Q::W * (kQKeys * Q::W) +
+                                 line_offset(key, (p * ROWS + col0) % Q::W, Q::W)),
                              "r"(w[p][0]), "r"(w[p][1]), "r"(w[p][2]), "r"(w[p][3])
                              : "memory");
             if (t0 + kQKeys > last) {  // slots behind the sequence may hold anything, and 0 times a NaN is none
-                const int st = gc % kQStages;
-                if (ok) ok = mbar_wait(&v_full[st], (gc / kQStages) & 1);
+                const int st = gc % Q::STAGES;
+                if (ok) ok = mbar_wait(&v_full[st], (gc / Q::STAGES) & 1);
                 if (t >= last)
                     for (int j = g; j < D / 16; j += Q::WG)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(kv_s + (st * 2 + 1) * Q::TILE + key * D + j * 16),
