@@ -23,13 +23,11 @@ struct sdv_qcache {
 
 namespace {
 
-// Attention of a batch is cut into this many times the CTAs that fit at once (two per SM), so that sequences of
-// different lengths even out; a single sequence into just as many as fit.
-#ifndef QW1
-#define QW1 1
-#define QWB 2
+constexpr int kQWaves = 4;       // turns of the CTAs that an attention is cut into at most
+#ifndef QT
+#define QT 2.0
 #endif
-constexpr int kQWaves = QWB;
+constexpr double kQTurn = QT;   // what a turn costs besides its chunks, in chunks
 
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -143,16 +141,24 @@ int attn_rows(int span_rows) { return span_rows <= 16 ? 16 : span_rows <= 32 ? 3
 struct AttnPlan {
     int rows, tiles, splits, ctas;
 };
-AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span) {
+AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int window) {
     AttnPlan p;
     const int span_rows = max_span * (q->c.n_q_heads / q->c.n_kv_heads);
     p.rows = attn_rows(span_rows);
     p.tiles = cdiv(span_rows, p.rows);
     p.ctas = (p.rows == 64 ? 1 : 2) * q->sm_count;
+    // Parts: the number that the CTAs get through soonest at the cache's full context, in turns of a unit each; a turn
+    // costs its chunks and about kQTurn more for its queries, first maximum and results. What a sequence's parts are
+    // depends on its own length and on this number only.
     const long long units = static_cast<long long>(B) * q->c.n_kv_heads * p.tiles;
-    const int waves = B > 1 ? QWB : QW1;
-    const long long s = static_cast<long long>(p.ctas) * waves / units;
-    p.splits = static_cast<int>(std::max(1LL, std::min<long long>(s, cdiv(q->c.max_context, kQKeys))));
+    const int keys = window > 0 ? std::min(q->c.max_context, window + max_span) : q->c.max_context;
+    const int chunks = cdiv(keys, kQKeys);
+    double best = 0;
+    p.splits = 1;
+    for (int s = 1; s <= chunks && units * s <= static_cast<long long>(kQWaves) * p.ctas; ++s) {
+        const double t = static_cast<double>((units * s + p.ctas - 1) / p.ctas) * (cdiv(chunks, s) + kQTurn);
+        if (s == 1 || t < best) best = t, p.splits = s;
+    }
     return p;
 }
 
@@ -371,7 +377,7 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     a.window = window;
     a.q_vec = aligned16(d_q, q_stride, dtype);
     a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(D));
-    const AttnPlan p = attn_plan(cache, B, max_span);
+    const AttnPlan p = attn_plan(cache, B, max_span, window);
     const size_t slots = attn_partials(cache->c, cache->sm_count);
     a.splits = p.splits;
     a.tiles = p.tiles;
