@@ -24,10 +24,7 @@ struct sdv_qcache {
 namespace {
 
 constexpr int kQWaves = 4;       // turns of the CTAs that an attention is cut into at most
-#ifndef QT
-#define QT 2.0
-#endif
-constexpr double kQTurn = QT;   // what a turn costs besides its chunks, in chunks
+constexpr double kQTurn = 4;    // what a unit costs besides its chunks, in chunks (16 ragged sequences: 46 us with 1, 38 with 4)
 
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -147,16 +144,19 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int window) {
     p.rows = attn_rows(span_rows);
     p.tiles = cdiv(span_rows, p.rows);
     p.ctas = (p.rows == 64 ? 1 : 2) * q->sm_count;
-    // Parts: the number that the CTAs get through soonest at the cache's full context, in turns of a unit each; a turn
-    // costs its chunks and about kQTurn more for its queries, first maximum and results. What a sequence's parts are
-    // depends on its own length and on this number only.
+    // Parts: the number that the CTAs get through soonest at the cache's full context; a unit costs its chunks and about
+    // kQTurn more for its queries, first maximum and results. One sequence's units are alike and go in turns; a batch's
+    // differ, so that a CTA has its share of the work (of sequences 0.6 of the longest on average) and then waits for
+    // the longest unit. What a sequence's parts are depends on its own length and on this number only.
     const long long units = static_cast<long long>(B) * q->c.n_kv_heads * p.tiles;
     const int keys = window > 0 ? std::min(q->c.max_context, window + max_span) : q->c.max_context;
     const int chunks = cdiv(keys, kQKeys);
     double best = 0;
     p.splits = 1;
     for (int s = 1; s <= chunks && units * s <= static_cast<long long>(kQWaves) * p.ctas; ++s) {
-        const double t = static_cast<double>((units * s + p.ctas - 1) / p.ctas) * (cdiv(chunks, s) + kQTurn);
+        const double unit = cdiv(chunks, s) + kQTurn;
+        const double t = B == 1 ? static_cast<double>((units * s + p.ctas - 1) / p.ctas) * unit
+                                : units * (0.6 * chunks + s * kQTurn) / p.ctas + unit;
         if (s == 1 || t < best) best = t, p.splits = s;
     }
     return p;
