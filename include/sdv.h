@@ -401,8 +401,9 @@ int sdv_noalloc_status(int32_t *h_status);
  *   scales [layer][page][K, V][kv_head][page_size / scale_block] fp32
  * Position p of sequence b lives in page table[b][p / page_size], slot
  * p % page_size; its value is code * scale of the slot's block. Scales that the
- * library writes are powers of two (2^-126 or more); attention and read take
- * any positive finite scale. Codes must not be NaN (0x7f, 0xff): a NaN in a
+ * library writes are powers of two (2^-126 to 2^120); read takes any scale,
+ * attention any from 0 to 2^72 (V scales above that lose keys whose V scale is
+ * below 2^-30 from a row's sum of weights). Codes must not be NaN (0x7f, 0xff): a NaN in a
  * masked position would reach the rows that do not see it. sdv_qcache_write
  * stores none.
  * Spans are packed as everywhere: row row_off[b] + i is position base[b] + i of
@@ -423,6 +424,9 @@ typedef struct {
     int max_batch;                                 /* sequences a call, <= 256 */
     int max_rows, max_span, max_context; /* rows of a call, rows of a sequence in it, positions of a sequence */
 } sdv_qcache_cfg;
+/* Past these sdv_qcache_bytes and sdv_qcache_create answer SDV_ERR_UNSUPPORTED:
+ * 1024 q heads, 2^20 rows a call, 2^20 tokens a page, 2^30 positions a sequence,
+ * 2^32 - 2 pool rows a layer (n_pages * 2 * n_kv_heads * page_size). */
 
 /* Bytes of the caller-owned buffers: codes and scales (16-byte aligned) and
  * workspace (256-byte aligned; the status word and attention's partial
@@ -462,7 +466,8 @@ int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, c
 
 /* Paged attention over the codes, as sdv_op_attention over 16 bits: the row at
  * position p attends positions 0..p, or max(0, p - window + 1)..p for
- * window > 0; the span's own rows must have been written. d_q and d_out hold
+ * window > 0; the span's own rows must have been written. Page-table entries of
+ * pages that lie before every row's window are not used (they may be -1). d_q and d_out hold
  * rows of [n_q_heads][head_dim] of `dtype` (SDV_BF16, SDV_FP16), q_stride and
  * out_stride elements apart; q after RoPE; scores are q.k / sqrt(head_dim).
  * A row's result depends on its own sequence, B, max_span and window only, not

@@ -374,7 +374,7 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.nq = cache->c.n_q_heads;
-    a.window = window;
+    a.window = window = window >= cache->c.max_context ? 0 : window;
     a.q_vec = aligned16(d_q, q_stride, dtype);
     a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(D));
     const AttnPlan p = attn_plan(cache, B, max_span, window);

@@ -19,7 +19,9 @@
 // w_t = s_t + log2 vs_t, x_t = 2^(w_t - M) multiplies the bare codes, M being a row's running maximum of w,
 // and the sum l takes 2^(s_t - M); o / l is the result, precise relative to the largest contribution
 // however far the scales lie apart. M follows the maximum only when that has grown by more than one
-// (hence x up to 2 . 64), so the accumulators are rarely rescaled.
+// (hence x up to 2 . 64), so the accumulators are rarely rescaled. A scale below 2^-90 (a block of zeros has
+// 2^-126) counts as 2^-90 for M, or the sum of its keys' 2^(s_t - M) would leave fp32's range: where all of a row's
+// keys have such scales, its result (below 2^-81) is off by 2^-100 at most.
 #pragma once
 
 #include "qcache.cuh"
@@ -47,6 +49,7 @@ struct QAttnArgs {
 };
 
 constexpr int kQKeys = 128;     // keys of a chunk
+constexpr float kQLeast = -90.f;   // log2 of a V scale as M counts it, at least
 constexpr float kQNoRef = -1e30f;  // a row's M before it has seen a key: below any w, and w - M is no NaN
 template <typename T, int D_, int ROWS_>
 struct QTile {
@@ -278,7 +281,7 @@ struct QRow {
 };
 enum { kUnitEnd, kUnitRows, kUnitRefused };
 struct QUnit {
-    int state, b, h, split, row0, n_rows, r0, S, p0, first, last, whole;  // whole: the sequence has one part
+    int state, b, h, split, row0, n_rows, r0, S, p0, lo, first, last, whole;  // lo: first key that any row sees; whole: one part
 };
 constexpr uint64_t kQUnitWaitNs = 10 * kWaitLimitNs;  // above any sum of the waits that a unit's end depends on
 
@@ -362,13 +365,13 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
     auto place = [&](const QUnit &u, int ch) {
         const int t0 = u.first + ch * kQKeys, tb = t0 + lane % 16 * a.box_rows;
         box = a.pool_rows;
-        if (lane % 16 * a.box_rows < kQKeys && tb < u.last && page[4] >= 0 && page[4] < c.n_pages)
+        if (lane % 16 * a.box_rows < kQKeys && tb + a.box_rows > u.lo && tb < u.last && page[4] >= 0 && page[4] < c.n_pages)
             box = (page[4] * 2 * c.nkv + u.h) * c.page_size + tb - at[4] * c.page_size;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t = t0 + j * 32 + lane;
             rows[j] = 0xffffffffu;
-            if (t < u.last) {
+            if (t >= u.lo && t < u.last) {  // pages before the window may be gone
                 if (page[j] >= 0 && page[j] < c.n_pages) {
                     const uint32_t ph = static_cast<uint32_t>(page[j]) * 2 * c.nkv + u.h, slot = t - at[j] * c.page_size;
                     rows[j] = ph * c.page_size + slot;
@@ -475,7 +478,8 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                 u.whole = cut.parts == 1;
                 u.first = cut.origin + u.split * cut.keys;
                 u.last = min(u.first + cut.keys, pos_hi + 1);
-                if (a.window > 0) u.first = max(u.first, max(0, pos_lo - a.window + 1) / kQKeys * kQKeys);
+                u.lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
+                u.first = max(u.first, u.lo / kQKeys * kQKeys);
                 if (k >= 2 && !mbar_wait_for(&unit_empty[k % 2], (k / 2 - 1) & 1, kQUnitWaitNs)) ok = false;
                 if (lane == 0) {
                     unit_s[k % 2] = u;
@@ -714,7 +718,8 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
             if (ok) ok = mbar_wait(&s_full[gc % Q::NSB], (gc / Q::NSB) & 1);
             tc_fence_after();
             const uint32_t s_col = tmem + lanes + gc % Q::NSB * Q::NQ + col0;
-            const float ks = kv_scale[gc % Q::SCALES][0][key] * unit, vs = t < last ? kv_scale[gc % Q::SCALES][1][key] : 1.f, lv = __log2f(vs);
+            const float ks = kv_scale[gc % Q::SCALES][0][key] * unit;
+            const float vs = t >= u.lo && t < last ? kv_scale[gc % Q::SCALES][1][key] : 1.f, lv = __log2f(vs), lv_ref = fmaxf(lv, kQLeast);
             // sixteen rows' scores of this key in log2 units, -inf where a row does not see it
             float sc[16];
             {
@@ -755,10 +760,10 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                 over = max3(max3(over, d.x, d.y), e.x, e.y);
             }
             if (ch > 0) accumulate(ch - 1);
-            if (bar_or(1 + g, 128, over + lv > 1.f)) {
+            if (bar_or(1 + g, 128, over + lv_ref > 1.f)) {
                 float v[16];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) v[r] = sc[r] + lv;
+                for (int r = 0; r < 16; ++r) v[r] = sc[r] + lv_ref;
                 const float top = transpose_max16(v, lane);
                 if (lane < 16) top_s[warp % 4][col0 + lane] = top;
                 named_bar_sync(1 + g, 128);
@@ -766,8 +771,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                     const int k = col0 + key;
                     const float now = fmaxf(fmaxf(top_s[0][k], top_s[1][k]), fmaxf(top_s[2][k], top_s[3][k])), was = -m_neg[k];
                     const bool moves = now > was + 1.f;
-                    // without a reference so far l holds keys of scale 0 alone, counted from 0
-                    m_step[k] = moves ? ex2(fminf((was == kQNoRef ? 0.f : was) - now, 120.f)) : 1.f;
+                    m_step[k] = moves ? ex2(was - now) : 1.f;
                     if (moves) m_neg[k] = -now;
                 }
                 named_bar_sync(1 + g, 128);
@@ -781,16 +785,13 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                 }
             }
             // x = 64 p as planes; a line of P holds this key's values of every row and plane. l takes x / (64 vs); keys
-            // whose scale is 0 or so small that x may vanish beside it (2^-60) send their warp to the exponential.
+            // whose scale is 0 or so small that x may vanish beside it (2^-30) send their warp to the exponential.
             const float lv6 = lv + 6.f;
-            const bool small = __any_sync(0xffffffffu, !(vs >= 0x1p-60f));
+            const bool small = __any_sync(0xffffffffu, !(vs >= 0x1p-30f));
             const float to_l = small ? 0.f : __fdividef(0x1p-6f, vs);
             if (small) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float m = m_neg[col0 + r];
-                    l[r] += ex2(sc[r] + (m == -kQNoRef ? 0.f : m));
-                }
+                for (int r = 0; r < 16; ++r) l[r] += ex2(sc[r] + m_neg[col0 + r]);
             }
             uint32_t w[Q::PP][4];
 #pragma unroll
@@ -903,7 +904,7 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(const __gr
     float m = kQNoRef;
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[slot + p].x);
     m = redux_max(m);
-    if (m == kQNoRef) m = 0.f;
+    if (m == kQNoRef) m = 0.f;  // none of them: every weight 0
     float o[V], l = 0.f;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] = 0.f;
@@ -911,8 +912,7 @@ __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(const __gr
     constexpr int P = 8 * NW;
     for (int p0 = 0; p0 < parts; p0 += P) {
         const float2 ml = lane < P && p0 + lane < parts ? a.part_ml[slot + p0 + lane] : make_float2(kQNoRef, 0.f);
-        // l > 0 without a reference: keys of scale 0 alone, counted from 0
-        const float mine = ml.y == 0.f ? 0.f : ex2(fminf((ml.x == kQNoRef ? 0.f : ml.x) - m, 120.f));
+        const float mine = ex2(ml.x - m);
         float v[8][V];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

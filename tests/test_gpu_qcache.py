@@ -297,6 +297,34 @@ def test_attention_scales_far_apart():
     _check_attention(s, "bfloat16")
 
 
+@pytest.mark.parametrize("length, zeros", [(1000, 1000), (1000, 700), (40000, 39000)])
+@pytest.mark.parametrize("scale", [2.0 ** -126, 0.0])
+def test_attention_after_keys_without_a_value(length, zeros, scale):
+    """Long runs of keys whose V rows are all zero: they weigh like any other key, with scores up to hundreds of units."""
+    s = Setup(4, 2, 64, 16, 16, [length], [2], seed=14)
+    s.fill()
+    for p in range(zeros // 16):
+        page = int(s.table[0, p])
+        s.cache.codes[1, page, 1] = 0
+        s.cache.scales[1, page, 1] = scale
+        s.pool.val[page, 1], s.pool.scale[page, 1] = 0.0, scale
+    _check_attention(s, "bfloat16", spread=0.5)
+    _check_attention(s, "float16", spread=2.0)
+
+
+@pytest.mark.parametrize("ps, window", [(1, 5), (4, 130), (16, 20), (16, 300), (7, 40)])
+def test_pages_before_the_window_may_be_gone(ps, window):
+    """A sliding window's caller gives old pages back: their entries are -1, their contents anybody's."""
+    s = Setup(4, 2, 64, ps, ps, [700, 129], [3, 2], seed=15)
+    s.fill()
+    for b in range(s.B):
+        gone = max(0, s.lengths[b] - window + 1) // ps
+        s.table[b, :gone] = -1
+    s.d_table = _i32(s.table)
+    _check_attention(s, "bfloat16", window)
+    assert s.cache.get_status() == 0
+
+
 def test_attention_strides_and_second_device_buffers():
     """q inside a fused projection's rows and off a 16-byte boundary; the same results as dense rows."""
     import torch
