@@ -82,7 +82,8 @@ __device__ __forceinline__ int chunk_index(int v0, int j) {
 }
 
 // Statistics of one chunk of one row: grid (chunks, rows). The row's logits are asked for before its
-// sequence is known: 78 MB of them keep 4 waves of CTAs busy, and every latency in a CTA's chain counts in each.
+// sequence is known: 128 rows of 151,936 (78 MB) keep 4 waves of CTAs busy, and every latency in a CTA's chain counts
+// in each. Bound by memory: those in 19.5 us, 4.0 TB/s (CTAs that stay and ask for their next chunk ahead: 23.5 us).
 __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSampledArgs p) {
     pdl_wait();
     pdl_trigger();
@@ -146,7 +147,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSamp
 
 // The accepted prefix of a sequence (every CTA finds it from the chunk statistics), the race over one
 // chunk of the vocabulary at its last row, and, in the CTA that comes last, the outputs and loop state as
-// accept_kernel writes them. Grid (chunks, B). The best key is the same in any order of arrival.
+// accept_kernel writes them. Grid (chunks, B). The best key is the same in any order of arrival. One sequence of
+// eight rows, both kernels: 10.4 us, a chain of launches and dependent reads; 16 with drafter probabilities: 30.4 us.
 __global__ void __launch_bounds__(kAcceptThreads, 4) accept_draw_kernel(AcceptSampledArgs p) {
     pdl_wait();
     pdl_trigger();

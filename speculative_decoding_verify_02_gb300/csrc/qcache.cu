@@ -24,7 +24,7 @@ struct sdv_qcache {
 namespace {
 
 constexpr int kQWaves = 4;       // turns of the CTAs that an attention is cut into at most
-constexpr double kQTurn = 4;    // what a unit costs besides its chunks, in chunks (16 ragged sequences: 46 us with 1, 38 with 4)
+constexpr double kQTurn = 4;     // what a unit costs besides its chunks, in chunks (16 ragged sequences: 46 us with 1, 38 with 4)
 
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -132,7 +132,8 @@ bool element_aligned(const void *p, int dtype) { return reinterpret_cast<uintptr
 
 // ---- attention: tile rows, parts of a sequence and workspace
 // Rows of a tile: 16, 32 or 64, the smallest that holds a span's rows of one kv head. Long spans read every key once a
-// tile, out of L2: with tiles of 32 rows, two CTAs an SM waited for keys a third of the time (128 rows at 32K: 225 us).
+// tile, out of L2: with tiles of 32 rows, two CTAs an SM waited for keys a third of the time (128 rows at 32K: 240 us
+// against 212 with 64).
 int attn_rows(int span_rows) { return span_rows <= 16 ? 16 : span_rows <= 32 ? 32 : 64; }
 
 struct AttnPlan {

@@ -3,10 +3,10 @@
 // For one kv head, ROWS query rows (span row x head of the group) against 128 keys at a time:
 //     S^T [128 keys x rows] = K . Q^T          (A = the K codes as they lie in the cache, B = Q)
 //     O^T [dims x rows]     = V^T . P^T        (A = the V codes read along the other axis, B = P)
-// so K and V enter the tensor cores as the bytes they are, a key (then a dim) to a TMEM lane, and the
-// few query rows of a verify step are the narrow operand: an MMA of 128 lanes costs 45 clocks for any
-// width up to 64 (measured), 365 for the eight of a chunk, against the 1,370 that the chunk's 32 KB take
-// at this SM's share of HBM.
+// so K and V enter the tensor cores as the bytes they are, a key (then a dim) to a TMEM lane, and the few query rows of
+// a verify step are the narrow operand: an MMA of 128 lanes and 32 of depth costs 46 clocks for any width up to 64, 56
+// at 96, 64 at 128 (measured), 400 for the eight of a chunk of 32 rows, against the 1,370 that its 32 KB take at this
+// SM's share of HBM.
 //
 // The 16-bit operand of each product is split into e4m3 planes laid side by side along the width:
 //   q = 2^-e (q0 + 2^-5 q1 + 2^-10 q2), e from the tile's largest |q|: two planes hold a bf16's eight
@@ -22,6 +22,13 @@
 // (hence x up to 2 . 64), so the accumulators are rarely rescaled. A scale below 2^-90 (a block of zeros has
 // 2^-126) counts as 2^-90 for M, or the sum of its keys' 2^(s_t - M) would leave fp32's range: where all of a row's
 // keys have such scales, its result (below 2^-81) is off by 2^-100 at most.
+//
+// What bounds it (GB300, 32 q heads on 8 kv heads of 128, bf16): with spans of eight rows a CTA's chain, not the
+// bytes: a chunk is two commits, two TMEM reads and 27 instructions a score, and a unit costs 6,000 to 8,000 clocks more
+// for its queries, first maximum and results. 32,768 keys in 25.7 us (2.6 TB/s; loads alone reach 6.5), 16 sequences of
+// 512 to 4,096 keys in 38.5 us; 848 keys in 9.0 us, two launches and one chunk. Long spans read the keys out of L2 once
+// a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 212 us, 3,200 clocks a chunk of
+// 64 x 128 scores, half of the issue slots used (tensor pipe 17%).
 #pragma once
 
 #include "qcache.cuh"
