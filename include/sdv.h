@@ -223,7 +223,9 @@ int sdv_accept_greedy(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_ro
  *   d_draft_probs [R] rows of fp32, probs_stride floats apart, or NULL (the
  *                 stride is then ignored). The last row of a span is not read.
  *   rows          rows that d_tokens, d_logits, d_uniform and d_draft_probs hold;
- *                 at most the context's 128 are used. A span past them is refused.
+ *                 at most 128 and B times the longest span (the smaller of
+ *                 max_commit and the context's max_span) are used. A span past
+ *                 them is refused.
  *   max_commit    row stride of d_committed; a span longer than it is refused.
  * Device errors: a refused span (SDV_ERR_ARG; outputs as for an empty one); a
  * draft outside [0, vocab) counts as refused and a row without a logit above

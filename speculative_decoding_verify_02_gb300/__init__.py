@@ -180,6 +180,7 @@ def _ptr(t) -> int:
 
 
 _raw_stream = _device = None
+_many = True  # more than one GPU is visible (until CUDA has been asked)
 
 
 def _stream(stream) -> int:
@@ -187,11 +188,12 @@ def _stream(stream) -> int:
     costs about as much as a launch)."""
     if stream is not None:
         return int(stream.cuda_stream)
-    global _raw_stream, _device
+    global _raw_stream, _device, _many
     if _raw_stream is None:
         import torch
         torch.cuda.init()
         _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _many = torch.cuda.device_count() > 1
     return _raw_stream(_device())
 
 
@@ -208,9 +210,15 @@ def _dtype(name):
     return t
 
 
+def _elsewhere(t):
+    """Whether a device tensor is on another GPU than the current one, where the kernels run."""
+    import torch
+    return t.get_device() != torch.cuda.current_device()
+
+
 def _vector(t, n, name, dtype):
-    """A contiguous device tensor of at least n elements; returns its address."""
-    if t.dtype is not dtype or not t.is_cuda or t.numel() < n or not t.is_contiguous():
+    """A contiguous tensor of at least n elements on the current device; returns its address."""
+    if t.dtype is not dtype or not t.is_cuda or _many and _elsewhere(t) or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} device tensor of at least {n} elements is needed, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -218,7 +226,7 @@ def _vector(t, n, name, dtype):
 
 def _f32_rows(t, rows, cols, name):
     """Row stride of a device matrix of at least `rows` float32 rows of at least `cols` elements."""
-    if t.dtype is not _dtype("float32") or not t.is_cuda or t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols \
+    if t.dtype is not _dtype("float32") or not t.is_cuda or _many and _elsewhere(t) or t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols \
             or t.stride(1) != 1:
         raise ValueError(f"{name}: a float32 device matrix of {rows} rows of {cols} is needed, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -467,7 +475,7 @@ class QuantCache:
     def _rows(self, t, heads, name, floats=3):
         """(address, rows, row stride, type) of a device tensor [R, heads, dim] with dense rows."""
         kind, shape = self._dtypes.get(t.dtype, floats), t.shape
-        if kind < floats and len(shape) == 3 and t.is_cuda and shape[1] == heads and shape[2] == self._dim:
+        if kind < floats and len(shape) == 3 and t.is_cuda and not (_many and _elsewhere(t)) and shape[1] == heads and shape[2] == self._dim:
             st = t.stride()
             if st[2] == 1 and (st[1] == self._dim or heads == 1):
                 return t.data_ptr(), shape[0], (st[0] if shape[0] > 1 else max(st[0], heads * self._dim)), kind

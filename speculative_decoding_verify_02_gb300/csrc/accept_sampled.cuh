@@ -36,7 +36,7 @@ struct AcceptSampledArgs {
 // First row and length of sequence b's span; length 0 where the span is empty or not usable.
 __device__ __forceinline__ int2 accept_span(const AcceptSampledArgs &p, int b) {
     const int r0 = p.row_off[b], S = p.row_off[b + 1] - r0;
-    const bool ok = S > 0 && S <= p.max_span && r0 >= 0 && r0 + S <= p.rows_cap;
+    const bool ok = S > 0 && S <= p.max_span && r0 >= 0 && r0 <= p.rows_cap - S;  // S is small: no overflow
     return make_int2(r0, ok ? S : 0);
 }
 

@@ -218,6 +218,20 @@ def test_refused_spans():
     v.close()
 
 
+def test_offsets_at_the_ends_of_32_bits():
+    rng = np.random.default_rng(12)
+    v = _verifier(700, 1, 6)
+    x = _inputs(rng, [2], 700, False, [1.0])
+    _forward(v, [2])
+    import torch
+    n_acc, com, n_com, new = (torch.full((k,), -9, dtype=torch.int32, device="cuda") for k in (1, 6, 1, 1))
+    for off in ([2**31 - 1, -2**31], [-2**31, 2**31 - 1], [2**31 - 2, 2**31 - 1], [-1, 1], [0, 2**31 - 1]):
+        v.accept_sampled(_i32(x["tokens"]), _i32(off), _f32(x["logits"]), _f32(x["temps"]), _f32(x["u"]),
+                         _f32(x["noise"]), 1, 6, n_acc, com, n_com, new)
+        assert v.get_status() == -1 and n_acc.item() == -1 and n_com.item() == 0 and (com == -9).all()
+    v.close()
+
+
 def test_certain_drafts_at_temperature_zero_are_greedy_acceptance():
     """Temperature 0 and certain drafts: the same outputs and loop state as accept_greedy on the argmax."""
     rng = np.random.default_rng(9)

@@ -254,6 +254,17 @@ def test_attention_matches_oracle(nq, nkv, D, ps, sb, lengths, spans, window, dt
     print(f"worst error / tolerance {worst:.3f}")
 
 
+@pytest.mark.parametrize("B, nq, nkv, longest, window", [(256, 4, 2, 200, 0), (20, 16, 16, 700, 0), (33, 40, 20, 300, 50)])
+def test_attention_of_many_sequences(B, nq, nkv, longest, window):
+    """More units than the GPU holds at once: the CTAs take turns, up to 32 sequences by length."""
+    rng = np.random.default_rng(B)
+    s = Setup(nq, nkv, 64, 16, 16, rng.integers(0, longest, B).tolist(), rng.integers(0, 3, B).tolist(), seed=B)
+    s.fill()
+    for dtype in ("bfloat16", "float16"):
+        _check_attention(s, dtype, window)
+    assert s.cache.get_status() == 0
+
+
 def test_attention_of_peaked_and_flat_rows():
     """Scores spread over hundreds of units (one key takes all), rows of zeros (all keys alike), and a long flat tail
     under one large score."""
@@ -436,6 +447,26 @@ def test_binding_refusals_on_device():
         with pytest.raises(SdvError):
             f()
     assert s.cache.get_status() == 0
+
+
+def test_tensors_on_another_device_are_refused(monkeypatch):
+    import torch
+    import speculative_decoding_verify_02_gb300 as sdv
+    s = Setup(2, 1, 64, 16, 16, [3], [1])
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    s.cache.attention(1, q, *s.args(), q)
+    monkeypatch.setattr(sdv, "_many", True)
+    s.cache.attention(1, q, *s.args(), q)                             # all of them where the kernels run
+    monkeypatch.setattr(sdv, "_elsewhere", lambda t: t is s.d_base)
+    with pytest.raises(ValueError, match="base"):
+        s.cache.attention(1, q, *s.args(), q)
+    monkeypatch.setattr(sdv, "_elsewhere", lambda t: t is q)
+    with pytest.raises(ValueError, match="q: a device tensor"):
+        s.cache.attention(1, q, *s.args(), q)
+    monkeypatch.undo()
+    assert not sdv._elsewhere(q)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert sdv._elsewhere(q)
 
 
 def test_captured_graph_follows_lengths_and_streams():
