@@ -24,6 +24,7 @@ struct sdv_qcache {
 namespace {
 
 constexpr int kQWaves = 4;       // turns of the CTAs that an attention is cut into at most
+constexpr double kQMerge = .5;   // what a merge kernel costs over a cluster's joining, in chunks
 constexpr double kQTurn = 4;     // what a unit costs besides its chunks, in chunks (16 ragged sequences: 46 us with 1, 38 with 4)
 
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -80,18 +81,24 @@ bool encode_pool_rows(CUtensorMap *tm, void *codes, const sdv_qcache_cfg &c, int
 }
 
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, void *stream, Args &&...args) {
+int launch_clusters(void (*kern)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem, void *stream, Args &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? SDV_OK : SDV_ERR_CUDA;
+}
+template <typename... KArgs, typename... Args>
+int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, void *stream, Args &&...args) {
+    return launch_clusters(kern, 1, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 // Arguments that every call shares, checked; SDV_OK and the kernels' block, or the error.
@@ -147,8 +154,8 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int window) {
     p.ctas = (p.rows == 64 ? 1 : 2) * q->sm_count;
     // Parts: the number that the CTAs get through soonest at the cache's full context; a unit costs its chunks and about
     // kQTurn more for its queries, first maximum and results. One sequence's units are alike and go in turns; a batch's
-    // differ, so that a CTA has its share of the work (of sequences 0.6 of the longest on average) and then waits for
-    // the longest unit. What a sequence's parts are depends on its own length and on this number only.
+    // differ, so that past one turn a CTA has its share of the work (of sequences 0.6 of the longest on average) and
+    // then waits for the longest unit. Parts that no cluster joins cost a kernel more. What a sequence's parts are depends on its own length and on this number only.
     const long long units = static_cast<long long>(B) * q->c.n_kv_heads * p.tiles;
     const int keys = window > 0 ? std::min(q->c.max_context, window + max_span) : q->c.max_context;
     const int chunks = cdiv(keys, kQKeys);
@@ -156,8 +163,9 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int window) {
     p.splits = 1;
     for (int s = 1; s <= chunks && units * s <= static_cast<long long>(kQWaves) * p.ctas; ++s) {
         const double unit = cdiv(chunks, s) + kQTurn;
-        const double t = B == 1 ? static_cast<double>((units * s + p.ctas - 1) / p.ctas) * unit
+        double t = B == 1 || units * s <= p.ctas ? static_cast<double>((units * s + p.ctas - 1) / p.ctas) * unit
                                 : units * (0.6 * chunks + s * kQTurn) / p.ctas + unit;
+        if (s > kQJoin || units * s > p.ctas) t += s > 1 ? kQMerge : 0;
         if (s == 1 || t < best) best = t, p.splits = s;
     }
     return p;
@@ -175,10 +183,11 @@ template <typename T, int D, int ROWS>
 int launch_attn_rows(const CUtensorMap &pool, const QAttnArgs &a, const AttnPlan &p, void *stream) {
     typedef QTile<T, D, ROWS> Q;
     const dim3 grid(static_cast<unsigned>(std::min(a.units, p.ctas)));
-    const int r = launch(qcache_attn_kernel<T, D, ROWS>, grid, Q::THREADS, Q::SMEM, stream, pool, a);
-    if (r != SDV_OK || p.splits == 1) return r;
+    const int r = launch_clusters(qcache_attn_kernel<T, D, ROWS>, a.cluster ? p.splits : 1, grid, Q::THREADS, Q::SMEM,
+                                  stream, pool, a);
+    if (r != SDV_OK || p.splits == 1 || a.cluster) return r;
     const long long items = static_cast<long long>(a.c.max_span) * a.nq;
-    if (p.splits <= 8 && items * a.c.B > 1024)  // few items: four warps each are done sooner (848 keys: 1.2 against 1.9 us)
+    if (p.splits <= kQJoin)
         return launch(qcache_merge_kernel<T, D, 1>, dim3(cdiv(items, 4), a.c.B), kQMergeThreads, 0, stream, a);
     return launch(qcache_merge_kernel<T, D, 4>, dim3(static_cast<unsigned>(items), a.c.B), kQMergeThreads, 0, stream, a);
 }
@@ -386,6 +395,7 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     const long long units = static_cast<long long>(B) * p.splits * a.c.nkv * p.tiles;
     if (units > (1 << 30)) return SDV_ERR_UNSUPPORTED;
     a.units = static_cast<int>(units);
+    a.cluster = p.splits > 1 && p.splits <= kQJoin && a.units <= p.ctas;
     a.counter = reinterpret_cast<int *>(cache->ws) + 1;
     a.by_tiles = FastDiv::of(a.tiles);
     a.by_kv = FastDiv::of(a.c.nkv);

@@ -26,8 +26,9 @@
 // What bounds it (GB300, 32 q heads on 8 kv heads of 128, bf16): with spans of eight rows a CTA's chain, not the
 // bytes: a chunk is two commits, two TMEM reads and 27 instructions a score, and a unit costs 6,000 to 8,000 clocks more
 // for its queries, first maximum and results. 32,768 keys in 25.7 us (2.6 TB/s; loads alone reach 6.5), 16 sequences of
-// 512 to 4,096 keys in 38.5 us; 848 keys in 9.0 us, two launches and one chunk. Long spans read the keys out of L2 once
-// a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 212 us, 3,200 clocks a chunk of
+// 512 to 4,096 keys in 36.4 us; 848 keys in 8.3 us, one chunk and the joining of seven parts in a cluster (9.0 with a
+// merge kernel, and 1.5 us of host more). Long spans read the keys out of L2 once
+// a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 210 us, 3,200 clocks a chunk of
 // 64 x 128 scores, half of the issue slots used (tensor pipe 17%).
 #pragma once
 
@@ -44,6 +45,7 @@ struct QAttnArgs {
     int units;                       // B x splits x nkv x tiles
     int *counter;                    // units taken beyond the first of each CTA, CTAs done; both zero between calls
     int splits;                      // parts a sequence's keys are cut into at most
+    int cluster;                     // a tile's parts are the CTAs of a cluster, which join them
     int tiles;                       // row tiles of a span of max_span rows
     int grp;                         // q heads a kv head
     int q_vec;                       // q rows are 16-byte aligned
@@ -56,6 +58,7 @@ struct QAttnArgs {
 };
 
 constexpr int kQKeys = 128;     // keys of a chunk
+constexpr int kQJoin = 8;          // parts that a cluster joins (its portable size), or one warp a row
 constexpr float kQLeast = -90.f;   // log2 of a V scale as M counts it, at least
 constexpr float kQNoRef = -1e30f;  // a row's M before it has seen a key: below any w, and w - M is no NaN
 template <typename T, int D_, int ROWS_>
@@ -264,7 +267,9 @@ __device__ __forceinline__ uint32_t hscale2_u(uint32_t a, float s) {
 // side by side. A sequence of L keys is cut into parts of ceil(L / splits) keys, rounded up to whole chunks:
 // the cut depends on the sequence's own length and the call's B and max_span only. A CTA starts with the unit
 // of its number and takes the next one from a counter; the order changes no result. Its load warp is
-// ahead of the others by up to two units, so that only the first one's page tables and keys are waited for.
+// ahead of the others by up to two units, so that only the first one's page tables and keys are waited for. Where every
+// unit has a CTA of its own and a tile at most kQJoin parts, the parts are a cluster: they stay in shared memory and
+// each CTA joins its share of the rows.
 // With a window the cut starts at the chunk of the first key that any row of the span sees.
 struct QCut {
     int origin, keys, parts;  // parts of `keys` keys from `origin` to the sequence's end
@@ -288,7 +293,7 @@ struct QRow {
 };
 enum { kUnitEnd, kUnitRows, kUnitRefused };
 struct QUnit {
-    int state, b, h, split, row0, n_rows, r0, S, p0, lo, first, last, whole;  // lo: first key that any row sees; whole: one part
+    int state, b, h, split, row0, n_rows, r0, S, p0, lo, first, last, parts;  // lo: first key that any row sees; parts: of its sequence
 };
 constexpr uint64_t kQUnitWaitNs = 10 * kWaitLimitNs;  // above any sum of the waits that a unit's end depends on
 
@@ -311,10 +316,15 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
     __shared__ float top_s[4][ROWS], l_s[4][ROWS], amax_s[2][Q::WG * 4];
     __shared__ uint64_t unit_full[2], unit_empty[2], q_full;
     __shared__ QUnit unit_s[2];
+    __shared__ float2 ml_s[ROWS];
+    float *part_s = reinterpret_cast<float *>(smem_raw + (smem - smem_u32(smem_raw)));  // the first chunk's place, once read
+    static_assert(ROWS * D * 4 <= 2 * Q::TILE, "a part's rows in a stage");
+    __shared__ int joined_s, joined_rows_s;  // parts and rows that this CTA's cluster has to join
     __shared__ float kv_scale[Q::SCALES][2][kQKeys];
     const bool is_load = warp == Q::WG * 4, is_mma = warp == Q::WG * 4 + 1;
     // what needs no data goes before the wait for the kernel ahead
     if (tid == 0) {
+        joined_s = 0;
         for (int i = 0; i < Q::STAGES; ++i) {
             mbar_init(&k_full[i], 33);
             mbar_init(&v_full[i], 33);
@@ -354,6 +364,43 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
         return QRow{u.r0 + i, u.h * grp + u.row0 + r - i * grp, i};
     };
     auto chunks_of = [&](const QUnit &u) { return max(0, (u.last - u.first + kQKeys - 1) / kQKeys); };
+
+    // The rows of a tile, shared out over the CTAs of its parts, a warp each: o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i
+    // in the order of the parts, every part's values in flight.
+    auto join_rows = [&]() {
+        constexpr int V = D / 32;
+        const int rank = blockIdx.x % a.splits, joined = joined_s, joined_rows = joined_rows_s;
+        const uint32_t o_at = smem, ml_at = smem_u32(ml_s);
+        for (int r = rank + warp * joined; r < joined_rows; r += joined * Q::WG * 4) {
+            alignas(16) float v[kQJoin][V];
+            const float2 ml = lane < joined ? ld_dsmem_f2(mapa_shared(ml_at + r * 8, lane)) : make_float2(kQNoRef, 0.f);
+#pragma unroll
+            for (int p = 0; p < kQJoin; ++p) {
+#pragma unroll
+                for (int d = 0; d < V; ++d) v[p][d] = 0.f;
+                if (p < joined) {
+                    const uint32_t src = mapa_shared(o_at + (r * D + lane * V) * 4, p);
+                    if constexpr (V == 4)
+                        *reinterpret_cast<float4 *>(v[p]) = ld_dsmem_f4(src);
+                    else
+                        *reinterpret_cast<float2 *>(v[p]) = ld_dsmem_f2(src);
+                }
+            }
+            const float top = redux_max(ml.x), mine = ex2(ml.x - (top == kQNoRef ? 0.f : top)), l = warp_sum(mine * ml.y);
+            float o[V];
+#pragma unroll
+            for (int d = 0; d < V; ++d) o[d] = 0.f;
+#pragma unroll
+            for (int p = 0; p < kQJoin; ++p) {
+                const float f = __shfl_sync(0xffffffffu, mine, p);
+#pragma unroll
+                for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[p][d], o[d]);
+            }
+            T *dst = out + to_s[r] + lane * V;
+#pragma unroll
+            for (int d = 0; d < V; ++d) dst[d] = from_f32<T>(l == 0.f ? 0.f : o[d] / l);
+        }
+    };
 
     // ---- the load warp: a chunk's K rows with both scales, then its V rows. Pages of a multiple of eight tokens come in
     // TMA boxes, a lane a box (a box past the pool is zeros); others in 16-byte pieces.
@@ -459,10 +506,17 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
             }
             QUnit u;
             const int nt = a.by_tiles.div(n), ns = a.by_kv.div(nt);
-            const int tile = n - nt * a.tiles;
+            int tile = n - nt * a.tiles;
             u.h = nt - ns * c.nkv;
             u.b = a.by_splits.div(ns);
             u.split = ns - u.b * a.splits;
+            if (a.cluster) {  // the parts side by side
+                const int t = a.by_splits.div(n), bh = a.by_tiles.div(t);
+                u.split = n - t * a.splits;
+                tile = t - bh * a.tiles;
+                u.b = a.by_kv.div(bh);
+                u.h = bh - u.b * c.nkv;
+            }
             if (by_length) u.b = __shfl_sync(0xffffffffu, ranked, u.b);
             const QSpan s = qcache_span(c, u.b);
             u.r0 = s.r0, u.S = s.S, u.p0 = s.p0;
@@ -482,7 +536,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
             }
             if (u.state != kUnitEnd) {
                 const int pos_lo = s.p0 + a.by_grp.div(u.row0), pos_hi = s.p0 + a.by_grp.div(u.row0 + max(u.n_rows, 1) - 1);
-                u.whole = cut.parts == 1;
+                u.parts = cut.parts;
                 u.first = cut.origin + u.split * cut.keys;
                 u.last = min(u.first + cut.keys, pos_hi + 1);
                 u.lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
@@ -645,7 +699,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
             const QRow w = row_of(u, min(tid, n_rows - 1));
             m_neg[tid] = -kQNoRef;
             pos_s[tid] = tid < n_rows ? u.p0 + w.i : -1;
-            to_s[tid] = u.whole ? w.row * a.out_stride + w.hq * D
+            to_s[tid] = u.parts == 1 || a.cluster ? w.row * a.out_stride + w.hq * D
                                 : static_cast<long long>(qattn_slot(a, u.b, w.i, w.hq) + u.split) * D;
         }
         if (!asked_q) ask_q(u);
@@ -863,35 +917,52 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
         named_bar_sync(1 + g, 128);
         const int rows = min(CW, n_rows - col0);
         if (key < D) {
-            if (u.whole) {
+            if (u.parts == 1) {
 #pragma unroll
                 for (int r = 0; r < CW; ++r) {
                     const int k = col0 + r;
                     const float total = (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]);
                     if (r < rows) out[to_s[k] + key] = from_f32<T>(total == 0.f ? 0.f : __fdividef(acc[r], total));
                 }
+            } else if (a.cluster) {
+#pragma unroll
+                for (int r = 0; r < CW; ++r) part_s[(col0 + r) * D + key] = acc[r];
             } else {
 #pragma unroll
                 for (int r = 0; r < CW; ++r)
                     if (r < rows) a.part_o[to_s[col0 + r] + key] = acc[r];
             }
         }
-        if (!u.whole && key < rows) {
+        if (u.parts > 1 && key < rows) {
             const int k = col0 + key;
-            a.part_ml[to_s[k] / D] = make_float2(-m_neg[k], (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]));
+            const float2 ml = make_float2(-m_neg[k], (l_s[0][k] + l_s[1][k]) + (l_s[2][k] + l_s[3][k]));
+            if (a.cluster)
+                ml_s[k] = ml;
+            else
+                a.part_ml[to_s[k] / D] = ml;
         }
+        if (u.parts > 1 && tid == 0) joined_s = u.parts, joined_rows_s = n_rows;
         base += n_chunks;
         }
         tc_fence_before();
     }
-    __syncthreads();
+    if (a.cluster) {
+        __syncwarp();
+        cluster_sync();
+        if (!is_load && !is_mma && joined_s) join_rows();
+        __syncwarp();
+        cluster_arrive();
+    } else {
+        __syncthreads();
+    }
     if (is_mma) tmem_dealloc(tmem, Q::COLS);
+    if (a.cluster) cluster_wait();  // nobody leaves while its part may be read
 }
 
 constexpr int kQMergeThreads = 128;
 
-// NW warps join the parts of one (row, q head): o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i, every NW-th part a
-// warp, the warps in order. NW = 1 up to eight parts (the loads that a warp has under way), else 4.
+// Where no cluster does: NW warps join the parts of one (row, q head), every NW-th part a warp, the warps in order.
+// NW = 1 up to eight parts (the loads that a warp has under way), else 4.
 // Grid (span row x head in groups of 4 / NW, sequence).
 template <typename T, int D, int NW>
 __global__ void __launch_bounds__(kQMergeThreads) qcache_merge_kernel(const __grid_constant__ QAttnArgs a) {
