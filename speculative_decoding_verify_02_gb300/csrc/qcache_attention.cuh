@@ -28,8 +28,8 @@
 // for its queries, first maximum and results. 32,768 keys in 25.7 us (2.6 TB/s; loads alone reach 6.5), 16 sequences of
 // 512 to 4,096 keys in 36.4 us; 848 keys in 8.3 us, one chunk and the joining of seven parts in a cluster (9.0 with a
 // merge kernel, and 1.5 us of host more). Long spans read the keys out of L2 once
-// a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 210 us, 3,200 clocks a chunk of
-// 64 x 128 scores, half of the issue slots used (tensor pipe 17%).
+// a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 194 us, 2,900 clocks a chunk of
+// 64 x 128 scores, half of the issue slots used (tensor pipe 18%).
 #pragma once
 
 #include "qcache.cuh"
@@ -78,6 +78,10 @@ struct QTile {
     static constexpr int NSB = 2 * NQ + NP <= TMEM ? 2 : 1;                       // S^T of the next chunk beside this one's
     static constexpr int O_COL = (NSB * NQ + 31) / 32 * 32;                       // TMEM column of O^T
     static constexpr int COLS = O_COL + NP <= 128 ? 128 : O_COL + NP <= 256 ? 256 : 512;
+    // O^T of a unit's chunks grows in TMEM and is taken over where a reference moves, or every chunk's is added up in
+    // registers: the long units of long spans move theirs rarely (128 rows at 32K: 194 us against 210), short ones lose
+    // (848 keys x 8 rows: 8.5 against 8.3 us, 16 sequences 37.1 against 36.6).
+    static constexpr bool GROWS = ROWS == 64;
     static constexpr int THREADS = WG * 128 + 64;  // softmax warps, the load warp, the MMA warp
     static_assert(ROWS == 16 || ROWS == 32 || ROWS == 64, "tile rows");
     static_assert(COLS <= TMEM && O_COL + NP <= COLS, "TMEM columns");
@@ -197,6 +201,12 @@ template <typename... V>
 __device__ __forceinline__ void tmem_ld_wait(V &...v) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     (tmem_ld_pass(v), ...);
+}
+__device__ __forceinline__ void tmem_zero16(uint32_t taddr) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr),
+        "r"(0)
+        : "memory");
 }
 // Lanes j and j + 16 receive the sum over all 32 lanes of v[j].
 __device__ __forceinline__ float transpose_sum16(float (&v)[16], int lane) {
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
 #pragma unroll
                     for (int k4 = 0; k4 < kQKeys / 32; ++k4)
                         umma_e4m3(tmem + Q::O_COL, line_desc(v_s + 32 * k4 * D, D),
-                                  line_desc(p_s + 32 * k4 * Q::W, Q::W, kQKeys * Q::W), id_o, k4 > 0);
+                                  line_desc(p_s + 32 * k4 * Q::W, Q::W, kQKeys * Q::W), id_o, (Q::GROWS && ch > base) || k4 > 0);
                     umma_commit(&o_full);
                     umma_commit(&v_empty[st]);
                     if (Q::NSB == 2 && asked == ch + 1 && asked < end) issue_scores();
@@ -753,8 +763,8 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
         float acc[CW], l[CW];
 #pragma unroll
         for (int r = 0; r < CW; ++r) acc[r] = l[r] = 0.f;
-        // adds the product of the chunk last sent to the tensor cores
-        auto accumulate = [&](int ch) {
+        // adds the products since the last time, up to that of chunk ch, planes joined
+        auto collect = [&](int ch) {
             if (ok) ok = mbar_wait(&o_full, (base + ch) & 1);
             tc_fence_after();
             float v[3][16];
@@ -820,7 +830,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                 const float2 e = __fadd2_rn(make_float2(sc[r + 2], sc[r + 3]), make_float2(m.z, m.w));
                 over = max3(max3(over, d.x, d.y), e.x, e.y);
             }
-            if (ch > 0) accumulate(ch - 1);
+            if (!Q::GROWS && ch > 0) collect(ch - 1);
             if (bar_or(1 + g, 128, over + lv_ref > 1.f)) {
                 float v[16];
 #pragma unroll
@@ -837,6 +847,12 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                 }
                 named_bar_sync(1 + g, 128);
                 if (ch > 0) {
+                    if constexpr (Q::GROWS) {
+                        collect(ch - 1);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) tmem_zero16(tmem + lanes + Q::O_COL + p * ROWS + col0);
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    }
 #pragma unroll
                     for (int r = 0; r < 16; r += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(&m_step[col0 + r]);
@@ -880,6 +896,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                     }
                 }
             }
+            if (Q::GROWS && ch > 0 && ok) ok = mbar_wait(&o_full, (gc - 1) & 1);  // the last product is done with P
 #pragma unroll
             for (int p = 0; p < Q::PP; ++p)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
@@ -909,7 +926,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                 asked_q = true;
             }
         }
-        if (n_chunks > 0) accumulate(n_chunks - 1);
+        if (n_chunks > 0) collect(n_chunks - 1);
         if (!ok && lane == 0) set_status(c.status, SDV_ERR_DEVICE_TIMEOUT);
         // ---- sums over the keys, and the rows out
         const float mine = transpose_sum16(l, lane);

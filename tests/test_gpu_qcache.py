@@ -297,6 +297,21 @@ def test_attention_of_peaked_and_flat_rows():
         assert (np.abs(out.double().cpu().numpy() - ref) <= _tolerance(ref, mag, top, 64, dtype)).all()
 
 
+@pytest.mark.parametrize("nq, nkv, length, span", [(16, 1, 1500, 9), (16, 4, 1500, 6), (8, 4, 1500, 2)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_attention_whose_maximum_keeps_growing(nq, nkv, length, span, dtype):
+    """Keys that grow along the sequence, in tiles of 64, 32 and 16 rows: the references move from chunk to chunk."""
+    s = Setup(nq, nkv, 128, 16, 16, [length], [span], seed=21)
+    s.fill()
+    for p, page in enumerate(s.table[0]):
+        s.pool.scale[page, 0] = 2.0 ** -12 * (1 + p // 8)
+    s.cache.scales[1].copy_(_dev(s.pool.scale.astype(np.float32)))
+    _check_attention(s, dtype, spread=0.5)
+    s.cache.scales[1].copy_(_dev((s.pool.scale * 8).astype(np.float32)))
+    s.pool.scale = s.pool.scale * 8
+    _check_attention(s, dtype, spread=0.5)
+
+
 def test_attention_scales_far_apart():
     """Blocks whose scales differ by 2^40 in one sequence, and scales that are no powers of two."""
     s = Setup(4, 2, 64, 16, 4, [300], [3], seed=4)
