@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(QTile<T, D, ROWS>::THREADS, QTile<T, D, ROWS>:
                 over = max3(max3(over, d.x, d.y), e.x, e.y);
             }
             if (!Q::GROWS && ch > 0) collect(ch - 1);
-            if (bar_or(1 + g, 128, over + lv_ref > 1.f)) {
+            if (ch == 0 || bar_or(1 + g, 128, over + lv_ref > 1.f)) {  // the first chunk's always do
                 float v[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) v[r] = sc[r] + lv_ref;
