@@ -473,7 +473,11 @@ int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, c
  * rows of [n_q_heads][head_dim] of `dtype` (SDV_BF16, SDV_FP16), q_stride and
  * out_stride elements apart; q after RoPE; scores are q.k / sqrt(head_dim).
  * A row's result depends on its own sequence, B, max_span and window only, not
- * on the other sequences. */
+ * on the other sequences. Rows of a span share the scale of their q: a score is
+ * off by 2^-22 of the largest |q_d| of the rows and heads computed beside it
+ * (up to 64) times sum |k_d| / sqrt(head_dim), so a row 2^16 times smaller than
+ * another of its span keeps six bits of its scores (bf16). Infinity or NaN in q
+ * gives NaN in its own row and head only. */
 int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t q_stride, int dtype, int rows,
                          const int32_t *d_page_table, const int32_t *d_row_off, const int32_t *d_base, int B,
                          int max_span, int window, void *d_out, int64_t out_stride, void *stream);

@@ -226,11 +226,12 @@ def _vector(t, n, name, dtype):
 
 def _f32_rows(t, rows, cols, name):
     """Row stride of a device matrix of at least `rows` float32 rows of at least `cols` elements."""
-    if t.dtype is not _dtype("float32") or not t.is_cuda or _many and _elsewhere(t) or t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols \
-            or t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _dtype("float32") or not t.is_cuda or _many and _elsewhere(t) or len(shape) != 2 or \
+            shape[0] < rows or shape[1] < cols or stride[1] != 1:
         raise ValueError(f"{name}: a float32 device matrix of {rows} rows of {cols} is needed, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+                         f"{tuple(shape)} on {t.device}")
+    return stride[0] if shape[0] > 1 else max(stride[0], cols)
 
 
 def paged_attention_noalloc(q, kv_layer, page_table, pages_per_seq, page_size, n_pages, row_off, base, B,
