@@ -19,6 +19,7 @@ struct sdv_qcache {
     FastDiv by_page{}, by_block{}, by_heads{};
     int box_rows = 0;                 // pool rows of a TMA box (0: the page size fits none)
     std::vector<CUtensorMap> pools;   // one map a layer over its pool rows
+    int clusters[kQJoin + 1] = {};    // clusters of 2..kQJoin attention CTAs of 64 rows that the device holds at once
 };
 
 namespace {
@@ -145,6 +146,7 @@ int attn_rows(int span_rows) { return span_rows <= 16 ? 16 : span_rows <= 32 ? 3
 
 struct AttnPlan {
     int rows, tiles, splits, ctas;
+    bool cluster;  // a tile's parts are a cluster
 };
 AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int window) {
     AttnPlan p;
@@ -161,12 +163,14 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int window) {
     const int chunks = cdiv(keys, kQKeys);
     double best = 0;
     p.splits = 1;
+    p.cluster = false;
     for (int s = 1; s <= chunks && units * s <= static_cast<long long>(kQWaves) * p.ctas; ++s) {
         const double unit = cdiv(chunks, s) + kQTurn;
         double t = B == 1 || units * s <= p.ctas ? static_cast<double>((units * s + p.ctas - 1) / p.ctas) * unit
                                 : units * (0.6 * chunks + s * kQTurn) / p.ctas + unit;
-        if (s > kQJoin || units * s > p.ctas) t += s > 1 ? kQMerge : 0;
-        if (s == 1 || t < best) best = t, p.splits = s;
+        const bool cluster = s > 1 && s <= kQJoin && units * s <= p.ctas && (p.rows < 64 || units <= q->clusters[s]);
+        if (s > 1 && !cluster) t += kQMerge;
+        if (s == 1 || t < best) best = t, p.splits = s, p.cluster = cluster;
     }
     return p;
 }
@@ -209,6 +213,27 @@ cudaError_t set_attn() {
     cudaError_t e = cudaFuncSetAttribute(qcache_attn_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          QTile<T, D, ROWS>::SMEM);
     return e == cudaSuccess ? set_carveout(qcache_attn_kernel<T, D, ROWS>) : e;
+}
+// Clusters of each size that run at once, of CTAs that fill an SM: their SMs must be neighbours (15 clusters of eight
+// on 152 SMs), and one that waits costs a whole turn (two sequences of 8,164 keys and 14 rows: 50 us, 28 without). Of
+// smaller CTAs two share an SM, and those over start soon (four sequences of 1,000 keys and 8 rows, 32 clusters of
+// eight: 11.4 us, 12.5 without).
+cudaError_t count_clusters(int (&n)[kQJoin + 1]) {
+    typedef QTile<bf16, 128, 64> Q;  // the other types fill an SM, too
+    for (int s = 2; s <= kQJoin; ++s) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(s);
+        cfg.blockDim = dim3(Q::THREADS);
+        cfg.dynamicSmemBytes = Q::SMEM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {static_cast<unsigned>(s), 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n[s], qcache_attn_kernel<bf16, 128, 64>, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 template <typename T, int D>
 cudaError_t set_attn_all() {
@@ -297,6 +322,10 @@ int sdv_qcache_create(const sdv_qcache_cfg *cfg, void *d_codes, void *d_scales, 
     q->by_block = FastDiv::of(cfg->scale_block);
     q->by_heads = FastDiv::of(2 * cfg->n_kv_heads);
     q->box_rows = box_rows_of(*cfg);
+    if (count_clusters(q->clusters) != cudaSuccess) {
+        delete q;
+        return SDV_ERR_CUDA;
+    }
     bool maps = true;
     try {
         q->pools.resize(cfg->n_layers);
@@ -395,7 +424,7 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
     const long long units = static_cast<long long>(B) * p.splits * a.c.nkv * p.tiles;
     if (units > (1 << 30)) return SDV_ERR_UNSUPPORTED;
     a.units = static_cast<int>(units);
-    a.cluster = p.splits > 1 && p.splits <= kQJoin && a.units <= p.ctas;
+    a.cluster = p.cluster;
     a.counter = reinterpret_cast<int *>(cache->ws) + 1;
     a.by_tiles = FastDiv::of(a.tiles);
     a.by_kv = FastDiv::of(a.c.nkv);

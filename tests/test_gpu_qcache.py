@@ -239,6 +239,8 @@ ATTENTION = [
     (16, 1, 128, 128, 128, [1000, 3], [17, 9], 0),                   # many rows a kv head
     (5, 5, 64, 16, 16, [40, 200], [60, 33], 0),                      # spans longer than their prefix
     (40, 8, 128, 32, 16, [2000], [13], 0),                           # five heads a kv head
+    (32, 8, 64, 24, 8, [1100, 1150], [14, 9], 0),                    # tiles of 64 rows, more clusters than fit at once
+    (16, 2, 64, 16, 16, [1100], [8], 0),                             # tiles of 64 rows, clusters
     (32, 8, 128, 16, 16, [4090], [8], 0),
     (128, 1, 128, 16, 16, [200], [1], 0),                            # more heads than a tile
 ]
