@@ -141,7 +141,7 @@ bool element_aligned(const void *p, int dtype) { return reinterpret_cast<uintptr
 // ---- attention: tile rows, parts of a sequence and workspace
 // Rows of a tile: 16, 32 or 64, the smallest that holds a span's rows of one kv head. Long spans read every key once a
 // tile, out of L2: with tiles of 32 rows, two CTAs an SM waited for keys a third of the time (128 rows at 32K: 240 us
-// against 212 with 64, now 194).
+// against 212 with 64, now 193).
 int attn_rows(int span_rows) { return span_rows <= 16 ? 16 : span_rows <= 32 ? 32 : 64; }
 
 struct AttnPlan {

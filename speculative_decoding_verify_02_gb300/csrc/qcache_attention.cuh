@@ -24,11 +24,11 @@
 // keys have such scales, its result (below 2^-81) is off by 2^-100 at most.
 //
 // What bounds it (GB300, 32 q heads on 8 kv heads of 128, bf16): with spans of eight rows a CTA's chain, not the
-// bytes: a chunk is two commits, two TMEM reads and 27 instructions a score, and a unit costs 6,000 to 8,000 clocks more
+// bytes: a chunk is two commits, two TMEM reads and 25 to 27 instructions a score, and a unit costs 6,000 to 8,000 clocks more
 // for its queries, first maximum and results. 32,768 keys in 25.7 us (2.6 TB/s; loads alone reach 6.5), 16 sequences of
 // 512 to 4,096 keys in 36.4 us; 848 keys in 8.3 us, one chunk and the joining of seven parts in a cluster (9.0 with a
 // merge kernel, and 1.5 us of host more). Long spans read the keys out of L2 once
-// a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 194 us, 2,900 clocks a chunk of
+// a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 193 us, 2,900 clocks a chunk of
 // 64 x 128 scores, half of the issue slots used (tensor pipe 18%).
 #pragma once
 
@@ -79,7 +79,7 @@ struct QTile {
     static constexpr int O_COL = (NSB * NQ + 31) / 32 * 32;                       // TMEM column of O^T
     static constexpr int COLS = O_COL + NP <= 128 ? 128 : O_COL + NP <= 256 ? 256 : 512;
     // O^T of a unit's chunks grows in TMEM and is taken over where a reference moves, or every chunk's is added up in
-    // registers: the long units of long spans move theirs rarely (128 rows at 32K: 194 us against 210), short ones lose
+    // registers: the long units of long spans move theirs rarely (128 rows at 32K: 193 us against 209), short ones lose
     // (848 keys x 8 rows: 8.5 against 8.3 us, 16 sequences 37.1 against 36.6).
     static constexpr bool GROWS = ROWS == 64;
     static constexpr int THREADS = WG * 128 + 64;  // softmax warps, the load warp, the MMA warp
