@@ -41,10 +41,10 @@ __device__ __forceinline__ int2 accept_span(const AcceptSampledArgs &p, int b) {
 }
 
 // Weight of logit x against the row's maximum m: exp((x - m) / T) with c = log2(e) / T. NaN and -inf
-// weigh nothing; the maximum weighs one whatever it is (an infinite maximum shares the row).
+// weigh nothing, in a row that holds nothing else either; any other maximum weighs one (+inf shares the row).
 __device__ __forceinline__ float logit_weight(float x, float m, float c) {
-    if (x == m) return 1.f;
-    return x > -INFINITY && x < m ? exp2f((x - m) * c) : 0.f;
+    if (!(x > -INFINITY)) return 0.f;
+    return x == m ? 1.f : x < m ? exp2f((x - m) * c) : 0.f;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -232,8 +232,10 @@ __global__ void __launch_bounds__(kAcceptThreads, 4) accept_draw_kernel(AcceptSa
     const bool rejected = m < S - 1;
     const float xm = row_m[m];
     int token = 0;
-    if (greedy) {
-        token = xm > -INFINITY ? row_best[m] : 0;
+    if (!(xm > -INFINITY)) {  // no logit to draw: token 0, from one CTA
+        if (blockIdx.x > 0) return;
+    } else if (greedy) {
+        token = row_best[m];
     } else {
         const float inv_l = 1.f / row_l[m];
         const int drop = rejected && !p.probs ? p.tokens[r + 1] : -1;  // a certain draft leaves no weight
