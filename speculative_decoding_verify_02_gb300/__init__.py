@@ -224,6 +224,15 @@ def _vector(t, n, name, dtype):
     return t.data_ptr()
 
 
+def _int_rows(t, rows, cols, name):
+    """A contiguous int32 tensor of at least rows x cols elements, flat or in rows of `cols` (the kernels step by it;
+    one row may be longer); returns its address."""
+    shape = t.shape
+    if rows > 1 and len(shape) > 1 and shape[-1] != cols:
+        raise ValueError(f"{name}: rows of {cols} are needed, got {tuple(shape)}")
+    return _vector(t, rows * cols, name, _dtype("int32"))
+
+
 def _f32_rows(t, rows, cols, name):
     """Row stride of a device matrix of at least `rows` float32 rows of at least `cols` elements."""
     shape, stride = t.shape, t.stride()
@@ -486,7 +495,7 @@ class QuantCache:
 
     def _index(self, page_table, row_off, base, B):
         i32 = _dtype("int32")
-        return (_vector(page_table, B * self.pages_per_seq, "page_table", i32),
+        return (_int_rows(page_table, B, self.pages_per_seq, "page_table"),
                 _vector(row_off, B + 1, "row_off", i32), _vector(base, B, "base", i32))
 
     def write(self, layer, k, v, page_table, row_off, base, B, max_span, stream=None):

@@ -76,3 +76,36 @@ def test_loop_refuses_uniforms_without_temperature(sdv):
     loop.v, loop.B = None, 1
     with pytest.raises(ValueError, match="temperature"):
         loop.step(uniforms=torch.zeros(1))
+
+
+class _Held:
+    """What the binding looks at of a device tensor."""
+    def __init__(self, *shape, dtype=torch.int32):
+        self.shape, self.dtype, self.is_cuda, self.device = torch.Size(shape), dtype, True, "cuda:0"
+
+    def numel(self):
+        return self.shape.numel()
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_page_tables_of_another_width_are_refused(sdv, monkeypatch):
+    """The kernels step from one sequence's pages to the next by the cache's own width: a wider table would give the
+    second sequence pages of the first. One sequence's entries begin alike in a table of any width."""
+    monkeypatch.setattr(sdv, "_many", False)
+    q = object.__new__(sdv.QuantCache)
+    q.pages_per_seq = 8
+    off, base = _Held(3), _Held(2)
+    for table in (_Held(2, 8), _Held(16), _Held(5, 8), _Held(1, 2, 8)):
+        assert q._index(table, off, base, 2) == (4096, 4096, 4096)
+    for table in (_Held(2, 9), _Held(4, 4), _Held(2, 16), _Held(2, 2, 16)):
+        with pytest.raises(ValueError, match="page_table"):
+            q._index(table, off, base, 2)
+    assert q._index(_Held(1, 16), off, base, 1) == (4096, 4096, 4096)
