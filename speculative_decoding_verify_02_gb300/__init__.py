@@ -385,7 +385,7 @@ class Verifier:
             self.ctx, _vector(tokens, R, "tokens", i32), _vector(row_off, B + 1, "row_off", i32), logits.data_ptr(),
             l_stride, _vector(temperature, B, "temperature", f32), _vector(uniforms, R, "uniforms", f32),
             noise.data_ptr(), e_stride, _ptr(draft_probs), q_stride, R, B, max_commit,
-            _vector(n_accept, B, "n_accept", i32), _vector(committed, B * max_commit, "committed", i32),
+            _vector(n_accept, B, "n_accept", i32), _int_rows(committed, B, max_commit, "committed"),
             _vector(n_commit, B, "n_commit", i32), _vector(new_len, B, "new_len", i32), _stream(stream)),
             "accept_sampled")
 

@@ -109,3 +109,34 @@ def test_page_tables_of_another_width_are_refused(sdv, monkeypatch):
         with pytest.raises(ValueError, match="page_table"):
             q._index(table, off, base, 2)
     assert q._index(_Held(1, 16), off, base, 1) == (4096, 4096, 4096)
+
+
+def test_committed_rows_of_another_width_are_refused(sdv, monkeypatch):
+    """accept_sampled writes row b at b * max_commit: a wider matrix would be filled across its rows."""
+    import types
+    calls = []
+    monkeypatch.setattr(sdv, "_many", False)
+    monkeypatch.setattr(sdv, "_stream", lambda s: 0)
+    monkeypatch.setattr(sdv, "lib", lambda: types.SimpleNamespace(sdv_accept_sampled=lambda *a: calls.append(a) or 0))
+    v = object.__new__(sdv.Verifier)
+    v.ctx, v.mcfg, v.ccfg = None, types.SimpleNamespace(vocab=70), types.SimpleNamespace(max_rows=32)
+
+    def matrix(rows):
+        t = _Held(rows, 70, dtype=torch.float32)
+        t.stride = lambda: (70, 1)
+        return t
+
+    def accept(B, max_commit, committed):
+        f32 = torch.float32
+        v.accept_sampled(_Held(12), _Held(B + 1), matrix(12), _Held(B, dtype=f32), _Held(12, dtype=f32), matrix(B), B,
+                         max_commit, _Held(B), committed, _Held(B), _Held(B))
+
+    for committed in (_Held(3, 4), _Held(12), _Held(4, 4)):
+        accept(3, 4, committed)
+    accept(1, 4, _Held(1, 17))
+    assert len(calls) == 4
+    for committed in (_Held(3, 5), _Held(3, 17), _Held(6, 2)):
+        with pytest.raises(ValueError, match="committed"):
+            accept(3, 4, committed)
+    assert len(calls) == 4
+    v.ctx = None
