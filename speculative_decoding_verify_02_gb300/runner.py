@@ -103,9 +103,12 @@ class SpecLoop:
         device tensor [B]), accept, rewind, and commit to the n-gram index. With `uniforms` (float32
         [max_rows] in [0, 1)) and `noise` (float32 [B, vocab], exponential) the drafts are accepted
         against the target's probabilities at `temperature` instead of matched by token;
-        `draft_probs` [max_rows, vocab] is the drafter's distribution (None: certain drafts). Both
-        are read on the device, so a captured step takes what they hold when it is replayed."""
+        `draft_probs` [max_rows, vocab] is the drafter's distribution (None: certain drafts). All
+        three are read on the device, so a captured step takes what they hold when it is replayed.
+        They are the step's random numbers: `seed` is that of the token-matching step alone."""
         v, B = self.v, self.B
+        if uniforms is None and (noise is not None or draft_probs is not None):
+            raise ValueError("noise and draft_probs belong to the acceptance against probabilities, which needs uniforms")
         if uniforms is not None:
             if temperature is None or noise is None:
                 raise ValueError("acceptance against probabilities needs temperature, uniforms and noise")

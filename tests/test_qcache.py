@@ -140,3 +140,14 @@ def test_committed_rows_of_another_width_are_refused(sdv, monkeypatch):
             accept(3, 4, committed)
     assert len(calls) == 4
     v.ctx = None
+
+
+@pytest.mark.parametrize("kw", [dict(noise=1), dict(draft_probs=1), dict(noise=1, draft_probs=1),
+                                dict(noise=1, temperature=1), dict(draft_probs=1, temperature=1)])
+def test_loop_refuses_noise_and_draft_probs_without_uniforms(sdv, kw):
+    """They belong to the acceptance against probabilities; without uniforms the loop matches tokens, another law."""
+    from speculative_decoding_verify_02_gb300.runner import SpecLoop
+    loop = object.__new__(SpecLoop)
+    loop.v, loop.B = None, 1
+    with pytest.raises(ValueError, match="uniforms"):
+        loop.step(**{k: torch.zeros(1) for k in kw})
