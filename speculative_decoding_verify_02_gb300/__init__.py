@@ -192,8 +192,9 @@ def _stream(stream) -> int:
     if _raw_stream is None:
         import torch
         torch.cuda.init()
-        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         _many = torch.cuda.device_count() > 1
+        _device = torch._C._cuda_getDevice
+        _raw_stream = torch._C._cuda_getCurrentRawStream  # last: another thread that sees it calls both
     return _raw_stream(_device())
 
 
