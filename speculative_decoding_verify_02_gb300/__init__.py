@@ -458,15 +458,18 @@ class QuantCache:
         self.cfg = QCacheCfg(n_layers, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, scale_block, max_batch,
                              max_rows, max_span, max_context)
         sizes = [ctypes.c_size_t() for _ in range(3)]
-        _check(lib().sdv_qcache_bytes(ctypes.byref(self.cfg), *(ctypes.byref(n) for n in sizes)), "qcache_bytes")
-        self.codes = torch.empty(n_layers, n_pages, 2, n_kv_heads, page_size, head_dim, dtype=torch.uint8, device="cuda")
-        self.scales = torch.empty(n_layers, n_pages, 2, n_kv_heads, page_size // scale_block, dtype=torch.float32,
-                                  device="cuda")
-        self.workspace = torch.empty(sizes[2].value + 256, dtype=torch.uint8, device="cuda")
         c = ctypes.c_void_p()
-        _check(lib().sdv_qcache_create(ctypes.byref(self.cfg), _ptr(self.codes), _ptr(self.scales),
-                                       (_ptr(self.workspace) + 255) // 256 * 256, _stream(stream), ctypes.byref(c)),
-               "qcache_create")
+        # on the stream that clears them: memory that another stream had may still be in use there
+        with torch.cuda.stream(stream):
+            _check(lib().sdv_qcache_bytes(ctypes.byref(self.cfg), *(ctypes.byref(n) for n in sizes)), "qcache_bytes")
+            self.codes = torch.empty(n_layers, n_pages, 2, n_kv_heads, page_size, head_dim, dtype=torch.uint8,
+                                     device="cuda")
+            self.scales = torch.empty(n_layers, n_pages, 2, n_kv_heads, page_size // scale_block, dtype=torch.float32,
+                                      device="cuda")
+            self.workspace = torch.empty(sizes[2].value + 256, dtype=torch.uint8, device="cuda")
+            _check(lib().sdv_qcache_create(ctypes.byref(self.cfg), _ptr(self.codes), _ptr(self.scales),
+                                           (_ptr(self.workspace) + 255) // 256 * 256, _stream(stream), ctypes.byref(c)),
+                   "qcache_create")
         self.cache = c
         self.pages_per_seq = -(-max_context // page_size)
         self._dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}

@@ -51,3 +51,32 @@ def test_first_calls_of_two_threads(sdv):
         assert seen == 703
         where += 1
     assert where > 20
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_cache_memory_belongs_to_the_stream_that_clears_it(sdv, monkeypatch, given):
+    """Memory of another stream may still be in use there when the cache is cleared."""
+    current, held = ["main"], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, current[0] = current[0], stream if stream is not None else current[0]
+        yield
+        current[0] = before
+
+    empty = torch.empty
+
+    def fake_empty(*shape, dtype, device):
+        held.append(current[0])
+        return empty(*shape, dtype=dtype)
+
+    cleared = []
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", fake_empty)
+    side = types.SimpleNamespace(cuda_stream=9)
+    calls = types.SimpleNamespace(sdv_qcache_bytes=lambda *a: 0, sdv_qcache_destroy=lambda c: 0,
+                                  sdv_qcache_create=lambda *a: cleared.append(a[4]) or 0)
+    monkeypatch.setattr(sdv, "lib", lambda: calls)
+    sdv.QuantCache(1, 2, 1, 64, n_pages=4, max_context=32, stream=side if given else None)
+    assert cleared == [9 if given else 703]
+    assert held == [side if given else "main"] * 3 and current == ["main"]
