@@ -41,10 +41,11 @@ __device__ __forceinline__ int2 accept_span(const AcceptSampledArgs &p, int b) {
 }
 
 // Weight of logit x against the row's maximum m: exp((x - m) / T) with c = log2(e) / T. NaN and -inf
-// weigh nothing, in a row that holds nothing else either; any other maximum weighs one (+inf shares the row).
+// weigh nothing; the maximum weighs one whatever it is (an infinite maximum shares the row). A row without a logit,
+// m = -inf, is the caller's to leave out (asked here, for every logit, it costs 8 rows 2 us of 12.4).
 __device__ __forceinline__ float logit_weight(float x, float m, float c) {
-    if (!(x > -INFINITY)) return 0.f;
-    return x == m ? 1.f : x < m ? exp2f((x - m) * c) : 0.f;
+    if (x == m) return 1.f;
+    return x > -INFINITY && x < m ? exp2f((x - m) * c) : 0.f;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
