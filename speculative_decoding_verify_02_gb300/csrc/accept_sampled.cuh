@@ -146,6 +146,26 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_stats_kernel(AcceptSamp
     }
 }
 
+__device__ __forceinline__ double logit_weight64(float x, float m, float T) {
+    if (!(x > -INFINITY)) return 0.;
+    return x == m ? 1. : exp((static_cast<double>(x) - static_cast<double>(m)) / static_cast<double>(T));
+}
+// u q < w(x) / l in 64 bits, by a whole warp. The row's float sum l decides where it can: its weights are off by
+// 2.3 a 2^-24 (a = (m - x) / T log2 e; the roundings of x - m, log2 e / T and their product) and two exp2f's
+// 4 2^-24, a averages log2 of the vocabulary at most over the weights, and at most 34 + n_chunks / 32 additions follow one
+// another: below (90 + n_chunks) 2^-24 altogether for n_chunks * 4,096 logits. Nearer than that to the border, at most one draft in
+// 2^16, the row is summed again: 1.2 ms for 151,936 logits, bound by 64-bit products.
+__device__ __forceinline__ bool accept_near(const float *row, int vocab, int n_chunks, float x, float m, float l, float T, float u,
+                                         float q) {
+    const double uq = static_cast<double>(u) * static_cast<double>(q), w = logit_weight64(x, m, T), lw = uq * l;
+    if (!(w > 0.) || fabs(lw - w) > (90 + n_chunks) * 0x1p-24 * w) return lw < w;
+    double sum = 0.;
+    for (int v = threadIdx.x % 32; v < vocab; v += 32) sum += logit_weight64(row[v], m, T);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return uq * sum < w;
+}
+
 // The accepted prefix of a sequence (every CTA finds it from the chunk statistics), the race over one
 // chunk of the vocabulary at its last row, and, in the CTA that comes last, the outputs and loop state as
 // accept_kernel writes them. Grid (chunks, B). The best key is the same in any order of arrival. One sequence of
@@ -198,27 +218,23 @@ __global__ void __launch_bounds__(kAcceptThreads, 4) accept_draw_kernel(AcceptSa
         }
         l = warp_sum(l);
         best = __reduce_min_sync(0xffffffffu, best);
+        bool ok = false;
+        if (draft && m > -INFINITY) {
+            if (greedy) {
+                ok = d == best && u * q < 1.f;
+            } else {
+                const float uq = u * q, pd = logit_weight(x, m, c) / l;
+                ok = uq < pd;
+                // the draft's own weight is off by 2.3 (m - x) / T log2 e + 4 of 2^-24, its exponent below 150, and the
+                // sum as said at accept_near: together below 512 + n_chunks. Where p is no normal number: 2^-140
+                if (fabsf(uq - pd) <= (512 + p.n_chunks) * 0x1p-24f * pd + 0x1p-140f)
+                    ok = accept_near(p.logits + r * p.logits_stride, p.vocab, p.n_chunks, x, m, l, T, u, q);
+            }
+        }
         if (lane == 0) {
             row_m[i] = m;
             row_l[i] = l;
             row_best[i] = best;
-            bool ok = false;
-            if (draft && m > -INFINITY) {
-                if (greedy) {
-                    ok = d == best && u * q < 1.f;
-                } else {
-                    const float uq = u * q, pd = logit_weight(x, m, c) / l;
-                    ok = uq < pd;
-                    // next to the border the draft's own weight is taken in 64 bits: fp32's is off by |x - m| / T 2^-23
-                    // and a few 2^-24 at most, 2^-15 up to 100 units below the maximum
-                    if (fabsf(uq - pd) <= 0x1p-15f * pd) {
-                        const double w = x == m ? 1.0
-                                                : exp((static_cast<double>(x) - static_cast<double>(m)) /
-                                                      static_cast<double>(T));
-                        ok = static_cast<double>(u) * static_cast<double>(q) < w / l;
-                    }
-                }
-            }
             row_ok[i] = ok;
         }
     }
