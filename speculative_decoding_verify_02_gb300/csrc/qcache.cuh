@@ -29,7 +29,6 @@ struct FastDiv {
     __device__ __forceinline__ int div(int n) const {
         return static_cast<int>(static_cast<unsigned long long>(static_cast<uint32_t>(n)) * m >> shift);
     }
-    __device__ __forceinline__ int mod(int n, int d) const { return n - div(n) * d; }
 };
 
 struct QCacheArgs {
@@ -125,13 +124,6 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T *src) {
     }
     return r;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *src, float (&x)[8]) {
-    const Raw8<T> r = load_raw8<T, VEC>(src);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = r.at(k);
-}
-
 // Two fp32 values as e4m3 codes (round to nearest even, clamped to +-448): lo in bits 0-7.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
