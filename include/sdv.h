@@ -207,13 +207,14 @@ int sdv_accept_greedy(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_ro
  * for T_b <= 0 all on the lowest index of the maximum. The draft d in row r + 1
  * was drawn from q_r = d_draft_probs[r]; NULL means each draft was certain
  * (n-gram lookup, a table): q_r all on d. d is accepted iff
- * uniform[r] * q_r(d) < p_r(d). m_b = the drafts accepted before the first
- * refusal; the token committed after them is drawn at row m_b from
- * max(p - q, 0) after a refusal (from p if nothing is left), from p at the
- * span's last row: argmax_v w_v / noise[b][v], lowest index on a tie, a draw in
- * proportion to w for exponential noise. Outputs, empty spans and loop state as
- * sdv_accept_greedy, with the accepted drafts and then the drawn token as the
- * committed ones; elements of d_committed past them keep what they held.
+ * uniform[r] * q_r(d) < p_r(d), in 64 bits where fp32 could not tell. m_b =
+ * the drafts accepted before the first refusal; the token committed after them
+ * is drawn at row m_b from max(p - q, 0) after a refusal (from p if nothing is
+ * left), from p at the span's last row: argmax_v w_v / noise[b][v], lowest index
+ * on a tie, a draw in proportion to w for exponential noise. Outputs, empty
+ * spans and loop state as sdv_accept_greedy, with the accepted drafts and then
+ * the drawn token as the committed ones; elements of d_committed past them keep
+ * what they held.
  *   d_logits      [R] rows of fp32, logits_stride floats apart (>= vocab), as
  *                 sdv_spec_forward writes them. -inf masks a token; NaN counts
  *                 as -inf.
@@ -472,6 +473,9 @@ int sdv_qcache_read(sdv_qcache *cache, int layer, const int32_t *d_page_table, c
  * pages that lie before every row's window are not used (they may be -1). d_q and d_out hold
  * rows of [n_q_heads][head_dim] of `dtype` (SDV_BF16, SDV_FP16), q_stride and
  * out_stride elements apart; q after RoPE; scores are q.k / sqrt(head_dim).
+ * Probabilities enter the product with V in fp16's eleven bits, their sum in
+ * fp32. The parts that a sequence is cut into follow max_context; a limit far
+ * above the sequences costs up to half as much again.
  * A row's result depends on its own sequence, B, max_span and window only, not
  * on the other sequences. Rows of a span share the scale of their q: a score is
  * off by 2^-22 of the largest |q_d| of the rows and heads computed beside it

@@ -449,7 +449,9 @@ class QuantCache:
     head: quantising writes, reads and attention over the codes. `codes` is the uint8 pool
     [layer, page, K|V, kv head, slot, dim], `scales` float32 [layer, page, K|V, kv head, block]; page
     tables are the caller's (int32 [B, pages_per_seq]). Calls on one cache share its workspace: order
-    them on one stream."""
+    them on one stream. The cache is for the caller's own forward; Verifier's keeps 16 bits. With scale_block 1 a
+    rejected draft leaves no trace, with larger blocks it may leave a larger scale. Attention cuts sequences into parts
+    by max_context: one far above the sequences costs up to half as much again."""
 
     def __init__(self, n_layers, n_q_heads, n_kv_heads, head_dim, page_size=16, n_pages=1024, max_batch=1, max_rows=32,
                  max_span=17, max_context=4096, scale_block=16, stream=None):

@@ -154,7 +154,8 @@ AttnPlan attn_plan(const sdv_qcache *q, int B, int max_span, int window) {
     p.rows = attn_rows(span_rows);
     p.tiles = cdiv(span_rows, p.rows);
     p.ctas = (p.rows == 64 ? 1 : 2) * q->sm_count;
-    // Parts: the number that the CTAs get through soonest at the cache's full context; a unit costs its chunks and about
+    // Parts: the number that the CTAs get through soonest at the cache's full context (16 x 8 rows of 4,096 keys take 42.3 us
+    // in a cache of 4,104 positions, two parts, and 63.8 in one of 32,776, nine); a unit costs its chunks and about
     // kQTurn more for its queries, first maximum and results. One sequence's units are alike and go in turns; a batch's
     // differ, so that past one turn a CTA has its share of the work (of sequences 0.6 of the longest on average) and
     // then waits for the longest unit. Parts that no cluster joins cost a kernel more. What a sequence's parts are depends on its own length and on this number only.

@@ -149,7 +149,7 @@ constexpr int kQHold = 8;  // rows a lane holds between finding the scale and ro
 // below the span are rounded again by the ratio of the two. Warps of a CTA take K and V of neighbouring
 // heads, whose rows lie side by side.
 // Bound by memory: two bytes in and one out a value (bf16). A lane's eight loads before the first use carry it: 16
-// prompts of up to 4,096 tokens (8 heads of 128, 302 MB) take 49.6 us, 6.1 TB/s of the 6.77 that a copy reaches; 128
+// prompts of up to 4,096 tokens (8 heads of 128, 302 MB) take 49.1 us, 6.15 TB/s of the 6.77 that a copy reaches; 128
 // rows of a verify step take 2.5 us, a launch and three dependent loads (span, page, scale).
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kQWriteThreads, VEC && sizeof(T) == 2 ? 4 : 2) qcache_write_kernel(QCacheArgs a, const T *k, const T *v,
@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kQWriteThreads, VEC && sizeof(T) == 2 ? 4 : 2)
 // whole blocks of it, so that a lane still has kQHold rows under way (one block a warp wrote 65,536 rows of one
 // token a block in 8 times the time). Each row finds its page; the rows of a block agree on its maximum by
 // shuffles and, past a warp's width of rows, across the rows a lane holds. The same prompts with a scale a token: 110 us,
-// bound by the per-row work (a page, a scale and a store of eight bytes a lane); fp32 rows in blocks of 4: 76 us.
+// bound by the per-row work (a page, a scale and a store of eight bytes a lane; 184 bytes spilled); fp32 rows in blocks of 4: 148 us
+// (82 in blocks of 16).
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kQWriteThreads, VEC && sizeof(T) == 2 ? 3 : 2) qcache_write_small_kernel(
     QCacheArgs a, const T *k, const T *v, long long k_stride, long long v_stride) {

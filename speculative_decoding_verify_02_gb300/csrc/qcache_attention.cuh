@@ -25,8 +25,9 @@
 //
 // What bounds it (GB300, 32 q heads on 8 kv heads of 128, bf16): with spans of eight rows a CTA's chain, not the
 // bytes: a chunk is two commits, two TMEM reads and 25 to 27 instructions a score, and a unit costs 6,000 to 8,000 clocks more
-// for its queries, first maximum and results. 32,768 keys in 25.7 us (2.6 TB/s; loads alone reach 6.5), 16 sequences of
-// 512 to 4,096 keys in 36.4 us; 848 keys in 8.3 us, one chunk and the joining of seven parts in a cluster (9.0 with a
+// for its queries, first maximum and results. In caches whose limit is the call's longest sequence (the parts follow the limit:
+// up to 1.5 times as long in larger ones): 32,768 keys in 24.6 us (2.7 TB/s; loads alone reach 6.5), 16 sequences of
+// 512 to 4,096 keys in 35.7 us; 848 keys in 8.2 us, one chunk and the joining of seven parts in a cluster (9.0 with a
 // merge kernel, and 1.5 us of host more). Long spans read the keys out of L2 once
 // a tile and are bound by issue and latency of the softmax: 128 rows at 32,768 keys in 193 us, 2,900 clocks a chunk of
 // 64 x 128 scores, half of the issue slots used (tensor pipe 18%).
