@@ -3,7 +3,7 @@ the roundings that the kernel makes are counted, that a call repeats itself, and
 import numpy as np
 import pytest
 
-from tests.test_gpu_qcache import Setup, _dev, _i32
+from tests.test_gpu_qcache import Setup, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,27 @@ def test_caches_whose_limit_is_far_above_the_call(nq, nkv, D, lengths, spans, li
             other = err + mag * (2 * np.expm1((D + 8) * 2.0 ** -23 * top) + 2.0 ** -16)
             assert (np.abs(got[r] - o) <= 2.0 ** -8 * (np.abs(o) + other) + other).all()
     assert cache.get_status() == 0 and ctx <= limit
+
+
+def test_cache_made_and_used_on_a_side_stream():
+    """A cache that a side stream clears, writes, reads and attends on gives what the current stream's gives."""
+    import torch
+    from speculative_decoding_verify_02_gb300 import QuantCache
+    s = Setup(4, 2, 64, 16, 16, [0], [40], seed=1)
+    kv, _ = s.values((s.rows, 2, 2, 64), "bfloat16")
+    q, _ = s.values((s.rows, 4, 64), "bfloat16")
+    side, results = torch.cuda.Stream(), []
+    for stream in (None, side):
+        torch.cuda.synchronize()
+        cache = QuantCache(2, 4, 2, 64, n_pages=s.n_pages, max_rows=s.rows, max_span=s.rows, max_context=64, stream=stream)
+        table = _i32(np.resize(s.table, (1, 4)))
+        k, v, out = torch.zeros_like(kv[:, 0]), torch.zeros_like(kv[:, 1]), torch.zeros_like(q)
+        torch.cuda.synchronize()
+        cache.write(1, kv[:, 0], kv[:, 1], table, s.d_off, s.d_base, 1, s.rows, stream=stream)
+        cache.read(1, table, s.d_off, s.d_base, 1, s.rows, k, v, stream=stream)
+        cache.attention(1, q, table, s.d_off, s.d_base, 1, s.rows, out, stream=stream)
+        torch.cuda.synchronize()
+        assert cache.get_status() == 0 and int(cache.codes[0].sum()) == 0
+        results.append((k, v, out))
+    for a, b in zip(*results):
+        assert torch.equal(a, b) and bool(a.ne(0).any())
