@@ -489,6 +489,60 @@ int sdv_qcache_attention(sdv_qcache *cache, int layer, const void *d_q, int64_t 
 /* As sdv_get_status, for the cache's own status word. */
 int sdv_qcache_get_status(sdv_qcache *cache, int32_t *h_status);
 
+/* ---- Attention for groups of sequences that share a prefix: several continuations of one prompt, each verifying or
+ * decoding its own span. The prefix's K and V are read once for all of a group's rows instead of once a sequence. The pages
+ * have no counterpart; this is a variant of sdv_op_attention for a caller's own forward, over any 16-bit pool laid out as
+ * in sdv_kv_pool_bytes (a context's own one, too):
+ *   pool [layer][page][K = 0, V = 1][kv_head][slot (page_size)][head_dim], bf16 or fp16
+ * Position p of sequence b lives in page table[b][p / page_size], slot p % page_size. */
+typedef struct sdv_shared sdv_shared; /* opaque; owns only host-side state */
+typedef struct {
+    int n_layers, n_q_heads, n_kv_heads, head_dim; /* head_dim 64 or 128; n_kv_heads divides n_q_heads */
+    int page_size, n_pages;                        /* tokens a page (any; multiples of eight are fastest), pages in the pool */
+    int dtype;                                     /* SDV_BF16 or SDV_FP16: of the pool, of q and of the results */
+    int max_batch;                                 /* sequences a call, <= 256 */
+    int max_rows, max_span, max_context; /* rows of a call, rows of a sequence in it, positions of a sequence */
+} sdv_shared_cfg;
+/* Past these sdv_shared_bytes and sdv_shared_create answer SDV_ERR_UNSUPPORTED: 1024 q heads, 2^16 rows a call, 2^20 tokens
+ * a page, 2^30 positions a sequence, 2147483000 pool rows a layer (n_pages * 2 * n_kv_heads * page_size), and limits whose
+ * work (tiles of 256 rows x heads times pieces of 128 keys, all at their largest) passes 10^9. */
+
+/* Bytes of a pool of that shape, and of the caller-owned workspace (256-byte aligned: the status word and parts of results;
+ * about 2 max_rows n_q_heads (head_dim + 2) 4 bytes and 50 MB more). Ask on the device that will be used. */
+int sdv_shared_bytes(const sdv_shared_cfg *cfg, size_t *pool, size_t *workspace);
+
+/* Create on the current device, over the caller's pool (16-byte aligned; read only). Later calls must be made with that
+ * device current (else SDV_ERR_ARG). Calls on one handle share its workspace: order them on one stream or by events,
+ * replays of captured graphs included. */
+int sdv_shared_create(const sdv_shared_cfg *cfg, const void *d_pool, void *d_workspace, void *stream, sdv_shared **out);
+int sdv_shared_destroy(sdv_shared *s);
+
+/* Spans are packed as everywhere: row row_off[b] + i is position base[b] + i of sequence b and attends the keys t <= its own
+ * position pos, with window > 0 those of the last `window` positions, its own among them. The span's own K and V must
+ * have been written. d_q and d_out hold `rows` rows of [n_q_heads][head_dim], q_stride and out_stride elements apart (at most
+ * max_rows and B * max_span of them are used). A score is cap * tanh(q.k / sqrt(head_dim) / cap) - slope[head] * (pos - t);
+ * softcap 0: q.k / sqrt(head_dim); d_slopes [n_q_heads] fp32 or NULL: no bias.
+ * Groups: G > 0 cuts the batch into groups of neighbouring sequences, group g those from d_group_off[g] to
+ * d_group_off[g + 1] - 1 (d_group_off [G + 1], from 0 to B, never falling; G <= B, G <= 128), which hold the same K and V at
+ * positions 0 .. d_prefix_len[g] - 1: those are read through the table of the group's first sequence, so a partial page that
+ * each has its own copy of counts, too. The prefix lies before every span of the group: d_prefix_len[g] <= base[b]. G = 0:
+ * no prefixes (both pointers are ignored).
+ * d_page_table is [B][ceil(max_context / page_size)]; entries of pages that lie before every row's window are not used.
+ * Probabilities enter the product with V as two 16-bit planes, sixteen (bf16) or twenty-two bits, their sum in fp32. What K
+ * and V hold in positions that a row does not see, infinities and NaN among it, does not reach it; an infinity or NaN in a V
+ * that it does see makes at least that dim of its result NaN or infinite. In which order a row's keys are added follows the
+ * whole call's lengths.
+ * Device errors: a span longer than max_span or outside the call's rows, or a group that breaks the rules above
+ * (SDV_ERR_ARG), a span past max_context (SDV_ERR_CAPACITY): the sequence's rows become NaN. A page id outside [0, n_pages)
+ * sets SDV_ERR_CAPACITY and reads as zeros. */
+int sdv_shared_attention(sdv_shared *s, int layer, const void *d_q, int64_t q_stride, int rows, const int32_t *d_page_table,
+                         const int32_t *d_row_off, const int32_t *d_base, int B, const int32_t *d_group_off,
+                         const int32_t *d_prefix_len, int G, int max_span, int window, float softcap, const float *d_slopes,
+                         void *d_out, int64_t out_stride, void *stream);
+
+/* As sdv_get_status, for the handle's own status word. */
+int sdv_shared_get_status(sdv_shared *s, int32_t *h_status);
+
 /* Speculation cost governor ([TS] SpeculationCostGovernor and the paragraphs on
  * the shared governor): a host-side policy, one per (model, drafter, device),
  * that decides before each step whether it drafts, from the measured time of

@@ -35,6 +35,7 @@ EXPORTS = (
     "sdv_governor_decide", "sdv_governor_record", "sdv_governor_new_request", "sdv_governor_stats",
     "sdv_accept_sampled", "sdv_qcache_bytes", "sdv_qcache_create", "sdv_qcache_destroy", "sdv_qcache_write",
     "sdv_qcache_read", "sdv_qcache_attention", "sdv_qcache_get_status",
+    "sdv_shared_bytes", "sdv_shared_create", "sdv_shared_destroy", "sdv_shared_attention", "sdv_shared_get_status",
 )
 PHASES = ("prepare", "qkv_gemm", "attention", "o_gemm", "gateup_gemm", "down_gemm", "lmhead_gemm")
 # sdv_fwd_trace: stamps per CTA, CTAs per region (one region per launch of a forward)
@@ -63,6 +64,11 @@ class CacheCfg(ctypes.Structure):
 class QCacheCfg(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("n_layers", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
                                             "scale_block", "max_batch", "max_rows", "max_span", "max_context")]
+
+
+class SharedCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_layers", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                                            "dtype", "max_batch", "max_rows", "max_span", "max_context")]
 
 
 class GovernorCfg(ctypes.Structure):
@@ -118,6 +124,12 @@ def lib():
     L.sdv_qcache_read.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, i32, vp]
     L.sdv_qcache_attention.argtypes = [vp, i32, vp, i64, i32, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp]
     L.sdv_qcache_get_status.argtypes = [vp, P(ctypes.c_int32)]
+    L.sdv_shared_bytes.argtypes = [P(SharedCfg), P(sz), P(sz)]
+    L.sdv_shared_create.argtypes = [P(SharedCfg), vp, vp, vp, P(vp)]
+    L.sdv_shared_destroy.argtypes = [vp]
+    L.sdv_shared_attention.argtypes = [vp, i32, vp, i64, i32, vp, vp, vp, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, i64,
+                                       vp]
+    L.sdv_shared_get_status.argtypes = [vp, P(ctypes.c_int32)]
     L.sdv_rewind_cache.argtypes = [vp, vp, i32, vp]
     L.sdv_cache_seq_len.argtypes = [vp, vp, vp]
     L.sdv_page_table.argtypes = [vp, vp, vp, vp, vp]
@@ -536,4 +548,92 @@ class QuantCache:
     def get_status(self) -> int:
         v = ctypes.c_int32()
         _check(lib().sdv_qcache_get_status(self.cache, ctypes.byref(v)), "qcache_get_status")
+        return v.value
+
+
+class SharedAttention:
+    """Attention over a 16-bit paged pool [layer, page, K|V, kv head, slot, dim] (bf16 or fp16) for groups of sequences that
+    share a prefix, which is read once a group. `pool` is the caller's tensor of those bytes, a Verifier's `pool` for one; None
+    allocates one, `pool` of this object, cleared. Page tables are the caller's (int32 [B, pages_per_seq]). Calls on one object
+    share its workspace: order them on one stream."""
+
+    def __init__(self, n_layers, n_q_heads, n_kv_heads, head_dim, page_size=16, n_pages=1024, max_batch=1, max_rows=32,
+                 max_span=17, max_context=4096, dtype=None, pool=None, stream=None):
+        import torch
+        self.handle = None
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        kinds = {torch.bfloat16: 0, torch.float16: 1}
+        if self.dtype not in kinds:
+            raise ValueError(f"dtype: bf16 or fp16 is needed, got {self.dtype}")
+        self.cfg = SharedCfg(n_layers, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, kinds[self.dtype], max_batch, max_rows,
+                             max_span, max_context)
+        pool_bytes, ws_bytes, h = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_void_p()
+        # on the stream that clears them: memory that another stream had may still be in use there
+        with torch.cuda.stream(stream):
+            _check(lib().sdv_shared_bytes(ctypes.byref(self.cfg), ctypes.byref(pool_bytes), ctypes.byref(ws_bytes)), "shared_bytes")
+            if pool is None:
+                pool = torch.zeros(n_layers, n_pages, 2, n_kv_heads, page_size, head_dim, dtype=self.dtype, device="cuda")
+            if not pool.is_cuda or _elsewhere(pool) or not pool.is_contiguous() or \
+                    pool.numel() * pool.element_size() < pool_bytes.value or pool.dtype not in (self.dtype, torch.uint8):
+                raise ValueError(f"pool: a contiguous device tensor of {pool_bytes.value} bytes in {self.dtype} (or bytes) is "
+                                 f"needed, got {pool.dtype} {tuple(pool.shape)} on {pool.device}")
+            self.pool = pool
+            self.workspace = torch.empty(ws_bytes.value + 256, dtype=torch.uint8, device="cuda")
+            _check(lib().sdv_shared_create(ctypes.byref(self.cfg), _ptr(pool), (_ptr(self.workspace) + 255) // 256 * 256,
+                                           _stream(stream), ctypes.byref(h)), "shared_create")
+        self.handle = h
+        self.pages_per_seq = -(-max_context // page_size)
+        self._heads, self._dim = n_q_heads, head_dim
+
+    def close(self):
+        if self.handle:
+            lib().sdv_shared_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _rows(self, t, name):
+        """(address, rows, row stride) of a device tensor [R, heads, dim] with dense rows."""
+        shape = t.shape
+        if t.dtype is self.dtype and t.is_cuda and not (_many and _elsewhere(t)) and len(shape) == 3 and \
+                shape[1] == self._heads and shape[2] == self._dim:
+            st = t.stride()
+            if st[2] == 1 and (st[1] == self._dim or self._heads == 1):
+                return t.data_ptr(), shape[0], (st[0] if shape[0] > 1 else max(st[0], self._heads * self._dim))
+        raise ValueError(f"{name}: a device tensor [rows, {self._heads}, {self._dim}] of {self.dtype} with dense rows is needed, "
+                         f"got {t.dtype} {tuple(shape)} on {t.device}")
+
+    def attention(self, layer, q, page_table, row_off, base, B, max_span, out, group_off=None, prefix_len=None, G=0, window=0,
+                  softcap=0.0, slopes=None, stream=None):
+        """Attention of the rows q [R, n_q_heads, head_dim] at positions base[b] + i over their sequence's pages, into out.
+        With G > 0 groups, group_off [G + 1] cuts the batch and group g's sequences hold the same K and V in their first
+        prefix_len[g] positions, which are read through its first sequence's table. window: positions that a row sees, its
+        own the last (0: all); softcap: scores become softcap * tanh(score / softcap); slopes [n_q_heads] float32: less
+        slope * distance."""
+        qp, qr, qs = self._rows(q, "q")
+        op, orows, os_ = self._rows(out, "out")
+        if qr != orows:
+            raise ValueError("q and out: the same rows are needed")
+        i32 = _dtype("int32")
+        gp = pp = sp = 0
+        if G > 0:
+            if group_off is None or prefix_len is None:
+                raise ValueError("groups need group_off and prefix_len")
+            gp, pp = _vector(group_off, G + 1, "group_off", i32), _vector(prefix_len, G, "prefix_len", i32)
+        elif group_off is not None or prefix_len is not None:
+            raise ValueError("group_off and prefix_len belong to G > 0 groups")
+        if slopes is not None:
+            sp = _vector(slopes, self._heads, "slopes", _dtype("float32"))
+        _check(lib().sdv_shared_attention(
+            self.handle, layer, qp, qs, qr, _int_rows(page_table, B, self.pages_per_seq, "page_table"),
+            _vector(row_off, B + 1, "row_off", i32), _vector(base, B, "base", i32), B, gp, pp, G, max_span, window, softcap, sp,
+            op, os_, _stream(stream)), "shared_attention")
+
+    def get_status(self) -> int:
+        v = ctypes.c_int32()
+        _check(lib().sdv_shared_get_status(self.handle, ctypes.byref(v)), "shared_get_status")
         return v.value

@@ -1,0 +1,909 @@
+// Attention over a 16-bit paged cache for groups of sequences that share a prefix.
+//
+// The keys of a group's prefix are the same for every row of the group, so its rows are the rows of one product:
+//     S [rows x 128 keys] = Q K^T,   O [rows x dims] += P V,   rows = (row of the group) x (head of the kv head's group)
+// and the prefix is read once for all of them. Each sequence's own keys (the rest of its prompt, what it generated, its
+// span) are a product of their own. A row's parts join as o = sum 2^(M_i - M) o_i / sum 2^(M_i - M) l_i.
+//
+// A score is z = cap tanh(q.k / (sqrt(D) cap)) - slope_h (pos - t) for key t <= pos (no cap: q.k / sqrt(D)), within the
+// window if there is one.
+#pragma once
+
+#include "qcache_attention.cuh"
+
+namespace sdv {
+
+constexpr int kSKeys = 128;      // keys of a chunk
+constexpr int kSTile = 256;      // rows of a tile: one of 128 for each of two softmax warpgroups
+constexpr int kSGroups = 128;    // groups of a call at most
+constexpr int kSBatch = 256;     // sequences of a call at most
+constexpr int kSEntries = kSGroups + kSBatch;
+constexpr int kSOverhead = 3;    // what a tile's queries and results cost, in chunks
+constexpr float kSGrow = 8.f;    // a row's reference follows its maximum once that is more than 2^8 above it
+constexpr int kSThreads = 384;   // two softmax warpgroups, the load warp, the MMA warp; as many as entries
+
+struct SharedArgs {
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;  // elements between rows
+    const void *pool;                // the layer's [n_pages][2][nkv][page_size][D]
+    const int *page_table, *row_off, *base, *group_off, *prefix_len;
+    const float *slopes;             // [nq], or null
+    int *status;
+    int pages_per_seq, page_size, n_pages, nq, nkv, grp, B, G, max_span, max_rows, max_context, window;
+    int q_vec, out_vec;              // rows are 16-byte aligned
+    int box_rows, pool_rows;         // rows of a TMA box (0: pages that none fits); rows of the layer's pool: a box there reads zeros
+    FastDiv by_page, by_grp;
+    float scale, scale_log2, cap;    // 1 / sqrt(D), log2(e) / sqrt(D), the cap or 0
+    int ctas;                        // CTAs of the attention kernel, which the cut into parts follows
+    int part_rows;                   // partial rows of a kv head
+    float *part_o;                   // partial results: [nkv][part_rows] rows of sequences' own tiles, as many of prefix tiles,
+                                     // [ctas][kSTile] of pieces that begin inside of a tile
+    float2 *part_ml;                 // (M, l) of each
+    struct SEntry *plan;             // the plan's entries, for the kernel that joins the parts
+    int *plan_cut;                   // its q and ov
+    int *row_seq;                    // [max_rows]: a row's sequence, kRowNone, or kRowRefused
+};
+constexpr int kRowNone = -1, kRowRefused = -2;
+
+// ------------------------------------------------------------------ the work and its cut
+// Work is a list of entries, the groups' prefixes and then the sequences' own keys. An entry is tiles of up to kSTile rows
+// for each kv head, a tile is chunks. Chunks lie one behind another on a line of costs (a tile's first costs `ov` more, and a
+// chunk of more than 128 rows counts twice), and CTA i takes those that begin in [i q, (i + 1) q). So the CTAs finish
+// together whatever the lengths are, every one of them knows the whole cut, and a tile is cut where the line is.
+// The lengths are read once, side by side, and all else is worked out in shared memory: as reads that wait for one another it
+// took 20 us.
+struct SEntry {
+    int start, end;   // its part of the line
+    int b;            // sequence whose page table is read
+    int r0, rows;     // rows of the call
+    int p0;           // own: position of the first row; prefix: -1
+    int kv0, kv1;     // its keys
+    int lo;           // first key that any row sees
+    int max_lo, min_hi;  // every row sees [max_lo, min_hi)
+    int c0, nc;       // first chunk, chunks
+    int per, wc;      // cost of a tile, of a chunk
+    int group;        // own: its group, -1 without one
+};
+struct SPlan {
+    SEntry e[kSEntries];
+    int row_off[kSBatch + 1], base[kSBatch], group_off[kSGroups + 1], prefix[kSGroups];
+    int g_min[kSGroups], g_max[kSGroups];  // lowest and highest position of a group's rows
+    int total, q, ov, ok, steps, tiles;
+    int warp_sum[kSThreads / 32];
+};
+
+__device__ __forceinline__ int shared_last(const int *off, int n, int v) {  // the last of n offsets that is not above v
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (off[mid] <= v) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+__device__ __forceinline__ int shared_tiles(const SharedArgs &a, const SEntry &n) { return (n.rows * a.grp + kSTile - 1) / kSTile; }
+
+// The plan, by kSThreads threads. Thread e works out entry e: first the sequences', a sequence being refused as by
+// qcache_span or where its rows do not all lie behind its group's prefix, then the groups'.
+__device__ __forceinline__ void shared_plan(const SharedArgs &a, SPlan &pl, bool writes) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid <= a.B) pl.row_off[tid] = a.row_off[tid];
+    if (tid < a.B) pl.base[tid] = a.base[tid];
+    if (tid <= a.G && a.G) pl.group_off[tid] = a.group_off[tid];
+    if (tid < a.G) pl.prefix[tid] = a.prefix_len[tid], pl.g_min[tid] = 0x7fffffff, pl.g_max[tid] = -1;
+    if (tid == 0) pl.ok = 1, pl.steps = pl.tiles = 0;
+    __syncthreads();
+    if (tid < a.G && (pl.group_off[tid] > pl.group_off[tid + 1] || (tid == 0 && pl.group_off[0] != 0) ||
+                      (tid == a.G - 1 && pl.group_off[a.G] != a.B)))
+        pl.ok = 0;
+    __syncthreads();
+    SEntry n{};
+    n.group = -1;
+    int code = SDV_OK;
+    const int b = tid - a.G;
+    if (b >= 0 && b < a.B) {
+        n.b = b;
+        n.r0 = pl.row_off[b];
+        n.rows = pl.row_off[b + 1] - n.r0;
+        n.p0 = pl.base[b];
+        if (n.rows != 0) {
+            if (n.rows < 0 || n.r0 < 0 || n.rows > a.max_rows || n.r0 > a.max_rows - n.rows || n.rows > a.max_span) {
+                code = SDV_ERR_ARG;
+            } else if (n.p0 < 0 || n.p0 > a.max_context - n.rows) {
+                code = SDV_ERR_CAPACITY;
+            } else if (a.G) {
+                code = SDV_ERR_ARG;
+                if (pl.ok) {
+                    const int g = shared_last(pl.group_off, a.G, b);
+                    const int first = pl.row_off[pl.group_off[g]], last = pl.row_off[pl.group_off[g + 1]];
+                    n.kv0 = pl.prefix[g];
+                    if (n.kv0 >= 0 && n.kv0 <= n.p0 && first >= 0 && last <= a.max_rows && n.r0 >= first && n.r0 + n.rows <= last) {
+                        code = SDV_OK;
+                        n.group = g;
+                        atomicMin(&pl.g_min[g], n.p0);
+                        atomicMax(&pl.g_max[g], n.p0 + n.rows - 1);
+                    }
+                }
+            }
+            if (code != SDV_OK) {
+                n.rows = 0;
+                if (writes) set_status(a.status, code);
+            }
+        }
+        n.kv1 = n.p0 + n.rows;
+        n.lo = a.window > 0 ? max(n.kv0, n.p0 - a.window + 1) : n.kv0;
+        n.max_lo = a.window > 0 ? max(n.kv0, n.kv1 - a.window) : n.kv0;
+        n.min_hi = n.p0 + 1;
+    }
+    __syncthreads();
+    if (tid < a.G && pl.ok && pl.g_min[tid] <= pl.g_max[tid]) {  // some row of the group is read
+        n.p0 = -1;
+        n.b = pl.group_off[tid];
+        n.r0 = pl.row_off[n.b];
+        n.rows = pl.row_off[pl.group_off[tid + 1]] - n.r0;
+        n.kv1 = pl.prefix[tid];
+        n.lo = a.window > 0 ? max(0, pl.g_min[tid] - a.window + 1) : 0;
+        n.max_lo = a.window > 0 ? max(0, pl.g_max[tid] - a.window + 1) : 0;
+        n.min_hi = n.kv1;
+    }
+    n.c0 = n.lo / kSKeys;
+    n.nc = n.rows && n.lo < n.kv1 ? (n.kv1 + kSKeys - 1) / kSKeys - n.c0 : 0;
+    n.wc = n.rows * a.grp > kSTile / 2 ? 2 : 1;
+    const int tiles = n.nc ? a.nkv * shared_tiles(a, n) : 0, steps = tiles * n.nc * n.wc;
+    const int all_steps = __reduce_add_sync(0xffffffffu, steps), all_tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (lane == 0 && all_steps) {
+        atomicAdd(&pl.steps, all_steps);
+        atomicAdd(&pl.tiles, all_tiles);
+    }
+    __syncthreads();
+    // with a chunk for each CTA at most, the cut is one a chunk
+    const int ov = pl.steps <= a.ctas ? 0 : kSOverhead, cost = steps + ov * tiles;
+    int sum = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) pl.warp_sum[warp] = sum;
+    __syncthreads();
+    int before = lane < warp ? pl.warp_sum[lane] : 0;
+    before = __reduce_add_sync(0xffffffffu, before);
+    n.end = before + sum;
+    n.start = n.end - cost;
+    n.per = ov + n.nc * n.wc;
+    const int q = max(1, (pl.steps + ov * pl.tiles + a.ctas - 1) / a.ctas);
+    pl.e[tid] = n;
+    if (tid == 0) pl.total = pl.steps + ov * pl.tiles, pl.ov = ov, pl.q = q;
+    __syncthreads();
+    if (writes) {
+        if (tid < a.G + a.B) a.plan[tid] = n;
+        if (tid == 0) a.plan_cut[0] = q, a.plan_cut[1] = ov;
+        for (int r = tid; r < a.max_rows; r += kSThreads) {
+            const int of = shared_last(pl.row_off, a.B, r);
+            const bool in = r >= pl.row_off[of] && r < pl.row_off[of + 1];
+            a.row_seq[r] = !in ? kRowNone : pl.e[a.G + of].rows ? of : kRowRefused;
+        }
+    }
+}
+// First chunk of a tile that begins at or after `rel` on the line, from the tile's start.
+__device__ __forceinline__ int shared_chunk(const SEntry &n, int ov, int rel) {
+    if (rel <= 0) return 0;
+    return min(n.nc, rel <= ov + n.wc ? 1 : (rel - ov + n.wc - 1) / n.wc);
+}
+struct SPiece {
+    int entry;
+    int h, tile, rows;  // kv head, tile, rows x heads of it
+    int c0, n;          // its first chunk, from the entry's first, and how many
+    bool more;          // it begins inside of the tile: the result goes to the CTA's own rows
+};
+// The next piece of the line's [x, x1), false at its end.
+__device__ __forceinline__ bool shared_next(const SharedArgs &a, const SPlan &pl, int &x, int x1, SPiece &p) {
+    while (x < x1) {
+        int lo = 0, hi = a.G + a.B - 1;  // the first entry that ends behind x
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (pl.e[mid].end > x) hi = mid; else lo = mid + 1;
+        }
+        const SEntry &n = pl.e[lo];
+        const int per = n.per, th = (x - n.start) / per, at = n.start + th * per, tiles = shared_tiles(a, n);
+        const int stop = min(x1, at + per), from = shared_chunk(n, pl.ov, x - at);
+        const int to = stop == at + per ? n.nc : shared_chunk(n, pl.ov, stop - at);
+        x = stop;
+        if (to <= from) continue;
+        p.entry = lo;
+        p.h = th / tiles;
+        p.tile = th - p.h * tiles;
+        p.rows = min(kSTile, n.rows * a.grp - p.tile * kSTile);
+        p.c0 = from;
+        p.n = to - from;
+        p.more = from > 0;
+        return true;
+    }
+    return false;
+}
+// Where a tile's partial result lies: its first row.
+__device__ __forceinline__ long long shared_slot(const SharedArgs &a, bool prefix, int r0, int h, int tile, int cta) {
+    const long long side = static_cast<long long>(a.nkv) * a.part_rows;
+    if (cta >= 0) return 2 * side + static_cast<long long>(cta) * kSTile;
+    return (prefix ? side : 0) + static_cast<long long>(h) * a.part_rows + r0 * a.grp + tile * kSTile;
+}
+
+// ------------------------------------------------------------------ PTX
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor, kind::f16: fp32 D; bf16 or fp16 operands; mn: B runs along N in memory.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool mn) {
+    constexpr uint32_t t = __is_same(T, bf16) ? 1u : 0u;
+    return (1u << 4) | (t << 7) | (t << 10) | (mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+// 32 TMEM columns of this thread's lane; tmem_wait_ld before the values are used.
+__device__ __forceinline__ void tmem_get32(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_pass32(float *v) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]),
+                          "+f"(v[i + 7]));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_put32(uint32_t taddr, const float *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
+        "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]),
+        "f"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+// A box of 64 columns of the pool's rows into shared memory, completion counted on `bar`.
+__device__ __forceinline__ void load_box_at(uint32_t dst, const CUtensorMap *tm, uint64_t *bar, int col, int row) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(col), "r"(row)
+        : "memory");
+}
+
+// Two probabilities as a pair of 16-bit planes, each two to a word: p = hi + lo to 2^-17 (bf16) or 2^-23 (fp16).
+template <typename T>
+__device__ __forceinline__ void split_p(float2 p, uint32_t &hi, uint32_t &lo) {
+    if constexpr (__is_same(T, bf16)) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        const float2 r = __fadd2_rn(p, make_float2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u)));
+        const __nv_bfloat162 l = __floats2bfloat162_rn(r.x, r.y);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    } else {
+        const __half2 h = __floats2half2_rn(p.x, p.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        const float2 f = __half22float2(h), r = __fadd2_rn(p, make_float2(-f.x, -f.y));
+        const __half2 l = __floats2half2_rn(r.x, r.y);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float x, float y) {
+    if constexpr (__is_same(T, bf16)) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+// Whether any of eight 16-bit values is an infinity or a NaN.
+template <typename T>
+__device__ __forceinline__ bool not_finite8(uint4 u) {
+    constexpr uint32_t e = __is_same(T, bf16) ? 0x7f80u : 0x7c00u, ee = e | e << 16;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = (i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w) & ee;
+        bad |= (w & 0xffffu) == e || (w >> 16) == e;
+    }
+    return bad;
+}
+
+struct SShared {
+    uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full;
+    uint32_t tmem;
+    uint32_t bad[2][2][4];
+    float2 ml[2][128];  // (M, l) of the rows that two warpgroups share
+    SPlan plan;
+};
+
+template <typename T, int D_>
+struct STile {
+    static constexpr int D = D_, HALVES = D / 64;
+    static constexpr int SLOT = kSKeys * D * 2;              // bytes of a K or V chunk, as halves of 64 columns
+    static constexpr int Q_BYTES = 128 * D * 2;              // and of 128 rows of Q
+    static constexpr int SLOTS = D == 128 ? 4 : 8;
+    static constexpr int SMEM = 2 * Q_BYTES + SLOTS * SLOT + static_cast<int>((sizeof(SShared) + 127) / 128 * 128);
+    static constexpr int O_COL = 256;                        // TMEM: S of each warpgroup, then O of each
+    // p carries a factor 2^6 in fp16, whose smallest values lie at 2^-24; 2^(6 + kSGrow) is its largest
+    static constexpr float BIAS = __is_same(T, bf16) ? 0.f : 6.f;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+// ------------------------------------------------------------------ attention
+// One CTA an SM; a piece of the line after another. EXTRA: scores with a cap or a bias.
+template <typename T, int D, bool EXTRA>
+__global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_constant__ CUtensorMap pool,
+                                                                   const __grid_constant__ SharedArgs a) {
+    typedef STile<T, D> Q;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t q_s = smem_u32(smem_raw), kv_s = q_s + 2 * Q::Q_BYTES;
+    SShared &sh = *reinterpret_cast<SShared *>(smem_raw + 2 * Q::Q_BYTES + Q::SLOTS * Q::SLOT);
+    const bool is_load = warp == 8, is_mma = warp == 9;
+    if (tid == 0) {
+        for (int i = 0; i < Q::SLOTS; ++i) {
+            mbar_init(&sh.full[i], a.box_rows ? 1 : 32);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.o_done[i], 1);
+        }
+        mbar_init(&sh.q_full, 256);
+        fence_mbar_init();
+    }
+    if (is_mma) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();  // after the wait: what starts behind this kernel may read what came before it
+    tc_fence_before();
+    shared_plan(a, sh.plan, blockIdx.x == 0);
+    tc_fence_after();
+    const SPlan &pl = sh.plan;
+    const uint32_t tmem = sh.tmem;
+    const int cta = blockIdx.x;
+    int x = cta * pl.q;
+    const int x1 = min(pl.total, x + pl.q);
+    bool ok = true;  // false once a wait gave up: the rest runs without waiting, and the status word says so
+    SPiece p;
+
+    if (is_load) {
+        // ---- the load warp: K and V chunks in the order in which the products want them
+        int slot = 0;
+        const int nb = a.box_rows ? kSKeys / a.box_rows : 0;
+        while (shared_next(a, pl, x, x1, p)) {
+            const SEntry &en = pl.e[p.entry];
+            const int *table = a.page_table + static_cast<size_t>(en.b) * a.pages_per_seq;
+            const int n = p.n, t00 = (en.c0 + p.c0) * kSKeys, seen_lo = en.lo, seen_hi = en.kv1;
+            // In boxes a lane brings one; its page is asked for a chunk ahead. A chunk's V lies behind its K in the same pages.
+            const int j = a.box_rows ? lane % nb : 0, half = a.box_rows ? lane / nb : 0;
+            int asked = -1, rows[2] = {0, 0};  // the next chunk's page, pool rows of the last two chunks' boxes
+            auto wants = [&](int c) {
+                const int t = t00 + c * kSKeys + j * a.box_rows;
+                return c < n && half < Q::HALVES && t + a.box_rows > seen_lo && t < seen_hi;
+            };
+            auto ask = [&](int c) { return wants(c) ? table[a.by_page.div(t00 + c * kSKeys + j * a.box_rows)] : -1; };
+            if (a.box_rows) asked = ask(0);
+            auto put = [&](int c, bool v) {
+                const int st = slot % Q::SLOTS, use = slot / Q::SLOTS;
+                const uint32_t dst = kv_s + st * Q::SLOT;
+                ++slot;
+                if (a.box_rows) {
+                    if (!v) {  // a box outside the keys that some row sees is zeros
+                        const int t = t00 + c * kSKeys + j * a.box_rows, page = asked;
+                        int row = a.pool_rows;
+                        if (wants(c)) {
+                            if (page >= 0 && page < a.n_pages)
+                                row = (page * 2 * a.nkv + p.h) * a.page_size + t - a.by_page.div(t) * a.page_size;
+                            else
+                                set_status(a.status, SDV_ERR_CAPACITY);
+                        }
+                        if (c & 1) rows[1] = row; else rows[0] = row;
+                        asked = ask(c + 1);
+                    }
+                    int row = c & 1 ? rows[1] : rows[0];
+                    if (v && row < a.pool_rows) row += a.nkv * a.page_size;
+                    if (use > 0 && ok) ok = mbar_wait(&sh.empty[st], (use - 1) & 1);
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], Q::SLOT);
+                    __syncwarp();
+                    if (lane < nb * Q::HALVES)
+                        load_box_at(dst + half * (kSKeys * 128) + j * a.box_rows * 128, &pool, &sh.full[st], half * 64, row);
+                } else {
+                    const int t0 = t00 + c * kSKeys;
+                    if (use > 0 && ok) ok = mbar_wait(&sh.empty[st], (use - 1) & 1);
+                    constexpr int PPR = D / 8, RPI = 32 / PPR;  // 16-byte pieces of a row, rows a copy
+                    const int piece = lane % PPR;
+#pragma unroll 4
+                    for (int r = lane / PPR; r < kSKeys; r += RPI) {
+                        const int t = t0 + r;
+                        const uint8_t *src = static_cast<const uint8_t *>(a.pool);
+                        bool in = false;
+                        if (t >= seen_lo && t < seen_hi) {
+                            const int at = a.by_page.div(t), page = table[at];
+                            in = page >= 0 && page < a.n_pages;
+                            if (in)
+                                src += (((static_cast<size_t>(page) * 2 + (v ? 1 : 0)) * a.nkv + p.h) * a.page_size + t -
+                                        at * a.page_size) * (D * 2) + piece * 16;
+                            else
+                                set_status(a.status, SDV_ERR_CAPACITY);
+                        }
+                        cp_async16(dst + piece / 8 * (kSKeys * 128) + line_offset(r, piece % 8 * 16, 128), src, in);
+                    }
+                    cp_async_arrive(&sh.full[st]);
+                }
+            };
+            const bool wide = p.rows > 128;
+            // K 0, K 1, V 0, K 2, V 1, ..; a wide tile wants K 0, V 0, K 1, V 1, ..
+#pragma unroll 1
+            for (int i = 0; i < 2 * n; ++i) {
+                const bool v = wide ? i & 1 : i == 2 * n - 1 || (i > 0 && i % 2 == 0);
+                put(wide ? i >> 1 : v ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2, v);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok) {  // no copy may land after this CTA's shared memory is someone else's
+            for (int i = max(0, slot - Q::SLOTS); i < slot; ++i) mbar_wait(&sh.full[i % Q::SLOTS], i / Q::SLOTS & 1);
+            if (lane == 0) set_status(a.status, SDV_ERR_DEVICE_TIMEOUT);
+        }
+    } else if (is_mma) {
+        // ---- MMA issue. Step s of a piece is softmax warpgroup s % 2's: of its own 128 rows of a tile of more than 128, every
+        // chunk for each in turn, else of the tile's rows and every other chunk.
+        // The whole warp keeps step and one lane issues: with a lane of its own (lane 0 alone in the loop) an MMA took 80 to
+        // 100 clocks to issue, its operands passing from lane to uniform registers.
+        constexpr uint32_t id_s = idesc_16<T>(128, kSKeys, false), id_o = idesc_16<T>(128, D, true);
+        int ring = 0, pieces = 0, done[2] = {0, 0};  // slots before this piece, pieces, steps of each warpgroup
+        while (shared_next(a, pl, x, x1, p)) {
+            const bool wide = p.rows > 128;
+            const int n = p.n, steps = wide ? 2 * n : n;
+            auto k_slot = [&](int c) { return ring + (wide ? 2 * c : c ? 2 * c - 1 : 0); };
+            auto v_slot = [&](int c) { return ring + (wide ? 2 * c + 1 : c == n - 1 ? 2 * n - 1 : 2 * c + 2); };
+            if (ok) ok = mbar_wait(&sh.q_full, pieces & 1);
+            ++pieces;
+            tc_fence_after();
+            // Waits until the slots at `v` and `k` of the ring are full and, for step s >= 0, its probabilities are there: a lane
+            // each, since a look at a barrier takes 100 clocks.
+            auto await = [&](int s, int v, int k) {
+                const int at = lane == 1 ? v : k;
+                uint64_t *bar = lane == 0 ? &sh.p_full[s & 1] : &sh.full[at % Q::SLOTS];
+                const uint32_t parity = lane == 0 ? (done[s & 1] + (s >> 1)) & 1 : at / Q::SLOTS & 1;
+                const bool mine = lane == 0 ? s >= 0 : lane == 1 ? v >= 0 : lane == 2 && k >= 0;
+                if (ok && !__all_sync(0xffffffffu, !mine || mbar_try_wait(bar, parity))) {
+                    const uint64_t since = globaltimer();
+                    while (!__all_sync(0xffffffffu, !mine || mbar_try_wait(bar, parity)))
+                        if (__any_sync(0xffffffffu, globaltimer() - since > kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                }
+                tc_fence_after();
+                fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
+            };
+            auto scores = [&](int s) {  // one lane
+                const int w = s & 1, c = wide ? s >> 1 : s, st = k_slot(c) % Q::SLOTS;
+                const uint64_t kd = sw128_desc(kv_s + st * Q::SLOT), qd = sw128_desc(q_s + (wide && w ? Q::Q_BYTES : 0));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4 * (128 * 128) + k % 4 * 32) >> 4;
+                    umma_bf16(tmem + w * kSKeys, qd + off, kd + off, id_s, k > 0);
+                }
+                umma_commit(&sh.s_full[w]);
+                if (!wide || w) umma_commit(&sh.empty[st]);
+            };
+#pragma unroll 1
+            for (int s = -2; s < steps; ++s) {  // the products with V of step s, the scores of step s + 2
+                const int w = s & 1, c = wide ? s >> 1 : s, at = v_slot(c), ahead = wide ? (s + 2) >> 1 : s + 2;
+                const bool more = s + 2 < steps;
+                await(s, s >= 0 ? at : -1, more ? k_slot(ahead) : -1);
+                if (elect_one()) {
+                    if (s >= 0) {
+                        const int st = at % Q::SLOTS;
+                        const uint64_t vd = line_desc(kv_s + st * Q::SLOT, 128, kSKeys * 128);
+                        const uint32_t p_t = tmem + w * kSKeys, o_t = tmem + Q::O_COL + w * 128;
+#pragma unroll
+                        for (int k = 0; k < 2 * kSKeys / 16; ++k)  // 16 keys' hi plane, then lo: eight columns each
+                            umma_f16_ts(o_t, p_t + k / 4 * 32 + k % 2 * 16 + k / 2 % 2 * 8, vd + (k / 2 * 2048 >> 4), id_o, s > 1 || k > 0);
+                        umma_commit(&sh.o_done[w]);
+                        if (!wide || w) umma_commit(&sh.empty[st]);
+                    }
+                    if (more) scores(s + 2);
+                }
+                __syncwarp();
+            }
+            done[0] += (steps + 1) >> 1;
+            done[1] += steps >> 1;
+            ring += 2 * n;
+        }
+        if (!ok && lane == 0) set_status(a.status, SDV_ERR_DEVICE_TIMEOUT);
+        __syncwarp();
+    } else if (warp < 8) {
+        // ---- softmax: a thread is a row of its warpgroup's 128
+        const int w = warp / 4, m = tid % 128;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        const uint32_t s_t = tmem + lanes + w * kSKeys, o_t = tmem + lanes + Q::O_COL + w * 128;
+        int done = 0, ring = 0;  // this warpgroup's steps, slots before this piece
+        while (shared_next(a, pl, x, x1, p)) {
+            const SEntry &en = pl.e[p.entry];
+            const bool wide = p.rows > 128, prefix = en.p0 < 0;
+            const int n = p.n, r00 = en.r0, kv_lo = en.lo, kv_end = en.kv1, t00 = (en.c0 + p.c0) * kSKeys, steps = wide ? n : (n + 1 - w) >> 1;
+            const int all_lo = en.max_lo, all_hi = en.min_hi;  // what every row sees
+            const int m0 = p.tile * kSTile, row0 = wide ? w * 128 : 0, n_rows = min(128, p.rows - row0);
+            named_bar_sync(1, 256);  // nobody reads the last piece's rows or results any more
+            {
+                // queries into their swizzled halves, 16 bytes a thread at a time, zeros behind the tile's rows
+                constexpr int PPR = D / 8;
+                const uint32_t dst = q_s + (wide ? w * Q::Q_BYTES : 0);
+                const int first = wide ? m : tid, step = wide ? 128 : 256;
+                constexpr int N = PPR / 2;  // pieces of a thread, or of half of its pieces of a wide tile: all on their way at once
+                for (int e0 = first; e0 < 128 * PPR; e0 += N * step) {
+                    Raw8<T> raw[N];
+#pragma unroll
+                    for (int u = 0; u < N; ++u) {
+                        const int e = e0 + u * step, r = e / PPR, piece = e % PPR;
+                        raw[u].u[0] = make_uint4(0, 0, 0, 0);
+                        if (r < n_rows) {
+                            const int mm = m0 + row0 + r, i = a.by_grp.div(mm);
+                            const T *src = static_cast<const T *>(a.q) + (r00 + i) * a.q_stride +
+                                           (p.h * a.grp + mm - i * a.grp) * D + piece * 8;
+                            raw[u] = a.q_vec ? load_raw8<T, true>(src) : load_raw8<T, false>(src);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < N; ++u) {
+                        const int e = e0 + u * step, r = e / PPR, piece = e % PPR;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece / 8 * (128 * 128) +
+                                                                                      line_offset(r, piece % 8 * 16, 128)),
+                                     "r"(raw[u].u[0].x), "r"(raw[u].u[0].y), "r"(raw[u].u[0].z), "r"(raw[u].u[0].w)
+                                     : "memory");
+                    }
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(&sh.q_full);
+            // this thread's row: its position and the keys it sees
+            const int mm = m0 + row0 + max(0, min(m, n_rows - 1)), i = a.by_grp.div(mm), row = r00 + i;
+            const int hq = p.h * a.grp + mm - i * a.grp;
+            int pos = en.p0 + i;
+            if (prefix && (a.window > 0 || EXTRA)) {  // a prefix's rows belong to several sequences
+                const int b = shared_last(pl.row_off, a.B, row);
+                pos = pl.base[b] + row - pl.row_off[b];
+            }
+            const int see_hi = prefix ? kv_end : pos + 1, see_lo = a.window > 0 ? max(en.kv0, pos - a.window + 1) : en.kv0;
+            float slope2 = 0.f;  // log2(e) slope
+            if constexpr (EXTRA) slope2 = a.slopes ? a.slopes[hq] * 1.4426950408889634f : 0.f;
+            const bool live = warp % 4 * 32 < n_rows;  // rows of this warp
+            float M = kQNoRef;
+            float2 l2 = make_float2(0.f, 0.f);
+            bool poisoned = false;
+            for (int j = 0; j < steps; ++j) {
+                const int c = wide ? j : 2 * j + w, t0 = t00 + c * kSKeys;
+                const bool masked = t0 + kSKeys > all_hi || t0 < all_lo;
+                if (ok) ok = mbar_wait(&sh.s_full[w], (done + j) & 1);
+                tc_fence_after();
+                if (masked) {
+                    // (the scores are there, so of the chunk's slots the uses before this one are over)
+                    // V rows that some row does not see must not reach it: 0 times an infinity or a NaN is none. They are
+                    // cleared where no row sees them, and where they are not finite, which then spoils the rows that do.
+                    const int at = ring + (wide ? 2 * c + 1 : c == n - 1 ? 2 * n - 1 : 2 * c + 2), st = at % Q::SLOTS;
+                    if (ok) ok = mbar_wait(&sh.full[st], at / Q::SLOTS & 1);
+                    constexpr int ALL = Q::HALVES * 8;
+                    const int q0 = wide ? w * (ALL / 2) : 0, q1 = wide ? q0 + ALL / 2 : ALL;  // this thread's pieces of row m
+                    const uint32_t v_s = kv_s + st * Q::SLOT;
+                    bool bad = false;
+                    const bool in = t0 + m >= kv_lo && t0 + m < kv_end;
+                    if (in) {
+#pragma unroll 4
+                        for (int k = q0; k < q1; ++k) {
+                            uint4 u;
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                                         : "r"(v_s + k / 8 * (kSKeys * 128) + line_offset(m, k % 8 * 16, 128)));
+                            bad |= not_finite8<T>(u);
+                        }
+                    }
+                    if (!in || bad)
+                        for (int k = q0; k < q1; ++k)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v_s + k / 8 * (kSKeys * 128) +
+                                                                                          line_offset(m, k % 8 * 16, 128)),
+                                         "r"(0)
+                                         : "memory");
+                    const uint32_t word = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0) sh.bad[c & 1][w][warp % 4] = word;
+                    fence_async_smem();
+                    if (wide)
+                        named_bar_sync(2, 256);
+                    else if (w == 0)
+                        named_bar_sync(3, 128);
+                    else
+                        named_bar_sync(4, 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t b = sh.bad[c & 1][w][k] | (wide ? sh.bad[c & 1][1 - w][k] : 0u);
+                        const int lo = min(max(see_lo - t0 - 32 * k, 0), 32), hi = min(max(see_hi - t0 - 32 * k, 0), 32);
+                        const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1, below_lo = lo == 32 ? 0xffffffffu : (1u << lo) - 1;
+                        poisoned |= (b & below_hi & ~below_lo) != 0;
+                    }
+                }
+                if (live) {
+                    // 32 keys at a time, in loops that stay loops: unrolled, a piece's first step waited 6,000 clocks for its
+                    // own instructions
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < kSKeys; k0 += 32) {
+                        float s[32];
+                        tmem_get32(s_t + k0, s);
+                        tmem_wait_ld();
+                        tmem_pass32(s);
+                        if constexpr (EXTRA) {
+                            // in log2 units; cap tanh(z / cap) = cap (1 - 2 / (1 + 2^(2 log2(e) z / cap)))
+                            if (a.cap > 0.f) {
+                                const float up = 2.f * a.scale_log2 / a.cap, cap2 = a.cap * 1.4426950408889634f;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) s[k] = cap2 - __fdividef(2.f * cap2, 1.f + ex2(s[k] * up));
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) s[k] *= a.scale_log2;
+                            }
+                            const float away = static_cast<float>(t0 + k0 - pos);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[k] = fmaf(slope2, away + k, s[k]);
+                        }
+                        if (masked) {
+                            const int lo = see_lo - t0 - k0, hi = see_hi - t0 - k0;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (k < lo || k >= hi) s[k] = -INFINITY;
+                        }
+                        if (EXTRA || masked) tmem_put32(s_t + k0, s);
+                        float t[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) t[u] = max3(t[u], s[k + 2 * u], s[k + 2 * u + 1]);
+                        mx = fmaxf(max3(t[0], t[1], t[2]), t[3]);
+                    }
+                    if (EXTRA || masked) tmem_wait_st();
+                    if constexpr (!EXTRA) mx *= a.scale_log2;
+                    mx = fmaxf(mx, kQNoRef);
+                    if (j == 0) {
+                        M = mx;
+                    } else if (__any_sync(0xffffffffu, mx > M + kSGrow)) {
+                        // the reference moves: what O and l hold is brought to the new one
+                        if (ok) ok = mbar_wait(&sh.o_done[w], (done + j - 1) & 1);
+                        tc_fence_after();
+                        const bool moves = mx > M + kSGrow;
+                        const float f = moves ? ex2(M - mx) : 1.f;
+                        if (moves) M = mx;
+                        l2.x *= f, l2.y *= f;
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            float o[32];
+                            tmem_get32(o_t + k, o);
+                            tmem_wait_ld();
+                            tmem_pass32(o);
+#pragma unroll
+                            for (int d = 0; d < 32; ++d) o[d] *= f;
+                            tmem_put32(o_t + k, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    const float neg = Q::BIAS - M, unit = EXTRA ? 1.f : a.scale_log2;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < kSKeys; k0 += 32) {  // the probabilities take their scores' columns
+                        float s[32];
+                        uint32_t hi[16], lo[16];
+                        tmem_get32(s_t + k0, s);
+                        tmem_wait_ld();
+                        tmem_pass32(s);
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) {
+                            const float2 e = __ffma2_rn(make_float2(s[2 * u], s[2 * u + 1]), make_float2(unit, unit), make_float2(neg, neg));
+                            const float2 pr = make_float2(ex2(e.x), ex2(e.y));
+                            l2 = __fadd2_rn(l2, pr);
+                            split_p<T>(pr, hi[u], lo[u]);
+                        }
+                        tmem_put16(s_t + k0, hi);
+                        tmem_put16(s_t + k0 + 16, lo);
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[w]);
+            }
+            done += steps;
+            ring += 2 * n;
+            // ---- results: both warpgroups' columns of their own rows, or half of the columns each of the rows they share
+            if (steps > 0 && ok) ok = mbar_wait(&sh.o_done[w], (done - 1) & 1);
+            tc_fence_after();
+            if (!ok && lane == 0) set_status(a.status, SDV_ERR_DEVICE_TIMEOUT);
+            float l = poisoned ? NAN : l2.x + l2.y, f0 = 1.f, f1 = 0.f;
+            if (!wide) {
+                if (steps > 0) sh.ml[w][m] = make_float2(M, l);
+                tc_fence_before();
+                named_bar_sync(1, 256);
+                tc_fence_after();
+                const float2 x0 = sh.ml[0][m], x1 = n > 1 ? sh.ml[1][m] : make_float2(kQNoRef, 0.f);
+                M = fmaxf(x0.x, x1.x);
+                f0 = ex2(x0.x - M);
+                f1 = ex2(x1.x - M);
+                l = f0 * x0.y + f1 * x1.y;
+            }
+            if (!live) continue;
+            // the whole of its rows' keys: the result; else a part of it
+            const bool direct = !p.more && n == en.nc && !prefix && (en.group < 0 || pl.e[en.group].nc == 0), mine = m < n_rows;
+            const int cols = wide ? D : D / 2, col0 = wide ? 0 : w * (D / 2);
+            const long long slot = shared_slot(a, prefix, r00, p.h, p.tile, p.more ? cta : -1) + row0;
+            if (!direct && mine && (wide || w == 0)) a.part_ml[slot + m] = make_float2(M, l);
+            const float inv = direct ? 1.f / l : 1.f;
+            f0 *= inv, f1 *= inv;
+            const long long to = direct ? row * a.out_stride + hq * D : (slot + m) * D;
+            // a lane's row becomes a line of lanes in this warp's 4 KB of the used queries' place
+            float *turn = reinterpret_cast<float *>(smem_raw + w * Q::Q_BYTES) + warp % 4 * 1024;
+            const int here = min(32, n_rows - warp % 4 * 32);
+#pragma unroll 1
+            for (int k = 0; k < cols; k += 32) {
+                float o[32];
+                tmem_get32((wide ? o_t : tmem + lanes + Q::O_COL) + col0 + k, o);
+                tmem_wait_ld();
+                tmem_pass32(o);
+#pragma unroll
+                for (int d = 0; d < 32; ++d) o[d] *= f0;
+                if (!wide && n > 1) {
+                    float v[32];
+                    tmem_get32(tmem + lanes + Q::O_COL + 128 + col0 + k, v);
+                    tmem_wait_ld();
+                    tmem_pass32(v);
+#pragma unroll
+                    for (int d = 0; d < 32; ++d) o[d] = fmaf(f1, v[d], o[d]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int d = 0; d < 32; ++d) turn[lane * 32 + (d ^ lane)] = o[d];
+                __syncwarp();
+                if (direct) {
+#pragma unroll 4
+                    for (int r = 0; r < here; ++r)
+                        static_cast<T *>(a.out)[__shfl_sync(0xffffffffu, to, r) + col0 + k + lane] = from_f32<T>(turn[r * 32 + (lane ^ r)]);
+                } else {
+                    float *dst = a.part_o + (slot + warp % 4 * 32) * D + col0 + k + lane;
+#pragma unroll 8
+                    for (int r = 0; r < here; ++r) dst[r * D] = turn[r * 32 + (lane ^ r)];
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (is_mma) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ joining the parts
+constexpr int kSMergeThreads = 256;
+
+// A warp joins the parts of one (row, q head): those of its own tile, then those of the prefix's, CTA by CTA along the line.
+// Rows that one piece holds alone were written by the attention, those of refused spans become NaN.
+template <typename T, int D>
+__global__ void __launch_bounds__(kSMergeThreads) shared_merge_kernel(const __grid_constant__ SharedArgs a) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x % 32, idx = blockIdx.x * (kSMergeThreads / 32) + threadIdx.x / 32;
+    pdl_wait();  // in every CTA: this kernel's end stands for the attention's, too
+    pdl_trigger();
+    const int row = idx / a.nq, hq = idx - row * a.nq, h = a.by_grp.div(hq);
+    if (row >= a.max_rows) return;
+    const int b = a.row_seq[row], q = a.plan_cut[0], ov = a.plan_cut[1];
+    if (b == kRowNone) return;
+    T *out = static_cast<T *>(a.out) + row * a.out_stride + hq * D + lane * V;
+    if (b == kRowRefused) {
+#pragma unroll
+        for (int d = 0; d < V; ++d) out[d] = from_f32<T>(NAN);
+        return;
+    }
+    const SEntry own = a.plan[a.G + b];
+    const SEntry pre = own.group >= 0 ? a.plan[own.group] : SEntry{};
+    // a tile's start on the line, the CTA it begins in and the number of those it touches
+    auto tile_of = [&](const SEntry &n, int &tile, int &r, int &at, int &i0) {
+        const int m = (row - n.r0) * a.grp + hq - h * a.grp;
+        tile = m / kSTile;
+        r = m - tile * kSTile;
+        at = n.start + (h * shared_tiles(a, n) + tile) * n.per;
+        i0 = at / q;
+        return n.nc ? (at + n.per - 1) / q - i0 + 1 : 0;
+    };
+    int tile[2], r[2], at[2], i0[2];
+    const int n_own = tile_of(own, tile[0], r[0], at[0], i0[0]), n_pre = pre.nc ? tile_of(pre, tile[1], r[1], at[1], i0[1]) : 0;
+    // row of part k in the partial results, -1 where that CTA has no chunk of the tile
+    auto part = [&](int k) -> long long {
+        if (k >= n_own + n_pre) return -1;
+        const bool of = k >= n_own;
+        const SEntry &n = of ? pre : own;
+        const int i = (of ? i0[1] + k - n_own : i0[0] + k), rel = i * q - (of ? at[1] : at[0]);
+        const int from = shared_chunk(n, ov, rel), stop = rel + q >= n.per ? n.nc : shared_chunk(n, ov, rel + q);
+        if (stop <= from) return -1;
+        return shared_slot(a, of, n.r0, h, of ? tile[1] : tile[0], from > 0 ? i : -1) + (of ? r[1] : r[0]);
+    };
+    long long slot = part(lane);
+    if (n_pre == 0 && n_own <= 32 && __popc(__ballot_sync(0xffffffffu, slot >= 0)) == 1) return;  // written already
+    float2 ml = slot >= 0 ? a.part_ml[slot] : make_float2(kQNoRef, 0.f);
+    float M = ml.x;
+    for (int k = 32 + lane; k - lane < n_own + n_pre; k += 32) {
+        const long long s = part(k);
+        if (s >= 0) M = fmaxf(M, a.part_ml[s].x);
+    }
+    M = redux_max(M);
+    float o[V], l = 0.f;
+#pragma unroll
+    for (int d = 0; d < V; ++d) o[d] = 0.f;
+    for (int k0 = 0; k0 < n_own + n_pre; k0 += 32) {
+        if (k0 > 0) {
+            slot = part(k0 + lane);
+            ml = slot >= 0 ? a.part_ml[slot] : make_float2(kQNoRef, 0.f);
+        }
+        const float mine = slot >= 0 ? ex2(ml.x - M) : 0.f;
+        l += warp_sum(slot >= 0 ? mine * ml.y : 0.f);
+        const int count = min(32, n_own + n_pre - k0);
+#pragma unroll 1
+        for (int p0 = 0; p0 < count; p0 += 8) {
+            float v[8][V];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const long long s = __shfl_sync(0xffffffffu, slot, p0 + u);
+#pragma unroll
+                for (int d = 0; d < V; ++d) v[u][d] = 0.f;
+                if (s >= 0) {
+                    const float *src = a.part_o + s * D + lane * V;
+                    if constexpr (V == 4)
+                        *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(src);
+                    else
+                        *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(src);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float f = __shfl_sync(0xffffffffu, mine, p0 + u);
+#pragma unroll
+                for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[u][d], o[d]);
+            }
+        }
+    }
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int d = 0; d < V; ++d) out[d] = from_f32<T>(o[d] * inv);
+}
+
+}  // namespace sdv
