@@ -57,16 +57,16 @@ int part_rows(const sdv_shared_cfg &c) { return c.max_rows * (c.n_q_heads / c.n_
 size_t part_slots(const sdv_shared_cfg &c, int sms) {
     return static_cast<size_t>(2) * c.n_kv_heads * part_rows(c) + static_cast<size_t>(sms) * kSTile;
 }
-// Offsets into the workspace: the status word and the cut, the plan's entries, the rows' sequences, (M, l), O.
+// Offsets into the workspace: the status word and the cut, the plan's entries, the rows' entries, (M, l), O.
 struct Workspace {
-    size_t plan, row_seq, ml, o, end;
+    size_t plan, row_entry, ml, o, end;
 };
 Workspace workspace(const sdv_shared_cfg &c, int sms) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     Workspace w;
     w.plan = 256;
-    w.row_seq = up(w.plan + sizeof(SEntry) * kSEntries);
-    w.ml = up(w.row_seq + sizeof(int) * c.max_rows);
+    w.row_entry = up(w.plan + sizeof(SEntry) * kSEntries);
+    w.ml = up(w.row_entry + sizeof(int2) * c.max_rows);
     w.o = up(w.ml + sizeof(float2) * part_slots(c, sms));
     w.end = w.o + sizeof(float) * part_slots(c, sms) * c.head_dim;
     return w;
@@ -253,7 +253,7 @@ int sdv_shared_attention(sdv_shared *s, int layer, const void *d_q, int64_t q_st
     a.part_rows = part_rows(c);
     a.plan_cut = reinterpret_cast<int *>(s->ws) + 16;
     a.plan = reinterpret_cast<SEntry *>(s->ws + w.plan);
-    a.row_seq = reinterpret_cast<int *>(s->ws + w.row_seq);
+    a.row_entry = reinterpret_cast<int2 *>(s->ws + w.row_entry);
     a.part_ml = reinterpret_cast<float2 *>(s->ws + w.ml);
     a.part_o = reinterpret_cast<float *>(s->ws + w.o);
     const CUtensorMap &pool = s->pools[layer];

@@ -20,7 +20,7 @@ constexpr int kSBatch = 256;     // sequences of a call at most
 constexpr int kSEntries = kSGroups + kSBatch;
 constexpr int kSOverhead = 3;    // what a tile's queries and results cost, in chunks
 constexpr float kSGrow = 8.f;    // a row's reference follows its maximum once that is more than 2^8 above it
-constexpr int kSThreads = 384;   // two softmax warpgroups, the load warp, the MMA warp; as many as entries
+constexpr int kSThreads = 384;   // two softmax warpgroups, a warp for K, one for V, one that issues MMAs; as many as entries
 
 struct SharedArgs {
     const void *q;
@@ -42,7 +42,7 @@ struct SharedArgs {
     float2 *part_ml;                 // (M, l) of each
     struct SEntry *plan;             // the plan's entries, for the kernel that joins the parts
     int *plan_cut;                   // its q and ov
-    int *row_seq;                    // [max_rows]: a row's sequence, kRowNone, or kRowRefused
+    int2 *row_entry;                 // [max_rows]: a row's entry, kRowNone or kRowRefused, and that of its prefix or -1
 };
 constexpr int kRowNone = -1, kRowRefused = -2;
 
@@ -181,46 +181,66 @@ __device__ __forceinline__ void shared_plan(const SharedArgs &a, SPlan &pl, bool
         for (int r = tid; r < a.max_rows; r += kSThreads) {
             const int of = shared_last(pl.row_off, a.B, r);
             const bool in = r >= pl.row_off[of] && r < pl.row_off[of + 1];
-            a.row_seq[r] = !in ? kRowNone : pl.e[a.G + of].rows ? of : kRowRefused;
+            const SEntry &m = pl.e[a.G + of];
+            a.row_entry[r] = make_int2(!in ? kRowNone : m.rows ? a.G + of : kRowRefused, m.group >= 0 && pl.e[m.group].nc ? m.group : -1);
         }
     }
 }
 // First chunk of a tile that begins at or after `rel` on the line, from the tile's start.
 __device__ __forceinline__ int shared_chunk(const SEntry &n, int ov, int rel) {
     if (rel <= 0) return 0;
-    return min(n.nc, rel <= ov + n.wc ? 1 : (rel - ov + n.wc - 1) / n.wc);
+    return min(n.nc, rel <= ov + n.wc ? 1 : (rel - ov + n.wc - 1) >> (n.wc - 1));  // wc is 1 or 2
 }
+// The part of a tile that a CTA does. Each warp steps from one to the next by itself.
 struct SPiece {
-    int entry;
-    int h, tile, rows;  // kv head, tile, rows x heads of it
-    int c0, n;          // its first chunk, from the entry's first, and how many
-    bool more;          // it begins inside of the tile: the result goes to the CTA's own rows
+    int entry, h, tile, at;  // kv head, tile, where the tile starts on the line
+    int rows;                // rows x heads of the tile
+    int c0, n;               // its first chunk, from the entry's first, and how many
+    int tiles;             // tiles a kv head
 };
-// The next piece of the line's [x, x1), false at its end.
-__device__ __forceinline__ bool shared_next(const SharedArgs &a, const SPlan &pl, int &x, int x1, SPiece &p) {
-    while (x < x1) {
-        int lo = 0, hi = a.G + a.B - 1;  // the first entry that ends behind x
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (pl.e[mid].end > x) hi = mid; else lo = mid + 1;
-        }
-        const SEntry &n = pl.e[lo];
-        const int per = n.per, th = (x - n.start) / per, at = n.start + th * per, tiles = shared_tiles(a, n);
-        const int stop = min(x1, at + per), from = shared_chunk(n, pl.ov, x - at);
-        const int to = stop == at + per ? n.nc : shared_chunk(n, pl.ov, stop - at);
-        x = stop;
-        if (to <= from) continue;
-        p.entry = lo;
-        p.h = th / tiles;
-        p.tile = th - p.h * tiles;
-        p.rows = min(kSTile, n.rows * a.grp - p.tile * kSTile);
-        p.c0 = from;
-        p.n = to - from;
-        p.more = from > 0;
-        return true;
-    }
-    return false;
+// Takes the tile that p names; false where none of its chunks lies in [x, x1).
+__device__ __forceinline__ bool shared_take(const SharedArgs &a, const SPlan &pl, int x, int x1, SPiece &p) {
+    const SEntry &n = pl.e[p.entry];
+    p.c0 = shared_chunk(n, pl.ov, x - p.at);
+    p.n = (x1 >= p.at + n.per ? n.nc : shared_chunk(n, pl.ov, x1 - p.at)) - p.c0;
+    p.rows = min(kSTile, n.rows * a.grp - p.tile * kSTile);
+    return p.n > 0;
 }
+// The first piece of [x, x1) or the next one, false at the end.
+__device__ __forceinline__ bool shared_next(const SharedArgs &a, const SPlan &pl, int x, int x1, SPiece &p) {
+    do {
+        const SEntry &n = pl.e[p.entry];
+        p.at += n.per;
+        if (p.at >= x1) return false;
+        if (++p.tile == p.tiles) {
+            p.tile = 0;
+            if (++p.h == a.nkv) {
+                p.h = 0;
+                do ++p.entry;
+                while (pl.e[p.entry].end == p.at);  // entries without work; the line goes on, so one comes
+                p.tiles = shared_tiles(a, pl.e[p.entry]);
+            }
+        }
+    } while (!shared_take(a, pl, x, x1, p));
+    return true;
+}
+__device__ __forceinline__ bool shared_first(const SharedArgs &a, const SPlan &pl, int x, int x1, SPiece &p) {
+    if (x >= x1) return false;
+    int lo = 0, hi = a.G + a.B - 1;  // the first entry that ends behind x
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (pl.e[mid].end > x) hi = mid; else lo = mid + 1;
+    }
+    const SEntry &n = pl.e[lo];
+    const int th = (x - n.start) / n.per;
+    p.entry = lo;
+    p.tiles = shared_tiles(a, n);
+    p.h = th / p.tiles;
+    p.tile = th - p.h * p.tiles;
+    p.at = n.start + th * n.per;
+    return shared_take(a, pl, x, x1, p) || shared_next(a, pl, x, x1, p);
+}
+
 // Where a tile's partial result lies: its first row.
 __device__ __forceinline__ long long shared_slot(const SharedArgs &a, bool prefix, int r0, int h, int tile, int cta) {
     const long long side = static_cast<long long>(a.nkv) * a.part_rows;
@@ -284,6 +304,12 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *v) {
         "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// 32 bytes, a whole sector: lanes hold rows of their own.
+__device__ __forceinline__ void store8(float *dst, const float *v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
@@ -329,6 +355,11 @@ __device__ __forceinline__ uint32_t pack16(float x, float y) {
         return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
+// Of 32 keys those in [lo, hi), as bits.
+__device__ __forceinline__ uint32_t seen_bits(int lo, int hi) {
+    const uint32_t above = hi <= 0 ? 0u : hi >= 32 ? 0xffffffffu : (1u << hi) - 1;
+    return above & (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1));
+}
 // Whether any of eight 16-bit values is an infinity or a NaN.
 template <typename T>
 __device__ __forceinline__ bool not_finite8(uint4 u) {
@@ -342,10 +373,14 @@ __device__ __forceinline__ bool not_finite8(uint4 u) {
     return bad;
 }
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
 struct SShared {
-    uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full;
+    uint64_t full[8], empty[8], s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_empty;
     uint32_t tmem;
-    uint32_t bad[2][2][4];
+    uint32_t bad[2][2][4];  // [turn][warpgroup]: keys of the chunk that are not finite, as bits
     float2 ml[2][128];  // (M, l) of the rows that two warpgroups share
     SPlan plan;
 };
@@ -355,7 +390,8 @@ struct STile {
     static constexpr int D = D_, HALVES = D / 64;
     static constexpr int SLOT = kSKeys * D * 2;              // bytes of a K or V chunk, as halves of 64 columns
     static constexpr int Q_BYTES = 128 * D * 2;              // and of 128 rows of Q
-    static constexpr int SLOTS = D == 128 ? 4 : 8;
+    static constexpr int DEPTH = D == 128 ? 2 : 4;           // K chunks, and V chunks, in shared memory
+    static constexpr int SLOTS = 2 * DEPTH;
     static constexpr int SMEM = 2 * Q_BYTES + SLOTS * SLOT + static_cast<int>((sizeof(SShared) + 127) / 128 * 128);
     static constexpr int O_COL = 256;                        // TMEM: S of each warpgroup, then O of each
     // p carries a factor 2^6 in fp16, whose smallest values lie at 2^-24; 2^(6 + kSGrow) is its largest
@@ -372,7 +408,7 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t q_s = smem_u32(smem_raw), kv_s = q_s + 2 * Q::Q_BYTES;
     SShared &sh = *reinterpret_cast<SShared *>(smem_raw + 2 * Q::Q_BYTES + Q::SLOTS * Q::SLOT);
-    const bool is_load = warp == 8, is_mma = warp == 9;
+    if (tid < 16) sh.bad[tid / 8][tid / 4 % 2][tid % 4] = 0;
     if (tid == 0) {
         for (int i = 0; i < Q::SLOTS; ++i) {
             mbar_init(&sh.full[i], a.box_rows ? 1 : 32);
@@ -380,13 +416,15 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_half[i], 128);
             mbar_init(&sh.p_full[i], 128);
             mbar_init(&sh.o_done[i], 1);
         }
         mbar_init(&sh.q_full, 256);
+        mbar_init(&sh.q_empty, 1);
         fence_mbar_init();
     }
-    if (is_mma) {
+    if (warp == 10) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
@@ -398,54 +436,66 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
     const SPlan &pl = sh.plan;
     const uint32_t tmem = sh.tmem;
     const int cta = blockIdx.x;
-    int x = cta * pl.q;
-    const int x1 = min(pl.total, x + pl.q);
+    const int x = cta * pl.q, x1 = min(pl.total, x + pl.q);
     bool ok = true;  // false once a wait gave up: the rest runs without waiting, and the status word says so
     SPiece p;
+    bool more = shared_first(a, pl, x, x1, p);  // by all warps alike: the code comes in once
 
-    if (is_load) {
-        // ---- the load warp: K and V chunks in the order in which the products want them
-        int slot = 0;
+    // K of chunk c of a piece lies in slot c % DEPTH, V in DEPTH more. A slot is filled once more for every chunk: `used` counts
+    // the fillings before the piece, and tells the phase of the slot's barriers.
+    int used[Q::DEPTH] = {};
+    auto filling = [&](int c) {
+        int u = used[0];
+#pragma unroll
+        for (int i = 1; i < Q::DEPTH; ++i) u = c % Q::DEPTH == i ? used[i] : u;
+        return u + c / Q::DEPTH;
+    };
+    auto next_piece = [&](int n) {
+#pragma unroll
+        for (int i = 0; i < Q::DEPTH; ++i) used[i] += (n + Q::DEPTH - 1 - i) / Q::DEPTH;
+    };
+
+    if (warp == 8 || warp == 9) {
+        // ---- the load warps: one brings K chunks, one V chunks
+        const bool v = warp == 9;
         const int nb = a.box_rows ? kSKeys / a.box_rows : 0;
-        while (shared_next(a, pl, x, x1, p)) {
+        bool first = true;
+        for (; more; more = shared_next(a, pl, x, x1, p)) {
             const SEntry &en = pl.e[p.entry];
             const int *table = a.page_table + static_cast<size_t>(en.b) * a.pages_per_seq;
             const int n = p.n, t00 = (en.c0 + p.c0) * kSKeys, seen_lo = en.lo, seen_hi = en.kv1;
-            // In boxes a lane brings one; its page is asked for a chunk ahead. A chunk's V lies behind its K in the same pages.
+            // In boxes a lane brings one; its page is asked for a chunk ahead.
             const int j = a.box_rows ? lane % nb : 0, half = a.box_rows ? lane / nb : 0;
-            int asked = -1, rows[2] = {0, 0};  // the next chunk's page, pool rows of the last two chunks' boxes
-            auto wants = [&](int c) {
+            auto wants = [&](int c) {  // some row sees a key of the box
                 const int t = t00 + c * kSKeys + j * a.box_rows;
                 return c < n && half < Q::HALVES && t + a.box_rows > seen_lo && t < seen_hi;
             };
             auto ask = [&](int c) { return wants(c) ? table[a.by_page.div(t00 + c * kSKeys + j * a.box_rows)] : -1; };
-            if (a.box_rows) asked = ask(0);
-            auto put = [&](int c, bool v) {
-                const int st = slot % Q::SLOTS, use = slot / Q::SLOTS;
+            int page = a.box_rows ? ask(0) : 0;
+            // at the start the queries come first: behind everybody's keys they would wait for 5,000 clocks
+            if (first && v && ok) ok = mbar_wait(&sh.q_full, 0);
+#pragma unroll 1
+            for (int c = 0; c < n; ++c) {
+                const int st = (v ? Q::DEPTH : 0) + c % Q::DEPTH, use = filling(c), t0 = t00 + c * kSKeys;
                 const uint32_t dst = kv_s + st * Q::SLOT;
-                ++slot;
+                uint64_t *full = &sh.full[st];
+                if (first && !v && c == 1 && ok) ok = mbar_wait(&sh.q_full, 0);
                 if (a.box_rows) {
-                    if (!v) {  // a box outside the keys that some row sees is zeros
-                        const int t = t00 + c * kSKeys + j * a.box_rows, page = asked;
-                        int row = a.pool_rows;
-                        if (wants(c)) {
-                            if (page >= 0 && page < a.n_pages)
-                                row = (page * 2 * a.nkv + p.h) * a.page_size + t - a.by_page.div(t) * a.page_size;
-                            else
-                                set_status(a.status, SDV_ERR_CAPACITY);
-                        }
-                        if (c & 1) rows[1] = row; else rows[0] = row;
-                        asked = ask(c + 1);
+                    int row = a.pool_rows;  // zeros
+                    if (!wants(c)) {
+                    } else if (page >= 0 && page < a.n_pages) {
+                        const int t = t0 + j * a.box_rows;
+                        row = ((page * 2 + (v ? 1 : 0)) * a.nkv + p.h) * a.page_size + t - a.by_page.div(t) * a.page_size;
+                    } else {
+                        set_status(a.status, SDV_ERR_CAPACITY);
                     }
-                    int row = c & 1 ? rows[1] : rows[0];
-                    if (v && row < a.pool_rows) row += a.nkv * a.page_size;
+                    page = ask(c + 1);
                     if (use > 0 && ok) ok = mbar_wait(&sh.empty[st], (use - 1) & 1);
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], Q::SLOT);
+                    if (lane == 0) mbar_arrive_expect_tx(full, Q::SLOT);
                     __syncwarp();
                     if (lane < nb * Q::HALVES)
-                        load_box_at(dst + half * (kSKeys * 128) + j * a.box_rows * 128, &pool, &sh.full[st], half * 64, row);
+                        load_box_at(dst + half * (kSKeys * 128) + j * a.box_rows * 128, &pool, full, half * 64, row);
                 } else {
-                    const int t0 = t00 + c * kSKeys;
                     if (use > 0 && ok) ok = mbar_wait(&sh.empty[st], (use - 1) & 1);
                     constexpr int PPR = D / 8, RPI = 32 / PPR;  // 16-byte pieces of a row, rows a copy
                     const int piece = lane % PPR;
@@ -455,99 +505,106 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                         const uint8_t *src = static_cast<const uint8_t *>(a.pool);
                         bool in = false;
                         if (t >= seen_lo && t < seen_hi) {
-                            const int at = a.by_page.div(t), page = table[at];
-                            in = page >= 0 && page < a.n_pages;
+                            const int at = a.by_page.div(t), id = table[at];
+                            in = id >= 0 && id < a.n_pages;
                             if (in)
-                                src += (((static_cast<size_t>(page) * 2 + (v ? 1 : 0)) * a.nkv + p.h) * a.page_size + t -
+                                src += (((static_cast<size_t>(id) * 2 + (v ? 1 : 0)) * a.nkv + p.h) * a.page_size + t -
                                         at * a.page_size) * (D * 2) + piece * 16;
                             else
                                 set_status(a.status, SDV_ERR_CAPACITY);
                         }
                         cp_async16(dst + piece / 8 * (kSKeys * 128) + line_offset(r, piece % 8 * 16, 128), src, in);
                     }
-                    cp_async_arrive(&sh.full[st]);
+                    cp_async_arrive(full);
                 }
-            };
-            const bool wide = p.rows > 128;
-            // K 0, K 1, V 0, K 2, V 1, ..; a wide tile wants K 0, V 0, K 1, V 1, ..
-#pragma unroll 1
-            for (int i = 0; i < 2 * n; ++i) {
-                const bool v = wide ? i & 1 : i == 2 * n - 1 || (i > 0 && i % 2 == 0);
-                put(wide ? i >> 1 : v ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2, v);
             }
+            first = false;
+            next_piece(n);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (!ok) {  // no copy may land after this CTA's shared memory is someone else's
-            for (int i = max(0, slot - Q::SLOTS); i < slot; ++i) mbar_wait(&sh.full[i % Q::SLOTS], i / Q::SLOTS & 1);
+            for (int i = 0; i < Q::DEPTH; ++i)
+                if (used[i]) mbar_wait(&sh.full[(v ? Q::DEPTH : 0) + i], (used[i] - 1) & 1);
             if (lane == 0) set_status(a.status, SDV_ERR_DEVICE_TIMEOUT);
         }
-    } else if (is_mma) {
+    } else if (warp == 10) {
         // ---- MMA issue. Step s of a piece is softmax warpgroup s % 2's: of its own 128 rows of a tile of more than 128, every
-        // chunk for each in turn, else of the tile's rows and every other chunk.
-        // The whole warp keeps step and one lane issues: with a lane of its own (lane 0 alone in the loop) an MMA took 80 to
-        // 100 clocks to issue, its operands passing from lane to uniform registers.
+        // chunk for each in turn, else of the tile's rows and every other chunk. They keep their turns, so that one's softmax
+        // runs beside the other's products (with a warp that issues for each, both fell into step: 4,900 clocks for what now
+        // takes 4,200). The whole warp loops and one lane issues: with a lane of its own (lane 0 alone in the loop) an MMA took 80
+        // to 100 clocks to issue, 61 so.
+        // What steers the loop passes through a shuffle, so that it is known to be the same in every lane, and a wait that
+        // needs none is a single look: what the warp does beside its MMAs is time without products.
         constexpr uint32_t id_s = idesc_16<T>(128, kSKeys, false), id_o = idesc_16<T>(128, D, true);
-        int ring = 0, pieces = 0, done[2] = {0, 0};  // slots before this piece, pieces, steps of each warpgroup
-        while (shared_next(a, pl, x, x1, p)) {
-            const bool wide = p.rows > 128;
-            const int n = p.n, steps = wide ? 2 * n : n;
-            auto k_slot = [&](int c) { return ring + (wide ? 2 * c : c ? 2 * c - 1 : 0); };
-            auto v_slot = [&](int c) { return ring + (wide ? 2 * c + 1 : c == n - 1 ? 2 * n - 1 : 2 * c + 2); };
-            if (ok) ok = mbar_wait(&sh.q_full, pieces & 1);
-            ++pieces;
+        auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+        const uint32_t tm = same(tmem);
+        uint32_t k_bits = 0, v_bits = 0, p_bits = 0, q_bit = 0;  // the phase of each barrier that comes next
+        auto await = [&](uint64_t *bar, uint32_t parity) {
+            if (!mbar_try_wait(bar, parity) && ok) ok = mbar_wait(bar, parity);
+        };
+        for (; more; more = shared_next(a, pl, x, x1, p)) {
+            const bool wide = same(p.rows) > 128;
+            const int n = same(p.n), steps = wide ? 2 * n : n;
+            await(&sh.q_full, q_bit);
+            q_bit ^= 1;
             tc_fence_after();
-            // Waits until the slots at `v` and `k` of the ring are full and, for step s >= 0, its probabilities are there: a lane
-            // each, since a look at a barrier takes 100 clocks.
-            auto await = [&](int s, int v, int k) {
-                const int at = lane == 1 ? v : k;
-                uint64_t *bar = lane == 0 ? &sh.p_full[s & 1] : &sh.full[at % Q::SLOTS];
-                const uint32_t parity = lane == 0 ? (done[s & 1] + (s >> 1)) & 1 : at / Q::SLOTS & 1;
-                const bool mine = lane == 0 ? s >= 0 : lane == 1 ? v >= 0 : lane == 2 && k >= 0;
-                if (ok && !__all_sync(0xffffffffu, !mine || mbar_try_wait(bar, parity))) {
-                    const uint64_t since = globaltimer();
-                    while (!__all_sync(0xffffffffu, !mine || mbar_try_wait(bar, parity)))
-                        if (__any_sync(0xffffffffu, globaltimer() - since > kWaitLimitNs)) {
-                            ok = false;
-                            break;
-                        }
+            fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
+            auto step = [&](int s, auto W) {  // the products with V of step s, the scores of step s + 2
+                constexpr int w = decltype(W)::value;
+                const int c = wide ? s >> 1 : s, next = wide ? (s + 2) >> 1 : s + 2;
+                const bool more = s + 2 < steps, first = !wide || w == 0, last = !wide || w == 1;  // of the steps of its chunk
+                const uint32_t s_t = tm + w * kSKeys, o_t = tm + Q::O_COL + w * 128;
+                const int v_at = c % Q::DEPTH, k_at = next % Q::DEPTH;
+                const uint64_t vd = line_desc(kv_s + (Q::DEPTH + v_at) * Q::SLOT, 128, kSKeys * 128);
+                if (s >= 0) {
+                    await(&sh.p_half[w], p_bits >> w & 1);
+                    if (first) {
+                        await(&sh.full[Q::DEPTH + v_at], v_bits >> v_at & 1);
+                        v_bits ^= 1u << v_at;
+                    }
+                    tc_fence_after();
+                    if (!a.box_rows) fence_async_smem();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kSKeys / 16; ++k)  // 16 keys' hi plane, then lo: eight columns each
+                            umma_f16_ts(o_t, s_t + k / 4 * 32 + k % 2 * 16 + k / 2 % 2 * 8, vd + (k / 2 * 2048 >> 4), id_o, s > 1 || k > 0);
+                    }
+                    await(&sh.p_full[w], p_bits >> w & 1);
+                    p_bits ^= 1u << w;
+                }
+                if (more && first) {
+                    await(&sh.full[k_at], k_bits >> k_at & 1);
+                    k_bits ^= 1u << k_at;
                 }
                 tc_fence_after();
-                fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
-            };
-            auto scores = [&](int s) {  // one lane
-                const int w = s & 1, c = wide ? s >> 1 : s, st = k_slot(c) % Q::SLOTS;
-                const uint64_t kd = sw128_desc(kv_s + st * Q::SLOT), qd = sw128_desc(q_s + (wide && w ? Q::Q_BYTES : 0));
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4 * (128 * 128) + k % 4 * 32) >> 4;
-                    umma_bf16(tmem + w * kSKeys, qd + off, kd + off, id_s, k > 0);
-                }
-                umma_commit(&sh.s_full[w]);
-                if (!wide || w) umma_commit(&sh.empty[st]);
-            };
-#pragma unroll 1
-            for (int s = -2; s < steps; ++s) {  // the products with V of step s, the scores of step s + 2
-                const int w = s & 1, c = wide ? s >> 1 : s, at = v_slot(c), ahead = wide ? (s + 2) >> 1 : s + 2;
-                const bool more = s + 2 < steps;
-                await(s, s >= 0 ? at : -1, more ? k_slot(ahead) : -1);
+                if (!a.box_rows) fence_async_smem();
                 if (elect_one()) {
                     if (s >= 0) {
-                        const int st = at % Q::SLOTS;
-                        const uint64_t vd = line_desc(kv_s + st * Q::SLOT, 128, kSKeys * 128);
-                        const uint32_t p_t = tmem + w * kSKeys, o_t = tmem + Q::O_COL + w * 128;
 #pragma unroll
-                        for (int k = 0; k < 2 * kSKeys / 16; ++k)  // 16 keys' hi plane, then lo: eight columns each
-                            umma_f16_ts(o_t, p_t + k / 4 * 32 + k % 2 * 16 + k / 2 % 2 * 8, vd + (k / 2 * 2048 >> 4), id_o, s > 1 || k > 0);
+                        for (int k = kSKeys / 16; k < 2 * kSKeys / 16; ++k)
+                            umma_f16_ts(o_t, s_t + k / 4 * 32 + k % 2 * 16 + k / 2 % 2 * 8, vd + (k / 2 * 2048 >> 4), id_o, 1);
                         umma_commit(&sh.o_done[w]);
-                        if (!wide || w) umma_commit(&sh.empty[st]);
+                        if (last) umma_commit(&sh.empty[Q::DEPTH + v_at]);
                     }
-                    if (more) scores(s + 2);
+                    if (more) {
+                        const uint64_t kd = sw128_desc(kv_s + k_at * Q::SLOT), qd = sw128_desc(q_s + (wide && w ? Q::Q_BYTES : 0));
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = (k / 4 * (128 * 128) + k % 4 * 32) >> 4;
+                            umma_bf16(s_t, qd + off, kd + off, id_s, k > 0);
+                        }
+                        umma_commit(&sh.s_full[w]);
+                        if (last) umma_commit(&sh.empty[k_at]);
+                        if (s + 3 == steps) umma_commit(&sh.q_empty);
+                    }
                 }
                 __syncwarp();
+            };
+#pragma unroll 1
+            for (int s = -2; s < steps; s += 2) {
+                step(s, Int<0>{});
+                if (s + 1 < steps) step(s + 1, Int<1>{});
             }
-            done[0] += (steps + 1) >> 1;
-            done[1] += steps >> 1;
-            ring += 2 * n;
         }
         if (!ok && lane == 0) set_status(a.status, SDV_ERR_DEVICE_TIMEOUT);
         __syncwarp();
@@ -556,46 +613,43 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
         const int w = warp / 4, m = tid % 128;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
         const uint32_t s_t = tmem + lanes + w * kSKeys, o_t = tmem + lanes + Q::O_COL + w * 128;
-        int done = 0, ring = 0;  // this warpgroup's steps, slots before this piece
-        while (shared_next(a, pl, x, x1, p)) {
+        int done = 0, pieces = 0;  // this warpgroup's steps, pieces
+        // The queries of a piece go into their swizzled halves as soon as the last one's scores have read theirs, beside its last
+        // products and results. Rows behind the tile's keep what lies there: they only make results that nobody reads.
+        auto load_q = [&](const SPiece &p) {
+            constexpr int PPR = D / 8, RPI = 256 / PPR;  // 16-byte pieces of a row, rows a copy
+            const int piece = tid % PPR, r00 = pl.e[p.entry].r0;
+            if (pieces > 0 && ok) ok = mbar_wait(&sh.q_empty, (pieces - 1) & 1);
+            ++pieces;
+#pragma unroll 4
+            for (int r = tid / PPR; r < p.rows; r += RPI) {
+                const int mm = p.tile * kSTile + r, i = a.by_grp.div(mm);
+                const T *src = static_cast<const T *>(a.q) + (r00 + i) * a.q_stride + (p.h * a.grp + mm - i * a.grp) * D + piece * 8;
+                const uint32_t to = q_s + r / 128 * Q::Q_BYTES + piece / 8 * (128 * 128) + line_offset(r % 128, piece % 8 * 16, 128);
+                if (a.q_vec) {
+                    cp_async16(to, src, true);
+                } else {
+                    const Raw8<T> raw = load_raw8<T, false>(src);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(raw.u[0].x), "r"(raw.u[0].y),
+                                 "r"(raw.u[0].z), "r"(raw.u[0].w)
+                                 : "memory");
+                }
+            }
+            if (a.q_vec) {
+                cp_async_arrive(&sh.q_full);
+            } else {
+                fence_async_smem();
+                mbar_arrive(&sh.q_full);
+            }
+        };
+        if (more) load_q(p);
+        while (more) {
             const SEntry &en = pl.e[p.entry];
             const bool wide = p.rows > 128, prefix = en.p0 < 0;
             const int n = p.n, r00 = en.r0, kv_lo = en.lo, kv_end = en.kv1, t00 = (en.c0 + p.c0) * kSKeys, steps = wide ? n : (n + 1 - w) >> 1;
             const int all_lo = en.max_lo, all_hi = en.min_hi;  // what every row sees
             const int m0 = p.tile * kSTile, row0 = wide ? w * 128 : 0, n_rows = min(128, p.rows - row0);
-            named_bar_sync(1, 256);  // nobody reads the last piece's rows or results any more
-            {
-                // queries into their swizzled halves, 16 bytes a thread at a time, zeros behind the tile's rows
-                constexpr int PPR = D / 8;
-                const uint32_t dst = q_s + (wide ? w * Q::Q_BYTES : 0);
-                const int first = wide ? m : tid, step = wide ? 128 : 256;
-                constexpr int N = PPR / 2;  // pieces of a thread, or of half of its pieces of a wide tile: all on their way at once
-                for (int e0 = first; e0 < 128 * PPR; e0 += N * step) {
-                    Raw8<T> raw[N];
-#pragma unroll
-                    for (int u = 0; u < N; ++u) {
-                        const int e = e0 + u * step, r = e / PPR, piece = e % PPR;
-                        raw[u].u[0] = make_uint4(0, 0, 0, 0);
-                        if (r < n_rows) {
-                            const int mm = m0 + row0 + r, i = a.by_grp.div(mm);
-                            const T *src = static_cast<const T *>(a.q) + (r00 + i) * a.q_stride +
-                                           (p.h * a.grp + mm - i * a.grp) * D + piece * 8;
-                            raw[u] = a.q_vec ? load_raw8<T, true>(src) : load_raw8<T, false>(src);
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < N; ++u) {
-                        const int e = e0 + u * step, r = e / PPR, piece = e % PPR;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece / 8 * (128 * 128) +
-                                                                                      line_offset(r, piece % 8 * 16, 128)),
-                                     "r"(raw[u].u[0].x), "r"(raw[u].u[0].y), "r"(raw[u].u[0].z), "r"(raw[u].u[0].w)
-                                     : "memory");
-                    }
-                }
-            }
-            fence_async_smem();
-            tc_fence_before();
-            mbar_arrive(&sh.q_full);
+            named_bar_sync(1, 256);  // nobody reads the last piece's results any more
             // this thread's row: its position and the keys it sees
             const int mm = m0 + row0 + max(0, min(m, n_rows - 1)), i = a.by_grp.div(mm), row = r00 + i;
             const int hq = p.h * a.grp + mm - i * a.grp;
@@ -617,47 +671,43 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                 if (ok) ok = mbar_wait(&sh.s_full[w], (done + j) & 1);
                 tc_fence_after();
                 if (masked) {
-                    // (the scores are there, so of the chunk's slots the uses before this one are over)
-                    // V rows that some row does not see must not reach it: 0 times an infinity or a NaN is none. They are
-                    // cleared where no row sees them, and where they are not finite, which then spoils the rows that do.
-                    const int at = ring + (wide ? 2 * c + 1 : c == n - 1 ? 2 * n - 1 : 2 * c + 2), st = at % Q::SLOTS;
-                    if (ok) ok = mbar_wait(&sh.full[st], at / Q::SLOTS & 1);
-                    constexpr int ALL = Q::HALVES * 8;
-                    const int q0 = wide ? w * (ALL / 2) : 0, q1 = wide ? q0 + ALL / 2 : ALL;  // this thread's pieces of row m
-                    const uint32_t v_s = kv_s + st * Q::SLOT;
-                    bool bad = false;
-                    const bool in = t0 + m >= kv_lo && t0 + m < kv_end;
-                    if (in) {
-#pragma unroll 4
-                        for (int k = q0; k < q1; ++k) {
+                    // V rows that some row does not see must not reach it: 0 times an infinity or a NaN is none. What lies outside
+                    // of the keys is cleared (boxes without any are zeros), and what not all rows see where it is not finite,
+                    // which then spoils the rows that do. Rows [a0, a1) and [b0, b1) of the chunk, 16 bytes a thread.
+                    constexpr int PPR = D / 8;
+                    const int box = a.box_rows ? a.box_rows : 1;
+                    auto in_chunk = [&](int t) { return min(max(t - t0, 0), kSKeys); };
+                    const int a0 = in_chunk(kv_lo & -box), a1 = max(a0, in_chunk(all_lo)), b0 = max(a1, in_chunk(all_hi));
+                    const int rows_a = a1 - a0, rows = rows_a + max(0, in_chunk((kv_end + box - 1) & -box) - b0);
+                    if (rows > 0) {
+                        const int st = Q::DEPTH + c % Q::DEPTH, turn = (done + j) & 1;
+                        if (ok) ok = mbar_wait(&sh.full[st], filling(c) & 1);
+                        bool wrote = false;
+                        for (int i = wide ? tid : m; i < rows * PPR; i += wide ? 256 : 128) {
+                            const int r = i / PPR, row = r < rows_a ? a0 + r : b0 + r - rows_a, t = t0 + row, k = i % PPR;
+                            const uint32_t at = kv_s + st * Q::SLOT + k / 8 * (kSKeys * 128) + line_offset(row, k % 8 * 16, 128);
                             uint4 u;
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                                         : "r"(v_s + k / 8 * (kSKeys * 128) + line_offset(m, k % 8 * 16, 128)));
-                            bad |= not_finite8<T>(u);
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at));
+                            const bool in = t >= kv_lo && t < kv_end, bad = in && not_finite8<T>(u);
+                            if (!in || bad) {
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                                wrote = true;
+                            }
+                            if (bad) atomicOr(&sh.bad[turn][w][row / 32], 1u << row % 32);
                         }
-                    }
-                    if (!in || bad)
-                        for (int k = q0; k < q1; ++k)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v_s + k / 8 * (kSKeys * 128) +
-                                                                                          line_offset(m, k % 8 * 16, 128)),
-                                         "r"(0)
-                                         : "memory");
-                    const uint32_t word = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0) sh.bad[c & 1][w][warp % 4] = word;
-                    fence_async_smem();
-                    if (wide)
-                        named_bar_sync(2, 256);
-                    else if (w == 0)
-                        named_bar_sync(3, 128);
-                    else
-                        named_bar_sync(4, 128);
+                        if (wrote) fence_async_smem();
+                        if (wide)
+                            named_bar_sync(2, 256);
+                        else if (w == 0)
+                            named_bar_sync(3, 128);
+                        else
+                            named_bar_sync(4, 128);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t b = sh.bad[c & 1][w][k] | (wide ? sh.bad[c & 1][1 - w][k] : 0u);
-                        const int lo = min(max(see_lo - t0 - 32 * k, 0), 32), hi = min(max(see_hi - t0 - 32 * k, 0), 32);
-                        const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1, below_lo = lo == 32 ? 0xffffffffu : (1u << lo) - 1;
-                        poisoned |= (b & below_hi & ~below_lo) != 0;
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t b = sh.bad[turn][w][k] | (wide ? sh.bad[turn][1 - w][k] : 0u);
+                            if (b) poisoned |= (b & seen_bits(see_lo - t0 - 32 * k, see_hi - t0 - 32 * k)) != 0;
+                        }
+                        if (m < 4) sh.bad[1 - turn][w][m] = 0;  // nobody reads the last chunk's any more
                     }
                 }
                 if (live) {
@@ -665,35 +715,44 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                     // own instructions
                     float mx = -INFINITY;
 #pragma unroll 1
-                    for (int k0 = 0; k0 < kSKeys; k0 += 32) {
-                        float s[32];
+                    for (int k0 = 0; k0 < kSKeys; k0 += 64) {
+                        float s[64];
                         tmem_get32(s_t + k0, s);
+                        tmem_get32(s_t + k0 + 32, s + 32);
                         tmem_wait_ld();
                         tmem_pass32(s);
+                        tmem_pass32(s + 32);
                         if constexpr (EXTRA) {
                             // in log2 units; cap tanh(z / cap) = cap (1 - 2 / (1 + 2^(2 log2(e) z / cap)))
                             if (a.cap > 0.f) {
                                 const float up = 2.f * a.scale_log2 / a.cap, cap2 = a.cap * 1.4426950408889634f;
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) s[k] = cap2 - __fdividef(2.f * cap2, 1.f + ex2(s[k] * up));
+                                for (int k = 0; k < 64; ++k) s[k] = cap2 - __fdividef(2.f * cap2, 1.f + ex2(s[k] * up));
                             } else {
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) s[k] *= a.scale_log2;
+                                for (int k = 0; k < 64; ++k) s[k] *= a.scale_log2;
                             }
-                            const float away = static_cast<float>(t0 + k0 - pos);
+                            if (a.slopes) {
+                                const float away = static_cast<float>(t0 + k0 - pos);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = fmaf(slope2, away + k, s[k]);
+                                for (int k = 0; k < 64; ++k) s[k] = fmaf(slope2, away + k, s[k]);
+                            }
                         }
                         if (masked) {
-                            const int lo = see_lo - t0 - k0, hi = see_hi - t0 - k0;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (k < lo || k >= hi) s[k] = -INFINITY;
+                            for (int h = 0; h < 64; h += 32) {
+                                const uint32_t seen = seen_bits(see_lo - t0 - k0 - h, see_hi - t0 - k0 - h);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) s[h + k] = seen & (1u << k) ? s[h + k] : -INFINITY;
+                            }
                         }
-                        if (EXTRA || masked) tmem_put32(s_t + k0, s);
+                        if (EXTRA || masked) {
+                            tmem_put32(s_t + k0, s);
+                            tmem_put32(s_t + k0 + 32, s + 32);
+                        }
                         float t[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8)
+                        for (int k = 0; k < 64; k += 8)
 #pragma unroll
                             for (int u = 0; u < 4; ++u) t[u] = max3(t[u], s[k + 2 * u], s[k + 2 * u + 1]);
                         mx = fmaxf(max3(t[0], t[1], t[2]), t[3]);
@@ -724,30 +783,44 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                         tmem_wait_st();
                     }
                     const float neg = Q::BIAS - M, unit = EXTRA ? 1.f : a.scale_log2;
+                    float s[2][32];
+                    tmem_get32(s_t, s[0]);
 #pragma unroll 1
-                    for (int k0 = 0; k0 < kSKeys; k0 += 32) {  // the probabilities take their scores' columns
-                        float s[32];
-                        uint32_t hi[16], lo[16];
-                        tmem_get32(s_t + k0, s);
-                        tmem_wait_ld();
-                        tmem_pass32(s);
+                    for (int k0 = 0; k0 < kSKeys; k0 += 64) {  // the probabilities take their scores' columns
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) {
-                            const float2 e = __ffma2_rn(make_float2(s[2 * u], s[2 * u + 1]), make_float2(unit, unit), make_float2(neg, neg));
-                            const float2 pr = make_float2(ex2(e.x), ex2(e.y));
-                            l2 = __fadd2_rn(l2, pr);
-                            split_p<T>(pr, hi[u], lo[u]);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t hi[16], lo[16];
+                            tmem_wait_ld();
+                            tmem_pass32(s[h]);
+                            if (h == 0 || k0 == 0) tmem_get32(s_t + k0 + 32 * h + 32, s[1 - h]);  // the next ones, meanwhile
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) {
+                                const float2 e = __ffma2_rn(make_float2(s[h][2 * u], s[h][2 * u + 1]), make_float2(unit, unit), make_float2(neg, neg));
+                                const float2 pr = make_float2(ex2(e.x), ex2(e.y));
+                                l2 = __fadd2_rn(l2, pr);
+                                split_p<T>(pr, hi[u], lo[u]);
+                            }
+                            tmem_put16(s_t + k0 + 32 * h, hi);
+                            tmem_put16(s_t + k0 + 32 * h + 16, lo);
                         }
-                        tmem_put16(s_t + k0, hi);
-                        tmem_put16(s_t + k0 + 16, lo);
+                        if (k0 == 0) {  // the products with these 64 keys can begin
+                            tmem_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&sh.p_half[w]);
+                        }
                     }
                     tmem_wait_st();
+                } else {
+                    mbar_arrive(&sh.p_half[w]);
                 }
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[w]);
             }
             done += steps;
-            ring += 2 * n;
+            next_piece(n);
+            SPiece after = p;
+            more = shared_next(a, pl, x, x1, after);
+            if (more) load_q(after);
             // ---- results: both warpgroups' columns of their own rows, or half of the columns each of the rows they share
             if (steps > 0 && ok) ok = mbar_wait(&sh.o_done[w], (done - 1) & 1);
             tc_fence_after();
@@ -764,21 +837,22 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                 f1 = ex2(x1.x - M);
                 l = f0 * x0.y + f1 * x1.y;
             }
+            const SPiece here = p;
+            p = after;
             if (!live) continue;
             // the whole of its rows' keys: the result; else a part of it
-            const bool direct = !p.more && n == en.nc && !prefix && (en.group < 0 || pl.e[en.group].nc == 0), mine = m < n_rows;
+            const bool direct = n == en.nc && !prefix && (en.group < 0 || pl.e[en.group].nc == 0), mine = m < n_rows;
             const int cols = wide ? D : D / 2, col0 = wide ? 0 : w * (D / 2);
-            const long long slot = shared_slot(a, prefix, r00, p.h, p.tile, p.more ? cta : -1) + row0;
+            const long long slot = shared_slot(a, prefix, r00, here.h, here.tile, here.c0 > 0 ? cta : -1) + row0;
             if (!direct && mine && (wide || w == 0)) a.part_ml[slot + m] = make_float2(M, l);
             const float inv = direct ? 1.f / l : 1.f;
             f0 *= inv, f1 *= inv;
-            const long long to = direct ? row * a.out_stride + hq * D : (slot + m) * D;
-            // a lane's row becomes a line of lanes in this warp's 4 KB of the used queries' place
-            float *turn = reinterpret_cast<float *>(smem_raw + w * Q::Q_BYTES) + warp % 4 * 1024;
-            const int here = min(32, n_rows - warp % 4 * 32);
+            T *out = static_cast<T *>(a.out) + row * a.out_stride + hq * D + col0;
+            float *part = a.part_o + (slot + m) * D + col0;
 #pragma unroll 1
             for (int k = 0; k < cols; k += 32) {
                 float o[32];
+                __syncwarp();
                 tmem_get32((wide ? o_t : tmem + lanes + Q::O_COL) + col0 + k, o);
                 tmem_wait_ld();
                 tmem_pass32(o);
@@ -792,25 +866,26 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
 #pragma unroll
                     for (int d = 0; d < 32; ++d) o[d] = fmaf(f1, v[d], o[d]);
                 }
-                __syncwarp();
+                if (!mine) continue;
+                if (!direct) {
 #pragma unroll
-                for (int d = 0; d < 32; ++d) turn[lane * 32 + (d ^ lane)] = o[d];
-                __syncwarp();
-                if (direct) {
-#pragma unroll 4
-                    for (int r = 0; r < here; ++r)
-                        static_cast<T *>(a.out)[__shfl_sync(0xffffffffu, to, r) + col0 + k + lane] = from_f32<T>(turn[r * 32 + (lane ^ r)]);
+                    for (int d = 0; d < 32; d += 8) store8(part + k + d, o + d);
+                } else if (a.out_vec) {
+#pragma unroll
+                    for (int d = 0; d < 32; d += 8)
+                        *reinterpret_cast<uint4 *>(out + k + d) = make_uint4(pack16<T>(o[d], o[d + 1]), pack16<T>(o[d + 2], o[d + 3]),
+                                                                             pack16<T>(o[d + 4], o[d + 5]), pack16<T>(o[d + 6], o[d + 7]));
                 } else {
-                    float *dst = a.part_o + (slot + warp % 4 * 32) * D + col0 + k + lane;
-#pragma unroll 8
-                    for (int r = 0; r < here; ++r) dst[r * D] = turn[r * 32 + (lane ^ r)];
+#pragma unroll
+                    for (int d = 0; d < 32; ++d) out[k + d] = from_f32<T>(o[d]);
                 }
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         tc_fence_before();
     }
     __syncthreads();
-    if (is_mma) tmem_dealloc(tmem, 512);
+    if (warp == 10) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ joining the parts
@@ -826,16 +901,16 @@ __global__ void __launch_bounds__(kSMergeThreads) shared_merge_kernel(const __gr
     pdl_trigger();
     const int row = idx / a.nq, hq = idx - row * a.nq, h = a.by_grp.div(hq);
     if (row >= a.max_rows) return;
-    const int b = a.row_seq[row], q = a.plan_cut[0], ov = a.plan_cut[1];
-    if (b == kRowNone) return;
+    const int2 of = a.row_entry[row];
+    const int q = a.plan_cut[0], ov = a.plan_cut[1];
+    if (of.x == kRowNone) return;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + hq * D + lane * V;
-    if (b == kRowRefused) {
+    if (of.x == kRowRefused) {
 #pragma unroll
         for (int d = 0; d < V; ++d) out[d] = from_f32<T>(NAN);
         return;
     }
-    const SEntry own = a.plan[a.G + b];
-    const SEntry pre = own.group >= 0 ? a.plan[own.group] : SEntry{};
+    const SEntry own = a.plan[of.x], pre = of.y >= 0 ? a.plan[of.y] : SEntry{};
     // a tile's start on the line, the CTA it begins in and the number of those it touches
     auto tile_of = [&](const SEntry &n, int &tile, int &r, int &at, int &i0) {
         const int m = (row - n.r0) * a.grp + hq - h * a.grp;
@@ -857,11 +932,31 @@ __global__ void __launch_bounds__(kSMergeThreads) shared_merge_kernel(const __gr
         if (stop <= from) return -1;
         return shared_slot(a, of, n.r0, h, of ? tile[1] : tile[0], from > 0 ? i : -1) + (of ? r[1] : r[0]);
     };
+    const int count = n_own + n_pre;
     long long slot = part(lane);
     if (n_pre == 0 && n_own <= 32 && __popc(__ballot_sync(0xffffffffu, slot >= 0)) == 1) return;  // written already
+    // sixteen parts' values on their way at once, the first beside their maxima
+    constexpr int N = 16;
+    float v[N][V];
+    auto ask = [&](int p0) {
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const long long s = __shfl_sync(0xffffffffu, slot, p0 + u);
+#pragma unroll
+            for (int d = 0; d < V; ++d) v[u][d] = 0.f;
+            if (s >= 0) {
+                const float *src = a.part_o + s * D + lane * V;
+                if constexpr (V == 4)
+                    *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(src);
+                else
+                    *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(src);
+            }
+        }
+    };
     float2 ml = slot >= 0 ? a.part_ml[slot] : make_float2(kQNoRef, 0.f);
+    ask(0);
     float M = ml.x;
-    for (int k = 32 + lane; k - lane < n_own + n_pre; k += 32) {
+    for (int k = 32 + lane; k - lane < count; k += 32) {
         const long long s = part(k);
         if (s >= 0) M = fmaxf(M, a.part_ml[s].x);
     }
@@ -869,32 +964,18 @@ __global__ void __launch_bounds__(kSMergeThreads) shared_merge_kernel(const __gr
     float o[V], l = 0.f;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] = 0.f;
-    for (int k0 = 0; k0 < n_own + n_pre; k0 += 32) {
+    for (int k0 = 0; k0 < count; k0 += 32) {
         if (k0 > 0) {
             slot = part(k0 + lane);
             ml = slot >= 0 ? a.part_ml[slot] : make_float2(kQNoRef, 0.f);
         }
         const float mine = slot >= 0 ? ex2(ml.x - M) : 0.f;
         l += warp_sum(slot >= 0 ? mine * ml.y : 0.f);
-        const int count = min(32, n_own + n_pre - k0);
 #pragma unroll 1
-        for (int p0 = 0; p0 < count; p0 += 8) {
-            float v[8][V];
+        for (int p0 = 0; p0 < min(32, count - k0); p0 += N) {
+            if (k0 + p0 > 0) ask(p0);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const long long s = __shfl_sync(0xffffffffu, slot, p0 + u);
-#pragma unroll
-                for (int d = 0; d < V; ++d) v[u][d] = 0.f;
-                if (s >= 0) {
-                    const float *src = a.part_o + s * D + lane * V;
-                    if constexpr (V == 4)
-                        *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(src);
-                    else
-                        *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(src);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < N; ++u) {
                 const float f = __shfl_sync(0xffffffffu, mine, p0 + u);
 #pragma unroll
                 for (int d = 0; d < V; ++d) o[d] = fmaf(f, v[u][d], o[d]);
