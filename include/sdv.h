@@ -237,6 +237,46 @@ int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_r
                        int rows, int B, int max_commit, int32_t *d_n_accept, int32_t *d_committed, int32_t *d_n_commit,
                        int32_t *d_new_len, void *stream);
 
+/* ---- Several continuations of one prompt. The pages have no counterpart of the three calls below. */
+
+/* Sequences d_dst[i], which must be empty (length 0, no pages), continue sequence d_src[i] from its cache length L, for
+ * i < n (n <= max_batch; sources may repeat, destinations not, and no source is a destination): they share its whole pages,
+ * floor(L / page_size) of them, take a page each for the partial one, whose filled slots are copied in every layer, and
+ * take over its loop state and n-gram history and index. Pages come from the top of the free stack for i = 0 up.
+ * All-or-nothing: a pool that runs dry sets SDV_ERR_CAPACITY, anything else SDV_ERR_ARG, and nothing changes.
+ * A page goes back to the pool when its last holder lets go of it, in the order that sdv_rewind_cache gives (within a call
+ * the last of the holders that let go). A sequence cannot be rewound into a page that others hold, too, since what it
+ * wrote there next would be theirs: such a length, not a multiple of page_size and below the length, is refused by
+ * sdv_rewind_cache (SDV_ERR_ARG, nothing changes). The partial page is always its own, so verifying and rewinding
+ * behind the fork need no care. SDV_ERR_UNSUPPORTED with sliding-window layers, whose rings are written over. */
+int sdv_fork_seq(sdv_ctx *ctx, const int32_t *d_src, const int32_t *d_dst, int n, void *stream);
+
+/* Keep each row's likely tokens. Row r of sequence b (row_off as everywhere; temperature T_b) orders its tokens by logit,
+ * equal ones by index, and weighs them w = exp((logit - the row's largest) / T_b). Kept are the tokens that pass all of
+ *   top-k  the first d_top_k[b] (int32; <= 0: all),
+ *   top-p  of those, each before which the weights sum to less than d_top_p[b] of their total (>= 1: all),
+ *   min-p  w >= d_min_p[b] (<= 0: all),
+ * and always the first token; T_b <= 0 keeps it alone. Any of the three may be NULL. Decisions are those of exact
+ * arithmetic to 2^-37 of the row's total weight. -inf masks a token and NaN counts as -inf: neither is kept.
+ *   d_logits  fp32 rows, logits_stride floats apart (>= vocab); `rows` of them are there, at most the
+ *             context's max_rows and B times its max_span are used. A span past them or longer than max_span sets SDV_ERR_ARG and its rows are
+ *             left alone, as are rows of no span.
+ *   d_out     fp32 rows, out_stride floats apart: the kept logits as they are, -inf elsewhere. d_logits itself will do.
+ *   d_n_kept  [rows] int32, or NULL: tokens kept.
+ * A row without a logit above -inf keeps none (SDV_ERR_DEVICE). The rows made here can go to sdv_accept_sampled, which then
+ * verifies drafts against the filtered distribution. A vocabulary above 425,984 is SDV_ERR_UNSUPPORTED. */
+int sdv_filter_logits(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int rows, const int32_t *d_row_off, int B,
+                      const float *d_temperature, const int32_t *d_top_k, const float *d_top_p, const float *d_min_p, float *d_out,
+                      int64_t out_stride, int32_t *d_n_kept, void *stream);
+
+/* Draw a token for each row from what sdv_filter_logits keeps, in proportion to w: argmax w_v / noise[r][v], lowest index on
+ * a tie, decided as in 64 bits. d_noise: fp32 rows > 0, noise_stride floats apart (>= vocab), draws of the exponential
+ * distribution, read where a token is kept only. d_tokens [rows] int32. A row without a logit above -inf draws token 0
+ * (SDV_ERR_DEVICE). The rest as for sdv_filter_logits. */
+int sdv_sample(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int rows, const int32_t *d_row_off, const float *d_noise,
+               int64_t noise_stride, int B, const float *d_temperature, const int32_t *d_top_k, const float *d_top_p,
+               const float *d_min_p, int32_t *d_tokens, int32_t *d_n_kept, void *stream);
+
 /* [TS] SpecRewindCache; [PI] LIFO drop; [CA] rollback == do not advance.
  * Set each length to d_length[b] (< 0: leave b alone), which must not pass
  * the written length (else SDV_ERR_ARG in the device status, nothing

@@ -35,7 +35,7 @@ EXPORTS = (
     "sdv_governor_decide", "sdv_governor_record", "sdv_governor_new_request", "sdv_governor_stats",
     "sdv_accept_sampled", "sdv_qcache_bytes", "sdv_qcache_create", "sdv_qcache_destroy", "sdv_qcache_write",
     "sdv_qcache_read", "sdv_qcache_attention", "sdv_qcache_get_status",
-    "sdv_shared_bytes", "sdv_shared_create", "sdv_shared_destroy", "sdv_shared_attention", "sdv_shared_get_status",
+    "sdv_fork_seq", "sdv_filter_logits", "sdv_sample", "sdv_shared_bytes", "sdv_shared_create", "sdv_shared_destroy", "sdv_shared_attention", "sdv_shared_get_status",
 )
 PHASES = ("prepare", "qkv_gemm", "attention", "o_gemm", "gateup_gemm", "down_gemm", "lmhead_gemm")
 # sdv_fwd_trace: stamps per CTA, CTAs per region (one region per launch of a forward)
@@ -130,6 +130,9 @@ def lib():
     L.sdv_shared_attention.argtypes = [vp, i32, vp, i64, i32, vp, vp, vp, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, i64,
                                        vp]
     L.sdv_shared_get_status.argtypes = [vp, P(ctypes.c_int32)]
+    L.sdv_fork_seq.argtypes = [vp, vp, vp, i32, vp]
+    L.sdv_filter_logits.argtypes = [vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, i64, vp, vp]
+    L.sdv_sample.argtypes = [vp, vp, i64, i32, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp]
     L.sdv_rewind_cache.argtypes = [vp, vp, i32, vp]
     L.sdv_cache_seq_len.argtypes = [vp, vp, vp]
     L.sdv_page_table.argtypes = [vp, vp, vp, vp, vp]
@@ -401,6 +404,46 @@ class Verifier:
             _vector(n_accept, B, "n_accept", i32), _int_rows(committed, B, max_commit, "committed"),
             _vector(n_commit, B, "n_commit", i32), _vector(new_len, B, "new_len", i32), _stream(stream)),
             "accept_sampled")
+
+    def fork_seq(self, src, dst, n, stream=None):
+        """Sequences dst[i] (empty ones) continue src[i] from its length, i < n: whole pages are shared, the partial
+        one is copied, loop state and n-gram index are taken over. src and dst int32."""
+        i32 = _dtype("int32")
+        _check(lib().sdv_fork_seq(self.ctx, _vector(src, n, "src", i32), _vector(dst, n, "dst", i32), n, _stream(stream)),
+               "fork_seq")
+
+    def _settings(self, B, temperature, top_k, top_p, min_p):
+        """Addresses of the temperature and of each cut's settings, 0 for a cut that is not made."""
+        f32 = _dtype("float32")
+        return (_vector(temperature, B, "temperature", f32), 0 if top_k is None else _vector(top_k, B, "top_k", _dtype("int32")),
+                0 if top_p is None else _vector(top_p, B, "top_p", f32), 0 if min_p is None else _vector(min_p, B, "min_p", f32))
+
+    def filter_logits(self, logits, row_off, B, out, n_kept, temperature, top_k=None, top_p=None, min_p=None, stream=None):
+        """The rows of logits [R, vocab] (float32) with -inf outside of each row's top-k, top-p and min-p set, into
+        out (logits itself will do); n_kept [R] int32 or None: tokens kept. temperature, top_p, min_p [B] float32 and
+        top_k [B] int32 are the sequences'."""
+        V, i32 = self.mcfg.vocab, _dtype("int32")
+        l_stride = _f32_rows(logits, 0, V, "logits")
+        R = logits.shape[0]
+        used = min(R, self.ccfg.max_rows, B * self.ccfg.max_span)
+        _check(lib().sdv_filter_logits(
+            self.ctx, logits.data_ptr(), l_stride, R, _vector(row_off, B + 1, "row_off", i32), B,
+            *self._settings(B, temperature, top_k, top_p, min_p), out.data_ptr(), _f32_rows(out, used, V, "out"),
+            0 if n_kept is None else _vector(n_kept, used, "n_kept", i32), _stream(stream)), "filter_logits")
+
+    def sample(self, logits, row_off, noise, B, tokens, temperature, top_k=None, top_p=None, min_p=None, n_kept=None,
+               stream=None):
+        """A token for each row of logits [R, vocab], drawn from its top-k, top-p and min-p set with the given exponential
+        noise [R, vocab] (float32), into tokens [R] int32; settings and n_kept as filter_logits."""
+        V, i32 = self.mcfg.vocab, _dtype("int32")
+        l_stride = _f32_rows(logits, 0, V, "logits")
+        R = logits.shape[0]
+        used = min(R, self.ccfg.max_rows, B * self.ccfg.max_span)
+        _check(lib().sdv_sample(
+            self.ctx, logits.data_ptr(), l_stride, R, _vector(row_off, B + 1, "row_off", i32), noise.data_ptr(),
+            _f32_rows(noise, used, V, "noise"), B, *self._settings(B, temperature, top_k, top_p, min_p),
+            _vector(tokens, used, "tokens", i32), 0 if n_kept is None else _vector(n_kept, used, "n_kept", i32),
+            _stream(stream)), "sample")
 
     def rewind_cache(self, length, B, stream=None):
         _check(lib().sdv_rewind_cache(self.ctx, _ptr(length), B, _stream(stream)), "rewind_cache")

@@ -1,0 +1,805 @@
+// Filtered sampling: a row's tokens cut to its top-k, top-p and min-p set, and a draw from it by given random numbers.
+//
+// Tokens are ordered by logit, equal ones by index: a 64-bit key each, and a kept set is the keys at or above one of them.
+// With w = 2^-((m - x) log2(e) / T), m the row's largest logit, top-p keeps token i iff the weights before it sum to less than
+// p of the top-k set's. The row stays in the shared memory of a cluster of CTAs, and a histogram over (m - x) / T shows in
+// which bin the border lies. Where no more than kFilterList tokens lie down to it, as in most rows of a language model, they
+// go to one CTA, which sorts them and cuts and draws by itself; where more do, sums over the bin's edges confirm the bin, and
+// its tokens alone are compared with one another.
+//
+// Whether a token is kept is decided as exact arithmetic would: sums are fp32 weights in 64 bits and hold to 2^-17 of the
+// total each (kFilterNear); a border nearer than that is decided on weights of 2^-39 (weight_exact), summed as integers, whose
+// order does not matter.
+#pragma once
+
+#include "accept_sampled.cuh"
+
+namespace sdv {
+
+constexpr int kFilterThreads = 512;
+constexpr int kFilterBins = 1024;
+constexpr int kFilterFew = 256;                  // tokens that are compared with one another
+constexpr float kFilterRange = 40.f;             // log2 of the weights that the histogram's bins cover
+constexpr int kFilterCluster = 8;                // CTAs of a row
+constexpr int kFilterAlone = 8192;               // tokens of a row that one CTA takes
+constexpr int kFilterList = 2048;                // tokens that one CTA sorts
+constexpr int kFilterMost = 49152;               // tokens of a CTA at most (192 KB)
+// How far a sum of fp32 weights and p times another may lie from each other's exact values, over the total: an exponent
+// t = (m - x) log2(e) / T takes three roundings, 2.1 t 2^-24 after ln 2, and t averages log2 of the vocabulary at most over the
+// weights (19: 40 2^-24); ex2 is off by 4 2^-24, a thread's sum of up to 96 terms by 96 2^-24. 140 2^-24 each, 2^-15.9 both.
+constexpr double kFilterNear = 0x1p-15;
+
+struct FilterArgs {
+    int *status;
+    const int *row_off;
+    const float *logits, *temperature, *top_p, *min_p, *noise;
+    const int *top_k;
+    long long logits_stride, noise_stride, out_stride;  // floats between rows
+    float *out;      // filter: the kept logits, -inf elsewhere
+    int *tokens;     // sample: a token a row
+    int *n_kept;     // or null
+    int B, vocab, max_span, rows_cap, chunk;  // chunk: tokens of a CTA
+};
+
+__device__ __forceinline__ float filter_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int BYTES>
+__device__ __forceinline__ void filter_copy(float *dst, const float *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_dsmem_u64(uint32_t addr, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_dsmem_u32(uint32_t addr, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+    return old;
+}
+
+struct FilterSums {
+    double a, b;                          // summed
+    unsigned long long hi, lo;            // the largest, the smallest
+};
+struct FilterShared {
+    uint32_t hist[kFilterBins], total[kFilterBins];  // of this CTA, of the row
+    FilterSums warp[kFilterThreads / 32], part[2][kFilterCluster];
+    unsigned long long list[kFilterList];            // CTA 0's: keys, or the border's tokens' keys and then their weights
+    unsigned long long cut, scan_e[kFilterThreads / 32];
+    double mass;
+    uint32_t table_hi[64], table_lo[64];  // 2^(-j / 64) as the integer 2^58 times it
+    uint32_t n_cand, scan[kFilterThreads / 32], ambiguous, kept;
+    float scan_w[kFilterThreads / 32], about;
+    int found[3], seq, fails;
+};
+
+__device__ __forceinline__ unsigned long long filter_key(float x, int v) {  // -0 and 0 are equal
+    return static_cast<unsigned long long>(orderable(x + 0.f)) << 32 | static_cast<uint32_t>(~v);
+}
+
+// A row's constants.
+struct FilterRow {
+    float m, c_hi, c_lo, scale;  // the maximum, log2(e) / T in two parts, bins a logit
+    double T;
+};
+__device__ __forceinline__ float filter_weight(const FilterRow &r, float x) {
+    if (x == r.m) return 1.f;
+    const float t = (r.m - x) * r.c_hi;
+    return t < 150.f ? filter_ex2(-t) : 0.f;
+}
+// The weight as an integer times 2^-58, to 2^-39: the exponent in two fp32 parts, 2^-n/64 from a table and the rest, below
+// 2^-7, by the series of e^z in two parts.
+__device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, const FilterShared &sh, float x) {
+    if (x == r.m) return 1ull << 58;
+    const float s = r.m - x, bb = s - r.m, e = (r.m - (s - bb)) - (x + bb);  // s + e = m - x
+    const float p = s * r.c_hi;
+    if (!(p < 60.f)) return 0;
+    const float q = fmaf(s, r.c_hi, -p) + (s * r.c_lo + e * r.c_hi);         // p + q = (m - x) c
+    const int n = __float2int_rn(p * 64.f);
+    const float f = p - static_cast<float>(n) * 0.015625f;                   // exact
+    constexpr float L = -0.693147182f, L_lo = 1.90465421e-9f;                // L + L_lo = -ln 2
+    const float u = f * L, u_lo = fmaf(f, L, -u) + (f * L_lo + q * L);       // z = u + u_lo
+    const float g = u_lo + u * u * (0.5f + u * (0.16666667f + u * 0.041666668f));  // e^z - 1 = u + g
+    const unsigned long long t58 = static_cast<unsigned long long>(sh.table_hi[n & 63]) << 32 | sh.table_lo[n & 63];
+    const float tf = __ull2float_rn(t58) * 0x1p-58f;
+    const float tl = static_cast<float>(static_cast<long long>(t58 - static_cast<unsigned long long>(static_cast<double>(tf) * 0x1p58))) * 0x1p-58f;
+    const float a = tf * u, b = fmaf(tf, u, -a) + (tf * g + tl * u);         // t (e^z - 1)
+    const long long w = static_cast<long long>(t58) + __float2ll_rn(a * 0x1p58f) + __float2ll_rn(b * 0x1p58f);
+    return static_cast<unsigned long long>(w) >> (n >> 6);
+}
+
+__device__ __forceinline__ void filter_join(FilterSums &s, const FilterSums &o) {
+    s.a += o.a;
+    s.b += o.b;
+    s.hi = o.hi > s.hi ? o.hi : s.hi;
+    s.lo = o.lo < s.lo ? o.lo : s.lo;
+}
+// Over the row, in an order that does not change: by every thread of every CTA, who all get the result.
+__device__ FilterSums filter_reduce(FilterShared &sh, FilterSums s, int ctas, int rank, int turn) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int W = kFilterThreads / 32;
+    auto across = [&](int from) {
+#pragma unroll
+        for (int o = from; o > 0; o >>= 1) {
+            FilterSums t;
+            t.a = __shfl_xor_sync(0xffffffffu, s.a, o);
+            t.b = __shfl_xor_sync(0xffffffffu, s.b, o);
+            t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+            t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+            filter_join(s, t);
+        }
+    };
+    across(16);
+    if (lane == 0) sh.warp[warp] = s;
+    __syncthreads();
+    FilterSums (&part)[kFilterCluster] = sh.part[turn & 1];
+    if (warp == 0) {  // this CTA's sums to every CTA
+        s = sh.warp[lane % W];
+        across(W / 2);
+        if (lane < ctas) {
+            const uint32_t to = mapa_shared(smem_u32(&part[rank]), lane);
+            st_dsmem_u64(to, __double_as_longlong(s.a));
+            st_dsmem_u64(to + 8, __double_as_longlong(s.b));
+            st_dsmem_u64(to + 16, s.hi);
+            st_dsmem_u64(to + 24, s.lo);
+        }
+    }
+    if (ctas > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    s = part[0];
+    for (int r = 1; r < ctas; ++r) filter_join(s, part[r]);
+    return s;
+}
+__device__ __forceinline__ void filter_sync(int ctas) {
+    if (ctas > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+}
+
+// What a search looks for: the last token with fewer than `k` before it and, if by_mass, less than `target` of weight before it.
+struct FilterGoal {
+    bool by_mass;
+    int k;
+    double target, p, total;  // target = p total
+    double off;               // the histogram's total less the exact one
+    unsigned long long set;   // the mass's tokens: keys at or above it
+};
+
+__device__ __forceinline__ float filter_value(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+template <bool SAMPLE>
+__global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_constant__ FilterArgs a) {
+    extern __shared__ __align__(16) float x_s[];
+    __shared__ FilterShared sh;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
+    const int v0 = rank * a.chunk, n = max(0, min(a.chunk, a.vocab - v0)), n4 = (n + 3) / 4;
+    if (tid == 0) sh.seq = -1, sh.n_cand = 0;
+    pdl_wait();
+    pdl_trigger();
+    // the row's logits are asked for before its sequence is known; four at a time in every pass, -inf behind the last
+    const float *src = a.logits + row * a.logits_stride + v0;
+    if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+        for (int i = tid * 4; i + 3 < n; i += kFilterThreads * 4) filter_copy<16>(x_s + i, src + i);
+        for (int i = (n & ~3) + tid; i < n; i += kFilterThreads) filter_copy<4>(x_s + i, src + i);
+    } else {
+        for (int i = tid; i < n; i += kFilterThreads) filter_copy<4>(x_s + i, src + i);
+    }
+    if (tid < 4 && n + tid < 4 * n4) x_s[n + tid] = -INFINITY;
+    __syncthreads();
+    if (tid < a.B) {  // B <= 256 threads
+        const int r0 = a.row_off[tid], S = a.row_off[tid + 1] - r0;
+        const bool ok = S > 0 && S <= a.max_span && r0 >= 0 && r0 <= a.rows_cap - S;
+        if (ok && row >= r0 && row < r0 + S) sh.seq = tid;
+        if (!ok && S != 0 && row == 0 && rank == 0) set_status(a.status, SDV_ERR_ARG);
+    }
+    for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = 0;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    const int b = sh.seq;
+    if (b < 0) return;  // a row of no span: every CTA of the cluster leaves
+    const float T = a.temperature[b];
+    const float top_p = a.top_p ? a.top_p[b] : 2.f, min_p = a.min_p ? a.min_p[b] : 0.f;
+    const int top_k = a.top_k ? a.top_k[b] : 0;
+    int turn = 0;
+    const unsigned long long none = ~0ull;
+    float4 *x4 = reinterpret_cast<float4 *>(x_s);
+    auto each = [&](auto f) {  // f(logit, place in the chunk) of this thread's tokens above -inf
+        for (int i = tid; i < n4; i += kFilterThreads) {
+            const float4 x = x4[i];
+            if (x.x > -INFINITY) f(x.x, 4 * i);
+            if (x.y > -INFINITY) f(x.y, 4 * i + 1);
+            if (x.z > -INFINITY) f(x.z, 4 * i + 2);
+            if (x.w > -INFINITY) f(x.w, 4 * i + 3);
+        }
+    };
+    // ---- the maximum, and the tokens above -inf
+    FilterRow r;
+    int valid;
+    unsigned long long top;  // the first token
+    {
+        float m = -INFINITY;
+        int count = 0, first = 0;
+        for (int i = tid; i < n4; i += kFilterThreads) {
+            float4 x = x4[i];
+            const bool ok = x.x > -INFINITY && x.y > -INFINITY && x.z > -INFINITY && x.w > -INFINITY;
+            if (!ok) {  // NaN counts as -inf
+                x.x = x.x > -INFINITY ? x.x : -INFINITY, x.y = x.y > -INFINITY ? x.y : -INFINITY;
+                x.z = x.z > -INFINITY ? x.z : -INFINITY, x.w = x.w > -INFINITY ? x.w : -INFINITY;
+                x4[i] = x;
+                count -= (x.x == -INFINITY) + (x.y == -INFINITY) + (x.z == -INFINITY) + (x.w == -INFINITY);
+            }
+            count += 4;
+            const float four = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+            if (four > m) {  // a thread's indexes ascend
+                m = four;
+                first = v0 + 4 * i + (x.x == m ? 0 : x.y == m ? 1 : x.z == m ? 2 : 3);
+            }
+        }
+        FilterSums s = {static_cast<double>(count), 0., count ? filter_key(m, first) : 0ull, none};
+        s = filter_reduce(sh, s, ctas, rank, turn++);
+        valid = static_cast<int>(s.a);
+        top = s.hi;
+        r.m = filter_value(static_cast<uint32_t>(s.hi >> 32));
+    }
+    unsigned long long cut = 0;  // the kept set: keys at or above it
+    int kept = valid;
+    float *out = SAMPLE ? nullptr : a.out + row * a.out_stride + v0;
+    if (valid == 0) {  // nothing to keep
+        if (!SAMPLE)
+            for (int i = tid; i < n; i += kFilterThreads) out[i] = -INFINITY;
+        if (rank == 0 && tid == 0) {
+            if (SAMPLE) a.tokens[row] = 0;
+            if (a.n_kept) a.n_kept[row] = 0;
+            set_status(a.status, SDV_ERR_DEVICE);
+        }
+        if (ctas > 1) cluster_sync();
+        return;
+    }
+    r.T = T;
+    const double c = 1.4426950408889634 / static_cast<double>(T);
+    r.c_hi = static_cast<float>(c);
+    r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
+    r.scale = r.c_hi * (kFilterBins / kFilterRange);
+    if (!(T > 0.f) || min_p > 1.f || top_p <= 0.f) cut = top, kept = 1;  // the first token alone
+    const bool want_k = kept > 1 && top_k > 0 && top_k < valid, want_p = kept > 1 && top_p > 0.f && top_p < 1.f;
+    const bool want_m = kept > 1 && min_p > 0.f;
+    const double least = want_m ? static_cast<double>(r.m) + r.T * log(static_cast<double>(min_p)) : -INFINITY;
+    auto strong = [&](float x) { return !want_m || x == r.m || static_cast<double>(x) >= least; };
+    auto bin_of = [&](float x) { return min(kFilterBins - 1, static_cast<int>((r.m - x) * r.scale)); };
+    auto middle_weight = [](int i) { return filter_ex2(-(i + .5f) * (kFilterRange / kFilterBins)); };
+    bool precise = false, listed = false;  // listed: the kept tokens are CTA 0's first ones, in order
+
+    if (want_k || want_p) {
+        if (tid < 64) {  // for weight_exact
+            const unsigned long long t = static_cast<unsigned long long>(exp2(-tid / 64.) * 0x1p58);
+            sh.table_hi[tid] = static_cast<uint32_t>(t >> 32);
+            sh.table_lo[tid] = static_cast<uint32_t>(t);
+        }
+        // this CTA's histogram -> the row's, in every CTA
+        auto add_up = [&]() {
+            filter_sync(ctas);
+            const int share = kFilterBins / ctas;
+            for (int i = tid; i < share; i += kFilterThreads) {
+                const int bin = rank * share + i;
+                uint32_t part[kFilterCluster], sum = 0;
+#pragma unroll
+                for (int q = 0; q < kFilterCluster; ++q) part[q] = q < ctas ? ld_dsmem_u32(mapa_shared(smem_u32(&sh.hist[bin]), q)) : 0;
+#pragma unroll
+                for (int q = 0; q < kFilterCluster; ++q) sum += part[q];
+                for (int q = 0; q < ctas; ++q) st_dsmem_u32(mapa_shared(smem_u32(&sh.total[bin]), q), sum);
+            }
+            filter_sync(ctas);
+        };
+        // The first bin in [first, last] at which the tokens so far reach `k`, or about `mass` of weight (bin i's tokens weigh
+        // about weight(i) each), else the last: found[0]; tokens before it: found[1], in it: found[2], weight before it: about.
+        auto find_bin = [&](bool by_mass, int k, double mass, int first, int last, auto weight) {
+            const uint32_t n0 = sh.total[2 * tid], n1 = sh.total[2 * tid + 1];
+            __syncthreads();
+            if (tid == 0) sh.found[0] = last;
+            uint32_t count = n0 + n1;
+            const float w0 = by_mass ? n0 * weight(2 * tid) : 0.f, w1 = by_mass ? n1 * weight(2 * tid + 1) : 0.f;
+            float w = w0 + w1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t c2 = __shfl_up_sync(0xffffffffu, count, o);
+                const float w2 = __shfl_up_sync(0xffffffffu, w, o);
+                if (lane >= o) count += c2, w += w2;
+            }
+            if (lane == 31) sh.scan[warp] = count, sh.scan_w[warp] = w;
+            __syncthreads();
+            for (int i = 0; i < warp; ++i) count += sh.scan[i], w += sh.scan_w[i];
+            const uint32_t c0 = count - n1;
+            auto reaches = [&](uint32_t cnt, float ms) { return by_mass ? ms >= static_cast<float>(mass) : cnt >= static_cast<uint32_t>(k); };
+            const int here = reaches(c0, w - w1) ? 2 * tid : reaches(count, w) ? 2 * tid + 1 : kFilterBins;
+            if (here < kFilterBins) atomicMin(&sh.found[0], max(here, first));
+            __syncthreads();
+            const int j = sh.found[0];
+            if (j / 2 == tid) {
+                sh.found[1] = static_cast<int>(j & 1 ? c0 : c0 - n0);
+                sh.found[2] = static_cast<int>(j & 1 ? n1 : n0);
+                sh.about = w - w1 - (j & 1 ? 0.f : w0);
+            }
+            __syncthreads();
+        };
+        // Weight of the tokens for which in0 and in1 hold, and the keys for which in1 holds but not in0: smallest and largest.
+        auto sums = [&](auto in0, auto in1) {
+            FilterSums s = {0., 0., 0ull, none};
+            float f0 = 0.f, f1 = 0.f;
+            unsigned long long e0 = 0, e1 = 0;
+            each([&](float x, int i) {
+                if (!in1(x, i)) return;
+                const bool both = in0(x, i);
+                if (precise) {
+                    const unsigned long long w = weight_exact(r, sh, x) >> 7;  // a thread adds up to 96
+                    e1 += w;
+                    if (both) e0 += w;
+                } else {
+                    const float w = filter_weight(r, x);
+                    f1 += w;
+                    if (both) f0 += w;
+                }
+                if (!both) {
+                    const unsigned long long k = filter_key(x, v0 + i);
+                    s.hi = k > s.hi ? k : s.hi;
+                    s.lo = k < s.lo ? k : s.lo;
+                }
+            });
+            s.a = precise ? static_cast<double>(e0) * 0x1p-51 : static_cast<double>(f0);
+            s.b = precise ? static_cast<double>(e1) * 0x1p-51 : static_cast<double>(f1);
+            return filter_reduce(sh, s, ctas, rank, turn++);
+        };
+        auto set_total = [&](FilterGoal &g) {
+            g.total = sums([&](float, int) { return true; }, [&](float x, int i) { return filter_key(x, v0 + i) >= g.set; }).a;
+            g.target = g.p * g.total;
+        };
+        // The key of the goal's last token; kept: tokens down to it.
+        auto search = [&](FilterGoal g, int &kept_out) -> unsigned long long {
+            // ---- a bin of the histogram over (m - x) / T: by weight a guess, confirmed by the sums over its edges or made
+            // again from how far the sum before it is from the guess's
+            int first = 0, last = kFilterBins - 1, above, count;
+            double A = 0., guess = g.target + g.off;
+            unsigned long long hi = 0, lo = none;
+            for (int tries = 0;; ++tries) {
+                const int half = (first + last) / 2;  // guesses that do not settle
+                find_bin(g.by_mass, g.k, guess, tries < 4 ? first : half, tries < 4 ? last : half, middle_weight);
+                const int j = sh.found[0];
+                above = sh.found[1], count = sh.found[2];
+                const double about = sh.about;
+                for (;;) {
+                    const FilterSums s = sums([&](float x, int) { return bin_of(x) < j; }, [&](float x, int) { return bin_of(x) <= j; });
+                    A = s.a, hi = s.hi, lo = s.lo;
+                    if (g.by_mass && !precise && (fabs(A - g.target) <= kFilterNear * g.total || fabs(s.b - g.target) <= kFilterNear * g.total)) {
+                        precise = true;
+                        set_total(g);
+                        continue;
+                    }
+                    if (g.by_mass && A >= g.target)
+                        last = j - 1;
+                    else if (g.by_mass && s.b < g.target)
+                        first = j + 1;
+                    else
+                        last = -1;
+                    break;
+                }
+                if (first > last) break;
+                guess = g.target - (A - about);
+            }
+            // ---- while there are many tokens, a bin of the histogram over their keys' logits
+            while (count > kFilterFew) {
+                const uint32_t k_hi = static_cast<uint32_t>(hi >> 32), k_lo = static_cast<uint32_t>(lo >> 32);
+                if (k_hi == k_lo) break;
+                int shift = 0;
+                while ((k_hi - k_lo) >> shift >= kFilterBins) ++shift;
+                __syncthreads();
+                for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = 0;
+                __syncthreads();
+                each([&](float x, int) {
+                    const uint32_t k = orderable(x + 0.f);
+                    if (k <= k_hi && k >= k_lo) atomicAdd(&sh.hist[(k_hi - k) >> shift], 1u);
+                });
+                add_up();
+                find_bin(g.by_mass, g.k - above, g.target - A, 0, kFilterBins - 1,
+                         [&](int i) { return filter_weight(r, filter_value(k_hi - (static_cast<uint32_t>(i) << shift))); });
+                const int bin = sh.found[0], before = sh.found[1], inside = sh.found[2];
+                const uint32_t h = k_hi - (static_cast<uint32_t>(bin) << shift), width = 1u << shift;
+                const uint32_t l = h - k_lo >= width ? h - width + 1 : k_lo;
+                FilterSums s;
+                for (;;) {
+                    s = sums([&](float x, int) { return orderable(x + 0.f) > h; }, [&](float x, int) { return orderable(x + 0.f) >= l; });
+                    const double near = kFilterNear * g.total;
+                    if (g.by_mass && !precise && (fabs(s.a - g.target) <= near || fabs(s.b - g.target) <= near)) {
+                        precise = true;
+                        set_total(g);
+                        continue;
+                    }
+                    break;
+                }
+                if (g.by_mass && s.a >= g.target && before > 0) {  // above this bin
+                    lo = static_cast<unsigned long long>(h + 1) << 32;
+                    count = before;
+                } else if (g.by_mass && s.b < g.target && before + inside < count) {  // below it
+                    hi = static_cast<unsigned long long>(l - 1) << 32 | 0xffffffffu;
+                    above += before + inside;
+                    count -= before + inside;
+                    A = s.b;
+                } else {
+                    hi = s.hi, lo = s.lo;
+                    above += before;
+                    count = inside;
+                    A = s.a;
+                }
+            }
+            if (count > kFilterFew) {
+                // ---- many equal logits: the first of them by index
+                const uint32_t k = static_cast<uint32_t>(hi >> 32);
+                const float x = filter_value(k);
+                int want = min(count, g.k - above);
+                if (g.by_mass) {
+                    if (!precise) {
+                        precise = true;
+                        set_total(g);
+                        A = sums([&](float y, int) { return orderable(y + 0.f) > k; }, [&](float y, int) { return orderable(y + 0.f) > k; }).a;
+                    }
+                    const double w = static_cast<double>(weight_exact(r, sh, x)) * 0x1p-58, need = ceil((g.target - A) / w);
+                    if (w > 0. && need < want) want = max(1, static_cast<int>(need));
+                }
+                // tokens in order: CTAs, then threads, a run of the chunk each
+                const int run = (n + kFilterThreads - 1) / kFilterThreads, i0 = min(n, tid * run), i1 = min(n, i0 + run);
+                int mine = 0;
+                for (int i = i0; i < i1; ++i) mine += x_s[i] == x;
+                int sum = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += v;
+                }
+                __syncthreads();
+                if (lane == 31) sh.scan[warp] = sum;
+                __syncthreads();
+                int before = sum - mine, all = 0;
+                for (int i = 0; i < kFilterThreads / 32; ++i) {
+                    if (i < warp) before += sh.scan[i];
+                    all += sh.scan[i];
+                }
+                if (tid == 0) sh.kept = all;
+                filter_sync(ctas);
+                for (int q = 0; q < rank; ++q) before += ld_dsmem_u32(mapa_shared(smem_u32(&sh.kept), q));
+                filter_sync(ctas);
+                if (before < want && before + mine >= want) {
+                    int i = i0, seen = before;
+                    for (; i < i1; ++i)
+                        if (x_s[i] == x && ++seen == want) break;
+                    for (int q = 0; q < ctas; ++q) st_dsmem_u64(mapa_shared(smem_u32(&sh.cut), q), filter_key(x, v0 + i));
+                }
+                filter_sync(ctas);
+                kept_out = above + want;
+                const unsigned long long found = sh.cut;
+                __syncthreads();
+                return found;
+            }
+            // ---- the border's tokens, to the first CTA
+            const uint32_t counter = mapa_shared(smem_u32(&sh.n_cand), 0);
+            each([&](float x, int i) {
+                const unsigned long long k = filter_key(x, v0 + i);
+                if (k <= hi && k >= lo) {
+                    const uint32_t at = add_dsmem_u32(counter, 1);
+                    if (at < kFilterFew) {
+                        st_dsmem_u64(mapa_shared(smem_u32(&sh.list[at]), 0), k);
+                        st_dsmem_u64(mapa_shared(smem_u32(&sh.list[kFilterFew + at]), 0), g.by_mass ? weight_exact(r, sh, x) >> 8 : 0ull);
+                    }
+                }
+            });
+            filter_sync(ctas);
+            for (;;) {
+                if (rank == 0) {
+                    const int m = min(static_cast<int>(sh.n_cand), kFilterFew);
+                    if (tid == 0) sh.ambiguous = 0, sh.kept = 0;
+                    __syncthreads();
+                    if (tid < m) {
+                        const unsigned long long mine = sh.list[tid];
+                        unsigned long long before = 0;
+                        int place = above;
+                        for (int q = 0; q < m; ++q) {
+                            const bool earlier = sh.list[q] > mine;
+                            before += earlier ? sh.list[kFilterFew + q] : 0ull;
+                            place += earlier;
+                        }
+                        bool keep = place < g.k;
+                        if (g.by_mass) {
+                            const double mass = A + static_cast<double>(before) * 0x1p-50;
+                            if (!precise && fabs(mass - g.target) <= kFilterNear * g.total) sh.ambiguous = 1;
+                            keep = keep && mass < g.target;
+                        }
+                        if (keep || place == 0) atomicMax(&sh.kept, static_cast<uint32_t>(place + 1));
+                    }
+                    __syncthreads();
+                    const int last = max(static_cast<int>(sh.kept), above + 1);  // at least the first of them
+                    if (tid < m) {
+                        int place = above;
+                        const unsigned long long mine = sh.list[tid];
+                        for (int q = 0; q < m; ++q) place += sh.list[q] > mine;
+                        if (place + 1 == last) {
+                            for (int q = 0; q < ctas; ++q) {
+                                st_dsmem_u64(mapa_shared(smem_u32(&sh.cut), q), mine);
+                                st_dsmem_u32(mapa_shared(smem_u32(&sh.kept), q), last);
+                                st_dsmem_u32(mapa_shared(smem_u32(&sh.ambiguous), q), sh.ambiguous);
+                            }
+                        }
+                    }
+                }
+                filter_sync(ctas);
+                const bool again = g.by_mass && !precise && sh.ambiguous;
+                const unsigned long long found = sh.cut;
+                kept_out = static_cast<int>(sh.kept);
+                filter_sync(ctas);
+                if (!again) {
+                    if (rank == 0 && tid == 0) sh.n_cand = 0;
+                    return found;
+                }
+                precise = true;
+                set_total(g);
+                A = sums([&](float x, int i) { return filter_key(x, v0 + i) > hi; }, [&](float x, int i) { return filter_key(x, v0 + i) > hi; }).a;
+            }
+        };
+
+        // ---- the histogram, the total, and what it is with each token in the middle of its bin; the last bin's tokens are
+        // those that the others leave
+        auto count_bins = [&]() {
+            float f = 0.f, middle = 0.f;
+            each([&](float x, int) {
+                const int bin = bin_of(x);
+                if (bin < kFilterBins - 1) atomicAdd(&sh.hist[bin], 1u);
+                f += filter_weight(r, x);
+                middle += middle_weight(bin);
+            });
+            return make_float2(f, middle);
+        };
+        auto last_bin = [&]() {
+            const int others = static_cast<int>(sh.total[2 * tid] + (tid == kFilterThreads - 1 ? 0 : sh.total[2 * tid + 1]));
+            const int sum = __reduce_add_sync(0xffffffffu, others);
+            if (lane == 0) sh.scan[warp] = sum;
+            __syncthreads();
+            int all = 0;
+            for (int w = 0; w < kFilterThreads / 32; ++w) all += sh.scan[w];
+            if (tid == 0) sh.total[kFilterBins - 1] = valid - all;
+            __syncthreads();
+        };
+        FilterGoal g = {false, want_k ? top_k : valid, 0., static_cast<double>(top_p), 0., 0., 0ull};
+        const float2 all = count_bins();
+        FilterSums s = {static_cast<double>(all.x), static_cast<double>(all.y), 0ull, none};
+        s = filter_reduce(sh, s, ctas, rank, turn++);
+        g.total = s.a;
+        g.target = g.p * g.total;
+        g.off = s.b - s.a;
+        add_up();
+        last_bin();
+        // ---- few tokens: those of the bins down to the border. By weight it is guessed from the tail, which lies in narrow
+        // bins of light tokens, and a little too far.
+        find_bin(!want_k, g.k, g.target + g.off + 0.05 * (g.total - g.target), 0, kFilterBins - 1, middle_weight);
+        const int last = sh.found[0], in_list = sh.found[1] + sh.found[2];
+        if (in_list <= kFilterList) {
+            const uint32_t counter = mapa_shared(smem_u32(&sh.n_cand), 0);
+            each([&](float x, int i) {
+                if (bin_of(x) <= last) st_dsmem_u64(mapa_shared(smem_u32(&sh.list[add_dsmem_u32(counter, 1)]), 0), filter_key(x, v0 + i));
+            });
+            filter_sync(ctas);
+            int size = 32;
+            while (size < in_list) size *= 2;
+            if (rank == 0) {
+                for (int i = in_list + tid; i < size; i += kFilterThreads) sh.list[i] = 0;
+                __syncthreads();
+                for (int k = 2; k <= size; k *= 2)  // bitonic, largest first
+                    for (int j = k / 2; j > 0; j /= 2) {
+                        for (int i = tid; i < size / 2; i += kFilterThreads) {
+                            const int p = 2 * i - (i & (j - 1)), q = p + j;
+                            const unsigned long long u = sh.list[p], v = sh.list[q];
+                            if ((u < v) == ((p & k) == 0)) sh.list[p] = v, sh.list[q] = u;
+                        }
+                        __syncthreads();
+                    }
+            }
+            for (;;) {
+                if (rank == 0) {
+                    // weights before each token, in order: exact
+                    constexpr int PER = kFilterList / kFilterThreads;
+                    const int per = (in_list + kFilterThreads - 1) / kFilterThreads;
+                    unsigned long long w[PER], sum = 0;
+#pragma unroll
+                    for (int u = 0; u < PER; ++u) {
+                        const int i = tid * per + u;
+                        w[u] = want_p && u < per && i < in_list ? weight_exact(r, sh, filter_value(static_cast<uint32_t>(sh.list[i] >> 32))) >> 7 : 0ull;
+                        sum += w[u];
+                    }
+                    unsigned long long before = sum;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const unsigned long long v = __shfl_up_sync(0xffffffffu, before, o);
+                        if (lane >= o) before += v;
+                    }
+                    if (lane == 31) sh.scan_e[warp] = before;
+                    if (tid == 0) sh.fails = in_list, sh.ambiguous = 0, sh.mass = g.total;
+                    __syncthreads();
+                    before -= sum;
+                    for (int i = 0; i < warp; ++i) before += sh.scan_e[i];
+                    if (want_k) {  // the top-k set's weight
+                        unsigned long long upto = before;
+#pragma unroll
+                        for (int u = 0; u < PER; ++u) {
+                            upto += w[u];
+                            if (u < per && tid * per + u == g.k - 1) sh.mass = static_cast<double>(upto) * 0x1p-51;
+                        }
+                        __syncthreads();
+                    }
+                    const double target = g.p * sh.mass;
+#pragma unroll
+                    for (int u = 0; u < PER; ++u) {
+                        const int i = tid * per + u;
+                        if (u < per && i < in_list) {
+                            const double mass = static_cast<double>(before) * 0x1p-51;
+                            if (want_p && !want_k && !precise && fabs(mass - target) <= kFilterNear * g.total) sh.ambiguous = 1;
+                            if (i >= g.k || (want_p && !(mass < target)) || !strong(filter_value(static_cast<uint32_t>(sh.list[i] >> 32))))
+                                atomicMin(&sh.fails, max(i, 1));
+                            before += w[u];
+                        }
+                    }
+                    __syncthreads();
+                    // the list ends before the border: the search below
+                    if (tid == 0 && sh.fails == in_list && in_list < min(valid, g.k)) sh.ambiguous |= 2;
+                    __syncthreads();
+                    if (tid < ctas) {
+                        st_dsmem_u64(mapa_shared(smem_u32(&sh.cut), tid), sh.list[sh.fails - 1]);
+                        st_dsmem_u32(mapa_shared(smem_u32(&sh.kept), tid), sh.fails);
+                        if (tid > 0) st_dsmem_u32(mapa_shared(smem_u32(&sh.ambiguous), tid), sh.ambiguous);
+                    }
+                }
+                filter_sync(ctas);
+                const uint32_t state = sh.ambiguous;
+                cut = sh.cut, kept = static_cast<int>(sh.kept);
+                listed = !(state & 2);
+                if (!(state & 1)) break;
+                filter_sync(ctas);  // all have read it
+                precise = true;
+                set_total(g);
+            }
+            if (!listed) {
+                cut = 0, kept = valid;
+                if (rank == 0 && tid == 0) sh.n_cand = 0;
+            }
+        }
+        if (!listed) {
+            FilterGoal h = g;
+            if (want_k) cut = search(h, kept);
+            if (want_p && kept > 1) {
+                if (want_k) {  // the row's histogram again: a search may have used its place
+                    __syncthreads();
+                    for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = 0;
+                    __syncthreads();
+                    count_bins();
+                    add_up();
+                    last_bin();
+                    h.set = cut;
+                    set_total(h);
+                }
+                h.by_mass = true;
+                cut = search(h, kept);
+            }
+        }
+    }
+    // ---- what is kept
+    if constexpr (!SAMPLE) {
+        int count = 0;
+        const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+        const uint32_t cut_x = static_cast<uint32_t>(cut >> 32);
+        auto keep = [&](float x, int i) {
+            const uint32_t k = orderable(x + 0.f);
+            const bool yes = x > -INFINITY && (k > cut_x || (k == cut_x && filter_key(x, v0 + i) >= cut)) && (listed || strong(x));
+            count += yes;
+            return yes ? x : -INFINITY;
+        };
+        for (int i = tid; i < n4; i += kFilterThreads) {
+            float4 x = x4[i];
+            x.x = keep(x.x, 4 * i), x.y = keep(x.y, 4 * i + 1), x.z = keep(x.z, 4 * i + 2), x.w = keep(x.w, 4 * i + 3);
+            if (vec && 4 * i + 3 < n) {
+                *reinterpret_cast<float4 *>(out + 4 * i) = x;
+            } else {
+                out[4 * i] = x.x;
+                if (4 * i + 1 < n) out[4 * i + 1] = x.y;
+                if (4 * i + 2 < n) out[4 * i + 2] = x.z;
+                if (4 * i + 3 < n) out[4 * i + 3] = x.w;
+            }
+        }
+        if (a.n_kept) {
+            if (want_m && !listed) {
+                FilterSums s = {static_cast<double>(count), 0., 0ull, none};
+                kept = static_cast<int>(filter_reduce(sh, s, ctas, rank, turn++).a);
+            }
+            if (rank == 0 && tid == 0) a.n_kept[row] = kept;
+        }
+    } else {
+        // the race: w / noise, the two largest of a thread; 2^-14 apart they are decided. Of a list CTA 0 alone runs it.
+        const float *noise = a.noise + row * a.noise_stride;
+        const int racers = listed ? 1 : ctas;
+        if (!listed || rank == 0) {
+            auto runners = [&](auto f) {  // f(logit, token)
+                if (listed) {
+                    for (int i = tid; i < kept; i += kFilterThreads)
+                        f(filter_value(static_cast<uint32_t>(sh.list[i] >> 32)), static_cast<int>(~static_cast<uint32_t>(sh.list[i])));
+                } else if (kept == 1) {
+                    const int at = static_cast<int>(~static_cast<uint32_t>(cut)) - v0;
+                    if (tid == 0 && at >= 0 && at < n) f(x_s[at], v0 + at);
+                } else {
+                    each([&](float x, int i) {
+                        if ((cut == 0 || filter_key(x, v0 + i) >= cut) && strong(x)) f(x, v0 + i);
+                    });
+                }
+            };
+            auto score = [&](float x, int v) { return filter_weight(r, x) * __frcp_rn(noise[v]); };
+            float s1 = -1.f, s2 = -1.f;
+            int at = 0, count = 0;
+            runners([&](float x, int v) {
+                const float s = score(x, v);
+                ++count;
+                if (s > s1 || (s == s1 && v < at))
+                    s2 = s1, s1 = s, at = v;
+                else
+                    s2 = fmaxf(s2, s);
+            });
+            FilterSums s = {static_cast<double>(count), 0., s1 >= 0.f ? static_cast<unsigned long long>(__float_as_uint(s1)) << 32 | static_cast<uint32_t>(~at) : 0ull, none};
+            s = filter_reduce(sh, s, racers, rank, turn++);
+            kept = static_cast<int>(s.a);
+            unsigned long long won = s.hi ? s.hi : top;  // no noise above zero
+            const float best = __uint_as_float(static_cast<uint32_t>(s.hi >> 32)), near = best * (1.f - 0x1p-14f);
+            FilterSums t = {static_cast<double>((s1 >= near && s1 >= 0.f ? 1 : 0) + (s2 >= near && s2 >= 0.f ? 1 : 0)), 0., 0ull, none};
+            t = filter_reduce(sh, t, racers, rank, turn++);
+            if (t.a > 1.5) {  // near ones again, in 64 bits
+                double top_score = -1.;
+                int who = 0;
+                runners([&](float x, int v) {
+                    if (score(x, v) >= near) {
+                        const double w = x == r.m ? 1. : exp((static_cast<double>(x) - static_cast<double>(r.m)) / r.T);
+                        const double exact = w / static_cast<double>(noise[v]);
+                        if (exact > top_score || (exact == top_score && v < who)) top_score = exact, who = v;
+                    }
+                });
+                FilterSums u = {0., 0., top_score >= 0. ? static_cast<unsigned long long>(__double_as_longlong(top_score)) : 0ull, none};
+                const unsigned long long mine = u.hi;
+                u = filter_reduce(sh, u, racers, rank, turn++);
+                FilterSums f = {0., 0., 0ull, top_score >= 0. && mine == u.hi ? static_cast<unsigned long long>(who) : none};
+                f = filter_reduce(sh, f, racers, rank, turn++);
+                won = static_cast<uint32_t>(~static_cast<uint32_t>(f.lo));
+            }
+            if (rank == 0 && tid == 0) {
+                a.tokens[row] = static_cast<int>(~static_cast<uint32_t>(won));
+                if (a.n_kept) a.n_kept[row] = kept;
+            }
+        }
+    }
+    if (ctas > 1) cluster_sync();  // nobody leaves while its shared memory may be read
+}
+
+}  // namespace sdv

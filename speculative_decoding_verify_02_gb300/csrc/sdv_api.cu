@@ -13,6 +13,8 @@
 #include "attention.cuh"
 #include "attention_group.cuh"
 #include "common.cuh"
+#include "filter.cuh"
+#include "fork.cuh"
 #include "gemm.cuh"
 #include "small.cuh"
 
@@ -122,6 +124,7 @@ struct sdv_ctx {
     float2 *accept_part = nullptr;  // sampled acceptance: chunk statistics of the logit rows, best scores, arrivals
     unsigned long long *accept_keys = nullptr;
     int *accept_arrived = nullptr;
+    int4 *fork_copies = nullptr;  // partial pages that a fork copies
     int attn_splits = 1;
     int attn_group = kAttnGroup;  // key positions per attention group (1024, or 2048 for long sequences)
     int attn_lo = 1;  // attention products with hi/lo pairs (queries and probabilities)
@@ -314,7 +317,12 @@ size_t carve(const sdv_model_cfg &m, const sdv_cache_cfg &c, sdv_ctx *ctx, uint8
     auto *akeys = reinterpret_cast<unsigned long long *>(take(sizeof(unsigned long long) * 2 * B));
     int *aarrived = reinterpret_cast<int *>(take(sizeof(int) * B));
 
+    s.extra = reinterpret_cast<int *>(take(sizeof(int) * static_cast<size_t>(c.n_pages)));
+    s.n_extra = reinterpret_cast<int *>(take(sizeof(int)));
+    auto *copies = reinterpret_cast<int4 *>(take(sizeof(int4) * B));
+
     if (ctx) {
+        ctx->fork_copies = copies;
         ctx->accept_part = apart;
         ctx->accept_keys = akeys;
         ctx->accept_arrived = aarrived;
@@ -840,6 +848,8 @@ int sdv_create(const sdv_model_cfg *m, const sdv_cache_cfg *c, const sdv_weights
     if (e == cudaSuccess) e = set_smem(attn_kernel<64>, AttnShape<64>::SMEM);
     if (e == cudaSuccess) e = set_smem(attn_group_kernel<128>, GrpShape<128>::SMEM);
     if (e == cudaSuccess) e = set_smem(attn_group_kernel<64>, GrpShape<64>::SMEM);
+    if (e == cudaSuccess) e = set_smem(filter_kernel<false>, kFilterMost * static_cast<int>(sizeof(float)));
+    if (e == cudaSuccess) e = set_smem(filter_kernel<true>, kFilterMost * static_cast<int>(sizeof(float)));
     if (e != cudaSuccess) {
         delete ctx;
         return SDV_ERR_CUDA;
@@ -1061,6 +1071,88 @@ int sdv_accept_sampled(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_r
     if (e == cudaSuccess)
         e = launch(ctx, accept_draw_kernel, dim3(p.n_chunks, B), dim3(kAcceptThreads), 0, st, p);
     return rc(e);
+}
+
+int sdv_fork_seq(sdv_ctx *ctx, const int32_t *d_src, const int32_t *d_dst, int n, void *stream) {
+    if (!ctx || !d_src || !d_dst || n <= 0 || n > ctx->c.max_batch) return SDV_ERR_ARG;
+    if (ctx->swa_mask) return SDV_ERR_UNSUPPORTED;
+    ForkArgs p{};
+    p.s = ctx->st;
+    p.src = d_src;
+    p.dst = d_dst;
+    p.n = n;
+    p.copies = ctx->fork_copies;
+    p.pool = ctx->pool;
+    p.layer_stride = ctx->layer_stride;
+    p.n_layers = ctx->m.n_layers;
+    p.nkv = ctx->m.n_kv_heads;
+    p.D = ctx->m.head_dim;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch(ctx, fork_kernel, dim3(1), dim3(kForkThreads), 0, st, p);
+    if (e == cudaSuccess)
+        e = launch(ctx, fork_copy_kernel, dim3(n, p.n_layers + (ctx->ng_slots ? kForkIndexBlocks : 0)), dim3(kForkThreads), 0, st, p);
+    return rc(e);
+}
+
+}  // extern "C"
+
+namespace {
+// What sdv_filter_logits and sdv_sample share; `out` or `tokens` and `noise` are theirs.
+template <bool SAMPLE>
+int run_filter(sdv_ctx *ctx, FilterArgs a, int rows, int B, void *stream) {
+    const int V = ctx->m.vocab;
+    const int ctas = V <= kFilterAlone ? 1 : kFilterCluster;
+    a.status = ctx->st.status;
+    a.B = B;
+    a.vocab = V;
+    a.max_span = ctx->c.max_span;
+    a.rows_cap = static_cast<int>(std::min<long long>({rows, ctx->c.max_rows, static_cast<long long>(B) * ctx->c.max_span}));
+    a.chunk = ceil_div(ceil_div(V, ctas), 4) * 4;
+    if (a.chunk > kFilterMost) return SDV_ERR_UNSUPPORTED;
+    return rc(launch_cluster(ctx, filter_kernel<SAMPLE>, dim3(ctas, a.rows_cap), dim3(kFilterThreads), sizeof(float) * a.chunk,
+                             static_cast<cudaStream_t>(stream), ctas, a));
+}
+bool filter_args(const sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int rows, const int32_t *d_row_off, int B,
+                 const float *d_temperature, const int32_t *d_top_k, const float *d_top_p, const float *d_min_p, FilterArgs *a) {
+    if (!ctx || !d_logits || !d_row_off || !d_temperature || rows <= 0 || B <= 0 || B > ctx->c.max_batch ||
+        logits_stride < ctx->m.vocab)
+        return false;
+    a->logits = d_logits;
+    a->logits_stride = logits_stride;
+    a->row_off = d_row_off;
+    a->temperature = d_temperature;
+    a->top_k = d_top_k;
+    a->top_p = d_top_p;
+    a->min_p = d_min_p;
+    return true;
+}
+}  // namespace
+
+extern "C" {
+
+int sdv_filter_logits(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int rows, const int32_t *d_row_off, int B,
+                      const float *d_temperature, const int32_t *d_top_k, const float *d_top_p, const float *d_min_p, float *d_out,
+                      int64_t out_stride, int32_t *d_n_kept, void *stream) {
+    FilterArgs a{};
+    if (!filter_args(ctx, d_logits, logits_stride, rows, d_row_off, B, d_temperature, d_top_k, d_top_p, d_min_p, &a)) return SDV_ERR_ARG;
+    if (!d_out || out_stride < ctx->m.vocab) return SDV_ERR_ARG;
+    a.out = d_out;
+    a.out_stride = out_stride;
+    a.n_kept = d_n_kept;
+    return run_filter<false>(ctx, a, rows, B, stream);
+}
+
+int sdv_sample(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int rows, const int32_t *d_row_off, const float *d_noise,
+               int64_t noise_stride, int B, const float *d_temperature, const int32_t *d_top_k, const float *d_top_p,
+               const float *d_min_p, int32_t *d_tokens, int32_t *d_n_kept, void *stream) {
+    FilterArgs a{};
+    if (!filter_args(ctx, d_logits, logits_stride, rows, d_row_off, B, d_temperature, d_top_k, d_top_p, d_min_p, &a)) return SDV_ERR_ARG;
+    if (!d_noise || !d_tokens || noise_stride < ctx->m.vocab) return SDV_ERR_ARG;
+    a.noise = d_noise;
+    a.noise_stride = noise_stride;
+    a.tokens = d_tokens;
+    a.n_kept = d_n_kept;
+    return run_filter<true>(ctx, a, rows, B, stream);
 }
 
 int sdv_rewind_cache(sdv_ctx *ctx, const int32_t *d_length, int B, void *stream) {

@@ -31,6 +31,8 @@ struct DevState {
     int *cur_tok, *generated, *budget, *kcur;  // [max_batch]
     int *swa_keep;      // [max_batch] rows of the last forward's span kept by the last rewind (sliding window)
     int swa_window;     // > 0: the model has sliding-window layers
+    int *extra;         // [n_pages] holders of a page beyond the first (forked sequences)
+    int *n_extra;       // [1] sum of them
     int max_batch, pages_per_seq, page_size, n_pages_total, max_rows, max_span, work_cap;
     int ngram_cap, ng_slots, ng_orders;
 };
@@ -49,7 +51,10 @@ __device__ __forceinline__ uint32_t ng_hash(ulonglong2 key, int slots) {
 // ------------------------------------------------------------------ init / reset
 __global__ void init_state_kernel(DevState s) {
     const int tid = blockIdx.x * blockDim.x + threadIdx.x, nth = gridDim.x * blockDim.x;
-    for (int i = tid; i < s.n_pages_total; i += nth) s.free_stack[i] = s.n_pages_total - 1 - i;
+    for (int i = tid; i < s.n_pages_total; i += nth) {
+        s.free_stack[i] = s.n_pages_total - 1 - i;
+        s.extra[i] = 0;
+    }
     for (int i = tid; i < s.max_batch * s.pages_per_seq; i += nth) s.page_table[i] = -1;
     for (int i = tid; i < s.max_batch; i += nth) {
         s.seq_len[i] = 0;
@@ -67,6 +72,7 @@ __global__ void init_state_kernel(DevState s) {
         *s.status = 0;
         *s.nrows = 0;
         *s.n_work = 0;
+        *s.n_extra = 0;
     }
 }
 
@@ -269,12 +275,65 @@ __global__ void ensure_kernel(DevState s, const int *required, int B) {
     }
 }
 
+// Releases the last rel[b] pages of each sequence while pages are shared, in the order of a rewind: b = B-1 down to 0, highest
+// slot first. Of a page's holders that let go here, the last one frees it if nobody else holds it. Holders have a shared
+// page in the same slot: a thread takes a slot of all of them. `off` is scratch.
+__device__ __forceinline__ void release_shared(const DevState &s, const int *rel, int *off, int B, int top) {
+    __shared__ int let_go, lowest, highest;
+    if (threadIdx.x == 0) {
+        let_go = 0, lowest = s.pages_per_seq, highest = 0;
+        for (int b = 0; b < B; ++b)
+            if (rel[b] > 0) lowest = min(lowest, s.n_pages[b] - rel[b]), highest = max(highest, s.n_pages[b]);
+    }
+    for (int b = threadIdx.x; b < B; b += blockDim.x) off[b] = 0;
+    __syncthreads();
+    for (int j = lowest + static_cast<int>(threadIdx.x); j < highest; j += blockDim.x)
+        for (int b = B - 1; b >= 0; --b) {
+            const int n = s.n_pages[b];
+            if (j >= n || j < n - rel[b]) continue;
+            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + j;
+            const int page = *entry, others = s.extra[page];
+            if (others > 0) {
+                s.extra[page] = others - 1;
+                *entry = -1;
+                atomicAdd(&let_go, 1);
+            } else {
+                atomicAdd(&off[b], 1);
+            }
+        }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int total = 0;
+        for (int b = B - 1; b >= 0; --b) {
+            const int n = off[b];
+            off[b] = total;
+            total += n;
+        }
+        *s.free_top = top + total;
+        *s.n_extra -= let_go;
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {
+        const int n = s.n_pages[b];
+        int at = top + off[b];
+        for (int j = 0; j < rel[b]; ++j) {
+            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + n - 1 - j;
+            if (*entry < 0) continue;
+            s.free_stack[at++] = *entry;
+            *entry = -1;
+        }
+        s.n_pages[b] = n - rel[b];
+    }
+}
+
 __global__ void rewind_kernel(DevState s, const int *length, int B) {
     pdl_trigger();
     pdl_wait();
-    __shared__ int rel_s[256], off_s[256], ok_s, top_s;
+    __shared__ int rel_s[256], off_s[256], ok_s, top_s, shared_s;
     if (threadIdx.x == 0) {
         int ok = 1;
+        const int shared = *s.n_extra;
+        shared_s = shared;
         for (int b = 0; b < B; ++b) {
             const int len = length[b];
             rel_s[b] = 0;
@@ -289,6 +348,12 @@ __global__ void rewind_kernel(DevState s, const int *length, int B) {
                 continue;
             }
             const int keep = (len + s.page_size - 1) / s.page_size;
+            // rows that will be written from there on must not lie in a page that others hold, too
+            if (shared > 0 && len < s.seq_len[b] && len % s.page_size &&
+                s.extra[s.page_table[static_cast<size_t>(b) * s.pages_per_seq + keep - 1]] > 0) {
+                ok = 0;
+                continue;
+            }
             rel_s[b] = max(0, s.n_pages[b] - keep);
         }
         int total = 0;
@@ -299,21 +364,27 @@ __global__ void rewind_kernel(DevState s, const int *length, int B) {
         if (!ok) set_status(s.status, SDV_ERR_ARG);
         ok_s = ok;
         top_s = *s.free_top;
-        if (ok) *s.free_top = top_s + total;
+        if (ok && shared == 0) *s.free_top = top_s + total;
     }
     __syncthreads();
     if (!ok_s) return;
-    for (int b = threadIdx.x; b < B; b += blockDim.x) {
-        const int len = length[b];
-        if (len < 0) continue;
-        const int n = s.n_pages[b];
-        for (int j = 0; j < rel_s[b]; ++j) {
-            const int slot = n - 1 - j;
-            s.free_stack[top_s + off_s[b] + j] = s.page_table[b * s.pages_per_seq + slot];
-            s.page_table[b * s.pages_per_seq + slot] = -1;
+    if (shared_s > 0) {
+        release_shared(s, rel_s, off_s, B, top_s);
+        for (int b = threadIdx.x; b < B; b += blockDim.x)
+            if (length[b] >= 0) s.seq_len[b] = length[b];
+    } else {
+        for (int b = threadIdx.x; b < B; b += blockDim.x) {
+            const int len = length[b];
+            if (len < 0) continue;
+            const int n = s.n_pages[b];
+            for (int j = 0; j < rel_s[b]; ++j) {
+                const int slot = n - 1 - j;
+                s.free_stack[top_s + off_s[b] + j] = s.page_table[b * s.pages_per_seq + slot];
+                s.page_table[b * s.pages_per_seq + slot] = -1;
+            }
+            s.n_pages[b] = n - rel_s[b];
+            s.seq_len[b] = len;
         }
-        s.n_pages[b] = n - rel_s[b];
-        s.seq_len[b] = len;
     }
     // rows of the last forward kept (the rest are restored in the sliding-window rings)
     if (s.swa_window > 0)
@@ -352,14 +423,32 @@ __global__ void swa_restore_kernel(DevState s, bf16 *pool, size_t layer_stride, 
 
 __global__ void reset_seq_kernel(DevState s, int b) {
     pdl_wait();
-    if (threadIdx.x == 0) {
-        const int top = *s.free_top, n = s.n_pages[b];
-        for (int j = 0; j < n; ++j) {
-            const int slot = n - 1 - j;
-            s.free_stack[top + j] = s.page_table[b * s.pages_per_seq + slot];
-            s.page_table[b * s.pages_per_seq + slot] = -1;
+    __shared__ int let_go;
+    if (*s.n_extra > 0) {  // pages that others hold stay with them
+        if (threadIdx.x == 0) let_go = 0;
+        __syncthreads();
+        for (int j = threadIdx.x; j < s.n_pages[b]; j += blockDim.x) {
+            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + j;
+            const int page = *entry;
+            if (s.extra[page] > 0) {
+                s.extra[page] -= 1;
+                *entry = -1;
+                atomicAdd(&let_go, 1);
+            }
         }
-        *s.free_top = top + n;
+        __syncthreads();
+        if (threadIdx.x == 0) *s.n_extra -= let_go;
+    }
+    if (threadIdx.x == 0) {
+        const int n = s.n_pages[b];
+        int top = *s.free_top;
+        for (int j = 0; j < n; ++j) {
+            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + n - 1 - j;
+            if (*entry < 0) continue;
+            s.free_stack[top++] = *entry;
+            *entry = -1;
+        }
+        *s.free_top = top;
         s.n_pages[b] = 0;
         s.seq_len[b] = 0;
         s.hist_len[b] = 0;

@@ -91,6 +91,42 @@ class SpecLoop:
                 v.ngram_commit(allbuf, counts, B, stride)
         return first
 
+    def prefill_shared(self, prompt, chunk: int = 128, ngram: bool = False, temperature=None, noise=None, top_k=None,
+                       top_p=None, min_p=None):
+        """Forward one prompt as sequence 0 and let every other sequence continue it (fork_seq): the prompt is computed and
+        held once. With `noise` (float32 [B, vocab], exponential) each sequence's first token is drawn from the prompt's
+        last row at `temperature` (float32 [B]) within top_k, top_p and min_p, else it is the argmax. Returns the
+        first tokens (host numpy) and leaves them in self.first. The sequences must be empty."""
+        import torch
+        B, v = self.B, self.v
+        assert chunk <= v.ccfg.max_span and chunk <= v.ccfg.max_rows
+        if noise is not None and temperature is None:
+            raise ValueError("drawing the first tokens needs temperature and noise")
+        p = torch.from_numpy(np.asarray(prompt, dtype=np.int32)).cuda()
+        am = _i32(chunk)
+        logits = None
+        for c0 in range(0, len(p), chunk):
+            piece = p[c0:c0 + chunk].contiguous()
+            n = len(piece)
+            if noise is not None and c0 + n == len(p):
+                logits = torch.empty(n, v.mcfg.vocab, dtype=torch.float32, device="cuda")
+            v.ensure_capacity(torch.tensor([c0 + n], dtype=torch.int32, device="cuda"), 1)
+            v.spec_forward(piece, torch.tensor([0, n], dtype=torch.int32, device="cuda"), 1, n, n, am, logits)
+        if ngram:
+            v.ngram_commit(p, torch.tensor([len(p)], dtype=torch.int32, device="cuda"), 1, len(p))
+        if B > 1:
+            v.fork_seq(_i32(B - 1), torch.arange(1, B, dtype=torch.int32, device="cuda"), B - 1)
+        last = (len(p) - 1) % chunk
+        if noise is None:
+            self.first.copy_(am[last].expand(B))
+        else:
+            off = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+            v.sample(logits[last].expand(B, -1).contiguous(), off, noise, B, self.first, temperature, top_k=top_k, top_p=top_p,
+                     min_p=min_p)
+        if ngram:
+            v.ngram_commit(self.first, torch.ones(B, dtype=torch.int32, device="cuda"), B, 1)
+        return self.first.cpu().numpy()
+
     def start(self, budget, k_init: int, adaptive: bool = False, k_max: int = 7):
         import torch
         self.budget.copy_(torch.as_tensor(np.asarray(budget, dtype=np.int32)))
@@ -98,17 +134,20 @@ class SpecLoop:
 
     # ------------------------------------------------------------------ one step
     def step(self, drafter=SDV_DRAFT_NGRAM, table=None, table_stride=0, logits=None, ngram=True, temperature=None,
-             seed: int = 0, uniforms=None, noise=None, draft_probs=None):
+             seed: int = 0, uniforms=None, noise=None, draft_probs=None, top_k=None, top_p=None, min_p=None):
         """One transaction: propose, reserve, verify (greedy, or sampled at `temperature`, a float32
         device tensor [B]), accept, rewind, and commit to the n-gram index. With `uniforms` (float32
         [max_rows] in [0, 1)) and `noise` (float32 [B, vocab], exponential) the drafts are accepted
         against the target's probabilities at `temperature` instead of matched by token;
         `draft_probs` [max_rows, vocab] is the drafter's distribution (None: certain drafts). All
-        three are read on the device, so a captured step takes what they hold when it is replayed.
+        three are read on the device, so a captured step takes what they hold when it is replayed. top_k (int32 [B]),
+        top_p and min_p (float32 [B]) cut the target's distribution first (filter_logits); `draft_probs` is then best that
+        of a drafter with the same cuts.
         They are the step's random numbers: `seed` is that of the token-matching step alone."""
         v, B = self.v, self.B
-        if uniforms is None and (noise is not None or draft_probs is not None):
-            raise ValueError("noise and draft_probs belong to the acceptance against probabilities, which needs uniforms")
+        cuts = top_k is not None or top_p is not None or min_p is not None
+        if uniforms is None and (noise is not None or draft_probs is not None or cuts):
+            raise ValueError("noise, draft_probs and the cuts belong to the acceptance against probabilities, which needs uniforms")
         if uniforms is not None:
             if temperature is None or noise is None:
                 raise ValueError("acceptance against probabilities needs temperature, uniforms and noise")
@@ -125,6 +164,8 @@ class SpecLoop:
             v.spec_forward_sampled(self.tokens, self.row_off, B, self.max_rows, self.max_span, temperature, seed,
                                    self.argmax, logits)
         if uniforms is not None:
+            if cuts:
+                v.filter_logits(logits, self.row_off, B, logits, None, temperature, top_k=top_k, top_p=top_p, min_p=min_p)
             v.accept_sampled(self.tokens, self.row_off, logits, temperature, uniforms, noise, B, self.max_span,
                              self.n_accept, self.committed, self.n_commit, self.new_len, draft_probs=draft_probs)
         else:
