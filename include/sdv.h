@@ -264,7 +264,7 @@ int sdv_fork_seq(sdv_ctx *ctx, const int32_t *d_src, const int32_t *d_dst, int n
  *   d_out     fp32 rows, out_stride floats apart: the kept logits as they are, -inf elsewhere. d_logits itself will do.
  *   d_n_kept  [rows] int32, or NULL: tokens kept.
  * A row without a logit above -inf keeps none (SDV_ERR_DEVICE). The rows made here can go to sdv_accept_sampled, which then
- * verifies drafts against the filtered distribution. A vocabulary above 425,984 is SDV_ERR_UNSUPPORTED. */
+ * verifies drafts against the filtered distribution. A vocabulary above 393,216 is SDV_ERR_UNSUPPORTED. */
 int sdv_filter_logits(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int rows, const int32_t *d_row_off, int B,
                       const float *d_temperature, const int32_t *d_top_k, const float *d_top_p, const float *d_min_p, float *d_out,
                       int64_t out_stride, int32_t *d_n_kept, void *stream);

@@ -33,10 +33,12 @@ from .spec import accept_greedy, ngram_propose, adapt_k, ngram_propose_multi, re
 from .loop import generate, StepRecord
 from .sampling import draw_rows, perturbed, gumbel, uniforms
 from .quant import QuantPool, accept_sampled, code_values, e4m3, needed_scale
+from .continuations import SharedPool, attend, draw_kept, kept_tokens, scores
 
 __all__ = [
     "DenseDecoder", "SeqCache", "round_bf16", "rmsnorm", "silu", "rope_neox", "attention_rows", "argmax_lowest",
     "PagePool", "CapacityError", "accept_greedy", "ngram_propose", "adapt_k", "generate", "StepRecord",
     "draw_rows", "perturbed", "gumbel", "uniforms", "ngram_propose_multi", "required_order", "NgramIndex",
     "QuantPool", "accept_sampled", "code_values", "e4m3", "needed_scale",
+    "SharedPool", "attend", "draw_kept", "kept_tokens", "scores",
 ]

@@ -2,15 +2,19 @@
 //
 // Tokens are ordered by logit, equal ones by index: a 64-bit key each, and a kept set is the keys at or above one of them.
 // With w = 2^-((m - x) log2(e) / T), m the row's largest logit, top-p keeps token i iff the weights before it sum to less than
-// p of the top-k set's. The row stays in the shared memory of a cluster of CTAs, and a histogram over (m - x) / T shows in
-// which bin the border lies. Where no more than kFilterList tokens lie down to it, as in most rows of a language model, they
-// go to one CTA, which sorts them and cuts and draws by itself; where more do, sums over the bin's edges confirm the bin, and
-// its tokens alone are compared with one another.
+// p of the top-k set's. The row stays in the shared memory of a cluster of CTAs. Each thread's largest logit is known from the
+// search for the row's: k of those, or as many as weigh p of the total, are a bound that the border does not pass. Where no
+// more than kFilterList tokens lie above it, as in most rows of a language model, they go to one CTA, which sorts them and cuts
+// and draws by itself. Where more do, a histogram of all tokens over (m - x) / T shows the border's bin, sums over the bin's
+// edges confirm it, and its tokens alone are compared with one another.
 //
-// Whether a token is kept is decided as exact arithmetic would: sums are fp32 weights in 64 bits and hold to 2^-17 of the
-// total each (kFilterNear); a border nearer than that is decided on weights of 2^-39 (weight_exact), summed as integers, whose
-// order does not matter.
+// Whether a token is kept is decided as exact arithmetic would: sums of fp32 weights hold to 2^-17 of the total each
+// (kFilterNear); a border nearer than that is decided on weights of 2^-39 (weight_exact). Sums are integers, units of 2^-44,
+// whose order does not matter; 64-bit floats stay out of the way of most rows: this part does them at 1/64 of fp32's rate, and
+// the first kernel, which used them for sums and settings, took 75,000 clocks a row where it is 30,000 now.
 #pragma once
+
+#include <float.h>
 
 #include "accept_sampled.cuh"
 
@@ -21,13 +25,32 @@ constexpr int kFilterBins = 1024;
 constexpr int kFilterFew = 256;                  // tokens that are compared with one another
 constexpr float kFilterRange = 40.f;             // log2 of the weights that the histogram's bins cover
 constexpr int kFilterCluster = 8;                // CTAs of a row
-constexpr int kFilterAlone = 8192;               // tokens of a row that one CTA takes
-constexpr int kFilterList = 2048;                // tokens that one CTA sorts
+constexpr int kFilterList = 2048;                // tokens that one CTA sorts; a row of no more is one CTA's
 constexpr int kFilterMost = 49152;               // tokens of a CTA at most (192 KB)
 // How far a sum of fp32 weights and p times another may lie from each other's exact values, over the total: an exponent
 // t = (m - x) log2(e) / T takes three roundings, 2.1 t 2^-24 after ln 2, and t averages log2 of the vocabulary at most over the
 // weights (19: 40 2^-24); ex2 is off by 4 2^-24, a thread's sum of up to 96 terms by 96 2^-24. 140 2^-24 each, 2^-15.9 both.
-constexpr double kFilterNear = 0x1p-15;
+constexpr int kFilterNear = 15;  // 2^-15
+
+// 2^(58 - j / 64)
+__constant__ unsigned long long kFilterTable[64] = {
+    0x400000000000000ull, 0x3f4f83033d21b06ull, 0x3ea0ecb6dc8a80dull, 0x3df437dcc2b44efull,
+    0x3d495f454921b31ull, 0x3ca05dcf167fec5ull, 0x3bf92e66f736bd7ull, 0x3b53cc07b6650aeull,
+    0x3ab031b9f7490e5ull, 0x3a0e5a940f12f72ull, 0x396e41b9df20d23ull, 0x38cfe25cafa2969ull,
+    0x383337bb0aa5384ull, 0x37983d209783a45ull, 0x36feede5f6bc8ddull, 0x366745709e2bf5full,
+    0x35d13f32b5a75acull, 0x353cd6aaf3fb7e8ull, 0x34aa07647c4ab91ull, 0x3418ccf6bbcac96ull,
+    0x3389230547e1204ull, 0x32fb053fbc9c9f1ull, 0x326e6f619b8bc9full, 0x31e35d322aee6c5ull,
+    0x3159ca845541b6bull, 0x30d1b3368925d90ull, 0x304b1332999c251ull, 0x2fc5e66d9e9cc42ull,
+    0x2f4228e7d6030dbull, 0x2ebfd6ac84cf918ull, 0x2e3eebd1d8bee7cull, 0x2dbf6478ca345deull,
+    0x2d413cccfe77992ull, 0x2cc47104aa44492ull, 0x2c48fd6074ab096ull, 0x2bcede2b5a4290eull,
+    0x2b560fba90a852bull, 0x2ade8e6d6a4fb4dull, 0x2a6856ad3a9f03cull, 0x29f364ed3a594d6ull,
+    0x297fb5aa6c544e4ull, 0x290d456b8279a02ull, 0x289c10c0c3125a0ull, 0x282c1443ee5c53full,
+    0x27bd4c982468447ull, 0x274fb669cb3feddull, 0x26e34e6e7553955ull, 0x26781164c82dfeaull,
+    0x260dfc14636e2a6ull, 0x25a50b4dc806168ull, 0x253d3bea3fbdc26ull, 0x24d68acbc4f9ba5ull,
+    0x2470f4dceac470dull, 0x240c7710c519ac7ull, 0x23a90e62d17354full, 0x2346b7d6df96ea8ull,
+    0x22e57078faa2f5cull, 0x2285355d525bbf6ull, 0x222603a024b6a15ull, 0x21c7d865a7a3440ull,
+    0x216ab0d9f3121ecull, 0x210e8a30eb37901ull, 0x20b361a62b0ae87ull, 0x2059347cef00c1eull,
+};
 
 struct FilterArgs {
     int *status;
@@ -65,6 +88,11 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld_dsmem_u16(uint32_t addr) {
+    unsigned short v;
+    asm volatile("ld.shared::cluster.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ void st_dsmem_u64(uint32_t addr, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
@@ -78,18 +106,18 @@ __device__ __forceinline__ uint32_t add_dsmem_u32(uint32_t addr, uint32_t v) {
 }
 
 struct FilterSums {
-    double a, b;                          // summed
+    unsigned long long a, b;              // summed
     unsigned long long hi, lo;            // the largest, the smallest
 };
 struct FilterShared {
     uint32_t hist[kFilterBins], total[kFilterBins];  // of this CTA, of the row
     FilterSums warp[kFilterThreads / 32], part[2][kFilterCluster];
     unsigned long long list[kFilterList];            // CTA 0's: keys, or the border's tokens' keys and then their weights
+    uint16_t pick[kFilterList];                      // tokens of this CTA for the list, places in its chunk
     unsigned long long cut, scan_e[kFilterThreads / 32];
-    double mass;
-    uint32_t table_hi[64], table_lo[64];  // 2^(-j / 64) as the integer 2^58 times it
-    uint32_t n_cand, scan[kFilterThreads / 32], ambiguous, kept;
-    float scan_w[kFilterThreads / 32], about;
+    unsigned long long mass;
+    uint32_t n_cand, n_pick, scan[kFilterThreads / 32], ambiguous, kept;
+    float scan_w[kFilterThreads / 32], about, about_all;
     int found[3], seq, fails;
 };
 
@@ -99,8 +127,7 @@ __device__ __forceinline__ unsigned long long filter_key(float x, int v) {  // -
 
 // A row's constants.
 struct FilterRow {
-    float m, c_hi, c_lo, scale;  // the maximum, log2(e) / T in two parts, bins a logit
-    double T;
+    float m, c_hi, c_lo, scale, T;  // the maximum, log2(e) / T in two parts, bins a logit
 };
 __device__ __forceinline__ float filter_weight(const FilterRow &r, float x) {
     if (x == r.m) return 1.f;
@@ -109,7 +136,7 @@ __device__ __forceinline__ float filter_weight(const FilterRow &r, float x) {
 }
 // The weight as an integer times 2^-58, to 2^-39: the exponent in two fp32 parts, 2^-n/64 from a table and the rest, below
 // 2^-7, by the series of e^z in two parts.
-__device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, const FilterShared &sh, float x) {
+__device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, float x) {
     if (x == r.m) return 1ull << 58;
     const float s = r.m - x, bb = s - r.m, e = (r.m - (s - bb)) - (x + bb);  // s + e = m - x
     const float p = s * r.c_hi;
@@ -120,48 +147,55 @@ __device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, c
     constexpr float L = -0.693147182f, L_lo = 1.90465421e-9f;                // L + L_lo = -ln 2
     const float u = f * L, u_lo = fmaf(f, L, -u) + (f * L_lo + q * L);       // z = u + u_lo
     const float g = u_lo + u * u * (0.5f + u * (0.16666667f + u * 0.041666668f));  // e^z - 1 = u + g
-    const unsigned long long t58 = static_cast<unsigned long long>(sh.table_hi[n & 63]) << 32 | sh.table_lo[n & 63];
-    const float tf = __ull2float_rn(t58) * 0x1p-58f;
-    const float tl = static_cast<float>(static_cast<long long>(t58 - static_cast<unsigned long long>(static_cast<double>(tf) * 0x1p58))) * 0x1p-58f;
+    const unsigned long long t58 = kFilterTable[n & 63];
+    const float t_hi = __ull2float_rn(t58), tf = t_hi * 0x1p-58f;
+    const float tl = __ll2float_rn(static_cast<long long>(t58) - __float2ll_rn(t_hi)) * 0x1p-58f;
     const float a = tf * u, b = fmaf(tf, u, -a) + (tf * g + tl * u);         // t (e^z - 1)
     const long long w = static_cast<long long>(t58) + __float2ll_rn(a * 0x1p58f) + __float2ll_rn(b * 0x1p58f);
     return static_cast<unsigned long long>(w) >> (n >> 6);
 }
 
+// Which of the four a reduction takes along.
+constexpr int kSumA = 1, kSumB = 2, kHi = 4, kLo = 8;
+template <int F>
 __device__ __forceinline__ void filter_join(FilterSums &s, const FilterSums &o) {
-    s.a += o.a;
-    s.b += o.b;
-    s.hi = o.hi > s.hi ? o.hi : s.hi;
-    s.lo = o.lo < s.lo ? o.lo : s.lo;
+    if constexpr (F & kSumA) s.a += o.a;
+    if constexpr (F & kSumB) s.b += o.b;
+    if constexpr (F & kHi) s.hi = o.hi > s.hi ? o.hi : s.hi;
+    if constexpr (F & kLo) s.lo = o.lo < s.lo ? o.lo : s.lo;
 }
-// Over the row, in an order that does not change: by every thread of every CTA, who all get the result.
-__device__ FilterSums filter_reduce(FilterShared &sh, FilterSums s, int ctas, int rank, int turn) {
+// Over the row, by every thread of every CTA, who all get the result. `shift`: the sums lose that many bits once a warp's
+// are added up, which keeps theirs from overflowing.
+template <int F>
+__device__ __forceinline__ FilterSums filter_reduce(FilterShared &sh, FilterSums s, int ctas, int rank, int turn, int shift = 0) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     constexpr int W = kFilterThreads / 32;
     auto across = [&](int from) {
 #pragma unroll
         for (int o = from; o > 0; o >>= 1) {
-            FilterSums t;
-            t.a = __shfl_xor_sync(0xffffffffu, s.a, o);
-            t.b = __shfl_xor_sync(0xffffffffu, s.b, o);
-            t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
-            t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-            filter_join(s, t);
+            FilterSums t{};
+            if constexpr (F & kSumA) t.a = __shfl_xor_sync(0xffffffffu, s.a, o);
+            if constexpr (F & kSumB) t.b = __shfl_xor_sync(0xffffffffu, s.b, o);
+            if constexpr (F & kHi) t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+            if constexpr (F & kLo) t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+            filter_join<F>(s, t);
         }
     };
     across(16);
+    s.a >>= shift;
+    s.b >>= shift;
     if (lane == 0) sh.warp[warp] = s;
     __syncthreads();
     FilterSums (&part)[kFilterCluster] = sh.part[turn & 1];
-    if (warp == 0) {  // this CTA's sums to every CTA
+    if (warp == 0) {  // this CTA's to every CTA
         s = sh.warp[lane % W];
         across(W / 2);
         if (lane < ctas) {
             const uint32_t to = mapa_shared(smem_u32(&part[rank]), lane);
-            st_dsmem_u64(to, __double_as_longlong(s.a));
-            st_dsmem_u64(to + 8, __double_as_longlong(s.b));
-            st_dsmem_u64(to + 16, s.hi);
-            st_dsmem_u64(to + 24, s.lo);
+            if constexpr (F & kSumA) st_dsmem_u64(to, s.a);
+            if constexpr (F & kSumB) st_dsmem_u64(to + 8, s.b);
+            if constexpr (F & kHi) st_dsmem_u64(to + 16, s.hi);
+            if constexpr (F & kLo) st_dsmem_u64(to + 24, s.lo);
         }
     }
     if (ctas > 1)
@@ -169,7 +203,7 @@ __device__ FilterSums filter_reduce(FilterShared &sh, FilterSums s, int ctas, in
     else
         __syncthreads();
     s = part[0];
-    for (int r = 1; r < ctas; ++r) filter_join(s, part[r]);
+    for (int r = 1; r < ctas; ++r) filter_join<F>(s, part[r]);
     return s;
 }
 __device__ __forceinline__ void filter_sync(int ctas) {
@@ -183,10 +217,21 @@ __device__ __forceinline__ void filter_sync(int ctas) {
 struct FilterGoal {
     bool by_mass;
     int k;
-    double target, p, total;  // target = p total
-    double off;               // the histogram's total less the exact one
-    unsigned long long set;   // the mass's tokens: keys at or above it
+    float p;
+    unsigned long long target, total;  // target = p total, rounded up: a sum is below it iff it is below p total
+    float off;                         // what the histogram takes the total for less what it is
+    unsigned long long set;            // the mass's tokens: keys at or above it
 };
+constexpr float kFilterUnit = 0x1p-44f;
+// p v for 0 < p < 1, rounded up
+__device__ __forceinline__ unsigned long long filter_share(float p, unsigned long long v) {
+    const uint32_t u = __float_as_uint(p), e = u >> 23;
+    const unsigned long long m = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const int s = 150 - static_cast<int>(e ? e : 1);  // p = m 2^-s, 24 <= s
+    const unsigned long long hi = __umul64hi(v, m), lo = v * m;
+    if (s >= 64) return s - 64 >= 64 ? (hi | lo) != 0 : (hi >> (s - 64)) + (((hi & ((1ull << (s - 64)) - 1)) | lo) != 0);
+    return (hi << (64 - s) | lo >> s) + ((lo & ((1ull << s) - 1)) != 0);
+}
 
 __device__ __forceinline__ float filter_value(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
@@ -198,7 +243,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
     __shared__ FilterShared sh;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
     const int v0 = rank * a.chunk, n = max(0, min(a.chunk, a.vocab - v0)), n4 = (n + 3) / 4;
-    if (tid == 0) sh.seq = -1, sh.n_cand = 0;
+    if (tid == 0) sh.seq = -1, sh.n_cand = sh.n_pick = 0;
     pdl_wait();
     pdl_trigger();
     // the row's logits are asked for before its sequence is known; four at a time in every pass, -inf behind the last
@@ -241,8 +286,8 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
     FilterRow r;
     int valid;
     unsigned long long top;  // the first token
+    float m = -INFINITY;     // this thread's largest
     {
-        float m = -INFINITY;
         int count = 0, first = 0;
         for (int i = tid; i < n4; i += kFilterThreads) {
             float4 x = x4[i];
@@ -260,8 +305,8 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 first = v0 + 4 * i + (x.x == m ? 0 : x.y == m ? 1 : x.z == m ? 2 : 3);
             }
         }
-        FilterSums s = {static_cast<double>(count), 0., count ? filter_key(m, first) : 0ull, none};
-        s = filter_reduce(sh, s, ctas, rank, turn++);
+        FilterSums s = {static_cast<unsigned long long>(count), 0, count ? filter_key(m, first) : 0ull, none};
+        s = filter_reduce<kSumA | kHi>(sh, s, ctas, rank, turn++);
         valid = static_cast<int>(s.a);
         top = s.hi;
         r.m = filter_value(static_cast<uint32_t>(s.hi >> 32));
@@ -281,25 +326,32 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
         return;
     }
     r.T = T;
-    const double c = 1.4426950408889634 / static_cast<double>(T);
-    r.c_hi = static_cast<float>(c);
-    r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
+    {  // the quotient and its remainder's
+        constexpr float L = 1.44269502f, L_lo = 1.92596303e-8f;  // L + L_lo = log2(e)
+        r.c_hi = L / T;
+        r.c_lo = (fmaf(-r.c_hi, T, L) + L_lo) / T;
+    }
     r.scale = r.c_hi * (kFilterBins / kFilterRange);
-    if (!(T > 0.f) || min_p > 1.f || top_p <= 0.f) cut = top, kept = 1;  // the first token alone
+    if (!(T > 0.f) || min_p > 1.f || top_p <= 0.f || valid == 1) cut = top, kept = 1;  // the first token alone
     const bool want_k = kept > 1 && top_k > 0 && top_k < valid, want_p = kept > 1 && top_p > 0.f && top_p < 1.f;
     const bool want_m = kept > 1 && min_p > 0.f;
-    const double least = want_m ? static_cast<double>(r.m) + r.T * log(static_cast<double>(min_p)) : -INFINITY;
-    auto strong = [&](float x) { return !want_m || x == r.m || static_cast<double>(x) >= least; };
-    auto bin_of = [&](float x) { return min(kFilterBins - 1, static_cast<int>((r.m - x) * r.scale)); };
+    // w >= min_p: exponents are compared, (m - x) log2(e) / T with -log2(min_p), and in 64 bits where fp32 could not tell
+    const float weakest = want_m ? -log2f(min_p) : INFINITY;
+    auto strong = [&](float x) {
+        if (!want_m || x == r.m) return true;
+        const float t = (r.m - x) * r.c_hi, near = (fabsf(t) + weakest + 1.f) * 0x1p-20f;
+        if (!(fabsf(t - weakest) <= near)) return t < weakest;
+        return static_cast<double>(x) - static_cast<double>(r.m) >= static_cast<double>(T) * log(static_cast<double>(min_p));
+    };
+    auto place_of = [&](float x) { return x == r.m ? 0.f : (r.m - x) * r.scale; };  // on the line of bins
+    auto bin_of = [&](float x) {
+        const float t = place_of(x);
+        return t < kFilterBins - 1 ? static_cast<int>(t) : kFilterBins - 1;
+    };
     auto middle_weight = [](int i) { return filter_ex2(-(i + .5f) * (kFilterRange / kFilterBins)); };
     bool precise = false, listed = false;  // listed: the kept tokens are CTA 0's first ones, in order
 
     if (want_k || want_p) {
-        if (tid < 64) {  // for weight_exact
-            const unsigned long long t = static_cast<unsigned long long>(exp2(-tid / 64.) * 0x1p58);
-            sh.table_hi[tid] = static_cast<uint32_t>(t >> 32);
-            sh.table_lo[tid] = static_cast<uint32_t>(t);
-        }
         // this CTA's histogram -> the row's, in every CTA
         auto add_up = [&]() {
             filter_sync(ctas);
@@ -316,8 +368,9 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             filter_sync(ctas);
         };
         // The first bin in [first, last] at which the tokens so far reach `k`, or about `mass` of weight (bin i's tokens weigh
-        // about weight(i) each), else the last: found[0]; tokens before it: found[1], in it: found[2], weight before it: about.
-        auto find_bin = [&](bool by_mass, int k, double mass, int first, int last, auto weight) {
+        // about weight(i) each; mass < 0: all but -mass), else the last: found[0]; tokens before it: found[1], in it: found[2],
+        // weight before it: about, of all: about_all.
+        auto find_bin = [&](bool by_mass, int k, float mass, int first, int last, auto weight) {
             const uint32_t n0 = sh.total[2 * tid], n1 = sh.total[2 * tid + 1];
             __syncthreads();
             if (tid == 0) sh.found[0] = last;
@@ -332,9 +385,15 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             }
             if (lane == 31) sh.scan[warp] = count, sh.scan_w[warp] = w;
             __syncthreads();
-            for (int i = 0; i < warp; ++i) count += sh.scan[i], w += sh.scan_w[i];
+            float w_all = 0.f;
+#pragma unroll
+            for (int i = 0; i < kFilterThreads / 32; ++i) {
+                w_all += sh.scan_w[i];
+                if (i < warp) count += sh.scan[i], w += sh.scan_w[i];
+            }
+            if (mass < 0.f) mass += w_all;
             const uint32_t c0 = count - n1;
-            auto reaches = [&](uint32_t cnt, float ms) { return by_mass ? ms >= static_cast<float>(mass) : cnt >= static_cast<uint32_t>(k); };
+            auto reaches = [&](uint32_t cnt, float ms) { return by_mass ? ms >= mass : cnt >= static_cast<uint32_t>(k); };
             const int here = reaches(c0, w - w1) ? 2 * tid : reaches(count, w) ? 2 * tid + 1 : kFilterBins;
             if (here < kFilterBins) atomicMin(&sh.found[0], max(here, first));
             __syncthreads();
@@ -342,20 +401,20 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             if (j / 2 == tid) {
                 sh.found[1] = static_cast<int>(j & 1 ? c0 : c0 - n0);
                 sh.found[2] = static_cast<int>(j & 1 ? n1 : n0);
-                sh.about = w - w1 - (j & 1 ? 0.f : w0);
+                sh.about = w - w1 - (j & 1 ? 0.f : w0), sh.about_all = w_all;
             }
             __syncthreads();
         };
         // Weight of the tokens for which in0 and in1 hold, and the keys for which in1 holds but not in0: smallest and largest.
         auto sums = [&](auto in0, auto in1) {
-            FilterSums s = {0., 0., 0ull, none};
+            FilterSums s = {0, 0, 0ull, none};
             float f0 = 0.f, f1 = 0.f;
             unsigned long long e0 = 0, e1 = 0;
             each([&](float x, int i) {
                 if (!in1(x, i)) return;
                 const bool both = in0(x, i);
                 if (precise) {
-                    const unsigned long long w = weight_exact(r, sh, x) >> 7;  // a thread adds up to 96
+                    const unsigned long long w = weight_exact(r, x) >> 7;  // a thread adds up to 96
                     e1 += w;
                     if (both) e0 += w;
                 } else {
@@ -369,31 +428,35 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     s.lo = k < s.lo ? k : s.lo;
                 }
             });
-            s.a = precise ? static_cast<double>(e0) * 0x1p-51 : static_cast<double>(f0);
-            s.b = precise ? static_cast<double>(e1) * 0x1p-51 : static_cast<double>(f1);
-            return filter_reduce(sh, s, ctas, rank, turn++);
+            s.a = precise ? e0 : __float2ull_rn(f0 * 0x1p51f);
+            s.b = precise ? e1 : __float2ull_rn(f1 * 0x1p51f);
+            return filter_reduce<kSumA | kSumB | kHi | kLo>(sh, s, ctas, rank, turn++, 7);
         };
         auto set_total = [&](FilterGoal &g) {
             g.total = sums([&](float, int) { return true; }, [&](float x, int i) { return filter_key(x, v0 + i) >= g.set; }).a;
-            g.target = g.p * g.total;
+            g.target = filter_share(g.p, g.total);
+        };
+        auto close = [&](unsigned long long sum, const FilterGoal &g) {
+            return (sum > g.target ? sum - g.target : g.target - sum) <= g.total >> kFilterNear;
         };
         // The key of the goal's last token; kept: tokens down to it.
         auto search = [&](FilterGoal g, int &kept_out) -> unsigned long long {
             // ---- a bin of the histogram over (m - x) / T: by weight a guess, confirmed by the sums over its edges or made
             // again from how far the sum before it is from the guess's
             int first = 0, last = kFilterBins - 1, above, count;
-            double A = 0., guess = g.target + g.off;
+            unsigned long long A = 0;
+            float guess = g.target * kFilterUnit + g.off;
             unsigned long long hi = 0, lo = none;
             for (int tries = 0;; ++tries) {
                 const int half = (first + last) / 2;  // guesses that do not settle
                 find_bin(g.by_mass, g.k, guess, tries < 4 ? first : half, tries < 4 ? last : half, middle_weight);
                 const int j = sh.found[0];
                 above = sh.found[1], count = sh.found[2];
-                const double about = sh.about;
+                const float about = sh.about;
                 for (;;) {
                     const FilterSums s = sums([&](float x, int) { return bin_of(x) < j; }, [&](float x, int) { return bin_of(x) <= j; });
                     A = s.a, hi = s.hi, lo = s.lo;
-                    if (g.by_mass && !precise && (fabs(A - g.target) <= kFilterNear * g.total || fabs(s.b - g.target) <= kFilterNear * g.total)) {
+                    if (g.by_mass && !precise && (close(A, g) || close(s.b, g))) {
                         precise = true;
                         set_total(g);
                         continue;
@@ -407,7 +470,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     break;
                 }
                 if (first > last) break;
-                guess = g.target - (A - about);
+                guess = fmaxf(0.f, static_cast<float>(static_cast<long long>(g.target - A)) * kFilterUnit + about);
             }
             // ---- while there are many tokens, a bin of the histogram over their keys' logits
             while (count > kFilterFew) {
@@ -423,7 +486,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     if (k <= k_hi && k >= k_lo) atomicAdd(&sh.hist[(k_hi - k) >> shift], 1u);
                 });
                 add_up();
-                find_bin(g.by_mass, g.k - above, g.target - A, 0, kFilterBins - 1,
+                find_bin(g.by_mass, g.k - above, static_cast<float>(static_cast<long long>(g.target - A)) * kFilterUnit, 0, kFilterBins - 1,
                          [&](int i) { return filter_weight(r, filter_value(k_hi - (static_cast<uint32_t>(i) << shift))); });
                 const int bin = sh.found[0], before = sh.found[1], inside = sh.found[2];
                 const uint32_t h = k_hi - (static_cast<uint32_t>(bin) << shift), width = 1u << shift;
@@ -431,8 +494,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 FilterSums s;
                 for (;;) {
                     s = sums([&](float x, int) { return orderable(x + 0.f) > h; }, [&](float x, int) { return orderable(x + 0.f) >= l; });
-                    const double near = kFilterNear * g.total;
-                    if (g.by_mass && !precise && (fabs(s.a - g.target) <= near || fabs(s.b - g.target) <= near)) {
+                    if (g.by_mass && !precise && (close(s.a, g) || close(s.b, g))) {
                         precise = true;
                         set_total(g);
                         continue;
@@ -465,8 +527,10 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                         set_total(g);
                         A = sums([&](float y, int) { return orderable(y + 0.f) > k; }, [&](float y, int) { return orderable(y + 0.f) > k; }).a;
                     }
-                    const double w = static_cast<double>(weight_exact(r, sh, x)) * 0x1p-58, need = ceil((g.target - A) / w);
-                    if (w > 0. && need < want) want = max(1, static_cast<int>(need));
+                    // the first of them with weight enough before it: 2^-58 is 2^-14 of the sums' unit
+                    const unsigned long long w = weight_exact(r, x), lack = g.target > A ? g.target - A : 0;
+                    const double need = ceil(static_cast<double>(lack) * 0x1p14 / static_cast<double>(w));
+                    if (w > 0 && need < want) want = max(1, static_cast<int>(need));
                 }
                 // tokens in order: CTAs, then threads, a run of the chunk each
                 const int run = (n + kFilterThreads - 1) / kFilterThreads, i0 = min(n, tid * run), i1 = min(n, i0 + run);
@@ -510,7 +574,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     const uint32_t at = add_dsmem_u32(counter, 1);
                     if (at < kFilterFew) {
                         st_dsmem_u64(mapa_shared(smem_u32(&sh.list[at]), 0), k);
-                        st_dsmem_u64(mapa_shared(smem_u32(&sh.list[kFilterFew + at]), 0), g.by_mass ? weight_exact(r, sh, x) >> 8 : 0ull);
+                        st_dsmem_u64(mapa_shared(smem_u32(&sh.list[kFilterFew + at]), 0), g.by_mass ? weight_exact(r, x) >> 8 : 0ull);
                     }
                 }
             });
@@ -531,8 +595,8 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                         }
                         bool keep = place < g.k;
                         if (g.by_mass) {
-                            const double mass = A + static_cast<double>(before) * 0x1p-50;
-                            if (!precise && fabs(mass - g.target) <= kFilterNear * g.total) sh.ambiguous = 1;
+                            const unsigned long long mass = A + (before >> 6);
+                            if (!precise && close(mass, g)) sh.ambiguous = 1;
                             keep = keep && mass < g.target;
                         }
                         if (keep || place == 0) atomicMax(&sh.kept, static_cast<uint32_t>(place + 1));
@@ -567,19 +631,17 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             }
         };
 
-        // ---- the histogram, the total, and what it is with each token in the middle of its bin; the last bin's tokens are
-        // those that the others leave
+        // all tokens' histogram and the total; the last bin's tokens are those that the others leave
         auto count_bins = [&]() {
-            float f = 0.f, middle = 0.f;
+            float f = 0.f;
+            __syncthreads();
+            for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = 0;
+            __syncthreads();
             each([&](float x, int) {
-                const int bin = bin_of(x);
-                if (bin < kFilterBins - 1) atomicAdd(&sh.hist[bin], 1u);
-                f += filter_weight(r, x);
-                middle += middle_weight(bin);
+                const float t = place_of(x);
+                if (t < kFilterBins - 1) atomicAdd(&sh.hist[static_cast<int>(t)], 1u);
             });
-            return make_float2(f, middle);
-        };
-        auto last_bin = [&]() {
+            add_up();
             const int others = static_cast<int>(sh.total[2 * tid] + (tid == kFilterThreads - 1 ? 0 : sh.total[2 * tid + 1]));
             const int sum = __reduce_add_sync(0xffffffffu, others);
             if (lane == 0) sh.scan[warp] = sum;
@@ -588,43 +650,98 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             for (int w = 0; w < kFilterThreads / 32; ++w) all += sh.scan[w];
             if (tid == 0) sh.total[kFilterBins - 1] = valid - all;
             __syncthreads();
+            float off = 0.f;
+            for (int i = 0; i < 2; ++i) off += sh.total[2 * tid + i] * middle_weight(2 * tid + i);
+            off = warp_sum(off);
+            if (lane == 0) sh.scan_w[warp] = off;
+            __syncthreads();
+            for (int w = 0; w < kFilterThreads / 32; ++w) f += sh.scan_w[w];
+            return f;
         };
-        FilterGoal g = {false, want_k ? top_k : valid, 0., static_cast<double>(top_p), 0., 0., 0ull};
-        const float2 all = count_bins();
-        FilterSums s = {static_cast<double>(all.x), static_cast<double>(all.y), 0ull, none};
-        s = filter_reduce(sh, s, ctas, rank, turn++);
-        g.total = s.a;
-        g.target = g.p * g.total;
-        g.off = s.b - s.a;
-        add_up();
-        last_bin();
-        // ---- few tokens: those of the bins down to the border. By weight it is guessed from the tail, which lies in narrow
-        // bins of light tokens, and a little too far.
-        find_bin(!want_k, g.k, g.target + g.off + 0.05 * (g.total - g.target), 0, kFilterBins - 1, middle_weight);
-        const int last = sh.found[0], in_list = sh.found[1] + sh.found[2];
-        if (in_list <= kFilterList) {
-            const uint32_t counter = mapa_shared(smem_u32(&sh.n_cand), 0);
-            each([&](float x, int i) {
-                if (bin_of(x) <= last) st_dsmem_u64(mapa_shared(smem_u32(&sh.list[add_dsmem_u32(counter, 1)]), 0), filter_key(x, v0 + i));
-            });
+        FilterGoal g = {false, want_k ? top_k : valid, top_p, 0, 0, 0.f, 0ull};
+        auto sum_up = [&]() {
+            float f = 0.f;
+            each([&](float x, int) { f += filter_weight(r, x); });
+            FilterSums s = {__float2ull_rn(f * 0x1p51f), 0, 0ull, none};
+            g.total = filter_reduce<kSumA>(sh, s, ctas, rank, turn++, 7).a;
+            g.target = filter_share(g.p, g.total);
+        };
+        // ---- few tokens: those above the bound that the threads' largest give. Of weight, a bin's tokens count as its
+        // lightest would, and the total's error as missing.
+        const bool all = valid <= kFilterList;
+        if (!want_k) sum_up();
+        if (!all) {
+            if (m > -INFINITY) atomicAdd(&sh.hist[bin_of(m)], 1u);
+            add_up();
+            find_bin(!want_k, g.k, g.target * (kFilterUnit * 1.0001f), 0, kFilterBins - 1, [](int i) { return i < kFilterBins - 1 ? filter_ex2(-(i + 1) * (kFilterRange / kFilterBins)) : 0.f; });
+        }
+        const int last = all ? 0 : sh.found[0];
+        if (last < kFilterBins - 1) {
+            // the bins' end as a logit, a little below: a few tokens more do no harm
+            const float width = (last + 1) / r.scale, least = all ? -FLT_MAX : r.m - (width + (fabsf(r.m) + width) * 0x1p-20f);
+            auto pick = [&](float x, int i) {
+                if (!(x >= least) || x == -INFINITY) return;
+                const uint32_t at = atomicAdd(&sh.n_pick, 1u);
+                if (at < kFilterList) sh.pick[at] = static_cast<uint16_t>(i);
+            };
+#pragma unroll 4
+            for (int i = tid; i < n4; i += kFilterThreads) {
+                const float4 x = x4[i];
+                if (fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= least) pick(x.x, 4 * i), pick(x.y, 4 * i + 1), pick(x.z, 4 * i + 2), pick(x.w, 4 * i + 3);
+            }
             filter_sync(ctas);
+            int in_list = 0;
+            if (rank == 0) {  // fetches everybody's
+                int from[kFilterCluster + 1];
+                from[0] = 0;
+#pragma unroll
+                for (int q = 0; q < kFilterCluster; ++q)
+                    from[q + 1] = from[q] + (q < ctas ? static_cast<int>(ld_dsmem_u32(mapa_shared(smem_u32(&sh.n_pick), q))) : 0);
+                in_list = from[kFilterCluster];
+                if (in_list <= kFilterList)
+                    for (int i = tid; i < in_list; i += kFilterThreads) {
+                        int q = 0, first = 0;
+#pragma unroll
+                        for (int u = 1; u < kFilterCluster; ++u)
+                            if (i >= from[u]) q = u, first = from[u];
+                        const uint32_t at = ld_dsmem_u16(mapa_shared(smem_u32(&sh.pick[i - first]), q));
+                        const float x = __uint_as_float(ld_dsmem_u32(mapa_shared(smem_u32(x_s + at), q)));
+                        sh.list[i] = filter_key(x, q * a.chunk + static_cast<int>(at));
+                    }
+                __syncthreads();
+            }
+            const bool fits = in_list > 0 && in_list <= kFilterList;
             int size = 32;
             while (size < in_list) size *= 2;
-            if (rank == 0) {
+            if (rank == 0 && fits) {
                 for (int i = in_list + tid; i < size; i += kFilterThreads) sh.list[i] = 0;
                 __syncthreads();
-                for (int k = 2; k <= size; k *= 2)  // bitonic, largest first
-                    for (int j = k / 2; j > 0; j /= 2) {
-                        for (int i = tid; i < size / 2; i += kFilterThreads) {
-                            const int p = 2 * i - (i & (j - 1)), q = p + j;
-                            const unsigned long long u = sh.list[p], v = sh.list[q];
-                            if ((u < v) == ((p & k) == 0)) sh.list[p] = v, sh.list[q] = u;
+                if (size <= kFilterFew) {  // largest first: few by their number of larger ones, threads / size threads a token
+                    const int share = kFilterThreads / size, i = tid / share;
+                    const unsigned long long mine = sh.list[i];
+                    int place = 0;
+#pragma unroll 8
+                    for (int q = tid % share; q < in_list; q += share) place += sh.list[q] > mine;
+                    for (int o = share / 2; o > 0; o /= 2) place += __shfl_xor_sync(0xffffffffu, place, o);
+                    __syncthreads();
+                    if (i < in_list && tid % share == 0) sh.list[place] = mine;
+                    __syncthreads();
+                } else {  // more by a bitonic network
+                    for (int k = 2; k <= size; k *= 2)
+                        for (int j = k / 2; j > 0; j /= 2) {
+                            for (int i = tid; i < size / 2; i += kFilterThreads) {
+                                const int p = 2 * i - (i & (j - 1)), q = p + j;
+                                const unsigned long long u = sh.list[p], v = sh.list[q];
+                                if ((u < v) == ((p & k) == 0)) sh.list[p] = v, sh.list[q] = u;
+                            }
+                            __syncthreads();
                         }
-                        __syncthreads();
-                    }
+                }
             }
             for (;;) {
-                if (rank == 0) {
+                if (rank == 0 && !fits) {
+                    if (tid < ctas) st_dsmem_u32(mapa_shared(smem_u32(&sh.ambiguous), tid), 2);
+                } else if (rank == 0) {
                     // weights before each token, in order: exact
                     constexpr int PER = kFilterList / kFilterThreads;
                     const int per = (in_list + kFilterThreads - 1) / kFilterThreads;
@@ -632,7 +749,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
 #pragma unroll
                     for (int u = 0; u < PER; ++u) {
                         const int i = tid * per + u;
-                        w[u] = want_p && u < per && i < in_list ? weight_exact(r, sh, filter_value(static_cast<uint32_t>(sh.list[i] >> 32))) >> 7 : 0ull;
+                        w[u] = want_p && u < per && i < in_list ? weight_exact(r, filter_value(static_cast<uint32_t>(sh.list[i] >> 32))) >> 7 : 0ull;
                         sum += w[u];
                     }
                     unsigned long long before = sum;
@@ -651,17 +768,17 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
 #pragma unroll
                         for (int u = 0; u < PER; ++u) {
                             upto += w[u];
-                            if (u < per && tid * per + u == g.k - 1) sh.mass = static_cast<double>(upto) * 0x1p-51;
+                            if (u < per && tid * per + u == g.k - 1) sh.mass = upto >> 7;
                         }
                         __syncthreads();
                     }
-                    const double target = g.p * sh.mass;
+                    const unsigned long long target = want_p ? filter_share(g.p, sh.mass) : 0;
 #pragma unroll
                     for (int u = 0; u < PER; ++u) {
                         const int i = tid * per + u;
                         if (u < per && i < in_list) {
-                            const double mass = static_cast<double>(before) * 0x1p-51;
-                            if (want_p && !want_k && !precise && fabs(mass - target) <= kFilterNear * g.total) sh.ambiguous = 1;
+                            const unsigned long long mass = before >> 7;
+                            if (want_p && !want_k && !precise && close(mass, g)) sh.ambiguous = 1;
                             if (i >= g.k || (want_p && !(mass < target)) || !strong(filter_value(static_cast<uint32_t>(sh.list[i] >> 32))))
                                 atomicMin(&sh.fails, max(i, 1));
                             before += w[u];
@@ -686,22 +803,16 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 precise = true;
                 set_total(g);
             }
-            if (!listed) {
-                cut = 0, kept = valid;
-                if (rank == 0 && tid == 0) sh.n_cand = 0;
-            }
+            if (!listed) cut = 0, kept = valid;
         }
         if (!listed) {
+            const float about = count_bins();
+            if (want_p && !want_k) g.off = about - g.total * kFilterUnit;
             FilterGoal h = g;
             if (want_k) cut = search(h, kept);
             if (want_p && kept > 1) {
                 if (want_k) {  // the row's histogram again: a search may have used its place
-                    __syncthreads();
-                    for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = 0;
-                    __syncthreads();
                     count_bins();
-                    add_up();
-                    last_bin();
                     h.set = cut;
                     set_total(h);
                 }
@@ -714,29 +825,37 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
     if constexpr (!SAMPLE) {
         int count = 0;
         const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-        const uint32_t cut_x = static_cast<uint32_t>(cut >> 32);
-        auto keep = [&](float x, int i) {
-            const uint32_t k = orderable(x + 0.f);
-            const bool yes = x > -INFINITY && (k > cut_x || (k == cut_x && filter_key(x, v0 + i) >= cut)) && (listed || strong(x));
-            count += yes;
-            return yes ? x : -INFINITY;
-        };
-        for (int i = tid; i < n4; i += kFilterThreads) {
-            float4 x = x4[i];
-            x.x = keep(x.x, 4 * i), x.y = keep(x.y, 4 * i + 1), x.z = keep(x.z, 4 * i + 2), x.w = keep(x.w, 4 * i + 3);
-            if (vec && 4 * i + 3 < n) {
-                *reinterpret_cast<float4 *>(out + 4 * i) = x;
-            } else {
-                out[4 * i] = x.x;
-                if (4 * i + 1 < n) out[4 * i + 1] = x.y;
-                if (4 * i + 2 < n) out[4 * i + 2] = x.z;
-                if (4 * i + 3 < n) out[4 * i + 3] = x.w;
+        // keys as floats: the cut's logit, and of equal ones those up to its token
+        const float cut_x = cut ? filter_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
+        const int cut_i = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) - v0 : -1;
+        auto write = [&](auto keep) {
+#pragma unroll 4
+            for (int i = tid; i < n4; i += kFilterThreads) {
+                float4 x = x4[i];
+                x.x = keep(x.x, 4 * i) ? x.x : -INFINITY, x.y = keep(x.y, 4 * i + 1) ? x.y : -INFINITY;
+                x.z = keep(x.z, 4 * i + 2) ? x.z : -INFINITY, x.w = keep(x.w, 4 * i + 3) ? x.w : -INFINITY;
+                if (vec && 4 * i + 3 < n) {
+                    *reinterpret_cast<float4 *>(out + 4 * i) = x;
+                } else {
+                    out[4 * i] = x.x;
+                    if (4 * i + 1 < n) out[4 * i + 1] = x.y;
+                    if (4 * i + 2 < n) out[4 * i + 2] = x.z;
+                    if (4 * i + 3 < n) out[4 * i + 3] = x.w;
+                }
             }
-        }
+        };
+        if (want_m && !listed)
+            write([&](float x, int i) {
+                const bool yes = (x > cut_x || (x == cut_x && i <= cut_i)) && strong(x);
+                count += yes;
+                return yes;
+            });
+        else
+            write([&](float x, int i) { return x > cut_x || (x == cut_x && i <= cut_i); });
         if (a.n_kept) {
             if (want_m && !listed) {
-                FilterSums s = {static_cast<double>(count), 0., 0ull, none};
-                kept = static_cast<int>(filter_reduce(sh, s, ctas, rank, turn++).a);
+                FilterSums s = {static_cast<unsigned long long>(count), 0, 0ull, none};
+                kept = static_cast<int>(filter_reduce<kSumA>(sh, s, ctas, rank, turn++).a);
             }
             if (rank == 0 && tid == 0) a.n_kept[row] = kept;
         }
@@ -769,28 +888,29 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 else
                     s2 = fmaxf(s2, s);
             });
-            FilterSums s = {static_cast<double>(count), 0., s1 >= 0.f ? static_cast<unsigned long long>(__float_as_uint(s1)) << 32 | static_cast<uint32_t>(~at) : 0ull, none};
-            s = filter_reduce(sh, s, racers, rank, turn++);
+            FilterSums s = {static_cast<unsigned long long>(count), 0,
+                            s1 >= 0.f ? static_cast<unsigned long long>(__float_as_uint(s1)) << 32 | static_cast<uint32_t>(~at) : 0ull, none};
+            s = filter_reduce<kSumA | kHi>(sh, s, racers, rank, turn++);
             kept = static_cast<int>(s.a);
             unsigned long long won = s.hi ? s.hi : top;  // no noise above zero
             const float best = __uint_as_float(static_cast<uint32_t>(s.hi >> 32)), near = best * (1.f - 0x1p-14f);
-            FilterSums t = {static_cast<double>((s1 >= near && s1 >= 0.f ? 1 : 0) + (s2 >= near && s2 >= 0.f ? 1 : 0)), 0., 0ull, none};
-            t = filter_reduce(sh, t, racers, rank, turn++);
-            if (t.a > 1.5) {  // near ones again, in 64 bits
+            FilterSums t = {(s1 >= near && s1 >= 0.f ? 1ull : 0ull) + (s2 >= near && s2 >= 0.f ? 1ull : 0ull), 0, 0ull, none};
+            t = filter_reduce<kSumA>(sh, t, racers, rank, turn++);
+            if (t.a > 1) {  // near ones again, in 64 bits
                 double top_score = -1.;
                 int who = 0;
                 runners([&](float x, int v) {
                     if (score(x, v) >= near) {
-                        const double w = x == r.m ? 1. : exp((static_cast<double>(x) - static_cast<double>(r.m)) / r.T);
+                        const double w = x == r.m ? 1. : exp((static_cast<double>(x) - static_cast<double>(r.m)) / static_cast<double>(T));
                         const double exact = w / static_cast<double>(noise[v]);
                         if (exact > top_score || (exact == top_score && v < who)) top_score = exact, who = v;
                     }
                 });
-                FilterSums u = {0., 0., top_score >= 0. ? static_cast<unsigned long long>(__double_as_longlong(top_score)) : 0ull, none};
+                FilterSums u = {0, 0, top_score >= 0. ? static_cast<unsigned long long>(__double_as_longlong(top_score)) : 0ull, none};
                 const unsigned long long mine = u.hi;
-                u = filter_reduce(sh, u, racers, rank, turn++);
-                FilterSums f = {0., 0., 0ull, top_score >= 0. && mine == u.hi ? static_cast<unsigned long long>(who) : none};
-                f = filter_reduce(sh, f, racers, rank, turn++);
+                u = filter_reduce<kHi>(sh, u, racers, rank, turn++);
+                FilterSums f = {0, 0, 0ull, top_score >= 0. && mine == u.hi ? static_cast<unsigned long long>(who) : none};
+                f = filter_reduce<kLo>(sh, f, racers, rank, turn++);
                 won = static_cast<uint32_t>(~static_cast<uint32_t>(f.lo));
             }
             if (rank == 0 && tid == 0) {

@@ -10,7 +10,9 @@
 
 namespace sdv {
 
-constexpr int kForkThreads = 256;  // max_batch at most
+constexpr int kForkMost = 256;     // forks of a call: max_batch at most
+constexpr int kForkThreads = 1024;
+constexpr int kCopyThreads = 256;
 constexpr int kForkIndexBlocks = 8;  // CTAs that copy a sequence's n-gram index
 
 struct ForkArgs {
@@ -28,9 +30,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs p) {
     pdl_trigger();
     pdl_wait();
     DevState &s = p.s;
-    __shared__ int taken[kForkThreads], from[kForkThreads], full_s[kForkThreads], warp_sum[kForkThreads / 32], ok_s, added;
+    __shared__ int taken[kForkMost], from[kForkMost], full_s[kForkMost], warp_sum[kForkThreads / 32], ok_s, added;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    taken[tid] = 0;
+    if (tid < kForkMost) taken[tid] = 0;
     if (tid == 0) ok_s = SDV_OK, added = 0;
     __syncthreads();
     const bool mine = tid < p.n;
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs p) {
 
 // The filled slots of the partial pages: CTA (fork, layer), and behind the layers the CTAs that copy the n-gram index. Bound by
 // launch and latency for a few forks, else by memory.
-__global__ void __launch_bounds__(kForkThreads) fork_copy_kernel(ForkArgs p) {
+__global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(ForkArgs p) {
     pdl_trigger();
     pdl_wait();
     const DevState &s = p.s;
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_copy_kernel(ForkArgs p) {
         uint4 *to = reinterpret_cast<uint4 *>(p.pool + layer * p.layer_stride + c.y * page);
         const long long all = static_cast<long long>(2) * p.nkv * run;
 #pragma unroll 4
-        for (long long i = tid; i < all; i += kForkThreads) {
+        for (long long i = tid; i < all; i += kCopyThreads) {
             const int head = static_cast<int>(i / run);
             const size_t at = static_cast<size_t>(head) * whole + (i - static_cast<long long>(head) * run);
             to[at] = from[at];
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_copy_kernel(ForkArgs p) {
     }
     const int src = p.src[blockIdx.x], dst = p.dst[blockIdx.x];
     const size_t slots = static_cast<size_t>(s.ng_orders) * s.ng_slots;
-    const int first = (layer - p.n_layers) * kForkThreads + tid, step = kForkIndexBlocks * kForkThreads;
+    const int first = (layer - p.n_layers) * kCopyThreads + tid, step = kForkIndexBlocks * kCopyThreads;
     for (size_t i = first; i < slots; i += step) {
         s.ng_keys[dst * slots + i] = s.ng_keys[src * slots + i];
         s.ng_vals[dst * slots + i] = s.ng_vals[src * slots + i];

@@ -124,6 +124,7 @@ struct sdv_ctx {
     float2 *accept_part = nullptr;  // sampled acceptance: chunk statistics of the logit rows, best scores, arrivals
     unsigned long long *accept_keys = nullptr;
     int *accept_arrived = nullptr;
+    bool forked = false;          // a fork has been asked for: later releases may find shared pages, many at once
     int4 *fork_copies = nullptr;  // partial pages that a fork copies
     int attn_splits = 1;
     int attn_group = kAttnGroup;  // key positions per attention group (1024, or 2048 for long sequences)
@@ -1090,7 +1091,8 @@ int sdv_fork_seq(sdv_ctx *ctx, const int32_t *d_src, const int32_t *d_dst, int n
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch(ctx, fork_kernel, dim3(1), dim3(kForkThreads), 0, st, p);
     if (e == cudaSuccess)
-        e = launch(ctx, fork_copy_kernel, dim3(n, p.n_layers + (ctx->ng_slots ? kForkIndexBlocks : 0)), dim3(kForkThreads), 0, st, p);
+        e = launch(ctx, fork_copy_kernel, dim3(n, p.n_layers + (ctx->ng_slots ? kForkIndexBlocks : 0)), dim3(kCopyThreads), 0, st, p);
+    if (e == cudaSuccess) ctx->forked = true;
     return rc(e);
 }
 
@@ -1101,7 +1103,7 @@ namespace {
 template <bool SAMPLE>
 int run_filter(sdv_ctx *ctx, FilterArgs a, int rows, int B, void *stream) {
     const int V = ctx->m.vocab;
-    const int ctas = V <= kFilterAlone ? 1 : kFilterCluster;
+    const int ctas = V <= kFilterList ? 1 : kFilterCluster;
     a.status = ctx->st.status;
     a.B = B;
     a.vocab = V;
@@ -1158,7 +1160,7 @@ int sdv_sample(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int r
 int sdv_rewind_cache(sdv_ctx *ctx, const int32_t *d_length, int B, void *stream) {
     if (!ctx || !d_length || B <= 0 || B > ctx->c.max_batch) return SDV_ERR_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(ctx, rewind_kernel, dim3(1), dim3(256), 0, st, ctx->st, d_length, B);
+    cudaError_t e = launch(ctx, rewind_kernel, dim3(1), dim3(ctx->forked ? 1024 : 256), 0, st, ctx->st, d_length, B);
     if (e == cudaSuccess && ctx->swa_mask)
         e = launch(ctx, swa_restore_kernel, dim3(B, ctx->m.n_layers), dim3(256), 0, st, ctx->st, ctx->pool,
                    ctx->layer_stride, ctx->swa_mask, static_cast<const bf16 *>(ctx->swa_backup), ctx->swa_layer_elems,

