@@ -20,7 +20,7 @@ constexpr int kSBatch = 256;     // sequences of a call at most
 constexpr int kSEntries = kSGroups + kSBatch;
 constexpr int kSOverhead = 3;    // what a tile's queries and results cost, in chunks
 constexpr float kSGrow = 8.f;    // a row's reference follows its maximum once that is more than 2^8 above it
-constexpr int kSThreads = 384;   // two softmax warpgroups, a warp for K, one for V, one that issues MMAs; as many as entries
+constexpr int kSThreads = 384;   // two softmax warpgroups, a warp for K, one for V, two that issue MMAs; as many as entries
 
 struct SharedArgs {
     const void *q;
@@ -378,7 +378,7 @@ struct Int {
     static constexpr int value = N;
 };
 struct SShared {
-    uint64_t full[8], empty[8], s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_empty;
+    uint64_t full[8], empty[8], s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_empty, turn[2];
     uint32_t tmem;
     uint32_t bad[2][2][4];  // [turn][warpgroup]: keys of the chunk that are not finite, as bits
     float2 ml[2][128];  // (M, l) of the rows that two warpgroups share
@@ -412,16 +412,17 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
     if (tid == 0) {
         for (int i = 0; i < Q::SLOTS; ++i) {
             mbar_init(&sh.full[i], a.box_rows ? 1 : 32);
-            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_half[i], 128);
             mbar_init(&sh.p_full[i], 128);
             mbar_init(&sh.o_done[i], 1);
+            mbar_init(&sh.turn[i], 1);
         }
         mbar_init(&sh.q_full, 256);
-        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.q_empty, 2);
         fence_mbar_init();
     }
     if (warp == 10) {
@@ -527,83 +528,98 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                 if (used[i]) mbar_wait(&sh.full[(v ? Q::DEPTH : 0) + i], (used[i] - 1) & 1);
             if (lane == 0) set_status(a.status, SDV_ERR_DEVICE_TIMEOUT);
         }
-    } else if (warp == 10) {
-        // ---- MMA issue. Step s of a piece is softmax warpgroup s % 2's: of its own 128 rows of a tile of more than 128, every
-        // chunk for each in turn, else of the tile's rows and every other chunk. They keep their turns, so that one's softmax
-        // runs beside the other's products (with a warp that issues for each, both fell into step: 4,900 clocks for what now
-        // takes 4,200). The whole warp loops and one lane issues: with a lane of its own (lane 0 alone in the loop) an MMA took 80
-        // to 100 clocks to issue, 61 so.
-        // What steers the loop passes through a shuffle, so that it is known to be the same in every lane, and a wait that
-        // needs none is a single look: what the warp does beside its MMAs is time without products.
+    } else if (warp >= 10) {
+        // ---- MMA issue, a warp for each softmax warpgroup: for its own 128 rows of a tile of more than 128 and every chunk, else
+        // for the tile's rows and every other chunk. The warps take turns, a step's products with V and the next scores a turn,
+        // so that one warpgroup's softmax runs beside the other's products; a warp waits for what it needs before its turn, while
+        // the other's MMAs run (one warp for both left the tensor cores idle for 450 clocks of 2,090 a step; two without turns
+        // fell into step, 2,450). The whole warp loops and one lane issues: with a lane of its own (lane 0 alone in the loop)
+        // an MMA took 80 to 100 clocks to issue, 61 so. What steers the loop passes through a shuffle, so that it is known to
+        // be the same in every lane, and a wait that needs none is a single look.
         constexpr uint32_t id_s = idesc_16<T>(128, kSKeys, false), id_o = idesc_16<T>(128, D, true);
         auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
-        const uint32_t tm = same(tmem);
-        uint32_t k_bits = 0, v_bits = 0, p_bits = 0, q_bit = 0;  // the phase of each barrier that comes next
+        const uint32_t w = same(warp - 10), tm = same(tmem), s_t = tm + w * kSKeys, o_t = tm + Q::O_COL + w * 128;
+        uint32_t k_bits = 0, v_bits = 0, p_bit = 0, q_bit = 0, turn_bit = 0;  // the phase of each barrier that comes next
+        bool turns = w;  // the first turn of all is warp 0's without a wait
         auto await = [&](uint64_t *bar, uint32_t parity) {
             if (!mbar_try_wait(bar, parity) && ok) ok = mbar_wait(bar, parity);
         };
         for (; more; more = shared_next(a, pl, x, x1, p)) {
             const bool wide = same(p.rows) > 128;
-            const int n = same(p.n), steps = wide ? 2 * n : n;
+            const int n = same(p.n), steps = wide ? n : (n + 1 - static_cast<int>(w)) >> 1, rounds = wide ? n : (n + 1) >> 1;
             await(&sh.q_full, q_bit);
             q_bit ^= 1;
             tc_fence_after();
             fence_async_smem();  // copies in pieces are generic writes; the tensor cores read through the async proxy
-            auto step = [&](int s, auto W) {  // the products with V of step s, the scores of step s + 2
-                constexpr int w = decltype(W)::value;
-                const int c = wide ? s >> 1 : s, next = wide ? (s + 2) >> 1 : s + 2;
-                const bool more = s + 2 < steps, first = !wide || w == 0, last = !wide || w == 1;  // of the steps of its chunk
-                const uint32_t s_t = tm + w * kSKeys, o_t = tm + Q::O_COL + w * 128;
+            const uint64_t qd = sw128_desc(q_s + (wide && w ? Q::Q_BYTES : 0));
+            // Slots are filled for the other warp, too: their phases count every chunk of the piece.
+#pragma unroll 1
+            for (int j = -1; j < rounds; ++j) {  // the products with V of step j, the scores of step j + 1
+                const int c = wide ? j : 2 * j + static_cast<int>(w), next = wide ? j + 1 : c + 2;
+                const bool mine = j >= 0 && j < steps, ahead = j + 1 < steps;
                 const int v_at = c % Q::DEPTH, k_at = next % Q::DEPTH;
                 const uint64_t vd = line_desc(kv_s + (Q::DEPTH + v_at) * Q::SLOT, 128, kSKeys * 128);
-                if (s >= 0) {
-                    await(&sh.p_half[w], p_bits >> w & 1);
-                    if (first) {
-                        await(&sh.full[Q::DEPTH + v_at], v_bits >> v_at & 1);
-                        v_bits ^= 1u << v_at;
-                    }
-                    tc_fence_after();
-                    if (!a.box_rows) fence_async_smem();
-                    if (elect_one()) {
+                auto half = [&](int h) {  // 64 keys: of 16 the hi plane, then lo, eight columns each
 #pragma unroll
-                        for (int k = 0; k < kSKeys / 16; ++k)  // 16 keys' hi plane, then lo: eight columns each
-                            umma_f16_ts(o_t, s_t + k / 4 * 32 + k % 2 * 16 + k / 2 % 2 * 8, vd + (k / 2 * 2048 >> 4), id_o, s > 1 || k > 0);
+                    for (int i = 0; i < kSKeys / 16; ++i) {
+                        const int k = h * (kSKeys / 16) + i;
+                        umma_f16_ts(o_t, s_t + k / 4 * 32 + k % 2 * 16 + k / 2 % 2 * 8, vd + (k / 2 * 2048 >> 4), id_o, h > 0 || j > 0 || i > 0);
                     }
-                    await(&sh.p_full[w], p_bits >> w & 1);
-                    p_bits ^= 1u << w;
+                };
+                if (mine) {
+                    await(&sh.p_half[w], p_bit);
+                    await(&sh.full[Q::DEPTH + v_at], v_bits >> v_at & 1);
+                    v_bits ^= 1u << v_at;
                 }
-                if (more && first) {
+                if (ahead) {
                     await(&sh.full[k_at], k_bits >> k_at & 1);
                     k_bits ^= 1u << k_at;
                 }
+                if (turns) {
+                    await(&sh.turn[w], turn_bit);
+                    turn_bit ^= 1;
+                }
+                turns = true;
                 tc_fence_after();
                 if (!a.box_rows) fence_async_smem();
+                if (mine) {
+                    if (elect_one()) half(0);
+                    await(&sh.p_full[w], p_bit);
+                    p_bit ^= 1;
+                    tc_fence_after();
+                }
                 if (elect_one()) {
-                    if (s >= 0) {
-#pragma unroll
-                        for (int k = kSKeys / 16; k < 2 * kSKeys / 16; ++k)
-                            umma_f16_ts(o_t, s_t + k / 4 * 32 + k % 2 * 16 + k / 2 % 2 * 8, vd + (k / 2 * 2048 >> 4), id_o, 1);
+                    if (mine) {
+                        half(1);
                         umma_commit(&sh.o_done[w]);
-                        if (last) umma_commit(&sh.empty[Q::DEPTH + v_at]);
+                        umma_commit(&sh.empty[Q::DEPTH + v_at]);
+                        if (!wide) umma_commit(&sh.empty[Q::DEPTH + v_at]);  // for the other warp, which does not read it
                     }
-                    if (more) {
-                        const uint64_t kd = sw128_desc(kv_s + k_at * Q::SLOT), qd = sw128_desc(q_s + (wide && w ? Q::Q_BYTES : 0));
+                    if (ahead) {
+                        const uint64_t kd = sw128_desc(kv_s + k_at * Q::SLOT);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             const uint32_t off = (k / 4 * (128 * 128) + k % 4 * 32) >> 4;
                             umma_bf16(s_t, qd + off, kd + off, id_s, k > 0);
                         }
                         umma_commit(&sh.s_full[w]);
-                        if (last) umma_commit(&sh.empty[k_at]);
-                        if (s + 3 == steps) umma_commit(&sh.q_empty);
+                        umma_commit(&sh.empty[k_at]);
+                        if (!wide) umma_commit(&sh.empty[k_at]);
+                        if (j + 2 == steps) umma_commit(&sh.q_empty);
                     }
+                    mbar_arrive(&sh.turn[1 - w]);
                 }
                 __syncwarp();
-            };
-#pragma unroll 1
-            for (int s = -2; s < steps; s += 2) {
-                step(s, Int<0>{});
-                if (s + 1 < steps) step(s + 1, Int<1>{});
+            }
+            if (steps == 0 && lane == 0) mbar_arrive(&sh.q_empty);
+            if (!wide) {  // the slots that the other warp used moved on as well
+#pragma unroll
+                for (int i = 0; i < Q::DEPTH; ++i) {
+                    if (i % 2 == static_cast<int>(w)) continue;
+                    const uint32_t odd = (n + Q::DEPTH - 1 - i) / Q::DEPTH & 1;
+                    k_bits ^= odd << i;
+                    v_bits ^= odd << i;
+                }
             }
         }
         if (!ok && lane == 0) set_status(a.status, SDV_ERR_DEVICE_TIMEOUT);
