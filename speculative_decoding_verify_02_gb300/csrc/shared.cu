@@ -14,7 +14,7 @@ struct sdv_shared {
     const uint8_t *pool = nullptr;
     uint8_t *ws = nullptr;
     size_t layer_bytes = 0;
-    FastDiv by_page{}, by_grp{};
+    FastDiv by_page{}, by_grp{}, by_nq{};
     int box_rows = 0;                // pool rows of a TMA box (0: the page size fits none)
     std::vector<CUtensorMap> pools;  // one map a layer over its pool rows
 };
@@ -59,13 +59,14 @@ size_t part_slots(const sdv_shared_cfg &c, int sms) {
 }
 // Offsets into the workspace: the status word and the cut, the plan's entries, the rows' entries, (M, l), O.
 struct Workspace {
-    size_t plan, row_entry, ml, o, end;
+    size_t plan, plan_rows, row_entry, ml, o, end;
 };
 Workspace workspace(const sdv_shared_cfg &c, int sms) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     Workspace w;
     w.plan = 256;
-    w.row_entry = up(w.plan + sizeof(SEntry) * kSEntries);
+    w.plan_rows = up(w.plan + sizeof(int4) * kSEntries);
+    w.row_entry = up(w.plan_rows + sizeof(int2) * kSEntries);
     w.ml = up(w.row_entry + sizeof(int2) * c.max_rows);
     w.o = up(w.ml + sizeof(float2) * part_slots(c, sms));
     w.end = w.o + sizeof(float) * part_slots(c, sms) * c.head_dim;
@@ -177,6 +178,7 @@ int sdv_shared_create(const sdv_shared_cfg *cfg, const void *d_pool, void *d_wor
     s->layer_bytes = layer_bytes(*cfg);
     s->by_page = FastDiv::of(cfg->page_size);
     s->by_grp = FastDiv::of(s->grp);
+    s->by_nq = FastDiv::of(cfg->n_q_heads);
     s->box_rows = box_rows_of(*cfg);
     bool maps = true;
     try {
@@ -245,14 +247,17 @@ int sdv_shared_attention(sdv_shared *s, int layer, const void *d_q, int64_t q_st
     a.pool_rows = c.n_pages * 2 * c.n_kv_heads * c.page_size;
     a.by_page = s->by_page;
     a.by_grp = s->by_grp;
+    a.by_nq = s->by_nq;
     a.scale = 1.f / std::sqrt(static_cast<float>(c.head_dim));
     a.scale_log2 = 1.4426950408889634f * a.scale;
     a.cap = softcap;
     a.ctas = s->sm_count;
     const Workspace w = workspace(c, s->sm_count);
     a.part_rows = part_rows(c);
-    a.plan_cut = reinterpret_cast<int *>(s->ws) + 16;
-    a.plan = reinterpret_cast<SEntry *>(s->ws + w.plan);
+    a.plan_cut = reinterpret_cast<int2 *>(s->ws + 64);
+    a.by_cut = reinterpret_cast<FastDiv *>(s->ws + 96);
+    a.plan = reinterpret_cast<int4 *>(s->ws + w.plan);
+    a.plan_rows = reinterpret_cast<int2 *>(s->ws + w.plan_rows);
     a.row_entry = reinterpret_cast<int2 *>(s->ws + w.row_entry);
     a.part_ml = reinterpret_cast<float2 *>(s->ws + w.ml);
     a.part_o = reinterpret_cast<float *>(s->ws + w.o);

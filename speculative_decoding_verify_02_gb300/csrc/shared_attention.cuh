@@ -33,15 +33,18 @@ struct SharedArgs {
     int pages_per_seq, page_size, n_pages, nq, nkv, grp, B, G, max_span, max_rows, max_context, window;
     int q_vec, out_vec;              // rows are 16-byte aligned
     int box_rows, pool_rows;         // rows of a TMA box (0: pages that none fits); rows of the layer's pool: a box there reads zeros
-    FastDiv by_page, by_grp;
+    FastDiv by_page, by_grp, by_nq;
     float scale, scale_log2, cap;    // 1 / sqrt(D), log2(e) / sqrt(D), the cap or 0
     int ctas;                        // CTAs of the attention kernel, which the cut into parts follows
     int part_rows;                   // partial rows of a kv head
     float *part_o;                   // partial results: [nkv][part_rows] rows of sequences' own tiles, as many of prefix tiles,
                                      // [ctas][kSTile] of pieces that begin inside of a tile
     float2 *part_ml;                 // (M, l) of each
-    struct SEntry *plan;             // the plan's entries, for the kernel that joins the parts
-    int *plan_cut;                   // its q and ov
+    // the plan for the kernel that joins the parts: an entry's start on the line, cost of a tile, chunks and cost of one, and its
+    // first row and tiles a kv head; the length and overhead of the cut
+    int4 *plan;
+    int2 *plan_rows, *plan_cut;
+    FastDiv *by_cut;
     int2 *row_entry;                 // [max_rows]: a row's entry, kRowNone or kRowRefused, and that of its prefix or -1
 };
 constexpr int kRowNone = -1, kRowRefused = -2;
@@ -51,6 +54,8 @@ constexpr int kRowNone = -1, kRowRefused = -2;
 // for each kv head, a tile is chunks. Chunks lie one behind another on a line of costs (a tile's first costs `ov` more, and a
 // chunk of more than 128 rows counts twice), and CTA i takes those that begin in [i q, (i + 1) q). So the CTAs finish
 // together whatever the lengths are, every one of them knows the whole cut, and a tile is cut where the line is.
+// Where there are few tiles, a cut into pieces of one tile only is better, as long as they are no more than the CTAs: a second
+// piece costs about kSOverhead chunks (eight sequences of 848 keys with spans of eight: 18.1 us, 22.8 without).
 // The lengths are read once, side by side, and all else is worked out in shared memory: as reads that wait for one another it
 // took 20 us.
 struct SEntry {
@@ -69,8 +74,8 @@ struct SPlan {
     SEntry e[kSEntries];
     int row_off[kSBatch + 1], base[kSBatch], group_off[kSGroups + 1], prefix[kSGroups];
     int g_min[kSGroups], g_max[kSGroups];  // lowest and highest position of a group's rows
-    int total, q, ov, ok, steps, tiles;
-    int warp_sum[kSThreads / 32];
+    int total, q, ov, best;
+    int2 warp_sum[kSThreads / 32];
 };
 
 __device__ __forceinline__ int shared_last(const int *off, int n, int v) {  // the last of n offsets that is not above v
@@ -91,12 +96,10 @@ __device__ __forceinline__ void shared_plan(const SharedArgs &a, SPlan &pl, bool
     if (tid < a.B) pl.base[tid] = a.base[tid];
     if (tid <= a.G && a.G) pl.group_off[tid] = a.group_off[tid];
     if (tid < a.G) pl.prefix[tid] = a.prefix_len[tid], pl.g_min[tid] = 0x7fffffff, pl.g_max[tid] = -1;
-    if (tid == 0) pl.ok = 1, pl.steps = pl.tiles = 0;
+    if (tid == 0) pl.best = 0x7fffffff;
     __syncthreads();
-    if (tid < a.G && (pl.group_off[tid] > pl.group_off[tid + 1] || (tid == 0 && pl.group_off[0] != 0) ||
-                      (tid == a.G - 1 && pl.group_off[a.G] != a.B)))
-        pl.ok = 0;
-    __syncthreads();
+    const bool groups_ok = __syncthreads_and(tid >= a.G || (pl.group_off[tid] <= pl.group_off[tid + 1] && (tid > 0 || pl.group_off[0] == 0) &&
+                                                            (tid < a.G - 1 || pl.group_off[a.G] == a.B)));
     SEntry n{};
     n.group = -1;
     int code = SDV_OK;
@@ -113,7 +116,7 @@ __device__ __forceinline__ void shared_plan(const SharedArgs &a, SPlan &pl, bool
                 code = SDV_ERR_CAPACITY;
             } else if (a.G) {
                 code = SDV_ERR_ARG;
-                if (pl.ok) {
+                if (groups_ok) {
                     const int g = shared_last(pl.group_off, a.G, b);
                     const int first = pl.row_off[pl.group_off[g]], last = pl.row_off[pl.group_off[g + 1]];
                     n.kv0 = pl.prefix[g];
@@ -136,7 +139,7 @@ __device__ __forceinline__ void shared_plan(const SharedArgs &a, SPlan &pl, bool
         n.min_hi = n.p0 + 1;
     }
     __syncthreads();
-    if (tid < a.G && pl.ok && pl.g_min[tid] <= pl.g_max[tid]) {  // some row of the group is read
+    if (tid < a.G && groups_ok && pl.g_min[tid] <= pl.g_max[tid]) {  // some row of the group is read
         n.p0 = -1;
         n.b = pl.group_off[tid];
         n.r0 = pl.row_off[n.b];
@@ -149,35 +152,71 @@ __device__ __forceinline__ void shared_plan(const SharedArgs &a, SPlan &pl, bool
     n.c0 = n.lo / kSKeys;
     n.nc = n.rows && n.lo < n.kv1 ? (n.kv1 + kSKeys - 1) / kSKeys - n.c0 : 0;
     n.wc = n.rows * a.grp > kSTile / 2 ? 2 : 1;
-    const int tiles = n.nc ? a.nkv * shared_tiles(a, n) : 0, steps = tiles * n.nc * n.wc;
-    const int all_steps = __reduce_add_sync(0xffffffffu, steps), all_tiles = __reduce_add_sync(0xffffffffu, tiles);
-    if (lane == 0 && all_steps) {
-        atomicAdd(&pl.steps, all_steps);
-        atomicAdd(&pl.tiles, all_tiles);
-    }
-    __syncthreads();
-    // with a chunk for each CTA at most, the cut is one a chunk
-    const int ov = pl.steps <= a.ctas ? 0 : kSOverhead, cost = steps + ov * tiles;
-    int sum = cost;
+    const int tiles = n.nc ? a.nkv * shared_tiles(a, n) : 0, one = n.nc * n.wc, steps = tiles * one;
+    // sums over the entries before this one, of costs and of tiles
+    int sum = steps, count = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+        const int v = __shfl_up_sync(0xffffffffu, sum, o), u = __shfl_up_sync(0xffffffffu, count, o);
+        if (lane >= o) sum += v, count += u;
     }
-    if (lane == 31) pl.warp_sum[warp] = sum;
+    if (lane == 31) pl.warp_sum[warp] = make_int2(sum, count);
+    pl.e[tid].nc = one, pl.e[tid].rows = tiles;  // for a moment: cost of a tile, tiles
     __syncthreads();
-    int before = lane < warp ? pl.warp_sum[lane] : 0;
-    before = __reduce_add_sync(0xffffffffu, before);
-    n.end = before + sum;
-    n.start = n.end - cost;
-    n.per = ov + n.nc * n.wc;
-    const int q = max(1, (pl.steps + ov * pl.tiles + a.ctas - 1) / a.ctas);
+    int2 all = make_int2(0, 0), before = make_int2(0, 0);
+#pragma unroll
+    for (int w = 0; w < kSThreads / 32; ++w) {
+        const int2 v = pl.warp_sum[w];
+        all.x += v.x, all.y += v.y;
+        if (w < warp) before.x += v.x, before.y += v.y;
+    }
+    int ov = kSOverhead, cost = steps + ov * tiles, per = ov + one, total = all.x + ov * all.y;
+    int end = before.x + sum + ov * (before.y + count), q = max(1, (total + a.ctas - 1) / a.ctas);
+    if (all.y <= a.ctas && all.y > 0) {  // pieces of one tile each: a warp tries a length
+        const int tried = (all.x + a.ctas - 1) / a.ctas + warp;
+        int pieces = 0;
+        for (int e = lane; e < a.G + a.B; e += 32) pieces += pl.e[e].rows * ((pl.e[e].nc + tried - 1) / tried);
+        pieces = __reduce_add_sync(0xffffffffu, pieces);
+        if (lane == 0 && pieces <= a.ctas) atomicMin(&pl.best, tried);
+        __syncthreads();
+        if (pl.best <= q + 2) {
+            q = pl.best;
+            ov = 0;
+            per = (one + q - 1) / q * q;  // every tile begins with a CTA
+            cost = sum = tiles * per;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (lane == 31) pl.warp_sum[warp].x = sum;
+            __syncthreads();
+            total = 0;
+            end = sum;
+#pragma unroll
+            for (int w = 0; w < kSThreads / 32; ++w) {
+                const int v = pl.warp_sum[w].x;
+                total += v;
+                if (w < warp) end += v;
+            }
+        }
+    }
+    n.end = end;
+    n.start = end - cost;
+    n.per = per;
     pl.e[tid] = n;
-    if (tid == 0) pl.total = pl.steps + ov * pl.tiles, pl.ov = ov, pl.q = q;
+    if (tid == 0) pl.total = total, pl.ov = ov, pl.q = q;
     __syncthreads();
     if (writes) {
-        if (tid < a.G + a.B) a.plan[tid] = n;
-        if (tid == 0) a.plan_cut[0] = q, a.plan_cut[1] = ov;
+        if (tid < a.G + a.B) {
+            a.plan[tid] = make_int4(n.start, n.per, n.nc, n.wc);
+            a.plan_rows[tid] = make_int2(n.r0, shared_tiles(a, n));
+        }
+        if (tid == kSThreads - 1) {  // as FastDiv::of
+            const int l = q > 1 ? 32 - __clz(q - 1) : 0;
+            *a.by_cut = FastDiv{static_cast<uint32_t>((1ull << (31 + l)) / q + 1), 31 + l};
+            *a.plan_cut = make_int2(q, ov);
+        }
         for (int r = tid; r < a.max_rows; r += kSThreads) {
             const int of = shared_last(pl.row_off, a.B, r);
             const bool in = r >= pl.row_off[of] && r < pl.row_off[of + 1];
@@ -187,9 +226,9 @@ __device__ __forceinline__ void shared_plan(const SharedArgs &a, SPlan &pl, bool
     }
 }
 // First chunk of a tile that begins at or after `rel` on the line, from the tile's start.
-__device__ __forceinline__ int shared_chunk(const SEntry &n, int ov, int rel) {
+__device__ __forceinline__ int shared_chunk(int chunks, int wc, int ov, int rel) {
     if (rel <= 0) return 0;
-    return min(n.nc, rel <= ov + n.wc ? 1 : (rel - ov + n.wc - 1) >> (n.wc - 1));  // wc is 1 or 2
+    return min(chunks, rel <= ov + wc ? 1 : (rel - ov + wc - 1) >> (wc - 1));  // wc is 1 or 2
 }
 // The part of a tile that a CTA does. Each warp steps from one to the next by itself.
 struct SPiece {
@@ -201,8 +240,8 @@ struct SPiece {
 // Takes the tile that p names; false where none of its chunks lies in [x, x1).
 __device__ __forceinline__ bool shared_take(const SharedArgs &a, const SPlan &pl, int x, int x1, SPiece &p) {
     const SEntry &n = pl.e[p.entry];
-    p.c0 = shared_chunk(n, pl.ov, x - p.at);
-    p.n = (x1 >= p.at + n.per ? n.nc : shared_chunk(n, pl.ov, x1 - p.at)) - p.c0;
+    p.c0 = shared_chunk(n.nc, n.wc, pl.ov, x - p.at);
+    p.n = (x1 >= p.at + n.per ? n.nc : shared_chunk(n.nc, n.wc, pl.ov, x1 - p.at)) - p.c0;
     p.rows = min(kSTile, n.rows * a.grp - p.tile * kSTile);
     return p.n > 0;
 }
@@ -910,15 +949,15 @@ constexpr int kSMergeThreads = 256;
 // A warp joins the parts of one (row, q head): those of its own tile, then those of the prefix's, CTA by CTA along the line.
 // Rows that one piece holds alone were written by the attention, those of refused spans become NaN.
 template <typename T, int D>
-__global__ void __launch_bounds__(kSMergeThreads) shared_merge_kernel(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(kSMergeThreads, 3) shared_merge_kernel(const __grid_constant__ SharedArgs a) {
     constexpr int V = D / 32;
     const int lane = threadIdx.x % 32, idx = blockIdx.x * (kSMergeThreads / 32) + threadIdx.x / 32;
     pdl_wait();  // in every CTA: this kernel's end stands for the attention's, too
     pdl_trigger();
-    const int row = idx / a.nq, hq = idx - row * a.nq, h = a.by_grp.div(hq);
+    const int row = a.by_nq.div(idx), hq = idx - row * a.nq, h = a.by_grp.div(hq);
     if (row >= a.max_rows) return;
-    const int2 of = a.row_entry[row];
-    const int q = a.plan_cut[0], ov = a.plan_cut[1];
+    const int2 of = a.row_entry[row], cut = *a.plan_cut;
+    const FastDiv by_cut = *a.by_cut;
     if (of.x == kRowNone) return;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + hq * D + lane * V;
     if (of.x == kRowRefused) {
@@ -926,33 +965,42 @@ __global__ void __launch_bounds__(kSMergeThreads) shared_merge_kernel(const __gr
         for (int d = 0; d < V; ++d) out[d] = from_f32<T>(NAN);
         return;
     }
-    const SEntry own = a.plan[of.x], pre = of.y >= 0 ? a.plan[of.y] : SEntry{};
-    // a tile's start on the line, the CTA it begins in and the number of those it touches
-    auto tile_of = [&](const SEntry &n, int &tile, int &r, int &at, int &i0) {
-        const int m = (row - n.r0) * a.grp + hq - h * a.grp;
-        tile = m / kSTile;
-        r = m - tile * kSTile;
-        at = n.start + (h * shared_tiles(a, n) + tile) * n.per;
-        i0 = at / q;
-        return n.nc ? (at + n.per - 1) / q - i0 + 1 : 0;
-    };
-    int tile[2], r[2], at[2], i0[2];
-    const int n_own = tile_of(own, tile[0], r[0], at[0], i0[0]), n_pre = pre.nc ? tile_of(pre, tile[1], r[1], at[1], i0[1]) : 0;
+    // of the row's own tile and of the prefix's: start on the line, the CTA that it begins in and the number of those it
+    // touches, and the row's place in the partial results that begin with the tile, and in those of a CTA
+    int4 e[2];
+    int at[2], i0[2], n[2], r[2];
+    long long slot0[2];
+    const long long side = static_cast<long long>(a.nkv) * a.part_rows;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        n[k] = 0;
+        const int at_entry = k ? of.y : of.x;
+        if (at_entry < 0) continue;
+        e[k] = a.plan[at_entry];
+        const int2 rows = a.plan_rows[at_entry];
+        const int m = (row - rows.x) * a.grp + hq - h * a.grp, tile = m / kSTile;
+        r[k] = m - tile * kSTile;
+        slot0[k] = k * side + static_cast<long long>(h) * a.part_rows + rows.x * a.grp + m;
+        at[k] = e[k].x + (h * rows.y + tile) * e[k].y;
+        i0[k] = by_cut.div(at[k]);
+        n[k] = by_cut.div(at[k] + e[k].y - 1) - i0[k] + 1;
+    }
+    const int n_own = n[0], n_pre = n[1];
     // row of part k in the partial results, -1 where that CTA has no chunk of the tile
     auto part = [&](int k) -> long long {
         if (k >= n_own + n_pre) return -1;
-        const bool of = k >= n_own;
-        const SEntry &n = of ? pre : own;
-        const int i = (of ? i0[1] + k - n_own : i0[0] + k), rel = i * q - (of ? at[1] : at[0]);
-        const int from = shared_chunk(n, ov, rel), stop = rel + q >= n.per ? n.nc : shared_chunk(n, ov, rel + q);
+        const bool p = k >= n_own;
+        const int4 t = p ? e[1] : e[0];
+        const int i = p ? i0[1] + k - n_own : i0[0] + k, rel = i * cut.x - (p ? at[1] : at[0]);
+        const int from = shared_chunk(t.z, t.w, cut.y, rel), stop = rel + cut.x >= t.y ? t.z : shared_chunk(t.z, t.w, cut.y, rel + cut.x);
         if (stop <= from) return -1;
-        return shared_slot(a, of, n.r0, h, of ? tile[1] : tile[0], from > 0 ? i : -1) + (of ? r[1] : r[0]);
+        return from > 0 ? 2 * side + static_cast<long long>(i) * kSTile + (p ? r[1] : r[0]) : p ? slot0[1] : slot0[0];
     };
     const int count = n_own + n_pre;
     long long slot = part(lane);
     if (n_pre == 0 && n_own <= 32 && __popc(__ballot_sync(0xffffffffu, slot >= 0)) == 1) return;  // written already
-    // sixteen parts' values on their way at once, the first beside their maxima
-    constexpr int N = 16;
+    // eight parts' values on their way at once, the first beside their maxima
+    constexpr int N = 8;
     float v[N][V];
     auto ask = [&](int p0) {
 #pragma unroll
