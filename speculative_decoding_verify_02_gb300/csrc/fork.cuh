@@ -11,7 +11,7 @@
 namespace sdv {
 
 constexpr int kForkMost = 256;     // forks of a call: max_batch at most
-constexpr int kForkThreads = 1024;
+constexpr int kForkThreads = kForkMost;
 constexpr int kCopyThreads = 256;
 constexpr int kForkIndexBlocks = 8;  // CTAs that copy a sequence's n-gram index
 
@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs p) {
     pdl_trigger();
     pdl_wait();
     DevState &s = p.s;
-    __shared__ int taken[kForkMost], from[kForkMost], full_s[kForkMost], warp_sum[kForkThreads / 32], ok_s, added;
+    __shared__ int taken[kForkMost], warp_sum[kForkThreads / 32], ok_s, added;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid < kForkMost) taken[tid] = 0;
     if (tid == 0) ok_s = SDV_OK, added = 0;
@@ -69,8 +69,6 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs p) {
         return;
     }
     if (mine) {
-        from[tid] = src;
-        full_s[tid] = full;
         int page = -1;
         if (need) {
             page = s.free_stack[top - 1 - at];
@@ -85,28 +83,16 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs p) {
         s.budget[dst] = s.budget[src];
         s.kcur[dst] = s.kcur[src];
         atomicAdd(&added, full);
-        taken[tid] = dst;
     }
     __syncthreads();
     if (tid == 0) {
         *s.free_top = top - total;
         *s.n_extra += added;
     }
-    // the whole pages: a warp a fork
-    for (int i = warp; i < p.n; i += kForkThreads / 32) {
-        const int *have = s.page_table + static_cast<size_t>(from[i]) * s.pages_per_seq;
-        int *get = s.page_table + static_cast<size_t>(taken[i]) * s.pages_per_seq;
-#pragma unroll 4
-        for (int j = lane; j < full_s[i]; j += 32) {
-            const int page = have[j];
-            get[j] = page;
-            atomicAdd(&s.extra[page], 1);
-        }
-    }
 }
 
-// The filled slots of the partial pages: CTA (fork, layer), and behind the layers the CTAs that copy the n-gram index. Bound by
-// launch and latency for a few forks, else by memory.
+// The filled slots of the partial pages: CTA (fork, layer), a warp a head; behind the layers a CTA for the whole pages' entries and
+// those that copy the n-gram index. Bound by launch and latency for a few forks, else by memory.
 __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(ForkArgs p) {
     pdl_trigger();
     pdl_wait();
@@ -117,21 +103,30 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(ForkArgs p) {
     if (layer < p.n_layers) {
         if (c.z == 0 || c.x < 0 || c.x >= s.n_pages_total) return;
         const size_t page = static_cast<size_t>(2) * p.nkv * s.page_size * p.D;
-        const int row = p.D / 8, run = c.z * row, whole = s.page_size * row;  // 16-byte pieces: of a slot, filled, of a head
+        const int row = p.D / 8, run = c.z * row;  // 16-byte pieces of a slot, and filled ones of a head
+        const size_t whole = static_cast<size_t>(s.page_size) * row;
         const uint4 *from = reinterpret_cast<const uint4 *>(p.pool + layer * p.layer_stride + c.x * page);
         uint4 *to = reinterpret_cast<uint4 *>(p.pool + layer * p.layer_stride + c.y * page);
-        const long long all = static_cast<long long>(2) * p.nkv * run;
+        for (int head = tid / 32; head < 2 * p.nkv; head += kCopyThreads / 32)
 #pragma unroll 4
-        for (long long i = tid; i < all; i += kCopyThreads) {
-            const int head = static_cast<int>(i / run);
-            const size_t at = static_cast<size_t>(head) * whole + (i - static_cast<long long>(head) * run);
-            to[at] = from[at];
-        }
+            for (int i = tid % 32; i < run; i += 32) to[head * whole + i] = from[head * whole + i];
         return;
     }
     const int src = p.src[blockIdx.x], dst = p.dst[blockIdx.x];
+    if (layer == p.n_layers) {
+        const int *have = s.page_table + static_cast<size_t>(src) * s.pages_per_seq;
+        int *get = s.page_table + static_cast<size_t>(dst) * s.pages_per_seq;
+        const int full = s.seq_len[dst] / s.page_size;
+#pragma unroll 4
+        for (int j = tid; j < full; j += kCopyThreads) {
+            const int held = have[j];
+            get[j] = held;
+            atomicAdd(&s.extra[held], 1);
+        }
+        return;
+    }
     const size_t slots = static_cast<size_t>(s.ng_orders) * s.ng_slots;
-    const int first = (layer - p.n_layers) * kCopyThreads + tid, step = kForkIndexBlocks * kCopyThreads;
+    const int first = (layer - p.n_layers - 1) * kCopyThreads + tid, step = kForkIndexBlocks * kCopyThreads;
     for (size_t i = first; i < slots; i += step) {
         s.ng_keys[dst * slots + i] = s.ng_keys[src * slots + i];
         s.ng_vals[dst * slots + i] = s.ng_vals[src * slots + i];

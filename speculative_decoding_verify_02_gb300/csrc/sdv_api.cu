@@ -1091,7 +1091,7 @@ int sdv_fork_seq(sdv_ctx *ctx, const int32_t *d_src, const int32_t *d_dst, int n
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch(ctx, fork_kernel, dim3(1), dim3(kForkThreads), 0, st, p);
     if (e == cudaSuccess)
-        e = launch(ctx, fork_copy_kernel, dim3(n, p.n_layers + (ctx->ng_slots ? kForkIndexBlocks : 0)), dim3(kCopyThreads), 0, st, p);
+        e = launch(ctx, fork_copy_kernel, dim3(n, p.n_layers + 1 + (ctx->ng_slots ? kForkIndexBlocks : 0)), dim3(kCopyThreads), 0, st, p);
     if (e == cudaSuccess) ctx->forked = true;
     return rc(e);
 }

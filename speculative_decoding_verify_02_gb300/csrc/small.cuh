@@ -278,34 +278,40 @@ __global__ void ensure_kernel(DevState s, const int *required, int B) {
 // Releases the last rel[b] pages of each sequence while pages are shared, in the order of a rewind: b = B-1 down to 0, highest
 // slot first. A page's count of other holders falls by one for each that lets go; below zero nobody holds it any more, and the
 // lowest b that let go gives it back. `off` is scratch. (A thread a slot, going through the sequences: 68 us for 60 sequences
-// of 255 pages; now 46.)
+// of up to 255 pages; 13 now.)
 __device__ __forceinline__ void release_shared(const DevState &s, const int *rel, int *off, int B, int top) {
     constexpr int kOwner = 257;  // a page that b gives back holds b - kOwner meanwhile
-    __shared__ int held[256], let_go, most;
-    const int tid = threadIdx.x, threads = blockDim.x, lane = tid % 32;
-    if (tid == 0) let_go = most = 0;
-    __syncthreads();
+    __shared__ int held[256], let_go;
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid % 32, warps = threads / 32;
+    if (tid == 0) let_go = 0;
     for (int b = tid; b < B; b += threads) {
         held[b] = s.n_pages[b];
         off[b] = 0;
-        if (rel[b] > 0) atomicMax(&most, rel[b]);
     }
     __syncthreads();
-    const int wide = (most + 31) / 32 * 32, all = B * wide;  // (sequence, page from its end)
-    auto each = [&](auto f) {
-#pragma unroll 4
-        for (int i = tid; i < all; i += threads) {
-            const int b = i / wide, j = i - b * wide;
-            if (j < rel[b]) f(b, s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1 - j);
+    // a team of warps a sequence, from its last page, eight entries and counts of a thread on their way at once
+    const int team = max(1, warps / B), first = tid / 32 / team, member = tid / 32 - first * team;
+    auto each = [&](bool counts, auto f) {
+        for (int b = first; b < B; b += warps / team) {
+            int *end = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1;
+            for (int j0 = member * 256 + lane; j0 < rel[b]; j0 += team * 256) {
+                int page[8], extra[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) page[u] = j0 + 32 * u < rel[b] ? end[-j0 - 32 * u] : -1;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) extra[u] = counts && page[u] >= 0 ? __ldcg(&s.extra[page[u]]) : 0;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (page[u] >= 0) f(b, end - j0 - 32 * u, page[u], extra[u]);
+            }
         }
         __syncthreads();
     };
-    each([&](int, int *entry) { atomicSub(&s.extra[*entry], 1); });
-    each([&](int b, int *entry) {
-        if (*reinterpret_cast<volatile int *>(&s.extra[*entry]) < 0) atomicMin(&s.extra[*entry], b - kOwner);
+    each(false, [&](int, int *, int page, int) { atomicSub(&s.extra[page], 1); });
+    each(true, [&](int b, int *, int page, int extra) {
+        if (extra < 0) atomicMin(&s.extra[page], b - kOwner);
     });
-    each([&](int b, int *entry) {
-        const int extra = *reinterpret_cast<volatile int *>(&s.extra[*entry]);
+    each(true, [&](int b, int *entry, int, int extra) {
         if (extra == b - kOwner) {
             atomicAdd(&off[b], 1);
         } else {
@@ -313,29 +319,42 @@ __device__ __forceinline__ void release_shared(const DevState &s, const int *rel
             atomicAdd(&let_go, 1);
         }
     });
-    if (tid == 0) {
+    if (tid < 32) {  // what the sequences behind each give back
         int total = 0;
-        for (int b = B - 1; b >= 0; --b) {
-            const int n = off[b];
-            off[b] = total;
-            total += n;
+        for (int b0 = B - 1; b0 >= 0; b0 -= 32) {
+            const int b = b0 - lane, mine = b >= 0 ? off[b] : 0;
+            int sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (b >= 0) off[b] = total + sum - mine;
+            total += __shfl_sync(0xffffffffu, sum, 31);
         }
-        *s.free_top = top + total;
-        *s.n_extra -= let_go;
+        if (lane == 0) {
+            *s.free_top = top + total;
+            *s.n_extra -= let_go;
+        }
     }
     __syncthreads();
-    for (int b = tid / 32; b < B; b += threads / 32) {
+    for (int b = tid / 32; b < B; b += warps) {
         int at = top + off[b];
-        for (int j0 = 0; j0 < rel[b]; j0 += 32) {
-            int *entry = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1 - j0 - lane;
-            const int page = j0 + lane < rel[b] ? *entry : -1;
-            const uint32_t back = __ballot_sync(0xffffffffu, page >= 0);
-            if (page >= 0) {
-                s.free_stack[at + __popc(back & ((1u << lane) - 1))] = page;
-                s.extra[page] = 0;
-                *entry = -1;
+        int *end = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1;
+        for (int j0 = lane; j0 - lane < rel[b]; j0 += 256) {
+            int page[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) page[u] = j0 + 32 * u < rel[b] ? end[-j0 - 32 * u] : -1;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t back = __ballot_sync(0xffffffffu, page[u] >= 0);
+                if (page[u] >= 0) {
+                    s.free_stack[at + __popc(back & ((1u << lane) - 1))] = page[u];
+                    s.extra[page[u]] = 0;
+                    end[-j0 - 32 * u] = -1;
+                }
+                at += __popc(back);
             }
-            at += __popc(back);
         }
         if (lane == 0) s.n_pages[b] = held[b] - rel[b];
     }
@@ -344,61 +363,58 @@ __device__ __forceinline__ void release_shared(const DevState &s, const int *rel
 __global__ void rewind_kernel(DevState s, const int *length, int B) {
     pdl_trigger();
     pdl_wait();
-    __shared__ int rel_s[256], off_s[256], ok_s, top_s, shared_s;
-    if (threadIdx.x == 0) {
-        int ok = 1;
-        const int shared = *s.n_extra;
-        shared_s = shared;
-        for (int b = 0; b < B; ++b) {
-            const int len = length[b];
-            rel_s[b] = 0;
-            if (len < 0) continue;
-            if (len > s.seq_len[b]) {
-                ok = 0;
-                continue;
-            }
+    __shared__ int rel_s[256], off_s[256], warp_sum[8];
+    // a thread a sequence, from the last one down (by one thread, one after the other, 64 of them took 40 us)
+    const int tid = threadIdx.x, lane = tid % 32, b = B - 1 - tid, shared = *s.n_extra, top = *s.free_top;
+    bool ok = true;
+    int rel = 0;
+    if (b >= 0) {
+        const int len = length[b], have = s.seq_len[b], n = s.n_pages[b];
+        if (len >= 0) {
+            ok = len <= have;
             // sliding-window rings keep only what the last forward evicted
-            if (s.swa_window > 0 && len < s.seq_base[b] && s.seq_len[b] > s.swa_window) {
-                ok = 0;
-                continue;
-            }
+            if (s.swa_window > 0 && len < s.seq_base[b] && have > s.swa_window) ok = false;
             const int keep = (len + s.page_size - 1) / s.page_size;
             // rows that will be written from there on must not lie in a page that others hold, too
-            if (shared > 0 && len < s.seq_len[b] && len % s.page_size &&
-                s.extra[s.page_table[static_cast<size_t>(b) * s.pages_per_seq + keep - 1]] > 0) {
-                ok = 0;
-                continue;
-            }
-            rel_s[b] = max(0, s.n_pages[b] - keep);
+            if (ok && shared > 0 && len < have && len % s.page_size)
+                ok = s.extra[s.page_table[static_cast<size_t>(b) * s.pages_per_seq + keep - 1]] == 0;
+            rel = max(0, n - keep);
         }
-        int total = 0;
-        for (int b = B - 1; b >= 0; --b) {
-            off_s[b] = total;
-            total += rel_s[b];
-        }
-        if (!ok) set_status(s.status, SDV_ERR_ARG);
-        ok_s = ok;
-        top_s = *s.free_top;
-        if (ok && shared == 0) *s.free_top = top_s + total;
+        rel_s[b] = rel;
     }
-    __syncthreads();
-    if (!ok_s) return;
-    if (shared_s > 0) {
-        release_shared(s, rel_s, off_s, B, top_s);
-        for (int b = threadIdx.x; b < B; b += blockDim.x)
-            if (length[b] >= 0) s.seq_len[b] = length[b];
+    const bool all_ok = __syncthreads_and(ok);
+    if (!all_ok) {
+        if (tid == 0) set_status(s.status, SDV_ERR_ARG);
+        return;
+    }
+    if (shared > 0) {
+        release_shared(s, rel_s, off_s, B, top);
+        if (b >= 0 && length[b] >= 0) s.seq_len[b] = length[b];
     } else {
-        for (int b = threadIdx.x; b < B; b += blockDim.x) {
-            const int len = length[b];
-            if (len < 0) continue;
-            const int n = s.n_pages[b];
-            for (int j = 0; j < rel_s[b]; ++j) {
-                const int slot = n - 1 - j;
-                s.free_stack[top_s + off_s[b] + j] = s.page_table[b * s.pages_per_seq + slot];
-                s.page_table[b * s.pages_per_seq + slot] = -1;
+        int sum = rel;  // pages that this sequence and those behind it release
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31 && tid < 256) warp_sum[tid / 32] = sum;
+        __syncthreads();
+        for (int w = 0; w < min(tid / 32, 8); ++w) sum += warp_sum[w];
+        if (b >= 0) off_s[b] = sum - rel;
+        if (b == 0) *s.free_top = top + sum;
+        __syncthreads();
+        for (int q = tid / 32; q < B; q += blockDim.x / 32) {
+            const int n = s.n_pages[q];
+            int *last = s.page_table + static_cast<size_t>(q) * s.pages_per_seq + n - 1;
+            for (int j = lane; j < rel_s[q]; j += 32) {
+                s.free_stack[top + off_s[q] + j] = last[-j];
+                last[-j] = -1;
             }
-            s.n_pages[b] = n - rel_s[b];
-            s.seq_len[b] = len;
+        }
+        __syncthreads();
+        if (b >= 0 && length[b] >= 0) {
+            s.n_pages[b] -= rel;
+            s.seq_len[b] = length[b];
         }
     }
     // rows of the last forward kept (the rest are restored in the sliding-window rings)
