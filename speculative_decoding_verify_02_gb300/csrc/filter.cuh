@@ -11,7 +11,7 @@
 // Whether a token is kept is decided as exact arithmetic would: sums of fp32 weights hold to 2^-17 of the total each
 // (kFilterNear); a border nearer than that is decided on weights of 2^-39 (weight_exact). Sums are integers, units of 2^-44,
 // whose order does not matter; 64-bit floats stay out of the way of most rows: this part does them at 1/64 of fp32's rate, and
-// the first kernel, which used them for sums and settings, took 75,000 clocks a row where it is 30,000 now.
+// the first kernel, which used them for sums and settings, took 75,000 clocks a row where it is 26,000 now.
 #pragma once
 
 #include <float.h>
@@ -33,7 +33,7 @@ constexpr int kFilterMost = 49152;               // tokens of a CTA at most (192
 constexpr int kFilterNear = 15;  // 2^-15
 
 // 2^(58 - j / 64)
-__constant__ unsigned long long kFilterTable[64] = {
+__device__ const unsigned long long kFilterTable[64] = {
     0x400000000000000ull, 0x3f4f83033d21b06ull, 0x3ea0ecb6dc8a80dull, 0x3df437dcc2b44efull,
     0x3d495f454921b31ull, 0x3ca05dcf167fec5ull, 0x3bf92e66f736bd7ull, 0x3b53cc07b6650aeull,
     0x3ab031b9f7490e5ull, 0x3a0e5a940f12f72ull, 0x396e41b9df20d23ull, 0x38cfe25cafa2969ull,
@@ -115,14 +115,18 @@ struct FilterShared {
     unsigned long long list[kFilterList];            // CTA 0's: keys, or the border's tokens' keys and then their weights
     uint16_t pick[kFilterList];                      // tokens of this CTA for the list, places in its chunk
     unsigned long long cut, scan_e[kFilterThreads / 32];
-    unsigned long long mass;
-    uint32_t n_cand, n_pick, scan[kFilterThreads / 32], ambiguous, kept;
+    unsigned long long target, table[64];     // table: kFilterTable's
+    uint32_t n_cand, n_pick, scan[kFilterThreads / 32], warp_sum[kFilterThreads / 32], ambiguous, kept;
     float scan_w[kFilterThreads / 32], about, about_all;
     int found[3], seq, fails;
 };
 
 __device__ __forceinline__ unsigned long long filter_key(float x, int v) {  // -0 and 0 are equal
     return static_cast<unsigned long long>(orderable(x + 0.f)) << 32 | static_cast<uint32_t>(~v);
+}
+
+__device__ __forceinline__ float filter_value(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
 // A row's constants.
@@ -136,7 +140,7 @@ __device__ __forceinline__ float filter_weight(const FilterRow &r, float x) {
 }
 // The weight as an integer times 2^-58, to 2^-39: the exponent in two fp32 parts, 2^-n/64 from a table and the rest, below
 // 2^-7, by the series of e^z in two parts.
-__device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, float x) {
+__device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, float x, const unsigned long long *table) {
     if (x == r.m) return 1ull << 58;
     const float s = r.m - x, bb = s - r.m, e = (r.m - (s - bb)) - (x + bb);  // s + e = m - x
     const float p = s * r.c_hi;
@@ -147,11 +151,14 @@ __device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, f
     constexpr float L = -0.693147182f, L_lo = 1.90465421e-9f;                // L + L_lo = -ln 2
     const float u = f * L, u_lo = fmaf(f, L, -u) + (f * L_lo + q * L);       // z = u + u_lo
     const float g = u_lo + u * u * (0.5f + u * (0.16666667f + u * 0.041666668f));  // e^z - 1 = u + g
-    const unsigned long long t58 = kFilterTable[n & 63];
-    const float t_hi = __ull2float_rn(t58), tf = t_hi * 0x1p-58f;
-    const float tl = __ll2float_rn(static_cast<long long>(t58) - __float2ll_rn(t_hi)) * 0x1p-58f;
+    const unsigned long long t58 = table[n & 63];
+    const uint32_t t_hi = static_cast<uint32_t>(t58 >> 35), t_lo = static_cast<uint32_t>(t58 >> 3);  // 24 bits, 32 more
+    const float tf = __uint2float_rn(t_hi) * 0x1p-23f, tl = __uint2float_rn(t_lo) * 0x1p-55f;
     const float a = tf * u, b = fmaf(tf, u, -a) + (tf * g + tl * u);         // t (e^z - 1)
-    const long long w = static_cast<long long>(t58) + __float2ll_rn(a * 0x1p58f) + __float2ll_rn(b * 0x1p58f);
+    // as integers by 32-bit conversions, 64-bit ones being as slow as 64-bit floats: |a| < 2^-7, |b| < 2^-15
+    const float a37 = a * 0x1p37f;
+    const int a_hi = __float2int_rn(a37), a_lo = __float2int_rn((a37 - __int2float_rn(a_hi)) * 0x1p21f), b46 = __float2int_rn(b * 0x1p45f);
+    const long long w = static_cast<long long>(t58) + (static_cast<long long>(a_hi) << 21) + a_lo + (static_cast<long long>(b46) << 13);
     return static_cast<unsigned long long>(w) >> (n >> 6);
 }
 
@@ -213,6 +220,82 @@ __device__ __forceinline__ void filter_sync(int ctas) {
         __syncthreads();
 }
 
+// CTA 0's list in order, the largest key first: key[u] of a thread is the list's tid + u threads, `top` the largest of all.
+// Each goes to its bin between the largest logit and the list's smallest, and to its place among the bin's, which are a few;
+// bins are even over the square of the distance, as logits crowd at the list's end.
+// Where some bin holds more than kFilterFew (nearly all logits equal, or one far above the others) a bitonic network sorts.
+// 890 of a row's tokens take 5,700 clocks, by the network 22,000: 55 passes through shared memory, a barrier behind each.
+__device__ __forceinline__ void filter_sort(FilterShared &sh, const unsigned long long *key, int n, unsigned long long top) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    constexpr int PER = kFilterList / kFilterThreads;
+    for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = 0;
+    uint32_t least = 0xffffffffu;
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+        if (tid + u * kFilterThreads < n) least = min(least, static_cast<uint32_t>(key[u] >> 32));
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) sh.scan[warp] = least;
+    __syncthreads();
+    for (int i = 0; i < kFilterThreads / 32; ++i) least = min(least, sh.scan[i]);
+    const float m = filter_value(static_cast<uint32_t>(top >> 32)), range = m - filter_value(least);
+    const float scale = 1.f / range;  // no number where range is infinite or zero: bin 0
+    int bin[PER], at[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        if (tid + u * kFilterThreads >= n) continue;
+        const float t = (m - filter_value(static_cast<uint32_t>(key[u] >> 32))) * scale;  // monotone, rounded or not
+        bin[u] = t > 0.f ? static_cast<int>(fminf(kFilterBins * (t * t), kFilterBins - 1.f)) : 0;
+        at[u] = static_cast<int>(atomicAdd(&sh.hist[bin[u]], 1u));
+    }
+    __syncthreads();
+    const uint32_t n0 = sh.hist[2 * tid], n1 = sh.hist[2 * tid + 1];
+    uint32_t sum = n0 + n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) sh.warp_sum[warp] = sum;
+    const bool network = __syncthreads_or(max(n0, n1) > kFilterFew);
+    for (int i = 0; i < warp; ++i) sum += sh.warp_sum[i];
+    sh.total[2 * tid] = sum - n1 - n0;
+    sh.total[2 * tid + 1] = sum - n1;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+        if (tid + u * kFilterThreads < n) sh.list[sh.total[bin[u]] + at[u]] = key[u];
+    if (network) {
+        int size = 32;
+        while (size < n) size *= 2;
+        for (int i = n + tid; i < size; i += kFilterThreads) sh.list[i] = 0;
+        __syncthreads();
+        for (int k = 2; k <= size; k *= 2)
+            for (int j = k / 2; j > 0; j /= 2) {
+                for (int i = tid; i < size / 2; i += kFilterThreads) {
+                    const int p = 2 * i - (i & (j - 1)), q = p + j;
+                    const unsigned long long u = sh.list[p], v = sh.list[q];
+                    if ((u < v) == ((p & k) == 0)) sh.list[p] = v, sh.list[q] = u;
+                }
+                __syncthreads();
+            }
+        return;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        if (tid + u * kFilterThreads >= n) continue;
+        const int first = static_cast<int>(sh.total[bin[u]]), end = first + static_cast<int>(sh.hist[bin[u]]);
+        at[u] = first;
+#pragma unroll 8
+        for (int i = first; i < end; ++i) at[u] += sh.list[i] > key[u];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+        if (tid + u * kFilterThreads < n) sh.list[at[u]] = key[u];
+    __syncthreads();
+}
+
 // What a search looks for: the last token with fewer than `k` before it and, if by_mass, less than `target` of weight before it.
 struct FilterGoal {
     bool by_mass;
@@ -233,16 +316,13 @@ __device__ __forceinline__ unsigned long long filter_share(float p, unsigned lon
     return (hi << (64 - s) | lo >> s) + ((lo & ((1ull << s) - 1)) != 0);
 }
 
-__device__ __forceinline__ float filter_value(uint32_t key) {
-    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-}
-
 template <bool SAMPLE>
 __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_constant__ FilterArgs a) {
     extern __shared__ __align__(16) float x_s[];
     __shared__ FilterShared sh;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
     const int v0 = rank * a.chunk, n = max(0, min(a.chunk, a.vocab - v0)), n4 = (n + 3) / 4;
+    if (tid < 64) sh.table[tid] = kFilterTable[tid];
     if (tid == 0) sh.seq = -1, sh.n_cand = sh.n_pick = 0;
     pdl_wait();
     pdl_trigger();
@@ -314,9 +394,18 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
     unsigned long long cut = 0;  // the kept set: keys at or above it
     int kept = valid;
     float *out = SAMPLE ? nullptr : a.out + row * a.out_stride + v0;
+    const bool vec = !SAMPLE && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    auto fill = [&](float *to, int n) {
+        const float4 nil = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (vec) {
+            for (int i = tid; i < n / 4; i += kFilterThreads) reinterpret_cast<float4 *>(to)[i] = nil;
+            if (tid < n % 4) to[(n & ~3) + tid] = -INFINITY;
+        } else {
+            for (int i = tid; i < n; i += kFilterThreads) to[i] = -INFINITY;
+        }
+    };
     if (valid == 0) {  // nothing to keep
-        if (!SAMPLE)
-            for (int i = tid; i < n; i += kFilterThreads) out[i] = -INFINITY;
+        if constexpr (!SAMPLE) fill(out, n);
         if (rank == 0 && tid == 0) {
             if (SAMPLE) a.tokens[row] = 0;
             if (a.n_kept) a.n_kept[row] = 0;
@@ -414,7 +503,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 if (!in1(x, i)) return;
                 const bool both = in0(x, i);
                 if (precise) {
-                    const unsigned long long w = weight_exact(r, x) >> 7;  // a thread adds up to 96
+                    const unsigned long long w = weight_exact(r, x, sh.table) >> 7;  // a thread adds up to 96
                     e1 += w;
                     if (both) e0 += w;
                 } else {
@@ -528,7 +617,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                         A = sums([&](float y, int) { return orderable(y + 0.f) > k; }, [&](float y, int) { return orderable(y + 0.f) > k; }).a;
                     }
                     // the first of them with weight enough before it: 2^-58 is 2^-14 of the sums' unit
-                    const unsigned long long w = weight_exact(r, x), lack = g.target > A ? g.target - A : 0;
+                    const unsigned long long w = weight_exact(r, x, sh.table), lack = g.target > A ? g.target - A : 0;
                     const double need = ceil(static_cast<double>(lack) * 0x1p14 / static_cast<double>(w));
                     if (w > 0 && need < want) want = max(1, static_cast<int>(need));
                 }
@@ -574,7 +663,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     const uint32_t at = add_dsmem_u32(counter, 1);
                     if (at < kFilterFew) {
                         st_dsmem_u64(mapa_shared(smem_u32(&sh.list[at]), 0), k);
-                        st_dsmem_u64(mapa_shared(smem_u32(&sh.list[kFilterFew + at]), 0), g.by_mass ? weight_exact(r, x) >> 8 : 0ull);
+                        st_dsmem_u64(mapa_shared(smem_u32(&sh.list[kFilterFew + at]), 0), g.by_mass ? weight_exact(r, x, sh.table) >> 8 : 0ull);
                     }
                 }
             });
@@ -691,6 +780,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             }
             filter_sync(ctas);
             int in_list = 0;
+            unsigned long long key[kFilterList / kFilterThreads];
             if (rank == 0) {  // fetches everybody's
                 int from[kFilterCluster + 1];
                 from[0] = 0;
@@ -698,46 +788,31 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 for (int q = 0; q < kFilterCluster; ++q)
                     from[q + 1] = from[q] + (q < ctas ? static_cast<int>(ld_dsmem_u32(mapa_shared(smem_u32(&sh.n_pick), q))) : 0);
                 in_list = from[kFilterCluster];
-                if (in_list <= kFilterList)
-                    for (int i = tid; i < in_list; i += kFilterThreads) {
-                        int q = 0, first = 0;
 #pragma unroll
-                        for (int u = 1; u < kFilterCluster; ++u)
-                            if (i >= from[u]) q = u, first = from[u];
-                        const uint32_t at = ld_dsmem_u16(mapa_shared(smem_u32(&sh.pick[i - first]), q));
-                        const float x = __uint_as_float(ld_dsmem_u32(mapa_shared(smem_u32(x_s + at), q)));
-                        sh.list[i] = filter_key(x, q * a.chunk + static_cast<int>(at));
-                    }
-                __syncthreads();
-            }
-            const bool fits = in_list > 0 && in_list <= kFilterList;
-            int size = 32;
-            while (size < in_list) size *= 2;
-            if (rank == 0 && fits) {
-                for (int i = in_list + tid; i < size; i += kFilterThreads) sh.list[i] = 0;
-                __syncthreads();
-                if (size <= kFilterFew) {  // largest first: few by their number of larger ones, threads / size threads a token
-                    const int share = kFilterThreads / size, i = tid / share;
-                    const unsigned long long mine = sh.list[i];
-                    int place = 0;
-#pragma unroll 8
-                    for (int q = tid % share; q < in_list; q += share) place += sh.list[q] > mine;
-                    for (int o = share / 2; o > 0; o /= 2) place += __shfl_xor_sync(0xffffffffu, place, o);
-                    __syncthreads();
-                    if (i < in_list && tid % share == 0) sh.list[place] = mine;
-                    __syncthreads();
-                } else {  // more by a bitonic network
-                    for (int k = 2; k <= size; k *= 2)
-                        for (int j = k / 2; j > 0; j /= 2) {
-                            for (int i = tid; i < size / 2; i += kFilterThreads) {
-                                const int p = 2 * i - (i & (j - 1)), q = p + j;
-                                const unsigned long long u = sh.list[p], v = sh.list[q];
-                                if ((u < v) == ((p & k) == 0)) sh.list[p] = v, sh.list[q] = u;
-                            }
-                            __syncthreads();
-                        }
+                for (int u = 0; u < kFilterList / kFilterThreads; ++u) {
+                    const int i = tid + u * kFilterThreads;
+                    key[u] = 0;
+                    if (i >= in_list || in_list > kFilterList) continue;
+                    int q = 0, first = 0;
+#pragma unroll
+                    for (int w = 1; w < kFilterCluster; ++w)
+                        if (i >= from[w]) q = w, first = from[w];
+                    const uint32_t at = ld_dsmem_u16(mapa_shared(smem_u32(&sh.pick[i - first]), q));
+                    const float x = __uint_as_float(ld_dsmem_u32(mapa_shared(smem_u32(x_s + at), q)));
+                    key[u] = filter_key(x, q * a.chunk + static_cast<int>(at));
                 }
             }
+            // what is kept will be few: -inf everywhere, by the others while CTA 0 decides
+            if constexpr (!SAMPLE) {
+                if (ctas == 1) fill(out, n);
+                if (rank > 0) {
+                    fill(out, n);
+                    const int part = (a.chunk / 4 + ctas - 2) / (ctas - 1) * 4, first = (rank - 1) * part;  // of CTA 0's whole chunk
+                    fill(out - v0 + first, max(0, min(part, a.chunk - first)));
+                }
+            }
+            const bool fits = in_list > 0 && in_list <= kFilterList;
+            if (rank == 0 && fits) filter_sort(sh, key, in_list, top);
             for (;;) {
                 if (rank == 0 && !fits) {
                     if (tid < ctas) st_dsmem_u32(mapa_shared(smem_u32(&sh.ambiguous), tid), 2);
@@ -749,7 +824,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
 #pragma unroll
                     for (int u = 0; u < PER; ++u) {
                         const int i = tid * per + u;
-                        w[u] = want_p && u < per && i < in_list ? weight_exact(r, filter_value(static_cast<uint32_t>(sh.list[i] >> 32))) >> 7 : 0ull;
+                        w[u] = want_p && u < per && i < in_list ? weight_exact(r, filter_value(static_cast<uint32_t>(sh.list[i] >> 32)), sh.table) >> 7 : 0ull;
                         sum += w[u];
                     }
                     unsigned long long before = sum;
@@ -759,7 +834,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                         if (lane >= o) before += v;
                     }
                     if (lane == 31) sh.scan_e[warp] = before;
-                    if (tid == 0) sh.fails = in_list, sh.ambiguous = 0, sh.mass = g.total;
+                    if (tid == 0) sh.fails = in_list, sh.ambiguous = 0, sh.target = g.target;
                     __syncthreads();
                     before -= sum;
                     for (int i = 0; i < warp; ++i) before += sh.scan_e[i];
@@ -768,11 +843,12 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
 #pragma unroll
                         for (int u = 0; u < PER; ++u) {
                             upto += w[u];
-                            if (u < per && tid * per + u == g.k - 1) sh.mass = upto >> 7;
+                            if (want_p && u < per && tid * per + u == g.k - 1) sh.target = filter_share(g.p, upto >> 7);
                         }
                         __syncthreads();
                     }
-                    const unsigned long long target = want_p ? filter_share(g.p, sh.mass) : 0;
+                    const unsigned long long target = sh.target;
+                    int fails = in_list;  // this thread's first token that is not kept
 #pragma unroll
                     for (int u = 0; u < PER; ++u) {
                         const int i = tid * per + u;
@@ -780,10 +856,12 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                             const unsigned long long mass = before >> 7;
                             if (want_p && !want_k && !precise && close(mass, g)) sh.ambiguous = 1;
                             if (i >= g.k || (want_p && !(mass < target)) || !strong(filter_value(static_cast<uint32_t>(sh.list[i] >> 32))))
-                                atomicMin(&sh.fails, max(i, 1));
+                                fails = min(fails, max(i, 1));
                             before += w[u];
                         }
                     }
+                    fails = __reduce_min_sync(0xffffffffu, fails);
+                    if (lane == 0 && fails < in_list) atomicMin(&sh.fails, fails);
                     __syncthreads();
                     // the list ends before the border: the search below
                     if (tid == 0 && sh.fails == in_list && in_list < min(valid, g.k)) sh.ambiguous |= 2;
@@ -824,7 +902,6 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
     // ---- what is kept
     if constexpr (!SAMPLE) {
         int count = 0;
-        const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
         // keys as floats: the cut's logit, and of equal ones those up to its token
         const float cut_x = cut ? filter_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
         const int cut_i = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) - v0 : -1;
@@ -844,7 +921,13 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 }
             }
         };
-        if (want_m && !listed)
+        if (listed) {  // -inf is there already
+            for (int i = tid; i < static_cast<int>(sh.n_pick); i += kFilterThreads) {
+                const int at = sh.pick[i];
+                const float x = x_s[at];
+                if (x > cut_x || (x == cut_x && at <= cut_i)) out[at] = x;
+            }
+        } else if (want_m)
             write([&](float x, int i) {
                 const bool yes = (x > cut_x || (x == cut_x && i <= cut_i)) && strong(x);
                 count += yes;
