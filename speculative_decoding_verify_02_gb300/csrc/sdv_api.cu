@@ -1170,22 +1170,19 @@ int sdv_rewind_cache(sdv_ctx *ctx, const int32_t *d_length, int B, void *stream)
 
 int sdv_cache_seq_len(sdv_ctx *ctx, int32_t *d_len, void *stream) {
     if (!ctx || !d_len) return SDV_ERR_ARG;
-    return rc(cudaMemcpyAsync(d_len, ctx->st.seq_len, sizeof(int) * ctx->c.max_batch, cudaMemcpyDeviceToDevice,
-                              static_cast<cudaStream_t>(stream)));
+    CopyArgs p{};
+    p.from[0] = ctx->st.seq_len, p.to[0] = d_len, p.n[0] = ctx->c.max_batch;
+    return rc(launch(ctx, copy_state_kernel, dim3(1), dim3(256), 0, static_cast<cudaStream_t>(stream), p));
 }
 
 int sdv_page_table(sdv_ctx *ctx, int32_t *d_table, int32_t *d_n_pages, int32_t *d_free_top, void *stream) {
     if (!ctx) return SDV_ERR_ARG;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (d_table)
-        e = cudaMemcpyAsync(d_table, ctx->st.page_table, sizeof(int) * ctx->c.max_batch * ctx->pages_per_seq,
-                            cudaMemcpyDeviceToDevice, st);
-    if (e == cudaSuccess && d_n_pages)
-        e = cudaMemcpyAsync(d_n_pages, ctx->st.n_pages, sizeof(int) * ctx->c.max_batch, cudaMemcpyDeviceToDevice, st);
-    if (e == cudaSuccess && d_free_top)
-        e = cudaMemcpyAsync(d_free_top, ctx->st.free_top, sizeof(int), cudaMemcpyDeviceToDevice, st);
-    return rc(e);
+    CopyArgs p{};
+    p.from[0] = ctx->st.page_table, p.to[0] = d_table, p.n[0] = d_table ? ctx->c.max_batch * ctx->pages_per_seq : 0;
+    p.from[1] = ctx->st.n_pages, p.to[1] = d_n_pages, p.n[1] = d_n_pages ? ctx->c.max_batch : 0;
+    p.from[2] = ctx->st.free_top, p.to[2] = d_free_top, p.n[2] = d_free_top ? 1 : 0;
+    const int blocks = std::min(64, std::max(1, ceil_div(p.n[0], 1024)));
+    return rc(launch(ctx, copy_state_kernel, dim3(blocks), dim3(256), 0, static_cast<cudaStream_t>(stream), p));
 }
 
 int sdv_ngram_commit(sdv_ctx *ctx, const int32_t *d_tokens, const int32_t *d_counts, int B, int stride,

@@ -7,6 +7,16 @@
 //
 // A score is z = cap tanh(q.k / (sqrt(D) cap)) - slope_h (pos - t) for key t <= pos (no cap: q.k / sqrt(D)), within the
 // window if there is one.
+//
+// What bounds it (bf16, 32 heads on 8 of 128 dims; pages of 16; the whole call in a graph):
+//   16 x 8 rows after 32,768 shared keys  81 us, 850 TFLOP/s: the tensor cores, 85 % of the time of its products. Those with V
+//                                         are twice the scores', as p enters in two 16-bit planes
+//   64 sequences of one row after them, up to 512 keys of their own   66 us, 3.1 TB/s: half the time is the sequences' own tiles,
+//                                         64 x 8 of 4 rows, 7,000 clocks each from queries to results
+//   8 x 8 rows after 848 shared keys      18 us: latency, of the plan (4,500 clocks), of the first loads and of code that no
+//                                         cache holds, of the join (4 us)
+// Why two planes: one leaves p a relative error of 2^-9, which the sum over alike keys keeps; the result then is up to twice as far off
+// as its own rounding. With two that rounding is all of the error.
 #pragma once
 
 #include "qcache_attention.cuh"
@@ -367,7 +377,7 @@ __device__ __forceinline__ void load_box_at(uint32_t dst, const CUtensorMap *tm,
         : "memory");
 }
 
-// Two probabilities as a pair of 16-bit planes, each two to a word: p = hi + lo to 2^-17 (bf16) or 2^-23 (fp16).
+// Two probabilities, rounded to a pair of 16-bit planes, each two to a word: p = hi + lo to 2^-17 (bf16) or 2^-23 (fp16).
 template <typename T>
 __device__ __forceinline__ void split_p(float2 p, uint32_t &hi, uint32_t &lo) {
     if constexpr (__is_same(T, bf16)) {
@@ -438,7 +448,8 @@ struct STile {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 // ------------------------------------------------------------------ attention
-// One CTA an SM; a piece of the line after another. EXTRA: scores with a cap or a bias.
+// One CTA an SM; a piece of the line after another. EXTRA: scores with a cap or a bias, which take an exponential and a reciprocal
+// more each (a batch of 16 with a cap, 33 rows a tile and fewer: 53 us, 2.9 TB/s, bound by those of the one warp that has rows).
 template <typename T, int D, bool EXTRA>
 __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_constant__ CUtensorMap pool,
                                                                    const __grid_constant__ SharedArgs a) {
@@ -571,8 +582,8 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
         // ---- MMA issue, a warp for each softmax warpgroup: for its own 128 rows of a tile of more than 128 and every chunk, else
         // for the tile's rows and every other chunk. The warps take turns, a step's products with V and the next scores a turn,
         // so that one warpgroup's softmax runs beside the other's products; a warp waits for what it needs before its turn, while
-        // the other's MMAs run (one warp for both left the tensor cores idle for 450 clocks of 2,090 a step; two without turns
-        // fell into step, 2,450). The whole warp loops and one lane issues: with a lane of its own (lane 0 alone in the loop)
+        // the other's MMAs run (a step's products take 1,536 clocks and a step 1,750; 2,090 with one warp for both, 2,450 by two
+        // without turns, which fell into step). The whole warp loops and one lane issues: with a lane of its own (lane 0 alone in the loop)
         // an MMA took 80 to 100 clocks to issue, 61 so. What steers the loop passes through a shuffle, so that it is known to
         // be the same in every lane, and a wait that needs none is a single look.
         constexpr uint32_t id_s = idesc_16<T>(128, kSKeys, false), id_o = idesc_16<T>(128, D, true);
@@ -947,7 +958,8 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
 constexpr int kSMergeThreads = 256;
 
 // A warp joins the parts of one (row, q head): those of its own tile, then those of the prefix's, CTA by CTA along the line.
-// Rows that one piece holds alone were written by the attention, those of refused spans become NaN.
+// Rows that one piece holds alone were written by the attention, those of refused spans become NaN. Eight parts are on their way
+// at once (sixteen were slower: registers); 4 us for few rows, most of it three loads that wait for one another.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSMergeThreads, 3) shared_merge_kernel(const __grid_constant__ SharedArgs a) {
     constexpr int V = D / 32;
