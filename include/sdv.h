@@ -560,7 +560,7 @@ int sdv_shared_destroy(sdv_shared *s);
 /* Spans are packed as everywhere: row row_off[b] + i is position base[b] + i of sequence b and attends the keys t <= its own
  * position pos, with window > 0 those of the last `window` positions, its own among them. The span's own K and V must
  * have been written. d_q and d_out hold `rows` rows of [n_q_heads][head_dim], q_stride and out_stride elements apart (at most
- * max_rows and B * max_span of them are used). A score is cap * tanh(q.k / sqrt(head_dim) / cap) - slope[head] * (pos - t);
+ * max_rows and B * max_span of them are used) and share no memory. A score is cap * tanh(q.k / sqrt(head_dim) / cap) - slope[head] * (pos - t);
  * softcap 0: q.k / sqrt(head_dim); d_slopes [n_q_heads] fp32 or NULL: no bias.
  * Groups: G > 0 cuts the batch into groups of neighbouring sequences, group g those from d_group_off[g] to
  * d_group_off[g + 1] - 1 (d_group_off [G + 1], from 0 to B, never falling; G <= B, G <= 128), which hold the same K and V at

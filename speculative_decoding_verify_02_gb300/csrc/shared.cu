@@ -205,7 +205,7 @@ int sdv_shared_attention(sdv_shared *s, int layer, const void *d_q, int64_t q_st
                          const int32_t *d_row_off, const int32_t *d_base, int B, const int32_t *d_group_off,
                          const int32_t *d_prefix_len, int G, int max_span, int window, float softcap, const float *d_slopes,
                          void *d_out, int64_t out_stride, void *stream) {
-    if (!s || !d_q || !d_out || !d_page_table || !d_row_off || !d_base || layer < 0 || layer >= s->c.n_layers || rows <= 0 ||
+    if (!s || !d_q || !d_out || d_q == d_out || !d_page_table || !d_row_off || !d_base || layer < 0 || layer >= s->c.n_layers || rows <= 0 ||
         B <= 0 || B > s->c.max_batch || max_span <= 0 || max_span > s->c.max_span || window < 0)
         return SDV_ERR_ARG;
     if (G < 0 || G > B || G > kSGroups || (G > 0 && (!d_group_off || !d_prefix_len))) return SDV_ERR_ARG;

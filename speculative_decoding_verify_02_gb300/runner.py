@@ -99,6 +99,8 @@ class SpecLoop:
         first tokens (host numpy) and leaves them in self.first. The sequences must be empty."""
         import torch
         B, v = self.B, self.v
+        if len(prompt) == 0:
+            raise ValueError("prompt: empty")
         assert chunk <= v.ccfg.max_span and chunk <= v.ccfg.max_rows
         if noise is not None and temperature is None:
             raise ValueError("drawing the first tokens needs temperature and noise")

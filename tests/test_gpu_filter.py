@@ -121,6 +121,26 @@ def test_full_vocabulary(kind):
     _check(v, x, noise, np.arange(R + 1), T, k=[1, 50, 3000, 7, 100000, 2048], p=[0.5, 0.9, 0.99, 0.9, 0.8, 0.3], m=[0.1, 0.01, 0, 0.1, 0.5, 0.001])
 
 
+@pytest.mark.parametrize("V", [2049, 30001])
+def test_lists_that_crowd(V):
+    """Rows whose likely tokens lie close together: some hundreds to two thousand equal or nearly equal logits above the rest, or
+    below a single large one; infinite temperatures."""
+    rng = np.random.default_rng(11)
+    x = (rng.normal(size=(10, V)) - 50).astype(np.float32)
+    for r, n in enumerate((200, 255, 300, 900, 1990)):
+        at = rng.choice(V, n, replace=False)
+        x[2 * r, at] = 1.25                                        # equal
+        x[2 * r + 1, at] = 1.25 + 2.0 ** -20 * rng.integers(0, 40, n)  # nearly
+        if r % 2:
+            x[2 * r:2 * r + 2, at[0]] = 3e4                        # one far above
+    noise = rng.exponential(size=x.shape)
+    v = _verifier(V)
+    off = np.arange(11)
+    for T in ([1.0] * 10, [3e4] * 10, [np.inf] * 10):
+        for cuts in (dict(k=[150] * 10), dict(p=[0.4] * 10), dict(k=[180] * 10, p=[0.7] * 10), dict(k=[1500] * 10, p=[0.9] * 10, m=[1e-3] * 10)):
+            _check(v, x, noise, off, T, **cuts)
+
+
 def test_borders_next_to_a_token():
     """Equal weights, whose sums lie on p's border in exact arithmetic: the token at the border is dropped, since the weight
     before it is not less; one unit of p more keeps it."""

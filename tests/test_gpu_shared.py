@@ -327,6 +327,8 @@ def test_host_refusals():
         with pytest.raises(SdvError):
             s.run(**kw)
     with pytest.raises(SdvError):
+        s.run(out=s.q)
+    with pytest.raises(SdvError):
         s.plan.attention(1, s.q, s.d_table, s.d_off, s.d_base, s.B, s.max_span, s.q.clone())
     with pytest.raises(SdvError):
         s.plan.attention(0, s.q, s.d_table, s.d_off, s.d_base, s.B, s.max_span + 1, s.q.clone())

@@ -66,6 +66,14 @@ def test_types_are_checked_before_any_call(sdv):
         sdv.SharedAttention(1, 8, 2, 128, dtype=torch.float32)
 
 
+def test_a_prompt_to_share_has_tokens(sdv):
+    from speculative_decoding_verify_02_gb300.runner import SpecLoop
+    loop = SpecLoop.__new__(SpecLoop)
+    loop.v, loop.B = None, 4
+    with pytest.raises(ValueError, match="empty"):
+        loop.prefill_shared([])
+
+
 def test_a_step_with_cuts_needs_uniforms(sdv):
     from speculative_decoding_verify_02_gb300.runner import SpecLoop
     loop = SpecLoop.__new__(SpecLoop)
