@@ -3,7 +3,9 @@
 // Tokens are ordered by logit, equal ones by index: a 64-bit key each, and a kept set is the keys at or above one of them.
 // With w = 2^-((m - x) log2(e) / T), m the row's largest logit, top-p keeps token i iff the weights before it sum to less than
 // p of the top-k set's. The row stays in the shared memory of a cluster of CTAs. Each thread's largest logit is known from the
-// search for the row's: k of those, or as many as weigh p of the total, are a bound that the border does not pass. Where no
+// search for the row's: k of those, or as many as weigh p of the total, are a bound that the border does not pass. (For k up to
+// 256 the largest of each eight threads will do, which are few enough for every CTA to have them all: 8 rows 12.6 us, 13.2 by a
+// histogram that the CTAs add up.) Where no
 // more than kFilterList tokens lie above it, as in most rows of a language model, they go to one CTA, which sorts them and cuts
 // and draws by itself. Where more do, a histogram of all tokens over (m - x) / T shows the border's bin, sums over the bin's
 // edges confirm it, and its tokens alone are compared with one another.
@@ -25,6 +27,7 @@ constexpr int kFilterBins = 1024;
 constexpr int kFilterFew = 256;                  // tokens that are compared with one another
 constexpr float kFilterRange = 40.f;             // log2 of the weights that the histogram's bins cover
 constexpr int kFilterCluster = 8;                // CTAs of a row
+constexpr int kFilterGroups = kFilterCluster * kFilterThreads / 8;
 constexpr int kFilterList = 2048;                // tokens that one CTA sorts; a row of no more is one CTA's
 constexpr int kFilterMost = 49152;               // tokens of a CTA at most (192 KB)
 // How far a sum of fp32 weights and p times another may lie from each other's exact values, over the total: an exponent
@@ -114,6 +117,7 @@ struct FilterShared {
     FilterSums warp[kFilterThreads / 32], part[2][kFilterCluster];
     unsigned long long list[kFilterList];            // CTA 0's: keys, or the border's tokens' keys and then their weights
     uint16_t pick[kFilterList];                      // tokens of this CTA for the list, places in its chunk
+    float group[kFilterGroups];                      // of the row: the largest logit of each eight threads
     unsigned long long cut, scan_e[kFilterThreads / 32];
     unsigned long long target, table[64];     // table: kFilterTable's
     uint32_t n_cand, n_pick, scan[kFilterThreads / 32], warp_sum[kFilterThreads / 32], ambiguous, kept;
@@ -322,6 +326,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
     __shared__ FilterShared sh;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
     const int v0 = rank * a.chunk, n = max(0, min(a.chunk, a.vocab - v0)), n4 = (n + 3) / 4;
+    if (ctas > 1) cluster_arrive();  // others' shared memory is there once they have started
     if (tid < 64) sh.table[tid] = kFilterTable[tid];
     if (tid == 0) sh.seq = -1, sh.n_cand = sh.n_pick = 0;
     pdl_wait();
@@ -342,14 +347,16 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
         if (ok && row >= r0 && row < r0 + S) sh.seq = tid;
         if (!ok && S != 0 && row == 0 && rank == 0) set_status(a.status, SDV_ERR_ARG);
     }
-    for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = 0;
+    for (int i = tid; i < kFilterBins; i += kFilterThreads) sh.hist[i] = sh.total[i] = 0;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     const int b = sh.seq;
+    if (ctas > 1) cluster_wait();
     if (b < 0) return;  // a row of no span: every CTA of the cluster leaves
     const float T = a.temperature[b];
     const float top_p = a.top_p ? a.top_p[b] : 2.f, min_p = a.min_p ? a.min_p[b] : 0.f;
     const int top_k = a.top_k ? a.top_k[b] : 0;
+    const bool by_groups = ctas == kFilterCluster && top_k > 0 && top_k <= kFilterGroups / 2;
     int turn = 0;
     const unsigned long long none = ~0ull;
     float4 *x4 = reinterpret_cast<float4 *>(x_s);
@@ -384,6 +391,12 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 m = four;
                 first = v0 + 4 * i + (x.x == m ? 0 : x.y == m ? 1 : x.z == m ? 2 : 3);
             }
+        }
+        if (by_groups) {  // the largest of each eight threads, for every CTA
+            float most = m;
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            st_dsmem_u32(mapa_shared(smem_u32(&sh.group[(rank * (kFilterThreads / 32) + warp) * 4 + lane / 8]), lane % 8), __float_as_uint(most));
         }
         FilterSums s = {static_cast<unsigned long long>(count), 0, count ? filter_key(m, first) : 0ull, none};
         s = filter_reduce<kSumA | kHi>(sh, s, ctas, rank, turn++);
@@ -760,8 +773,14 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
         const bool all = valid <= kFilterList;
         if (!want_k) sum_up();
         if (!all) {
-            if (m > -INFINITY) atomicAdd(&sh.hist[bin_of(m)], 1u);
-            add_up();
+            if (by_groups && want_k) {  // few enough for every CTA to count by itself
+                const float most = sh.group[tid];
+                if (most > -INFINITY) atomicAdd(&sh.total[bin_of(most)], 1u);
+                __syncthreads();
+            } else {
+                if (m > -INFINITY) atomicAdd(&sh.hist[bin_of(m)], 1u);
+                add_up();
+            }
             find_bin(!want_k, g.k, g.target * (kFilterUnit * 1.0001f), 0, kFilterBins - 1, [](int i) { return i < kFilterBins - 1 ? filter_ex2(-(i + 1) * (kFilterRange / kFilterBins)) : 0.f; });
         }
         const int last = all ? 0 : sh.found[0];
