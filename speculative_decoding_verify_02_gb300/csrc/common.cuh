@@ -264,6 +264,9 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
 }
 // split cluster barrier: arrive once this CTA's reads of other CTAs' shared memory are done, wait
 // before leaving (no CTA exits while another may still read its shared memory)
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }

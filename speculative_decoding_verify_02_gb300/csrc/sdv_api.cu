@@ -1160,7 +1160,9 @@ int sdv_sample(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride, int r
 int sdv_rewind_cache(sdv_ctx *ctx, const int32_t *d_length, int B, void *stream) {
     if (!ctx || !d_length || B <= 0 || B > ctx->c.max_batch) return SDV_ERR_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(ctx, rewind_kernel, dim3(1), dim3(ctx->forked ? 1024 : 256), 0, st, ctx->st, d_length, B);
+    // shared pages are released by a cluster (64 sequences: 15 us with the launch, 18 by one CTA of 1,024 threads; eight: 10.9 either way)
+    cudaError_t e = ctx->forked ? launch_cluster(ctx, rewind_kernel, dim3(8), dim3(512), 0, st, 8, ctx->st, d_length, B)
+                                : launch(ctx, rewind_kernel, dim3(1), dim3(256), 0, st, ctx->st, d_length, B);
     if (e == cudaSuccess && ctx->swa_mask)
         e = launch(ctx, swa_restore_kernel, dim3(B, ctx->m.n_layers), dim3(256), 0, st, ctx->st, ctx->pool,
                    ctx->layer_stride, ctx->swa_mask, static_cast<const bf16 *>(ctx->swa_backup), ctx->swa_layer_elems,

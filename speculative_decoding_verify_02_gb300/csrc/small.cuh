@@ -295,22 +295,30 @@ __global__ void ensure_kernel(DevState s, const int *required, int B) {
 
 // Releases the last rel[b] pages of each sequence while pages are shared, in the order of a rewind: b = B-1 down to 0, highest
 // slot first. A page's count of other holders falls by one for each that lets go; below zero nobody holds it any more, and the
-// lowest b that let go gives it back. `off` is scratch. (A thread a slot, going through the sequences: 68 us for 60 sequences
-// of up to 255 pages; 13 now.)
+// lowest b that let go gives it back. By the CTAs of a cluster, sequence b by CTA b modulo their number, or by one. `off` is
+// scratch. (60 sequences of up to 255 pages: 10 us, 13 by one CTA of 1,024 threads, 68 by a thread a slot that goes through the
+// sequences.)
 __device__ __forceinline__ void release_shared(const DevState &s, const int *rel, int *off, int B, int top) {
     constexpr int kOwner = 257;  // a page that b gives back holds b - kOwner meanwhile
-    __shared__ int held[256], let_go;
+    __shared__ int held[256], all_off[256], let_go;
     const int tid = threadIdx.x, threads = blockDim.x, lane = tid % 32, warps = threads / 32;
+    const int ctas = gridDim.x, rank = blockIdx.x, most = (B + ctas - 1) / ctas;
+    auto sync = [&]() {
+        if (ctas > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
     if (tid == 0) let_go = 0;
     for (int b = tid; b < B; b += threads) {
         held[b] = s.n_pages[b];
         off[b] = 0;
     }
-    __syncthreads();
+    sync();  // and every CTA has read the state
     // a team of warps a sequence, from its last page, eight entries and counts of a thread on their way at once
-    const int team = max(1, warps / B), first = tid / 32 / team, member = tid / 32 - first * team;
+    const int team = max(1, warps / most), first = tid / 32 / team, member = tid / 32 - first * team;
     auto each = [&](bool counts, auto f) {
-        for (int b = first; b < B; b += warps / team) {
+        for (int b = rank + ctas * first; b < B; b += ctas * (warps / team)) {
             int *end = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1;
             for (int j0 = member * 256 + lane; j0 < rel[b]; j0 += team * 256) {
                 int page[8], extra[8];
@@ -323,7 +331,7 @@ __device__ __forceinline__ void release_shared(const DevState &s, const int *rel
                     if (page[u] >= 0) f(b, end - j0 - 32 * u, page[u], extra[u]);
             }
         }
-        __syncthreads();
+        sync();
     };
     each(false, [&](int, int *, int page, int) { atomicSub(&s.extra[page], 1); });
     each(true, [&](int b, int *, int page, int extra) {
@@ -337,10 +345,15 @@ __device__ __forceinline__ void release_shared(const DevState &s, const int *rel
             atomicAdd(&let_go, 1);
         }
     });
+    for (int i = tid; i < most * ctas; i += threads) {  // each CTA's to all
+        const int b = rank + i / ctas * ctas;
+        if (b < B) st_dsmem_u32(mapa_shared(smem_u32(&all_off[b]), i % ctas), off[b]);
+    }
+    sync();
     if (tid < 32) {  // what the sequences behind each give back
         int total = 0;
         for (int b0 = B - 1; b0 >= 0; b0 -= 32) {
-            const int b = b0 - lane, mine = b >= 0 ? off[b] : 0;
+            const int b = b0 - lane, mine = b >= 0 ? all_off[b] : 0;
             int sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -351,12 +364,12 @@ __device__ __forceinline__ void release_shared(const DevState &s, const int *rel
             total += __shfl_sync(0xffffffffu, sum, 31);
         }
         if (lane == 0) {
-            *s.free_top = top + total;
-            *s.n_extra -= let_go;
+            if (rank == 0) *s.free_top = top + total;
+            atomicSub(s.n_extra, let_go);
         }
     }
     __syncthreads();
-    for (int b = tid / 32; b < B; b += warps) {
+    for (int b = rank + ctas * (tid / 32); b < B; b += ctas * warps) {
         int at = top + off[b];
         int *end = s.page_table + static_cast<size_t>(b) * s.pages_per_seq + held[b] - 1;
         for (int j0 = lane; j0 - lane < rel[b]; j0 += 256) {
@@ -378,6 +391,7 @@ __device__ __forceinline__ void release_shared(const DevState &s, const int *rel
     }
 }
 
+// One CTA, or a cluster of them: all look at the lengths, and where no page is shared the first does the rest.
 __global__ void rewind_kernel(DevState s, const int *length, int B) {
     pdl_trigger();
     pdl_wait();
@@ -402,13 +416,13 @@ __global__ void rewind_kernel(DevState s, const int *length, int B) {
     }
     const bool all_ok = __syncthreads_and(ok);
     if (!all_ok) {
-        if (tid == 0) set_status(s.status, SDV_ERR_ARG);
+        if (tid == 0 && blockIdx.x == 0) set_status(s.status, SDV_ERR_ARG);
         return;
     }
     if (shared > 0) {
         release_shared(s, rel_s, off_s, B, top);
-        if (b >= 0 && length[b] >= 0) s.seq_len[b] = length[b];
-    } else {
+        if (b >= 0 && blockIdx.x == 0 && length[b] >= 0) s.seq_len[b] = length[b];
+    } else if (blockIdx.x == 0) {
         int sum = rel;  // pages that this sequence and those behind it release
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
