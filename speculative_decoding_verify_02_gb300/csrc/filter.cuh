@@ -4,7 +4,7 @@
 // With w = 2^-((m - x) log2(e) / T), m the row's largest logit, top-p keeps token i iff the weights before it sum to less than
 // p of the top-k set's. The row stays in the shared memory of a cluster of CTAs. Each thread's largest logit is known from the
 // search for the row's: k of those, or as many as weigh p of the total, are a bound that the border does not pass. (For k up to
-// 256 the largest of each eight threads will do, which are few enough for every CTA to have them all: 8 rows 12.6 us, 13.2 by a
+// 256 the largest of each eight threads will do, which are few enough for every CTA to have them all: 8 rows 12.4 us, 12.8 by a
 // histogram that the CTAs add up.) Where no
 // more than kFilterList tokens lie above it, as in most rows of a language model, they go to one CTA, which sorts them and cuts
 // and draws by itself. Where more do, a histogram of all tokens over (m - x) / T shows the border's bin, sums over the bin's
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
     const float T = a.temperature[b];
     const float top_p = a.top_p ? a.top_p[b] : 2.f, min_p = a.min_p ? a.min_p[b] : 0.f;
     const int top_k = a.top_k ? a.top_k[b] : 0;
-    const bool by_groups = ctas == kFilterCluster && top_k > 0 && top_k <= kFilterGroups / 2;
+    const bool by_groups = ctas == kFilterCluster && top_k > 0 && top_k <= min(kFilterThreads, a.chunk / 4) / 16 * kFilterCluster;
     int turn = 0;
     const unsigned long long none = ~0ull;
     float4 *x4 = reinterpret_cast<float4 *>(x_s);
@@ -770,15 +770,18 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
         const bool all = valid <= kFilterList;
         if (!want_k) sum_up();
         if (!all) {
-            if (by_groups && want_k) {  // few enough for every CTA to count by itself
-                const float most = sh.group[tid];
-                if (most > -INFINITY) atomicAdd(&sh.total[bin_of(most)], 1u);
-                __syncthreads();
-            } else {
-                if (m > -INFINITY) atomicAdd(&sh.hist[bin_of(m)], 1u);
-                add_up();
+            for (bool groups = by_groups && want_k;; groups = false) {  // few groups with a token: the threads' after all
+                if (groups) {  // few enough for every CTA to count by itself
+                    const float most = sh.group[tid];
+                    if (most > -INFINITY) atomicAdd(&sh.total[bin_of(most)], 1u);
+                    __syncthreads();
+                } else {
+                    if (m > -INFINITY) atomicAdd(&sh.hist[bin_of(m)], 1u);
+                    add_up();
+                }
+                find_bin(!want_k, g.k, g.target * (kFilterUnit * 1.0001f), 0, kFilterBins - 1, [](int i) { return i < kFilterBins - 1 ? filter_ex2(-(i + 1) * (kFilterRange / kFilterBins)) : 0.f; });
+                if (!groups || sh.found[0] < kFilterBins - 1) break;
             }
-            find_bin(!want_k, g.k, g.target * (kFilterUnit * 1.0001f), 0, kFilterBins - 1, [](int i) { return i < kFilterBins - 1 ? filter_ex2(-(i + 1) * (kFilterRange / kFilterBins)) : 0.f; });
         }
         const int last = all ? 0 : sh.found[0];
         if (last < kFilterBins - 1) {

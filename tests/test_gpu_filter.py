@@ -141,6 +141,19 @@ def test_lists_that_crowd(V):
             _check(v, x, noise, off, T, **cuts)
 
 
+def test_tokens_of_one_corner():
+    """All tokens above -inf lie next to one another, so that few threads hold them."""
+    rng = np.random.default_rng(12)
+    V = 30001
+    x = np.full((8, V), -np.inf, dtype=np.float32)
+    for r, (at, n) in enumerate(((0, 2500), (3800, 2500), (27000, 3001), (0, 2049), (100, 4000), (15000, 9000), (29999, 2), (7, 2100))):
+        x[r, at:at + n] = 2 * rng.normal(size=min(n, V - at))
+    noise = rng.exponential(size=x.shape)
+    v = _verifier(V)
+    for k in (5, 60, 100, 250, 256, 257, 1500):
+        _check(v, x, noise, np.arange(9), [0.8] * 8, k=[k] * 8, p=[0.95] * 8)
+
+
 def test_borders_next_to_a_token():
     """Equal weights, whose sums lie on p's border in exact arithmetic: the token at the border is dropped, since the weight
     before it is not less; one unit of p more keeps it."""
