@@ -141,6 +141,22 @@ def test_lists_that_crowd(V):
             _check(v, x, noise, off, T, **cuts)
 
 
+def test_largest_vocabulary():
+    """The largest that is taken, and one token more."""
+    from speculative_decoding_verify_02_gb300 import SdvError
+    rng = np.random.default_rng(13)
+    V, R = 393216, 4
+    x, noise = _rows(rng, R, V, "peaks"), rng.exponential(size=(R, V))
+    x[2] = 0.0
+    v = _verifier(V, max_batch=8)
+    for cuts in (dict(k=[40, 300, 200000, 7], p=[0.9, 0.99, 0.5, 1.0]), dict(p=[0.9, 0.7, 0.25, 0.9], m=[0.01, 0, 0, 0.2])):
+        _check(v, x, noise, np.arange(R + 1), [1.0, 0.8, 1.0, 1.5], **cuts)
+    v = _verifier(V + 1, max_batch=8)
+    big = _f32(np.zeros((1, V + 1)))
+    with pytest.raises(SdvError):
+        v.filter_logits(big, _i32([0, 1]), 1, big, None, _f32([1.0]))
+
+
 def test_tokens_of_one_corner():
     """All tokens above -inf lie next to one another, so that few threads hold them."""
     rng = np.random.default_rng(12)
