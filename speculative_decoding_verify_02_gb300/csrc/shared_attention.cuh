@@ -9,7 +9,7 @@
 // window if there is one.
 //
 // What bounds it (bf16, 32 heads on 8 of 128 dims; pages of 16; the whole call in a graph):
-//   16 x 8 rows after 32,768 shared keys  81 us, 850 TFLOP/s: the tensor cores, 85 % of the time of its products. Those with V
+//   16 x 8 rows after 32,768 shared keys  81 us, 850 TFLOP/s: the tensor cores, whose products take 81 % of a chunk. Those with V
 //                                         are twice the scores', as p enters in two 16-bit planes
 //   64 sequences of one row after them, up to 512 keys of their own   66 us, 3.1 TB/s: half the time is the sequences' own tiles,
 //                                         64 x 8 of 4 rows, 7,000 clocks each from queries to results
