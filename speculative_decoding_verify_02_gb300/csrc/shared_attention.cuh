@@ -11,9 +11,9 @@
 // What bounds it (bf16, 32 heads on 8 of 128 dims; pages of 16; the whole call in a graph):
 //   16 x 8 rows after 32,768 shared keys  81 us, 850 TFLOP/s: the tensor cores, whose products take 81 % of a chunk. Those with V
 //                                         are twice the scores', as p enters in two 16-bit planes
-//   64 sequences of one row after them, up to 512 keys of their own   66 us, 3.1 TB/s: half the time is the sequences' own tiles,
-//                                         64 x 8 of 4 rows, 7,000 clocks each from queries to results
-//   8 x 8 rows after 848 shared keys      18 us: latency, of the plan (4,500 clocks), of the first loads and of code that no
+//   64 sequences of one row after them, up to 512 keys of their own   66 us, 3.1 TB/s: two fifths of the time are the sequences' own tiles,
+//                                         64 x 8 of 4 rows, 11,300 clocks each, while the device reads 5 TB/s
+//   8 x 8 rows after 848 shared keys      18 us: latency, of the plan (5,600 clocks), of the first loads and of code that no
 //                                         cache holds, of the join (4 us)
 // Why two planes: one leaves p a relative error of 2^-9, which the sum over alike keys keeps; the result then is up to twice as far off
 // as its own rounding. With two that rounding is all of the error.
