@@ -429,7 +429,8 @@ struct Int {
 struct SShared {
     uint64_t full[8], empty[8], s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_empty, turn[2];
     uint32_t tmem;
-    uint32_t bad[2][2][4];  // [turn][warpgroup]: keys of the chunk that are not finite, as bits
+    // keys of a chunk that are not finite, as bits: [chunks that one warpgroup looks at, that both do][turn][warpgroup that found them]
+    uint32_t bad[2][2][2][4];
     float2 ml[2][128];  // (M, l) of the rows that two warpgroups share
     SPlan plan;
 };
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t q_s = smem_u32(smem_raw), kv_s = q_s + 2 * Q::Q_BYTES;
     SShared &sh = *reinterpret_cast<SShared *>(smem_raw + 2 * Q::Q_BYTES + Q::SLOTS * Q::SLOT);
-    if (tid < 16) sh.bad[tid / 8][tid / 4 % 2][tid % 4] = 0;
+    if (tid < 32) sh.bad[tid / 16][tid / 8 % 2][tid / 4 % 2][tid % 4] = 0;
     if (tid == 0) {
         for (int i = 0; i < Q::SLOTS; ++i) {
             mbar_init(&sh.full[i], a.box_rows ? 1 : 32);
@@ -681,6 +682,7 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
         const uint32_t s_t = tmem + lanes + w * kSKeys, o_t = tmem + lanes + Q::O_COL + w * 128;
         int done = 0, pieces = 0;  // this warpgroup's steps, pieces
+        uint32_t looks = 0;        // whose turn the marks in `bad` are: bit 0 alone, bit 1 (the same in both warpgroups) together
         // The queries of a piece go into their swizzled halves as soon as the last one's scores have read theirs, beside its last
         // products and results. Rows behind the tile's keep what lies there: they only make results that nobody reads.
         auto load_q = [&](const SPiece &p) {
@@ -747,7 +749,10 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                     const int a0 = in_chunk(kv_lo & -box), a1 = max(a0, in_chunk(all_lo)), b0 = max(a1, in_chunk(all_hi));
                     const int rows_a = a1 - a0, rows = rows_a + max(0, in_chunk((kv_end + box - 1) & -box) - b0);
                     if (rows > 0) {
-                        const int st = Q::DEPTH + c % Q::DEPTH, turn = (done + j) & 1;
+                        const int st = Q::DEPTH + c % Q::DEPTH;
+                        uint32_t(&found)[2][2][4] = sh.bad[wide];
+                        const uint32_t turn = looks >> (wide ? 1 : 0) & 1;
+                        looks ^= wide ? 2u : 1u;
                         if (ok) ok = mbar_wait(&sh.full[st], filling(c) & 1);
                         bool wrote = false;
                         for (int i = wide ? tid : m; i < rows * PPR; i += wide ? 256 : 128) {
@@ -760,7 +765,7 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
                                 wrote = true;
                             }
-                            if (bad) atomicOr(&sh.bad[turn][w][row / 32], 1u << row % 32);
+                            if (bad) atomicOr(&found[turn][w][row / 32], 1u << row % 32);
                         }
                         if (wrote) fence_async_smem();
                         if (wide)
@@ -771,10 +776,13 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
                             named_bar_sync(4, 128);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t b = sh.bad[turn][w][k] | (wide ? sh.bad[turn][1 - w][k] : 0u);
+                            const uint32_t b = found[turn][w][k] | (wide ? found[turn][1 - w][k] : 0u);
                             if (b) poisoned |= (b & seen_bits(see_lo - t0 - 32 * k, see_hi - t0 - 32 * k)) != 0;
                         }
-                        if (m < 4) sh.bad[1 - turn][w][m] = 0;  // nobody reads the last chunk's any more
+                        // Marks stand for this chunk's keys alone. Those of the chunk that was looked at before, by the same
+                        // threads, were read by all of them before they came here; a turn is a chunk that is looked at, not a
+                        // step, of which others lie between and of which the warpgroups can have done different numbers.
+                        if (m < 4) found[1 - turn][w][m] = 0;
                     }
                 }
                 if (live) {

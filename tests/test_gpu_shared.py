@@ -415,3 +415,67 @@ def test_pages_outside_of_the_pool_read_as_zeros(ps):
         s.d_table = _i32(table)
         s.check(s.run(), kv=kv)
         assert s.plan.get_status() == SDV_ERR_CAPACITY
+
+
+# ---------------------------------------------------------------- values that are not finite, where a CTA does many tiles
+
+def _bad_values(s, at, bad, window=0):
+    """V of sequence b's position at[b] becomes `bad` in one dim of kv head 1: rows that see it are spoilt in that head, all
+    others keep their bits."""
+    import torch
+    clean = s.run(window=window)
+    assert torch.isfinite(clean).all()
+    sees = torch.zeros(s.rows, s.nq, dtype=torch.bool, device="cuda")
+    grp = s.nq // s.nkv
+    for b, p in at.items():
+        s.pool[s.layer, int(s.table[b, p // s.ps]), 1, 1, p % s.ps, 5] = float(bad)
+        for r in range(s.off[b], s.off[b + 1]):
+            pos = int(s.base[b]) + r - s.off[b]
+            if p <= pos and (not window or p > pos - window):
+                sees[r, grp:2 * grp] = True
+    out = s.run(window=window)
+    assert sees.any() and not sees.all()
+    assert torch.equal(out[~sees], clean[~sees]), f"{int((out != clean).any(-1)[~sees].sum())} rows and heads of others changed"
+    assert not torch.isfinite(out[sees]).all(-1).any()
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("which", [(0,), (63,), range(0, 64, 3), range(64)])
+def test_one_sequences_bad_value_reaches_no_other(which, bad):
+    """More tiles than CTAs, of seven chunks each: a mark that outlives its tile would meet the next sequence's last chunk."""
+    s = Setup(sizes=[1] * 64, prefix=[0] * 64, own=[840] * 64, spans=[8] * 64, groups=False, nq=32, nkv=8, D=64)
+    _bad_values(s, {b: 840 + 3 for b in which}, bad)
+
+
+@pytest.mark.parametrize("lengths", [[140], [300], [140, 270, 400], [300, 900]])
+def test_bad_values_where_lengths_differ(lengths):
+    B = 96
+    own = [lengths[i % len(lengths)] + i % 5 for i in range(B)]
+    s = Setup(sizes=[1] * B, prefix=[0] * B, own=own, spans=[4] * B, groups=False, nq=16, nkv=4, D=64)
+    _bad_values(s, {b: own[b] + 2 for b in range(0, B, 2)}, np.nan)
+
+
+@pytest.mark.parametrize("at", [2, 12, 40])
+def test_a_bad_value_that_left_the_window(at):
+    """Chunks that all rows see between two that they do not: rows behind whose window the bad value lies keep their results, in
+    the last chunk too. Of 60 sequences, five chunks each."""
+    s = Setup(sizes=[1] * 60, prefix=[0] * 60, own=[515] * 60, spans=[60] * 60, groups=False, nq=4, nkv=4, D=64)
+    _bad_values(s, {b: 515 - 510 + 1 + at for b in range(0, 60, 2)}, np.nan, window=510)
+
+
+@pytest.mark.parametrize("spans", [[8, 40], [40, 8, 8], [72, 1], [33, 1, 64]])
+@pytest.mark.parametrize("own", [[100], [300, 130], [700, 60, 300]])
+def test_bad_values_where_narrow_and_wide_tiles_take_turns(spans, own):
+    """Tiles of up to 128 rows, of which two warpgroups take every other chunk, and of more, whose V both look at."""
+    B = 72
+    n, o = [spans[i % len(spans)] for i in range(B)], [own[i % len(own)] + i % 3 for i in range(B)]
+    s = Setup(sizes=[1] * B, prefix=[0] * B, own=o, spans=n, groups=False, nq=16, nkv=4, D=64)
+    for at in (0, 1):
+        _bad_values(s, {b: o[b] + min(at, n[b] - 1) for b in range(at, B, 2)}, np.nan)
+        s.pool.nan_to_num_(0.5)
+
+
+def test_bad_values_behind_a_shared_prefix():
+    B = 48
+    s = Setup(sizes=[30, 18], prefix=[400, 150], own=[i % 9 * 31 for i in range(B)], spans=[1 + i % 7 * 6 for i in range(B)], nq=16, nkv=4, D=64)
+    _bad_values(s, {b: int(s.base[b]) + min(2, int(s.spans[b]) - 1) for b in range(1, B, 3)}, np.nan)
