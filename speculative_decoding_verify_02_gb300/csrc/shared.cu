@@ -119,7 +119,7 @@ cudaError_t set_attn_all() {
 }
 template <typename T, int D>
 int launch_attn(const CUtensorMap &pool, const SharedArgs &a, void *stream) {
-    const bool extra = a.cap > 0.f || a.slopes;
+    const bool extra = a.cap2 > 0.f || a.slopes;
     const int r = launch(extra ? shared_attn_kernel<T, D, true> : shared_attn_kernel<T, D, false>, dim3(a.ctas), kSThreads,
                          STile<T, D>::SMEM, stream, pool, a);
     if (r != SDV_OK) return r;
@@ -248,9 +248,12 @@ int sdv_shared_attention(sdv_shared *s, int layer, const void *d_q, int64_t q_st
     a.by_page = s->by_page;
     a.by_grp = s->by_grp;
     a.by_nq = s->by_nq;
-    a.scale = 1.f / std::sqrt(static_cast<float>(c.head_dim));
-    a.scale_log2 = 1.4426950408889634f * a.scale;
-    a.cap = softcap;
+    const float scale = 1.f / std::sqrt(static_cast<float>(c.head_dim)), cap = std::min(softcap, 1e30f);
+    a.scale_log2 = 1.4426950408889634f * scale;
+    if (cap > 0.f) {
+        a.cap2 = 1.4426950408889634f * cap;
+        a.to_u = scale / cap;
+    }
     a.ctas = s->sm_count;
     const Workspace w = workspace(c, s->sm_count);
     a.part_rows = part_rows(c);

@@ -479,3 +479,56 @@ def test_bad_values_behind_a_shared_prefix():
     B = 48
     s = Setup(sizes=[30, 18], prefix=[400, 150], own=[i % 9 * 31 for i in range(B)], spans=[1 + i % 7 * 6 for i in range(B)], nq=16, nkv=4, D=64)
     _bad_values(s, {b: int(s.base[b]) + min(2, int(s.spans[b]) - 1) for b in range(1, B, 3)}, np.nan)
+
+
+# ---------------------------------------------------------------- caps of any size
+
+def _check_cap(s, out, cap, window=0):
+    """As Setup.check with a cap's own error. Up to 64, cap (1 - 2 / (1 + e)): half of e's relative error, 2^-22 and three roundings,
+    2^-22 of the quotient, below 1, and a rounding: 2^-21 of the cap covers them. Above, 2^-21.3 of the score and its exponent's
+    roundings: 2^-20 |z|, however large the cap."""
+    q = s.q.double().cpu().numpy()
+    o = out.double().cpu().numpy()
+    grp = s.nq // s.nkv
+    for b in range(s.B):
+        rows, pos = slice(s.off[b], s.off[b + 1]), s.base[b] + np.arange(s.spans[b])
+        k, v = s.kv[b].astype(np.float64)
+        for h in range(s.nq):
+            z = oracle.scores(q[rows, h], k[:, h // grp], pos, window, float(np.float32(cap)), 0.0)
+            ref = oracle.attend(z, v[:, h // grp])
+            seen = z > -np.inf
+            w = np.exp(z - z.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            mag = np.where(seen, np.abs(q[rows, h]) @ np.abs(k[:, h // grp]).T, 0).max() / np.sqrt(s.D)
+            top = np.abs(np.where(seen, z, 0)).max()
+            A = np.stack([w[i, m] @ np.abs(v[m, h // grp]) for i, m in enumerate(seen)])
+            off = 2.0 ** -21 * cap if cap <= 64 else 2.0 ** -20 * top
+            e = (s.D + 2) * 2.0 ** -24 * mag + 3 * 2.0 ** -24 * 1.45 * top + off + 2.0 ** -22 + 2.0 ** -16
+            tol = (2 * e + 2 * len(k) * 2.0 ** -24) * A + s.eps / 2 * np.abs(ref) * 1.01 + 2.0 ** -24
+            d = np.abs(o[rows, h] - ref)
+            assert np.isfinite(o[rows, h]).all(), f"sequence {b} head {h}"
+            assert (d <= tol).all(), f"sequence {b} head {h}: {d.max()} over {tol.flat[d.argmax()]}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("cap", [0.3, 5.0, 50.0, 64.0, 65.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e20, 1e30, 3e38])
+@pytest.mark.parametrize("name", ["prefix ends inside a page", "one kv head"])
+def test_caps_of_any_size(name, cap, dtype):
+    s = Setup(dtype=dtype, **CASES[name])
+    _check_cap(s, s.run(softcap=cap), cap)
+
+
+@pytest.mark.parametrize("cap", [20.0, 60.0, 1e3])
+def test_caps_of_scores_around_them(cap):
+    """Scores from far below the cap to far above it, in one row."""
+    s = Setup(**CASES["two groups, one without prefix"])
+    s.q *= 12
+    _check_cap(s, s.run(softcap=cap), cap)
+
+
+def test_a_large_cap_is_none():
+    """At a cap of 10^6 tanh takes a score's square times 3 10^-13 of it: the results are those without a cap, to a rounding."""
+    import torch
+    s = Setup(**CASES["tiles above 256 rows"])
+    a, b = s.run().float(), s.run(softcap=1e6).float()
+    assert (a - b).abs().max() <= 2 * s.eps * a.abs().max() and torch.isfinite(b).all()
