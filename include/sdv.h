@@ -562,7 +562,8 @@ int sdv_shared_destroy(sdv_shared *s);
  * have been written. d_q and d_out hold `rows` rows of [n_q_heads][head_dim], q_stride and out_stride elements apart (at most
  * max_rows and B * max_span of them are used) and share no memory. A score is cap * tanh(q.k / sqrt(head_dim) / cap) - slope[head] * (pos - t);
  * softcap 0: q.k / sqrt(head_dim); d_slopes [n_q_heads] fp32 or NULL: no bias. A cap of up to 64 puts a score off by 2^-21 of the
- * cap, a larger one by 2^-20 of the score; one above 10^30 counts as 10^30.
+ * cap, a larger one by 2^-20 of the score; one above 10^30 counts as 10^30, one below
+ * 2^-126 as that.
  * Groups: G > 0 cuts the batch into groups of neighbouring sequences, group g those from d_group_off[g] to
  * d_group_off[g + 1] - 1 (d_group_off [G + 1], from 0 to B, never falling; G <= B, G <= 128), which hold the same K and V at
  * positions 0 .. d_prefix_len[g] - 1: those are read through the table of the group's first sequence, so a partial page that

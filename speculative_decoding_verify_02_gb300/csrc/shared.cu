@@ -1,5 +1,6 @@
 // C ABI of the attention for groups of sequences that share a prefix.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -248,9 +249,10 @@ int sdv_shared_attention(sdv_shared *s, int layer, const void *d_q, int64_t q_st
     a.by_page = s->by_page;
     a.by_grp = s->by_grp;
     a.by_nq = s->by_nq;
-    const float scale = 1.f / std::sqrt(static_cast<float>(c.head_dim)), cap = std::min(softcap, 1e30f);
+    const float scale = 1.f / std::sqrt(static_cast<float>(c.head_dim));
     a.scale_log2 = 1.4426950408889634f * scale;
-    if (cap > 0.f) {
+    if (softcap > 0.f) {  // where 1 / cap is a normal number: below, its infinity would make a score of zero no number
+        const float cap = std::min(std::max(softcap, FLT_MIN), 1e30f);
         a.cap2 = 1.4426950408889634f * cap;
         a.to_u = scale / cap;
     }

@@ -532,3 +532,11 @@ def test_a_large_cap_is_none():
     s = Setup(**CASES["tiles above 256 rows"])
     a, b = s.run().float(), s.run(softcap=1e6).float()
     assert (a - b).abs().max() <= 2 * s.eps * a.abs().max() and torch.isfinite(b).all()
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1e-20, 1.2e-38, 1e-40, 1.5e-45])
+def test_tiny_caps(cap):
+    """All scores equal but for the cap: a mean of V, also of rows whose score is zero."""
+    s = Setup(**CASES["prefix ends inside a page"])
+    s.q[1] = 0
+    _check_cap(s, s.run(softcap=cap), cap)
