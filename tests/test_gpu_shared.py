@@ -475,6 +475,23 @@ def test_bad_values_where_narrow_and_wide_tiles_take_turns(spans, own):
         s.pool.nan_to_num_(0.5)
 
 
+@pytest.mark.parametrize("own", [40, 260])
+def test_bad_values_of_tiles_that_both_warpgroups_look_at(own):
+    """300 rows a head: a wide tile, then one of 44, an odd number of chunks each, so that the warpgroups' steps come apart. Every
+    row that sees a bad V is spoilt in every head."""
+    import torch
+    s = Setup(sizes=[1] * 60, prefix=[0] * 60, own=[own] * 60, spans=[75] * 60, groups=False, nq=32, nkv=8, D=64)
+    clean = s.run()
+    for b in range(60):
+        p = own + 5 + b
+        s.pool[0, int(s.table[b, p // s.ps]), 1, :, p % s.ps, b] = float("nan")
+    out, sees = s.run(), torch.zeros(s.rows, dtype=torch.bool, device="cuda")
+    for b in range(60):
+        sees[75 * b + 5 + b:75 * b + 75] = True
+    assert torch.equal(out[~sees], clean[~sees])
+    assert not torch.isfinite(out[sees]).all(-1).any()
+
+
 def test_bad_values_behind_a_shared_prefix():
     B = 48
     s = Setup(sizes=[30, 18], prefix=[400, 150], own=[i % 9 * 31 for i in range(B)], spans=[1 + i % 7 * 6 for i in range(B)], nq=16, nkv=4, D=64)
