@@ -591,14 +591,19 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 const uint32_t h = k_hi - (static_cast<uint32_t>(bin) << shift), width = 1u << shift;
                 const uint32_t l = h - k_lo >= width ? h - width + 1 : k_lo;
                 FilterSums s;
+                bool anew = false;  // once sums are exact, what lies before these tokens is summed up again, too
                 for (;;) {
-                    s = sums([&](float x, int) { return orderable(x + 0.f) > h; }, [&](float x, int) { return orderable(x + 0.f) >= l; });
-                    if (g.by_mass && !precise && (close(s.a, g) || close(s.b, g))) {
-                        precise = true;
+                    const unsigned long long over = anew ? hi : static_cast<unsigned long long>(h) << 32 | 0xffffffffu;
+                    s = sums([&](float x, int i) { return filter_key(x, v0 + i) > over; }, [&](float x, int) { return orderable(x + 0.f) >= l; });
+                    if (anew) {
+                        anew = false;
+                        A = s.a;
+                    } else if (g.by_mass && !precise && (close(s.a, g) || close(s.b, g))) {
+                        precise = anew = true;
                         set_total(g);
-                        continue;
+                    } else {
+                        break;
                     }
-                    break;
                 }
                 if (g.by_mass && s.a >= g.target && before > 0) {  // above this bin
                     lo = static_cast<unsigned long long>(h + 1) << 32;

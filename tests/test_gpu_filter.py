@@ -343,3 +343,27 @@ def test_binding_refusals():
         v.filter_logits(x, off, 4, x[:3], None, T)
     with pytest.raises(SdvError):
         v.sample(**dict(ok, B=0))
+
+
+
+def _crowds(rng, V, T, heavy, light):
+    """A row of one largest logit, `heavy` tokens of about its weight, and two crowds of light ones, 2^-3 to 2^-8, a unit of the last
+    place apart, in any order; a p whose border lies at most three tokens before the first crowd's end."""
+    T, m = np.float32(T), np.float32(rng.normal())
+    a = np.float32(m - T * rng.choice([0.0144, 0.02, 0.5, 1.01]) * np.log(2))
+    b = np.float32(m - T * rng.uniform(3, 8) * np.log(2))
+    x = np.full(V, np.nextafter(b, np.float32(-np.inf)))
+    x[0], x[1:1 + heavy], x[1 + heavy:1 + heavy + light] = m, a, b
+    w = np.exp((x.astype(np.float64) - float(m)) / float(T))
+    p = np.float32((w[:1 + heavy + light].sum() - rng.uniform(0, 3) * w[1 + heavy]) / w.sum())
+    return x[rng.permutation(V)], p
+
+
+def test_borders_between_neighbouring_logits():
+    """Sums of fp32 weights cannot tell the border, those that decide are exact, also of what lies before the crowd."""
+    V, rng = 393216, np.random.default_rng(17)
+    v = _verifier(V, max_batch=8)
+    noise = np.ones((8, V), dtype=np.float32)
+    for T in (0.2, 0.5, 0.8, 1.0, 1.3, 2.0):
+        x, p = zip(*(_crowds(rng, V, T, 49152 * int(rng.integers(1, 4)), int(rng.integers(20000, 220000))) for _ in range(8)))
+        _check(v, np.stack(x), noise, np.arange(9), [T] * 8, p=p)
