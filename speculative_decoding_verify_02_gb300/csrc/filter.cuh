@@ -11,7 +11,7 @@
 // edges confirm it, and its tokens alone are compared with one another.
 //
 // Whether a token is kept is decided as exact arithmetic would: sums of fp32 weights hold to 2^-17 of the total each
-// (kFilterNear); a border nearer than that is decided on weights of 2^-39 (weight_exact). Sums are integers, units of 2^-44,
+// (kFilterNear); a border nearer than that is decided on weights of 2^-37 (weight_exact). Sums are integers, units of 2^-44,
 // whose order does not matter; 64-bit floats stay out of the way of most rows: this part does them at 1/64 of fp32's rate, and
 // the first kernel, which used them for sums and settings, took 75,000 clocks a row where it is 26,000 now.
 #pragma once
@@ -139,7 +139,7 @@ __device__ __forceinline__ float filter_weight(const FilterRow &r, float x) {
     const float t = (r.m - x) * r.c_hi;
     return t < 150.f ? filter_ex2(-t) : 0.f;
 }
-// The weight as an integer times 2^-58, to 2^-39: the exponent in two fp32 parts, 2^-n/64 from a table and the rest, below
+// The weight as an integer times 2^-58, to 2^-37: the exponent in two fp32 parts, 2^-n/64 from a table and the rest, below
 // 2^-7, by the series of e^z in two parts.
 __device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, float x, const unsigned long long *table) {
     if (x == r.m) return 1ull << 58;
@@ -151,7 +151,8 @@ __device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, f
     const float f = p - static_cast<float>(n) * 0.015625f;                   // exact
     constexpr float L = -0.693147182f, L_lo = 1.90465421e-9f;                // L + L_lo = -ln 2
     const float u = f * L, u_lo = fmaf(f, L, -u) + (f * L_lo + q * L);       // z = u + u_lo
-    const float g = u_lo + u * u * (0.5f + u * (0.16666667f + u * 0.041666668f));  // e^z - 1 = u + g
+    const float g0 = u * u * (0.5f + u * (0.16666667f + u * 0.041666668f));  // e^u - 1 = u + g0
+    const float g = g0 + fmaf(u_lo, u + g0, u_lo);                           // e^z - 1 = u + g; u u_lo is up to 2^-26 (p near 25)
     const unsigned long long t58 = table[n & 63];
     const uint32_t t_hi = static_cast<uint32_t>(t58 >> 35), t_lo = static_cast<uint32_t>(t58 >> 3);  // 24 bits, 32 more
     const float tf = __uint2float_rn(t_hi) * 0x1p-23f, tl = __uint2float_rn(t_lo) * 0x1p-55f;

@@ -367,3 +367,32 @@ def test_borders_between_neighbouring_logits():
     for T in (0.2, 0.5, 0.8, 1.0, 1.3, 2.0):
         x, p = zip(*(_crowds(rng, V, T, 49152 * int(rng.integers(1, 4)), int(rng.integers(20000, 220000))) for _ in range(8)))
         _check(v, np.stack(x), noise, np.arange(9), [T] * 8, p=p)
+
+
+@pytest.mark.parametrize("least", [-32])
+def test_borders_of_crowds_of_equal_weights(least):
+    """Some hundred thousand tokens of two neighbouring logits behind a large one, and a p that brings the border within 2^least to
+    2^(least + 2) of the row's weight to a token's edge. A row's border in tokens of the first crowd is (p total - 1) / w."""
+    import torch
+    V, rng = 393216, np.random.default_rng(23)
+    v = _verifier(V, max_batch=8)
+    for T in (0.3, 0.5, 0.7, 0.9, 1.0, 1.3, 1.7, 2.4):
+        x, p, want = np.empty((8, V), dtype=np.float32), np.empty(8, dtype=np.float32), []
+        for r in range(8):
+            m = np.float32(rng.normal())
+            b = np.float32(m - np.float32(T) * rng.uniform(17, 21) * np.log(2))
+            c = np.nextafter(b, np.float32(-np.inf))
+            wb, wc = (np.exp((np.float64(y) - np.float64(m)) / np.float64(np.float32(T))) for y in (b, c))
+            n = int(rng.integers(100000, 250000))
+            total = 1 + n * wb + (V - 1 - n) * wc
+            tried = np.float32((1 + 0.9 * n * wb) / total) * np.float32(1) - np.arange(1 << 16) * np.float32(2.0 ** -24)
+            k = (tried.astype(np.float64) * total - 1) / wb
+            off = np.abs(k - np.rint(k)) * wb / total
+            i = int(np.flatnonzero((off > 2.0 ** least) & (off < 2.0 ** (least + 2)) & (k > 1) & (k < n - 2))[0])
+            x[r], x[r, 1:n + 1], x[r, 0], p[r] = c, b, m, tried[i]
+            x[r] = x[r, rng.permutation(V)]
+            want.append(1 + int(np.ceil(k[i])))
+        out, kept = _f32(x), _i32([0] * 8)
+        v.filter_logits(out, _i32(range(9)), 8, out, kept, _f32([T] * 8), top_p=_f32(p))
+        torch.cuda.synchronize()
+        assert kept.tolist() == want and (out > -np.inf).sum(-1).tolist() == want
