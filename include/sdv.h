@@ -257,7 +257,7 @@ int sdv_fork_seq(sdv_ctx *ctx, const int32_t *d_src, const int32_t *d_dst, int n
  *   top-p  of those, each before which the weights sum to less than d_top_p[b] of their total (>= 1: all),
  *   min-p  w >= d_min_p[b] (<= 0: all),
  * and always the first token; T_b <= 0 keeps it alone. Any of the three may be NULL. Decisions are those of exact
- * arithmetic to 2^-37 of the row's total weight. -inf masks a token and NaN counts as -inf: neither is kept.
+ * arithmetic to 2^-36 of the row's total weight. -inf masks a token and NaN counts as -inf: neither is kept.
  *   d_logits  fp32 rows, logits_stride floats apart (>= vocab); `rows` of them are there, at most the
  *             context's max_rows and B times its max_span are used. A span past them or longer than max_span sets SDV_ERR_ARG and its rows are
  *             left alone, as are rows of no span.

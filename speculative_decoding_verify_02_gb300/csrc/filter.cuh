@@ -11,7 +11,7 @@
 // edges confirm it, and its tokens alone are compared with one another.
 //
 // Whether a token is kept is decided as exact arithmetic would: sums of fp32 weights hold to 2^-17 of the total each
-// (kFilterNear); a border nearer than that is decided on weights of 2^-37 (weight_exact). Sums are integers, units of 2^-44,
+// (kFilterNear); a border nearer than that is decided on weights of 2^-37 (weight_exact), to 2^-36 of the total. Sums are integers, units of 2^-44,
 // whose order does not matter; 64-bit floats stay out of the way of most rows: this part does them at 1/64 of fp32's rate, and
 // the first kernel, which used them for sums and settings, took 75,000 clocks a row where it is 26,000 now.
 #pragma once
@@ -139,6 +139,10 @@ __device__ __forceinline__ float filter_weight(const FilterRow &r, float x) {
     const float t = (r.m - x) * r.c_hi;
     return t < 150.f ? filter_ex2(-t) : 0.f;
 }
+// v 2^-bits, rounded
+__device__ __forceinline__ unsigned long long filter_round(unsigned long long v, int bits) {
+    return bits ? (v >> bits) + (v >> (bits - 1) & 1) : v;
+}
 // The weight as an integer times 2^-58, to 2^-37: the exponent in two fp32 parts, 2^-n/64 from a table and the rest, below
 // 2^-7, by the series of e^z in two parts.
 __device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, float x, const unsigned long long *table) {
@@ -161,7 +165,7 @@ __device__ __forceinline__ unsigned long long weight_exact(const FilterRow &r, f
     const float a37 = a * 0x1p37f;
     const int a_hi = __float2int_rn(a37), a_lo = __float2int_rn((a37 - __int2float_rn(a_hi)) * 0x1p21f), b46 = __float2int_rn(b * 0x1p45f);
     const long long w = static_cast<long long>(t58) + (static_cast<long long>(a_hi) << 21) + a_lo + (static_cast<long long>(b46) << 13);
-    return static_cast<unsigned long long>(w) >> (n >> 6);
+    return filter_round(static_cast<unsigned long long>(w), n >> 6);
 }
 
 // Which of the four a reduction takes along.
@@ -173,8 +177,8 @@ __device__ __forceinline__ void filter_join(FilterSums &s, const FilterSums &o) 
     if constexpr (F & kHi) s.hi = o.hi > s.hi ? o.hi : s.hi;
     if constexpr (F & kLo) s.lo = o.lo < s.lo ? o.lo : s.lo;
 }
-// Over the row, by every thread of every CTA, who all get the result. `shift`: the sums lose that many bits once a warp's
-// are added up, which keeps theirs from overflowing.
+// Over the row, by every thread of every CTA, who all get the result. `shift`: the sums lose that many bits on the way, half once a
+// warp's are added up and the rest once a CTA's are, which keeps theirs from overflowing.
 template <int F>
 __device__ __forceinline__ FilterSums filter_reduce(FilterShared &sh, FilterSums s, int ctas, int rank, int turn, int shift = 0) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -191,14 +195,17 @@ __device__ __forceinline__ FilterSums filter_reduce(FilterShared &sh, FilterSums
         }
     };
     across(16);
-    s.a >>= shift;
-    s.b >>= shift;
+    const int late = shift / 2;
+    s.a = filter_round(s.a, shift - late);
+    s.b = filter_round(s.b, shift - late);
     if (lane == 0) sh.warp[warp] = s;
     __syncthreads();
     FilterSums (&part)[kFilterCluster] = sh.part[turn & 1];
     if (warp == 0) {  // this CTA's to every CTA
         s = sh.warp[lane % W];
         across(W / 2);
+        s.a = filter_round(s.a, late);
+        s.b = filter_round(s.b, late);
         if (lane < ctas) {
             const uint32_t to = mapa_shared(smem_u32(&part[rank]), lane);
             if constexpr (F & kSumA) st_dsmem_u64(to, s.a);
@@ -505,6 +512,8 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             }
             __syncthreads();
         };
+        // Exact sums: a token's weight is rounded to 2^-57, a thread's sum to 2^-51, a warp's to 2^-47 and a CTA's to 2^-44. That is
+        // off by 2^-38.5 at most, of 2^18.6 tokens; by tokens cut at 2^-51, all the same way where they are equal, it would be 2^-33.
         // Weight of the tokens for which in0 and in1 hold, and the keys for which in1 holds but not in0: smallest and largest.
         auto sums = [&](auto in0, auto in1) {
             FilterSums s = {0, 0, 0ull, none};
@@ -514,7 +523,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                 if (!in1(x, i)) return;
                 const bool both = in0(x, i);
                 if (precise) {
-                    const unsigned long long w = weight_exact(r, x, sh.table) >> 7;  // a thread adds up to 96
+                    const unsigned long long w = filter_round(weight_exact(r, x, sh.table), 1);  // a thread adds up to 96
                     e1 += w;
                     if (both) e0 += w;
                 } else {
@@ -528,8 +537,8 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     s.lo = k < s.lo ? k : s.lo;
                 }
             });
-            s.a = precise ? e0 : __float2ull_rn(f0 * 0x1p51f);
-            s.b = precise ? e1 : __float2ull_rn(f1 * 0x1p51f);
+            s.a = precise ? filter_round(e0, 6) : __float2ull_rn(f0 * 0x1p51f);
+            s.b = precise ? filter_round(e1, 6) : __float2ull_rn(f1 * 0x1p51f);
             return filter_reduce<kSumA | kSumB | kHi | kLo>(sh, s, ctas, rank, turn++, 7);
         };
         auto set_total = [&](FilterGoal &g) {

@@ -369,7 +369,7 @@ def test_borders_between_neighbouring_logits():
         _check(v, np.stack(x), noise, np.arange(9), [T] * 8, p=p)
 
 
-@pytest.mark.parametrize("least", [-32])
+@pytest.mark.parametrize("least", [-32, -35.5])
 def test_borders_of_crowds_of_equal_weights(least):
     """Some hundred thousand tokens of two neighbouring logits behind a large one, and a p that brings the border within 2^least to
     2^(least + 2) of the row's weight to a token's edge. A row's border in tokens of the first crowd is (p total - 1) / w."""
@@ -385,7 +385,7 @@ def test_borders_of_crowds_of_equal_weights(least):
             wb, wc = (np.exp((np.float64(y) - np.float64(m)) / np.float64(np.float32(T))) for y in (b, c))
             n = int(rng.integers(100000, 250000))
             total = 1 + n * wb + (V - 1 - n) * wc
-            tried = np.float32((1 + 0.9 * n * wb) / total) * np.float32(1) - np.arange(1 << 16) * np.float32(2.0 ** -24)
+            tried = np.float32((1 + 0.9 * n * wb) / total) * np.float32(1) - np.arange(1 << 18) * np.float32(2.0 ** -24)
             k = (tried.astype(np.float64) * total - 1) / wb
             off = np.abs(k - np.rint(k)) * wb / total
             i = int(np.flatnonzero((off > 2.0 ** least) & (off < 2.0 ** (least + 2)) & (k > 1) & (k < n - 2))[0])
