@@ -977,7 +977,8 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             if (rank == 0 && tid == 0) a.n_kept[row] = kept;
         }
     } else {
-        // the race: w / noise, the two largest of a thread; 2^-14 apart they are decided. Of a list CTA 0 alone runs it.
+        // the race: w / noise, the two largest of a thread; 2^-14 apart they are decided, if fp32 holds them. Of a list CTA 0 alone
+        // runs it.
         const float *noise = a.noise + row * a.noise_stride;
         const int racers = listed ? 1 : ctas;
         if (!listed || rank == 0) {
@@ -994,7 +995,11 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     });
                 }
             };
-            auto score = [&](float x, int v) { return filter_weight(r, x) * __frcp_rn(noise[v]); };
+            // infinite where a quotient could pass fp32's range; weights flushed to zero are below 2^-86 of any noise else
+            auto score = [&](float x, int v) {
+                const float e = noise[v];
+                return e > 0.f && e < 0x1p-40f ? INFINITY : filter_weight(r, x) * __frcp_rn(e);
+            };
             float s1 = -1.f, s2 = -1.f;
             int at = 0, count = 0;
             runners([&](float x, int v) {
@@ -1010,7 +1015,8 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
             s = filter_reduce<kSumA | kHi>(sh, s, racers, rank, turn++);
             kept = static_cast<int>(s.a);
             unsigned long long won = s.hi ? s.hi : top;  // no noise above zero
-            const float best = __uint_as_float(static_cast<uint32_t>(s.hi >> 32)), near = best * (1.f - 0x1p-14f);
+            const float best = __uint_as_float(static_cast<uint32_t>(s.hi >> 32));
+            const float near = best < INFINITY && best > 0x1p-60f ? best * (1.f - 0x1p-14f) : 0.f;  // else all
             FilterSums t = {(s1 >= near && s1 >= 0.f ? 1ull : 0ull) + (s2 >= near && s2 >= 0.f ? 1ull : 0ull), 0, 0ull, none};
             t = filter_reduce<kSumA>(sh, t, racers, rank, turn++);
             if (t.a > 1) {  // near ones again, in 64 bits

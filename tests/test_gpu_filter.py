@@ -396,3 +396,21 @@ def test_borders_of_crowds_of_equal_weights(least):
         v.filter_logits(out, _i32(range(9)), 8, out, kept, _f32([T] * 8), top_p=_f32(p))
         torch.cuda.synchronize()
         assert kept.tolist() == want and (out > -np.inf).sum(-1).tolist() == want
+
+
+@pytest.mark.parametrize("V", [40, 2048, 9001])
+def test_noise_of_any_size(V):
+    """Noise from the smallest positive fp32 to the largest: quotients past fp32's range are compared like all others."""
+    rng = np.random.default_rng(V)
+    R = 60
+    x = (-60 * rng.random((R, V))).astype(np.float32)
+    noise = np.maximum(10.0 ** rng.uniform(-46, 3, (R, V)), 1.5e-45).astype(np.float32)
+    noise[8:16] = rng.exponential(size=(8, V))
+    for r in range(8, 16):          # a few tiny ones among usual ones
+        noise[r, rng.integers(0, V, 3)] = [1.5e-45, 1e-39, 1e-30]
+    x[16:] *= 3
+    noise[56:] = 10.0 ** rng.uniform(-20, 38, (4, V))
+    v = _verifier(V)
+    assert (noise > 0).all() and np.isfinite(noise).all()
+    for cuts in (dict(), dict(k=[30] * R), dict(p=[0.999] * R), dict(m=[1e-30] * R)):
+        _check(v, x, noise, np.arange(R + 1), [1.0] * R, **cuts)
