@@ -447,7 +447,7 @@ struct Int {
     static constexpr int value = N;
 };
 struct SShared {
-    uint64_t full[8], empty[8], s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_empty, turn[2];
+    uint64_t full[8], empty[8], s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_empty, q_first, turn[2];
     uint32_t tmem;
     // keys of a chunk that are not finite, as bits: [chunks that one warpgroup looks at, that both do][turn][warpgroup that found them]
     uint32_t bad[2][2][2][4];
@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
         }
         mbar_init(&sh.q_full, 256);
         mbar_init(&sh.q_empty, 2);
+        mbar_init(&sh.q_first, 256);
         fence_mbar_init();
     }
     if (warp == 10) {
@@ -545,14 +546,15 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
             };
             auto ask = [&](int c) { return wants(c) ? table[a.by_page.div(t00 + c * kSKeys + j * a.box_rows)] : -1; };
             int page = a.box_rows ? ask(0) : 0;
-            // at the start the queries come first: behind everybody's keys they would wait for 5,000 clocks
-            if (first && v && ok) ok = mbar_wait(&sh.q_full, 0);
+            // at the start the queries come first: behind everybody's keys they would wait for 5,000 clocks. A barrier of their own,
+            // of one phase: the second queries may be there before this warp looks, and then the phase of q_full has passed by.
+            if (first && v && ok) ok = mbar_wait(&sh.q_first, 0);
 #pragma unroll 1
             for (int c = 0; c < n; ++c) {
                 const int st = (v ? Q::DEPTH : 0) + c % Q::DEPTH, use = filling(c), t0 = t00 + c * kSKeys;
                 const uint32_t dst = kv_s + st * Q::SLOT;
                 uint64_t *full = &sh.full[st];
-                if (first && !v && c == 1 && ok) ok = mbar_wait(&sh.q_full, 0);
+                if (first && !v && c == 1 && ok) ok = mbar_wait(&sh.q_first, 0);
                 if (a.box_rows) {
                     int row = a.pool_rows;  // zeros
                     if (!wants(c)) {
@@ -726,9 +728,11 @@ __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_
             }
             if (a.q_vec) {
                 cp_async_arrive(&sh.q_full);
+                if (pieces == 1) cp_async_arrive(&sh.q_first);
             } else {
                 fence_async_smem();
                 mbar_arrive(&sh.q_full);
+                if (pieces == 1) mbar_arrive(&sh.q_first);
             }
         };
         if (more) load_q(p);

@@ -498,6 +498,19 @@ def test_bad_values_behind_a_shared_prefix():
     _bad_values(s, {b: int(s.base[b]) + min(2, int(s.spans[b]) - 1) for b in range(1, B, 3)}, np.nan)
 
 
+def test_many_tiles_of_one_chunk():
+    """A CTA's queries follow one another as fast as they can: no warp may miss those it waits for. No wait runs out, the same bits."""
+    import torch
+    s = Setup(sizes=[1] * 250, prefix=[0] * 250, own=[i % 90 for i in range(250)], spans=[1 + i % 3 for i in range(250)], groups=False,
+              nq=16, nkv=8, D=128)
+    ref = s.run()
+    s.check(ref)
+    out = torch.zeros_like(ref)
+    for _ in range(200):
+        s.plan.attention(0, s.q, s.d_table, s.d_off, s.d_base, s.B, s.max_span, out)
+    assert torch.equal(out, ref) and s.plan.get_status() == 0
+
+
 # ---------------------------------------------------------------- caps of any size
 
 def _check_cap(s, out, cap, window=0):
