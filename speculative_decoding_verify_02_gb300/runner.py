@@ -95,15 +95,15 @@ class SpecLoop:
                        top_p=None, min_p=None):
         """Forward one prompt as sequence 0 and let every other sequence continue it (fork_seq): the prompt is computed and
         held once. With `noise` (float32 [B, vocab], exponential) each sequence's first token is drawn from the prompt's
-        last row at `temperature` (float32 [B]) within top_k, top_p and min_p, else it is the argmax. Returns the
-        first tokens (host numpy) and leaves them in self.first. The sequences must be empty."""
+        last row at `temperature` (float32 [B]) within top_k, top_p and min_p, else (none of them given) it is the argmax.
+        Returns the first tokens (host numpy) and leaves them in self.first. The sequences must be empty."""
         import torch
         B, v = self.B, self.v
         if len(prompt) == 0:
             raise ValueError("prompt: empty")
-        assert chunk <= v.ccfg.max_span and chunk <= v.ccfg.max_rows
-        if noise is not None and temperature is None:
+        if any(x is not None for x in (noise, temperature, top_k, top_p, min_p)) and (noise is None or temperature is None):
             raise ValueError("drawing the first tokens needs temperature and noise")
+        assert chunk <= v.ccfg.max_span and chunk <= v.ccfg.max_rows
         p = torch.from_numpy(np.asarray(prompt, dtype=np.int32)).cuda()
         am = _i32(chunk)
         logits = None

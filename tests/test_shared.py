@@ -81,3 +81,13 @@ def test_a_step_with_cuts_needs_uniforms(sdv):
     for kw in (dict(top_k=1), dict(top_p=1), dict(min_p=1)):
         with pytest.raises(ValueError, match="uniforms"):
             loop.step(**kw)
+
+
+def test_a_drawn_first_token_needs_noise(sdv):
+    from speculative_decoding_verify_02_gb300.runner import SpecLoop
+    loop = SpecLoop.__new__(SpecLoop)
+    loop.v, loop.B = None, 4
+    for kw in (dict(temperature=1), dict(top_k=1), dict(top_p=1), dict(min_p=1), dict(temperature=1, top_p=1), dict(noise=1),
+               dict(noise=1, top_k=1)):
+        with pytest.raises(ValueError, match="temperature and noise"):
+            loop.prefill_shared([1, 2], chunk=1, **kw)
