@@ -39,6 +39,7 @@ class SpecLoop:
         self.first = _i32(B)
         self.budget = _i32(B)
         self.logits = None
+        self.cut_logits = {}  # for a caller's logits, by their shape: captured steps go on writing there
         self.graph = None
         self.stream = torch.cuda.current_stream()
 
@@ -142,22 +143,27 @@ class SpecLoop:
         [max_rows] in [0, 1)) and `noise` (float32 [B, vocab], exponential) the drafts are accepted
         against the target's probabilities at `temperature` instead of matched by token;
         `draft_probs` [max_rows, vocab] is the drafter's distribution (None: certain drafts). All
-        three are read on the device, so a captured step takes what they hold when it is replayed. top_k (int32 [B]),
+        three are read on the device, so a captured step takes what they hold when it is replayed.
+        They are the step's random numbers: `seed` is that of the token-matching step alone. top_k (int32 [B]),
         top_p and min_p (float32 [B]) cut the target's distribution first (filter_logits); `draft_probs` is then best that
-        of a drafter with the same cuts.
-        They are the step's random numbers: `seed` is that of the token-matching step alone."""
+        of a drafter with the same cuts. `logits`, if given, takes the model's logits, before any cut."""
         v, B = self.v, self.B
         cuts = top_k is not None or top_p is not None or min_p is not None
         if uniforms is None and (noise is not None or draft_probs is not None or cuts):
             raise ValueError("noise, draft_probs and the cuts belong to the acceptance against probabilities, which needs uniforms")
+        target = logits  # what the drafts are accepted against
         if uniforms is not None:
+            import torch
             if temperature is None or noise is None:
                 raise ValueError("acceptance against probabilities needs temperature, uniforms and noise")
             if logits is None:
                 if self.logits is None:
-                    import torch
                     self.logits = torch.empty(self.max_rows, v.mcfg.vocab, dtype=torch.float32, device="cuda")
-                logits = self.logits
+                target = logits = self.logits
+            elif cuts:
+                target = self.cut_logits.get(logits.shape)
+                if target is None:
+                    target = self.cut_logits[logits.shape] = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         v.propose(drafter, table, table_stride, B, self.max_span, self.tokens, self.row_off, self.required)
         v.ensure_capacity(self.required, B)
         if temperature is None or uniforms is not None:
@@ -167,8 +173,8 @@ class SpecLoop:
                                    self.argmax, logits)
         if uniforms is not None:
             if cuts:
-                v.filter_logits(logits, self.row_off, B, logits, None, temperature, top_k=top_k, top_p=top_p, min_p=min_p)
-            v.accept_sampled(self.tokens, self.row_off, logits, temperature, uniforms, noise, B, self.max_span,
+                v.filter_logits(logits, self.row_off, B, target, None, temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+            v.accept_sampled(self.tokens, self.row_off, target, temperature, uniforms, noise, B, self.max_span,
                              self.n_accept, self.committed, self.n_commit, self.new_len, draft_probs=draft_probs)
         else:
             v.accept_greedy(self.tokens, self.row_off, self.argmax, B, self.max_span, self.n_accept, self.committed,

@@ -91,3 +91,31 @@ def test_a_drawn_first_token_needs_noise(sdv):
                dict(noise=1, top_k=1)):
         with pytest.raises(ValueError, match="temperature and noise"):
             loop.prefill_shared([1, 2], chunk=1, **kw)
+
+
+def test_a_step_with_cuts_leaves_the_callers_logits(sdv):
+    """The model's logits stay in the caller's tensor; the filter writes, and the acceptance reads, another one, the same for the
+    same shape. Without a tensor of the caller's the filter works in place."""
+    from speculative_decoding_verify_02_gb300.runner import SpecLoop
+    calls = {}
+
+    class Fake:
+        mcfg = sdv.ModelCfg(vocab=6)
+
+        def __getattr__(self, name):
+            return lambda *a, **kw: calls.setdefault(name, []).append(a)
+
+    loop = SpecLoop.__new__(SpecLoop)
+    loop.v, loop.B, loop.max_rows, loop.max_span, loop.logits, loop.cut_logits = Fake(), 2, 4, 2, torch.zeros(4, 6), {}
+    for name in ("tokens", "row_off", "required", "argmax", "n_accept", "committed", "n_commit", "new_len"):
+        setattr(loop, name, None)
+    kw = dict(temperature=1, uniforms=1, noise=1, top_k=1)
+    mine, other = torch.zeros(4, 6), torch.zeros(5, 6)
+    for t in (mine, mine, other, None):
+        loop.step(logits=t, **kw)
+    loop.step(logits=mine, temperature=1, uniforms=1, noise=1)
+    model, (src, out), read = [c[-1] for c in calls["spec_forward"]], zip(*((c[0], c[3]) for c in calls["filter_logits"])), \
+        [c[2] for c in calls["accept_sampled"]]
+    assert model[0] is mine and model[2] is other and model[3] is loop.logits and model[4] is mine
+    assert all(a is b for a, b in zip(src, model)) and all(a is b for a, b in zip(read, out)) and read[4] is mine
+    assert out[0] is not mine and out[0].shape == mine.shape and out[1] is out[0] and out[2].shape == other.shape and out[3] is loop.logits
