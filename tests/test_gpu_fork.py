@@ -192,6 +192,27 @@ def test_sliding_window_models_are_refused():
     assert e.value.code == SDV_ERR_UNSUPPORTED
 
 
+def test_a_rewind_captured_before_the_first_fork():
+    """A graph's rewind, made while nothing was shared, releases shared pages and refuses lengths inside of them all the same."""
+    import torch
+    from speculative_decoding_verify_02_gb300 import SDV_ERR_ARG
+    t = Pair(n_pages=60, B=9)
+    t.grow([70, 33] + [-1] * 7)
+    lengths = _i32([-1] * 9)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        t.v.rewind_cache(lengths, 9)
+    t.fork([0, 0, 1, 0, 1, 0, 0], [2, 3, 4, 5, 6, 7, 8])
+    for n, ok in (([-1, -1, 0, 64, 32, -1, 0, 70, 16], True), ([20] + [-1] * 8, False), ([0, 0] + [-1] * 7, True), ([-1] * 9, True),
+                  ([0] * 9, True)):
+        lengths.copy_(_i32(n))
+        g.replay()
+        if ok:
+            t.o.rewind(n)
+        t.same(0 if ok else SDV_ERR_ARG)
+    assert len(t.o.free) == 60
+
+
 def test_a_page_goes_back_with_its_last_holder():
     t = Pair(n_pages=40, B=6)
     t.grow([70, -1, -1, -1, -1, -1])
