@@ -261,7 +261,8 @@ int sdv_fork_seq(sdv_ctx *ctx, const int32_t *d_src, const int32_t *d_dst, int n
  *   d_logits  fp32 rows, logits_stride floats apart (>= vocab); `rows` of them are there, at most the
  *             context's max_rows and B times its max_span are used. A span past them or longer than max_span sets SDV_ERR_ARG and its rows are
  *             left alone, as are rows of no span.
- *   d_out     fp32 rows, out_stride floats apart: the kept logits as they are, -inf elsewhere. d_logits itself will do.
+ *   d_out     fp32 rows, out_stride floats apart: the kept logits as they are, -inf elsewhere. d_logits itself will do, with its
+ *             stride (else SDV_ERR_ARG); otherwise the two share no memory.
  *   d_n_kept  [rows] int32, or NULL: tokens kept.
  * A row without a logit above -inf keeps none (SDV_ERR_DEVICE). The rows made here can go to sdv_accept_sampled, which then
  * verifies drafts against the filtered distribution. A vocabulary above 393,216 is SDV_ERR_UNSUPPORTED. */

@@ -1138,6 +1138,7 @@ int sdv_filter_logits(sdv_ctx *ctx, const float *d_logits, int64_t logits_stride
     FilterArgs a{};
     if (!filter_args(ctx, d_logits, logits_stride, rows, d_row_off, B, d_temperature, d_top_k, d_top_p, d_min_p, &a)) return SDV_ERR_ARG;
     if (!d_out || out_stride < ctx->m.vocab) return SDV_ERR_ARG;
+    if (d_out == d_logits && out_stride != logits_stride && rows > 1) return SDV_ERR_ARG;  // rows over one another's
     a.out = d_out;
     a.out_stride = out_stride;
     a.n_kept = d_n_kept;

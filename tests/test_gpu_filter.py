@@ -414,3 +414,19 @@ def test_noise_of_any_size(V):
     assert (noise > 0).all() and np.isfinite(noise).all()
     for cuts in (dict(), dict(k=[30] * R), dict(p=[0.999] * R), dict(m=[1e-30] * R)):
         _check(v, x, noise, np.arange(R + 1), [1.0] * R, **cuts)
+
+
+def test_in_place_rows_lie_where_the_logits_do():
+    import torch
+    from speculative_decoding_verify_02_gb300 import SdvError
+    v = _verifier(3000)
+    room = torch.randn(8 * 3000, device="cuda")
+    x, far = room[:4 * 3000].view(4, 3000), room.as_strided((4, 3000), (6000, 1))
+    keep, off, T = room.clone(), _i32(range(5)), _f32([1.0] * 4)
+    with pytest.raises(SdvError):
+        v.filter_logits(x, off, 4, far, None, T, top_k=_i32([3] * 4))
+    assert torch.equal(room, keep)
+    v.filter_logits(far, off, 4, far, None, T, top_k=_i32([3] * 4))
+    assert ((far > -np.inf).sum(-1) == 3).all() and torch.equal(room[3000:6000], keep[3000:6000])
+    v.filter_logits(x[:1], off[:2], 1, room.as_strided((1, 3000), (6000, 1)), None, T, top_k=_i32([2]))
+    assert int((x[0] > -np.inf).sum()) == 2
