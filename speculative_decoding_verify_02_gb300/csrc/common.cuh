@@ -250,7 +250,6 @@ __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
-// Every thread of every CTA in the cluster must reach this (warp-converged).
 __device__ __forceinline__ float2 ld_dsmem_f2(uint32_t addr) {
     float2 v;
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
@@ -262,17 +261,18 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
                  : "r"(addr));
     return v;
 }
-// split cluster barrier: arrive once this CTA's reads of other CTAs' shared memory are done, wait
-// before leaving (no CTA exits while another may still read its shared memory)
 __device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// split cluster barrier: arrive once this CTA's reads of other CTAs' shared memory are done, wait
+// before leaving (no CTA exits while another may still read its shared memory)
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Every thread of every CTA in the cluster must reach this (warp-converged).
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

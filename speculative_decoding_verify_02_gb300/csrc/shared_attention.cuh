@@ -9,10 +9,11 @@
 // window if there is one.
 //
 // What bounds it (bf16, 32 heads on 8 of 128 dims; pages of 16; the whole call in a graph):
-//   16 x 8 rows after 32,768 shared keys  81 us, 850 TFLOP/s: the tensor cores, whose products take 81 % of a chunk. Those with V
+//   16 x 8 rows after 32,768 shared keys  84 us, 820 TFLOP/s: the tensor cores, whose products take 81 % of a chunk. Those with V
 //                                         are twice the scores', as p enters in two 16-bit planes
-//   64 sequences of one row after them, up to 512 keys of their own   66 us, 3.1 TB/s: two fifths of the time are the sequences' own tiles,
-//                                         64 x 8 of 4 rows, 11,300 clocks each, while the device reads 5 TB/s
+//   64 sequences of one row after them, up to 512 keys of their own   67 us, 3.0 TB/s: a third of the time are the sequences' own tiles,
+//                                         64 x 8 of 4 rows, 11,300 clocks each: two steps of a warpgroup's chain (below) one
+//                                         after the other, at 3.4 TB/s; not the memory
 //   8 x 8 rows after 848 shared keys      18 us: latency, of the plan (5,600 clocks), of the first loads and of code that no
 //                                         cache holds, of the join (4 us)
 // Why two planes: one leaves p a relative error of 2^-9, which the sum over alike keys keeps; the result then is up to twice as far off
@@ -470,7 +471,7 @@ struct STile {
 };
 // ------------------------------------------------------------------ attention
 // One CTA an SM; a piece of the line after another. EXTRA: scores with a cap or a bias.
-// A batch of 16 sequences of 512 to 4,096 keys, up to 32 rows a tile, takes 41 us, 50 with a cap: each warpgroup's chain of scores, softmax
+// A batch of 16 sequences of 512 to 4,096 keys, up to 32 rows a tile, takes 41 us, 48 with a cap: each warpgroup's chain of scores, softmax
 // and product, 5,600 clocks a chunk or 7,400, of which two run at once (of 512 to 2,048 keys 28.7 us, 26.4 where L2 holds them).
 template <typename T, int D, bool EXTRA>
 __global__ void __launch_bounds__(kSThreads, 1) shared_attn_kernel(const __grid_constant__ CUtensorMap pool,
