@@ -11,9 +11,9 @@
 // edges confirm it, and its tokens alone are compared with one another.
 //
 // Whether a token is kept is decided as exact arithmetic would: sums of fp32 weights hold to 2^-17 of the total each
-// (kFilterNear); a border nearer than that is decided on weights of 2^-37 (weight_exact), to 2^-36 of the total. Sums are integers, units of 2^-44,
-// whose order does not matter; 64-bit floats stay out of the way of most rows: this part does them at 1/64 of fp32's rate, and
-// the first kernel, which used them for sums and settings, took 75,000 clocks a row where it is 26,000 now.
+// (kFilterNear); a border nearer than that is decided on weights of 2^-37 (weight_exact), to 2^-36 of the total. Sums are
+// integers, units of 2^-44, whose order does not matter; 64-bit floats stay out of the way of most rows: this part does them at
+// 1/64 of fp32's rate, and the first kernel, which used them for sums and settings, took 75,000 clocks a row where it is 26,000 now.
 #pragma once
 
 #include <float.h>
@@ -995,7 +995,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) filter_kernel(const __grid_
                     });
                 }
             };
-            // infinite where a quotient could pass fp32's range; weights flushed to zero are below 2^-86 of any noise else
+            // infinite where a quotient could pass fp32's range; elsewhere a weight that was flushed to zero scores below 2^-86
             auto score = [&](float x, int v) {
                 const float e = noise[v];
                 return e > 0.f && e < 0x1p-40f ? INFINITY : filter_weight(r, x) * __frcp_rn(e);
